@@ -18,7 +18,7 @@ LIB = os.path.join(PKG, "libgs.so")
 MEASURE_LIB = os.path.join(PKG, "libgs_measure.so")
 OBJDIR = os.path.join(PKG, "_build")
 SOURCES = ["api.hip", "preprocess.hip", "binning.hip", "render.hip", "preprocess_bwd.hip", "train.hip",
-           "densify.hip", "debug.hip"]
+           "densify.hip", "debug.hip", "linear.hip", "clip.hip"]
 MEASURE_SOURCES = ["calibrate.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -59,6 +59,23 @@ class GsGaussianSet(C.Structure):
                 ("exp_avg_sq", C.c_void_p * 5), ("densify_accum", C.c_void_p), ("densify_count", C.c_void_p)]
 
 
+class GsLinear(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("n_in", C.c_int32), ("n_out", C.c_int32), ("dtype", C.c_int32),
+                ("act", C.c_int32), ("ld_x", C.c_int64), ("ld_y", C.c_int64), ("ld_res", C.c_int64),
+                ("ld_dx", C.c_int64)]
+
+
+class GsGradTensor(C.Structure):
+    _fields_ = [("grad", C.c_void_p), ("out", C.c_void_p), ("count", C.c_int64), ("dtype", C.c_int32)]
+
+
+class GsAdamTensor(C.Structure):
+    _fields_ = [("param", C.c_void_p), ("grad", C.c_void_p), ("exp_avg", C.c_void_p), ("exp_avg_sq", C.c_void_p),
+                ("copy", C.c_void_p), ("rows", C.c_int64), ("row_len", C.c_int32), ("col_begin", C.c_int32),
+                ("col_end", C.c_int32), ("normalize_rows", C.c_int32), ("grad_dtype", C.c_int32),
+                ("copy_dtype", C.c_int32), ("lr", C.c_float)]
+
+
 SYMBOLS = ["gs_error_string", "gs_version", "gs_tile_grid", "gs_preprocess", "gs_preprocess_colorjac",
            "gs_bin_workspace_size",
            "gs_bin_sort", "gs_bin_sort_noalloc", "gs_bin_scratch_bytes", "gs_debug_sort_wait_limit", "gs_bin_keys", "gs_render_fwd", "gs_render_fwd_loss",
@@ -68,7 +85,9 @@ SYMBOLS = ["gs_error_string", "gs_version", "gs_tile_grid", "gs_preprocess", "gs
            "gs_preprocess_views", "gs_bin_workspace_size_views", "gs_bin_sort_views", "gs_render_fwd_views",
            "gs_render_fwd_loss_views", "gs_render_bwd_views", "gs_preprocess_bwd_views",
            "gs_preprocess_bwd_adam_views", "gs_count_pairs_views", "gs_count_nonfinite",
-           "gs_preprocess_h16", "gs_render_fwd_h16", "gs_render_bwd_h16", "gs_count_pairs_h16"]
+           "gs_preprocess_h16", "gs_render_fwd_h16", "gs_render_bwd_h16", "gs_count_pairs_h16",
+           "gs_linear_fwd", "gs_linear_bwd_workspace_size", "gs_linear_bwd", "gs_grad_workspace_size", "gs_grad_norm",
+           "gs_grad_clip", "gs_adam_step_clipped"]
 MAX_VIEWS = 8
 PARAM_ORDER = ("means", "log_scales", "quats", "opacity_logits", "sh")
 
@@ -130,6 +149,13 @@ def load_library(path=LIB_PATH):
     lib.gs_render_fwd_h16.argtypes = [P(GsCamera), P(GsSettings), _i32] + [_vp] * 9 + [_vp]
     lib.gs_render_bwd_h16.argtypes = [P(GsCamera), P(GsSettings), _i32] + [_vp] * 9 + [_i32, _vp]
     lib.gs_count_pairs_h16.argtypes = [P(GsCamera), P(GsSettings), _i32, _vp, _vp, _vp, _vp, _vp, _vp]
+    lib.gs_linear_fwd.argtypes = [P(GsLinear)] + [_vp] * 5 + [_vp]
+    lib.gs_linear_bwd_workspace_size.argtypes = [P(GsLinear), P(C.c_size_t)]
+    lib.gs_linear_bwd.argtypes = [P(GsLinear)] + [_vp] * 7 + [_vp, C.c_size_t, _vp]
+    lib.gs_grad_workspace_size.argtypes = [_i32, P(C.c_size_t)]
+    lib.gs_grad_norm.argtypes = [_i32, P(GsGradTensor), C.c_float, _vp, _vp, C.c_size_t, _vp]
+    lib.gs_grad_clip.argtypes = [_i32, P(GsGradTensor), C.c_float, _vp, _vp, C.c_size_t, _vp]
+    lib.gs_adam_step_clipped.argtypes = [_i32, P(GsAdamTensor), C.c_float, C.c_float, C.c_float, _i32, _vp, _vp]
     for name in SYMBOLS:
         if name not in ("gs_error_string",):
             getattr(lib, name).restype = C.c_int
@@ -730,6 +756,138 @@ def gs_count_pairs_views(cams, settings, n, tile_ranges, point_list, splats, cou
                                              _p(counts, torch.int64), _p(evaluated_px, torch.int32, "evaluated_px"),
                                              _stream())
     _check(rc, "gs_count_pairs_views")
+
+
+# ---------------------------------------------------------------------------
+# Networks beside the Gaussians: the fused linear layer, gradient clipping and
+# the clipped Adam step (the classes over them are in network.py).
+# ---------------------------------------------------------------------------
+
+DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+CLIP_STATE_FLOATS = 4
+
+
+def _rows(t, shape, dtype, name):
+    """(device pointer, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise GsError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype != dtype:
+        raise GsError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise GsError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    s0, s1 = t.stride()
+    if s1 != 1 and shape[1] > 1:
+        raise GsError(f"{name} must have contiguous rows")
+    if shape[0] <= 1:
+        s0 = shape[1]
+    return t.data_ptr(), s0
+
+
+def _linear_args(x, w, bias, act):
+    """GsLinear of x [rows, n_in] and w [n_out, n_in] with its dtype, and the device pointers of x, w and bias."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise GsError("x and w must be 2-D tensors")
+    if x.dtype not in DTYPES:
+        raise GsError(f"x must be float32, float16 or bfloat16, got {x.dtype}")
+    if act not in ACTS:
+        raise GsError(f"act must be one of {sorted(ACTS)}, got {act!r}")
+    rows, n_in = x.shape
+    n_out = w.shape[0]
+    d = GsLinear(rows, n_in, n_out, DTYPES[x.dtype], ACTS[act])
+    px, d.ld_x = _rows(x, (rows, n_in), x.dtype, "x")
+    if w.shape != (n_out, n_in):
+        raise GsError(f"w must have shape [n_out, {n_in}], got {tuple(w.shape)}")
+    if bias is not None and bias.shape != (n_out,):
+        raise GsError(f"bias must have shape ({n_out},), got {tuple(bias.shape)}")
+    return d, px, _p(w, x.dtype, "w"), _p(bias, x.dtype, "bias")
+
+
+def gs_linear_fwd(x, w, bias, residual, y, act="none"):
+    """y [rows, n_out] = act(x w^T + bias) + residual; bias and residual may be None.  Rows of x, residual and y
+    may be strided; a residual with row stride 0 is one row for all."""
+    d, px, pw, pb = _linear_args(x, w, bias, act)
+    shape = (d.rows, d.n_out)
+    pr = None
+    if residual is not None:
+        pr, d.ld_res = _rows(residual, shape, x.dtype, "residual")
+    py, d.ld_y = _rows(y, shape, x.dtype, "y")
+    _check(load_library().gs_linear_fwd(C.byref(d), px, pw, pb, pr, py, _stream()), "gs_linear_fwd")
+
+
+def gs_linear_bwd_workspace_size(x, w, act="none"):
+    d, _, _, _ = _linear_args(x, w, None, act)
+    b = C.c_size_t()
+    _check(load_library().gs_linear_bwd_workspace_size(C.byref(d), C.byref(b)), "gs_linear_bwd_workspace_size")
+    return b.value
+
+
+def gs_linear_bwd(x, w, bias, dy, dx, dw, db, workspace, act="none"):
+    """The layer's gradients from dy [rows, n_out] into dx, dw and db (each may be None: not computed);
+    workspace: uint8, gs_linear_bwd_workspace_size bytes, 256-byte aligned."""
+    d, px, pw, pb = _linear_args(x, w, bias, act)
+    pdy, d.ld_y = _rows(dy, (d.rows, d.n_out), x.dtype, "dy")
+    pdx = None
+    if dx is not None:
+        pdx, d.ld_dx = _rows(dx, (d.rows, d.n_in), x.dtype, "dx")
+    if dw is not None and dw.shape != w.shape:
+        raise GsError(f"dw must have shape {tuple(w.shape)}, got {tuple(dw.shape)}")
+    if db is not None and db.shape != (d.n_out,):
+        raise GsError(f"db must have shape ({d.n_out},), got {tuple(db.shape)}")
+    _check(load_library().gs_linear_bwd(C.byref(d), px, pw, pb, pdy, pdx, _p(dw, x.dtype, "dw"),
+                                        _p(db, x.dtype, "db"), _p(workspace, torch.uint8, "workspace"),
+                                        workspace.numel(), _stream()), "gs_linear_bwd")
+
+
+def gs_grad_workspace_size(n_tensors):
+    b = C.c_size_t()
+    _check(load_library().gs_grad_workspace_size(n_tensors, C.byref(b)), "gs_grad_workspace_size")
+    return b.value
+
+
+def _grad_array(grads, out):
+    arr = (GsGradTensor * max(len(grads), 1))()
+    for i, g in enumerate(grads):
+        a = arr[i]
+        a.grad = _p(g, None, f"gradient {i}")
+        if g.dtype not in DTYPES:
+            raise GsError(f"gradient {i} must be float32, float16 or bfloat16, got {g.dtype}")
+        a.count, a.dtype = g.numel(), DTYPES[g.dtype]
+        if out is not None:
+            if out[i].shape != g.shape:
+                raise GsError(f"out {i} must have its gradient's shape")
+            a.out = _p(out[i], g.dtype, f"out {i}")
+    return arr
+
+
+def _clip_state(clip):
+    if clip.numel() != CLIP_STATE_FLOATS:
+        raise GsError(f"the clipping state holds {CLIP_STATE_FLOATS} floats")
+    return _p(clip, torch.float32, "clip")
+
+
+def gs_grad_norm(grads, max_norm, clip, workspace):
+    """Global norm and clipping coefficient of the list grads into clip [4] float32 (words 0 and 1)."""
+    rc = load_library().gs_grad_norm(len(grads), _grad_array(grads, None), max_norm, _clip_state(clip),
+                                     _p(workspace, torch.uint8, "workspace"), workspace.numel(), _stream())
+    _check(rc, "gs_grad_norm")
+
+
+def gs_grad_clip(grads, out, max_norm, clip, workspace):
+    """gs_grad_norm, then out[i] = coefficient * grads[i] (out may be grads itself)."""
+    if len(out) != len(grads):
+        raise GsError("out needs one tensor for each gradient")
+    rc = load_library().gs_grad_clip(len(grads), _grad_array(grads, out), max_norm, _clip_state(clip),
+                                     _p(workspace, torch.uint8, "workspace"), workspace.numel(), _stream())
+    _check(rc, "gs_grad_clip")
+
+
+def gs_adam_step_clipped(tensors, beta1, beta2, eps, step, clip=None):
+    """One Adam step on coefficient * gradient for a ctypes array of GsAdamTensor; clip: the state of
+    gs_grad_norm, or None."""
+    rc = load_library().gs_adam_step_clipped(len(tensors), tensors, beta1, beta2, eps, step,
+                                             None if clip is None else _clip_state(clip), _stream())
+    _check(rc, "gs_adam_step_clipped")
 
 
 # ---------------------------------------------------------------------------

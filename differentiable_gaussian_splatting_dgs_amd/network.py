@@ -1,0 +1,172 @@
+"""Networks beside the Gaussians: the fused linear layer with its gradients, gradient
+clipping by the global norm, and an Adam optimizer that takes the clipping
+coefficient on the device.
+
+A network's rows are Gaussians (features decoded to Gaussian parameters, offsets for
+a time step) or views (an appearance code per camera); its outputs go to
+`gs.rasterize` and its gradients come back through it.  Plumbing over the C ABI
+(gs_linear_*, gs_grad_*, gs_adam_step_clipped): buffers and the order of the calls.
+"""
+from __future__ import annotations
+
+import ctypes as C
+
+import torch
+
+from . import gs
+from .gs import GsError
+
+
+def _workspace(nbytes, device):
+    """uint8 tensor of nbytes, 256-byte aligned."""
+    t = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+    off = (-t.data_ptr()) % 256
+    return t[off:off + nbytes]
+
+
+def _forward(x, w, bias, residual, act):
+    y = torch.empty((x.shape[0], w.shape[0]), dtype=x.dtype, device=x.device)
+    gs.gs_linear_fwd(x, w, bias, residual, y, act)
+    return y
+
+
+def linear_backward(dy, x, w, bias=None, act="none", need=(True, True, True)):
+    """dx, dw, db of y = act(x w^T + bias) from dy = dL/dy (None where need is False; db None without a bias).
+    The gradient of a residual added to y is dy itself."""
+    need_dx, need_dw, need_db = need
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
+    dw = torch.empty(w.shape, dtype=w.dtype, device=x.device) if need_dw else None
+    db = torch.empty(w.shape[:1], dtype=w.dtype, device=x.device) if need_db and bias is not None else None
+    ws = _workspace(gs.gs_linear_bwd_workspace_size(x, w, act), x.device)
+    gs.gs_linear_bwd(x, w, bias, dy, dx, dw, db, ws, act)
+    return dx, dw, db
+
+
+class LinearFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, bias, residual, act):
+        ctx.act, ctx.has_bias = act, bias is not None
+        ctx.save_for_backward(x, w, bias)
+        return _forward(x, w, bias, residual, act)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, bias = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx = dw = db = None
+        if any(need[:3]):
+            dx, dw, db = linear_backward(_plain_rows(dy), x, w, bias, ctx.act, need[:3])
+        return dx, dw, db, dy if need[3] else None, None
+
+
+def _plain_rows(t):
+    """t if its rows are contiguous and do not overlap, else a contiguous copy."""
+    s0, s1 = t.stride()
+    return t if (s1 == 1 or t.shape[1] <= 1) and (s0 >= t.shape[1] or t.shape[0] <= 1) else t.contiguous()
+
+
+def linear(x, w, bias=None, residual=None, act="none"):
+    """act(x w^T + bias) + residual, differentiable in all four tensors.
+
+    x [rows, n_in], w [n_out, n_in], bias [n_out], residual [rows, n_out], all of one type (float32, float16 or
+    bfloat16); x and residual may have strided rows.  act: "none", "relu", "silu" or "gelu" (tanh form)."""
+    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad) or
+                                    (residual is not None and residual.requires_grad)):
+        return LinearFunction.apply(x, w, bias, residual, act)
+    return _forward(x, w, bias, residual, act)
+
+
+class GradClip:
+    """Clipping of gradient lists to a global norm; owns the clipping state and the workspace.
+
+    norm() and clip() return the norm before clipping as a float32 device scalar (overwritten by the next call);
+    nothing synchronises."""
+
+    def __init__(self, max_norm):
+        self.max_norm = float(max_norm)
+        if not self.max_norm >= 0:
+            raise GsError("max_norm must be >= 0")
+        self.state = None
+
+    def _prepare(self, grads):
+        if not grads:
+            raise GsError("no gradients")
+        need = gs.gs_grad_workspace_size(len(grads))
+        if self.state is None or self.state.device != grads[0].device:
+            self.state = torch.zeros(gs.CLIP_STATE_FLOATS, dtype=torch.float32, device=grads[0].device)
+            self.value = self.state[0]
+            self.workspace = _workspace(need, grads[0].device)
+        elif self.workspace.numel() < need:
+            self.workspace = _workspace(need, grads[0].device)
+
+    def norm(self, grads):
+        """The global norm of the list; the coefficient is left in state[1] for gs_adam_step_clipped."""
+        self._prepare(grads)
+        gs.gs_grad_norm(grads, self.max_norm, self.state, self.workspace)
+        return self.value
+
+    def clip(self, grads, out=None):
+        """Scales the gradients by min(1, max_norm / (norm + 1e-6)), in place or into out."""
+        self._prepare(grads)
+        gs.gs_grad_clip(grads, grads if out is None else out, self.max_norm, self.state, self.workspace)
+        return self.value
+
+
+class Adam:
+    """Adam over float32 parameters with the gradients clipped to a global norm, in two passes: the norm, then the
+    update that takes its coefficient on the device.
+
+    params: float32 device tensors, updated in place.  lr: one rate, or one for each parameter.  copies: for each
+    parameter None or a 16-bit tensor of its shape that receives the updated values (the tensor a 16-bit network
+    computes with).  normalize_rows: indices of parameters whose rows are renormalised to unit length after the
+    update (quaternions).  exp_avg, exp_avg_sq: the moments, zeros by default.  A step whose norm is not finite
+    changes nothing on the device; it still counts in `t`."""
+
+    def __init__(self, params, lr, betas=(0.9, 0.999), eps=1e-8, max_norm=None, copies=None, normalize_rows=(),
+                 exp_avg=None, exp_avg_sq=None):
+        self.params = list(params)
+        n = len(self.params)
+        lrs = [float(lr)] * n if isinstance(lr, (int, float)) else [float(v) for v in lr]
+        self.copies = [None] * n if copies is None else list(copies)
+        self.exp_avg = [torch.zeros_like(p) for p in self.params] if exp_avg is None else list(exp_avg)
+        self.exp_avg_sq = [torch.zeros_like(p) for p in self.params] if exp_avg_sq is None else list(exp_avg_sq)
+        if not (len(lrs) == len(self.copies) == len(self.exp_avg) == len(self.exp_avg_sq) == n):
+            raise GsError("lr, copies and the moments need one entry for each parameter")
+        self.betas, self.eps, self.t = (float(betas[0]), float(betas[1])), float(eps), 0
+        self.clipper = None if max_norm is None else GradClip(max_norm)
+        self.table = (gs.GsAdamTensor * max(n, 1))()
+        for i, p in enumerate(self.params):
+            a = self.table[i]
+            a.param = gs._p(p, torch.float32, f"parameter {i}")
+            for t, k in ((self.exp_avg[i], "exp_avg"), (self.exp_avg_sq[i], "exp_avg_sq")):
+                if t.shape != p.shape:
+                    raise GsError(f"{k} {i} must have its parameter's shape")
+                setattr(a, k, gs._p(t, torch.float32, f"{k} {i}"))
+            if self.copies[i] is not None:
+                if self.copies[i].shape != p.shape or self.copies[i].dtype not in gs.DTYPES:
+                    raise GsError(f"copy {i} must have its parameter's shape and a floating type")
+                a.copy = gs._p(self.copies[i], None, f"copy {i}")
+                a.copy_dtype = gs.DTYPES[self.copies[i].dtype]
+            a.normalize_rows = 1 if i in normalize_rows else 0
+            a.row_len = p.shape[-1] if a.normalize_rows else 1
+            a.rows = p.numel() // max(a.row_len, 1)
+            a.col_end = a.row_len
+            a.lr = lrs[i]
+
+    def step(self, grads):
+        """One step with gradients grads (float32 or 16-bit, contiguous).  Returns the global norm before clipping
+        as a float32 device scalar (None without max_norm)."""
+        if len(grads) != len(self.params):
+            raise GsError(f"{len(self.params)} parameters, {len(grads)} gradients")
+        for i, g in enumerate(grads):
+            if g.shape != self.params[i].shape or g.dtype not in gs.DTYPES:
+                raise GsError(f"gradient {i} must have its parameter's shape and a floating type")
+            a = self.table[i]
+            a.grad = gs._p(g, None, f"gradient {i}")
+            a.grad_dtype = gs.DTYPES[g.dtype]
+        norm = self.clipper.norm(grads) if self.clipper is not None else None
+        self.t += 1
+        if self.params:
+            gs.gs_adam_step_clipped(self.table, self.betas[0], self.betas[1], self.eps, self.t,
+                                    self.clipper.state if self.clipper is not None else None)
+        return norm

@@ -12,6 +12,8 @@
  *  [P4] notes.huajishe.fun, "3DGS training and optimisation" (C.2 Adam with
  *       per-parameter learning rates, D.1 densification statistic, D.4
  *       quaternion renormalisation, E.1 training loop, E.3 tile rasterization).
+ *  [P2] qqiyuan.cn, "3D Gaussian forward and backward, from derivation to
+ *       efficient implementation" (gradient clipping).
  *  [P1] qqiyuan.cn, "3D Gaussian splatting backward propagation: chain-rule
  *       gradients explained" (the compositing equation).
  *
@@ -590,6 +592,130 @@ int gs_preprocess_bwd_adam_views(const gs_camera* cams, int32_t views, const gs_
 int gs_count_pairs_views(const gs_camera* cams, int32_t views, const gs_settings* set, int32_t n,
                          const uint32_t* tile_ranges, const uint32_t* point_list, const float* splats,
                          int64_t* counts, int32_t* evaluated_px /* [views, H, W] or NULL */, void* stream);
+
+/*
+ * Networks beside the Gaussians.  [P1] takes a Gaussian's opacity from
+ * sigmoid(MLP(mean, covariance)): a network whose rows are Gaussians (features
+ * to parameters, offsets for a time step) or views (an appearance code per
+ * camera), trained in the same loop.  The calls below are its fused linear
+ * layer and the optimizer step with the gradient clipping of [P2] (qqiyuan.cn,
+ * "3D Gaussian forward and backward", numerical stability).  Element types:
+ */
+enum { GS_F32 = 0, GS_F16 = 1, GS_BF16 = 2 };
+enum { GS_ACT_NONE = 0, GS_ACT_RELU = 1, GS_ACT_SILU = 2, GS_ACT_GELU = 3 };
+
+/*
+ * One linear layer: z = x w^T + bias, y = act(z) + residual.
+ * x [rows, n_in], residual, y, dy [rows, n_out], dx [rows, n_in], w and dw
+ * [n_out, n_in], bias and db [n_out], all of one type (dtype).  w, dw, bias and
+ * db are contiguous; the others have rows ld_* elements apart (ld_x, ld_dx >=
+ * n_in; ld_y (also dy's), ld_res >= n_out, or 0 for a residual that is one row
+ * for all).  Unlike the other calls these need only element alignment; rows
+ * that are 16-byte aligned (pointer and ld) are read and written faster.
+ * act: GS_ACT_RELU max(0, z) (derivative 0 at z = 0; NaN stays NaN),
+ * GS_ACT_SILU z / (1 + exp(-z)), GS_ACT_GELU z / (1 + exp(-2 c (z + 0.044715
+ * z^3))) with c = sqrt(2 / pi).  Products are summed in float32 and the
+ * epilogue runs in float32; results are rounded once.
+ * Limits: n_in and n_out <= 2^20, rows <= 2^31 - 1 (GS_ECAPACITY).
+ */
+typedef struct gs_linear {
+    int64_t rows;
+    int32_t n_in, n_out;
+    int32_t dtype, act;
+    int64_t ld_x, ld_y, ld_res, ld_dx;
+} gs_linear;
+
+/*
+ * gs_linear_fwd -- y from x, w, bias (NULL: none) and residual (NULL: none).
+ * y may be the residual's own buffer (same pointer and ld); it must not overlap
+ * anything else.  n_in == 0 gives act(bias) + residual.
+ */
+int gs_linear_fwd(const gs_linear* d, const void* x, const void* w, const void* bias, const void* residual, void* y,
+                  void* stream);
+
+/* Bytes of workspace gs_linear_bwd needs. */
+int gs_linear_bwd_workspace_size(const gs_linear* d, size_t* bytes);
+
+/*
+ * gs_linear_bwd -- the layer's gradients from dy = dL/dy: dz = dy act'(z),
+ * dx = dz w, dw = dz^T x, db = sum over rows of dz; the residual's gradient is
+ * dy itself.  z is recomputed from x, w and bias (the forward keeps nothing).
+ * Each of dx, dw and db may be NULL (not computed); a given one is overwritten.
+ * dz enters the products rounded to the layer's type; the sums over rows are
+ * split and joined in a fixed order, so results are the same from run to run.
+ * With rows == 0, dw and db are zero.  workspace: gs_linear_bwd_workspace_size()
+ * bytes, 256-byte aligned, contents on entry irrelevant.
+ */
+int gs_linear_bwd(const gs_linear* d, const void* x, const void* w, const void* bias, const void* dy, void* dx,
+                  void* dw, void* db, void* workspace, size_t workspace_bytes, void* stream);
+
+/* A gradient tensor: count elements of dtype, contiguous, element aligned
+   (16-byte aligned ones are read faster); out, of the same type and count, is
+   used by gs_grad_clip only and may be grad itself. */
+typedef struct gs_grad_tensor {
+    const void* grad;
+    void* out;
+    int64_t count;
+    int32_t dtype;
+} gs_grad_tensor;
+
+/* The clipping state the next three calls share, device memory of 16 bytes:
+   word 0 the global norm (float32), word 1 the coefficient (float32), words 2
+   and 3 the library's.  Zero it once, before its first use. */
+#define GS_CLIP_STATE_BYTES 16
+
+/* Bytes of workspace gs_grad_norm and gs_grad_clip need for n_tensors. */
+int gs_grad_workspace_size(int32_t n_tensors, size_t* bytes);
+
+/*
+ * gs_grad_norm -- the global norm sqrt(sum g^2) over all elements of all
+ * tensors, and the coefficient min(1, max_norm / (norm + 1e-6)), into clip.
+ * Squares are summed in float64 in a fixed order: no float32 gradient overflows
+ * or vanishes, and the value is deterministic.  A NaN or infinite element makes
+ * the coefficient NaN.  max_norm >= 0 (infinity: the coefficient is 1).
+ * n_tensors may be 0 (norm 0).  workspace: 256-byte aligned, contents on entry
+ * irrelevant.
+ */
+int gs_grad_norm(int32_t n_tensors, const gs_grad_tensor* tensors, float max_norm, float* clip, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
+/*
+ * gs_grad_clip -- gs_grad_norm, then out = coefficient * grad for every tensor
+ * (the product in float32, rounded to the tensor's type).  With a coefficient
+ * of 1 or NaN (a norm that is not finite) the values are copied as they are,
+ * and a tensor whose out is its grad is not touched.
+ */
+int gs_grad_clip(int32_t n_tensors, const gs_grad_tensor* tensors, float max_norm, float* clip, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
+/* One tensor of the clipped Adam step: as gs_adam_group, with a gradient of
+   grad_dtype and an optional copy (NULL: none) of the updated parameters,
+   rounded to copy_dtype, for a network that computes in 16 bits beside float32
+   parameters. */
+typedef struct gs_adam_tensor {
+    float* param;
+    const void* grad;
+    float* exp_avg;
+    float* exp_avg_sq;
+    void* copy;
+    int64_t rows;
+    int32_t row_len;
+    int32_t col_begin;
+    int32_t col_end;
+    int32_t normalize_rows;
+    int32_t grad_dtype;
+    int32_t copy_dtype;
+    float lr;
+} gs_adam_tensor;
+
+/*
+ * gs_adam_step_clipped -- gs_adam_step on coefficient * grad, any number of
+ * tensors.  clip: the state gs_grad_norm left (read on the device: nothing
+ * waits for the host), or NULL for a coefficient of 1.  When the coefficient is
+ * NaN (a norm that is not finite) the call changes nothing.
+ */
+int gs_adam_step_clipped(int32_t n_tensors, const gs_adam_tensor* tensors, float beta1, float beta2, float eps,
+                         int32_t step, const float* clip, void* stream);
 
 #ifdef __cplusplus
 }
