@@ -52,7 +52,8 @@ def _link(objs, out):
 def build(force=True, verbose=False):
     """Compile every HIP source and link both libraries.  Always rebuilds when force."""
     deps = [os.path.join(CSRC, s) for s in SOURCES + MEASURE_SOURCES] + [
-        os.path.join(CSRC, "gs_internal.h"), os.path.join(INCLUDE, "gs.h"), os.path.join(INCLUDE, "gs_measure.h")]
+        os.path.join(CSRC, "gs_internal.h"), os.path.join(CSRC, "linear_tile.h"),
+        os.path.join(INCLUDE, "gs.h"), os.path.join(INCLUDE, "gs_measure.h")]
     if (not force and all(os.path.exists(x) for x in (LIB, MEASURE_LIB)) and
             min(os.path.getmtime(LIB), os.path.getmtime(MEASURE_LIB)) >= max(os.path.getmtime(d) for d in deps)):
         return LIB

@@ -5,72 +5,348 @@
 //
 // Products are summed in float32, the activation runs in float32, and every
 // result is rounded once.
-#include "gs_internal.h"
+#include "linear_tile.h"
 
 namespace gs {
 namespace {
 
-template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
-    if (ACT == GS_ACT_RELU) return z < 0.f ? 0.f : z;  // NaN stays NaN
-    if (ACT == GS_ACT_SILU) return z / (1.f + __expf(-z));
-    if (ACT == GS_ACT_GELU) {
-        const float u = 1.5957691216057308f * (z + 0.044715f * z * z * z);
-        return z / (1.f + __expf(-u));
-    }
-    return z;
-}
+inline int size_of(int32_t dtype) { return dtype == GS_F32 ? 4 : 2; }
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline size_t pad256(size_t b) { return (b + 255) & ~(size_t)255; }
 
-template <int ACT>
-__device__ __forceinline__ float act_slope(float z) {
-    if (ACT == GS_ACT_RELU) return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);
-    if (ACT == GS_ACT_SILU) {
-        const float s = 1.f / (1.f + __expf(-z));
-        return s * (1.f + z * (1.f - s));
-    }
-    if (ACT == GS_ACT_GELU) {
-        const float u = 1.5957691216057308f * (z + 0.044715f * z * z * z);
-        const float s = 1.f / (1.f + __expf(-u));
-        return s * (1.f + z * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * z * z));
-    }
-    return 1.f;
-}
+// One product y = epilogue(a b^T): a [rows, depth] (x or dz), b [cols, depth]
+// (the weights, or their transpose for dx).
+enum { EPI_FWD, EPI_DZ, EPI_PLAIN };
 
-// C(i, j) = sum_k A(i, k) B(k, j) with element strides, one 64 x 64 tile per block.
-enum { EPI_FWD, EPI_DZ, EPI_PLAIN, EPI_PART };
-
-struct TileArgs {
+struct ProdArgs {
     const void* a;
     const void* b;
-    const void* bias;   // FWD, DZ: [cols]
-    const void* other;  // FWD: residual; DZ: dy
-    void* c;
-    int64_t rows, cols, depth;
-    int64_t sa_i, sa_k, sb_k, sb_j;
-    int64_t ld_other, ld_c;
-    int64_t depth_per;  // PART: depth of one split (blockIdx.z)
+    const void* bias;   // FWD, DZ: [cols] or NULL
+    const void* other;  // FWD: residual or NULL; DZ: dy
+    void* out;
+    int64_t rows, ld_a, ld_b, ld_other, ld_out;
+    int32_t cols, depth, epi, act;
 };
 
-template <typename T, int EPI, int ACT>
-__global__ __launch_bounds__(256) void k_tile(TileArgs p) {
+// The epilogue of one run: E consecutive outputs of one row, with the run of the
+// residual or dy already in `other`.
+template <typename T>
+__device__ __forceinline__ void finish_run(const ProdArgs& p, int64_t row, int n0, float (&v)[Tile<T>::E],
+                                           typename Tile<T>::Frag other) {
+    constexpr int E = Tile<T>::E;
+    if (p.epi == EPI_FWD) {
+        act_run<T>(p.act, v);
+        if (p.other) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] += (float)other[j];
+        }
+    } else if (p.epi == EPI_DZ) {
+        float g[E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) g[j] = (float)other[j];
+        slope_run<T>(p.act, v, g);
+    }
+    typename Tile<T>::Frag f;
+#pragma unroll
+    for (int j = 0; j < E; ++j) f[j] = (T)v[j];
+    store_run(static_cast<T*>(p.out) + row * p.ld_out, n0, p.cols, f);
+}
+
+// Few outputs or few rows: a block makes one group of KS outputs of 16 rows, its
+// four waves taking every fourth step of the sum and joining in LDS.  The weights
+// go straight from memory to the instruction: with few rows nothing would reuse
+// them from LDS, and the launch's latency is all there is.
+template <typename T>
+__global__ __launch_bounds__(256) void k_prod_few(ProdArgs p) {
+    constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG;
+    __shared__ f32x4 s_acc[4][TG][64];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int n0 = (int)blockIdx.x * KS;
+    const int64_t row = (int64_t)blockIdx.y * 16 + r;
+    const T* a = static_cast<const T*>(p.a) + (row < p.rows ? row : p.rows - 1) * p.ld_a;
+    const T* b[TG];
+#pragma unroll
+    for (int t = 0; t < TG; ++t) {
+        const int n = n0 + out_row<T>(t, r);
+        b[t] = static_cast<const T*>(p.b) + (int64_t)(n < p.cols ? n : p.cols - 1) * p.ld_b;
+    }
+    f32x4 acc[TG] = {};
+    const int whole = p.depth / KS;
+    int s = wave;
+    for (; s + 4 < whole; s += 8) {  // two steps' loads in flight
+        const int k0 = s * KS + E * g, k1 = k0 + 4 * KS;
+        const auto a0 = load16(a + k0), a1 = load16(a + k1);
+        typename Tile<T>::Frag b0[TG], b1[TG];
+#pragma unroll
+        for (int t = 0; t < TG; ++t) {
+            b0[t] = load16(b[t] + k0);
+            b1[t] = load16(b[t] + k1);
+        }
+#pragma unroll
+        for (int t = 0; t < TG; ++t) mma(acc[t], b0[t], a0);
+#pragma unroll
+        for (int t = 0; t < TG; ++t) mma(acc[t], b1[t], a1);
+    }
+    for (; s * KS < p.depth; s += 4) {
+        const int k0 = s * KS + E * g;
+        const auto a0 = load_frag(a, k0, p.depth);
+#pragma unroll
+        for (int t = 0; t < TG; ++t) mma(acc[t], load_frag(b[t], k0, p.depth), a0);
+    }
+#pragma unroll
+    for (int t = 0; t < TG; ++t) s_acc[wave][t][lane] = acc[t];
+    __syncthreads();
+    if (wave != 0 || row >= p.rows) return;
+    const int c0 = n0 + E * g;
+    float v[E];
+#pragma unroll
+    for (int t = 0; t < TG; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[4 * t + i] = (s_acc[0][t][lane][i] + s_acc[1][t][lane][i]) + (s_acc[2][t][lane][i] + s_acc[3][t][lane][i]);
+    if (p.bias) {
+        const auto bias = load_frag(static_cast<const T*>(p.bias), c0, p.cols);
+#pragma unroll
+        for (int j = 0; j < E; ++j) v[j] += (float)bias[j];
+    }
+    auto other = zero_frag<T>();
+    if (p.other) other = load_frag(static_cast<const T*>(p.other) + row * p.ld_other, c0, p.cols);
+    finish_run<T>(p, row, c0, v, other);
+}
+
+// Narrow layers over many rows: the weights stay in LDS as fragments for the
+// life of the block, and each wave walks tiles of 16 R rows, reading a row's whole
+// depth (SL steps) into registers once and making all its outputs: x is read once
+// and y written once, with no barrier in the loop.
+constexpr int kNarrowThreads = 512;  // at most
+template <typename T, int SL, int R>
+__global__ __launch_bounds__(kNarrowThreads) void k_prod_narrow(ProdArgs p) {
+    constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG;
+    typedef typename Tile<T>::Frag Frag;
+    extern __shared__ __align__(16) char s_mem[];
+    const int groups = (p.cols + KS - 1) / KS;
+    Frag* s_w = reinterpret_cast<Frag*>(s_mem);                                     // [groups][TG][SL][64]
+    f32x4* s_bias = reinterpret_cast<f32x4*>(s_w + (size_t)groups * TG * SL * 64);  // [groups][KS / 4]
+    for (int i = threadIdx.x; i < groups * TG * SL * 64; i += blockDim.x) {
+        const int l = i & 63, sl = (i >> 6) % SL, gt = (i >> 6) / SL;
+        const int n = gt / TG * KS + out_row<T>(gt % TG, l & 15);
+        s_w[i] = n < p.cols ? load_frag(static_cast<const T*>(p.b) + (int64_t)n * p.ld_b, sl * KS + E * (l >> 4), p.depth)
+                            : zero_frag<T>();
+    }
+    for (int i = threadIdx.x; i < groups * KS; i += blockDim.x)
+        reinterpret_cast<float*>(s_bias)[i] =
+            p.bias && i < p.cols ? (float)static_cast<const T*>(p.bias)[i] : 0.f;
+    __syncthreads();
+    const int waves = blockDim.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t tiles = (p.rows + 16 * R - 1) / (16 * R);
+    for (int64_t tile = (int64_t)blockIdx.x * waves + wave; tile < tiles; tile += (int64_t)gridDim.x * waves) {
+        const int left = (int)min(p.rows - tile * (16 * R), (int64_t)(16 * R));  // rows of this tile
+        Frag x[R][SL];
+        const T* a = static_cast<const T*>(p.a) + tile * (16 * R) * p.ld_a;
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const T* ar = a + (int64_t)min(16 * q + r, left - 1) * p.ld_a;
+#pragma unroll
+            for (int s = 0; s < SL - 1; ++s) x[q][s] = load16(ar + s * KS + E * g);
+            x[q][SL - 1] = load_frag(ar, (SL - 1) * KS + E * g, p.depth);
+        }
+        const T* o = static_cast<const T*>(p.other) + tile * (16 * R) * p.ld_other;
+        for (int n = 0; n < groups; ++n) {
+            const int c0 = n * KS + E * g;
+            Frag other[R];
+            if (p.other) {
+#pragma unroll
+                for (int q = 0; q < R; ++q)
+                    other[q] = load_frag(o + (int64_t)min(16 * q + r, left - 1) * p.ld_other, c0, p.cols);
+            }
+            f32x4 acc[R][TG];
+#pragma unroll
+            for (int t = 0; t < TG; ++t) {
+                const f32x4 b = s_bias[(n * KS + E * g) / 4 + t];
+#pragma unroll
+                for (int q = 0; q < R; ++q) acc[q][t] = b;
+            }
+#pragma unroll
+            for (int s = 0; s < SL; ++s)
+#pragma unroll
+                for (int t = 0; t < TG; ++t) {
+                    const Frag w = s_w[((n * TG + t) * SL + s) * 64 + lane];
+#pragma unroll
+                    for (int q = 0; q < R; ++q) mma(acc[q][t], w, x[q][s]);
+                }
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                if (16 * q + r >= left) continue;
+                float v[E];
+#pragma unroll
+                for (int j = 0; j < E; ++j) v[j] = acc[q][j / 4][j % 4];
+                finish_run<T>(p, tile * (16 * R) + 16 * q + r, c0, v, other[q]);
+            }
+        }
+    }
+}
+
+// Deep or wide layers: 128 x 128 outputs per block, 64 x 64 per wave.  Both
+// operands pass through LDS in rows of 128 bytes (2 steps), their 16-byte chunks
+// rotated by the row so that the fragments' reads meet no bank twice; the next
+// 128 bytes of every row are on their way while these are multiplied.
+constexpr int kBig = 128;  // rows and outputs of a block
+template <typename T>
+__global__ __launch_bounds__(256) void k_prod_big(ProdArgs p) {
+    constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG;
+    typedef typename Tile<T>::Frag Frag;
+    __shared__ Frag s_a[2][kBig * 8], s_b[2][kBig * 8];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
+    // blocks of one XCD take neighbouring tiles, outputs first: they share rows of a
+    const int64_t tn = (p.cols + kBig - 1) / kBig, total = (int64_t)gridDim.x, per = (total + 7) / 8;
+    const int64_t id = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    const int64_t tiles = tn * ((p.rows + kBig - 1) / kBig);
+    if (id >= tiles) return;
+    const int64_t m0 = id / tn * kBig;
+    const int n0 = (int)(id % tn) * kBig;
+    // staging: thread i brings chunk i % 8 of rows i / 8, + 32, + 64, + 96; the weights' rows in the order
+    // that interleaves a group's tiles
+    const int ch = threadIdx.x & 7, sr = threadIdx.x >> 3;
+    const T *ga[4], *gb[4];
+    Frag ra[4], rb[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int pos = sr + 32 * i;
+        const int64_t m = m0 + pos;
+        const int n = n0 + pos / KS * KS + out_row<T>(pos % KS / 16, pos % 16);
+        ga[i] = static_cast<const T*>(p.a) + (m < p.rows ? m : p.rows - 1) * p.ld_a;
+        gb[i] = static_cast<const T*>(p.b) + (int64_t)(n < p.cols ? n : p.cols - 1) * p.ld_b;
+    }
+    const int steps = (p.depth + 2 * KS - 1) / (2 * KS);
+    auto fetch = [&](int s) {
+        const int k0 = s * 2 * KS + E * ch;
+        if ((s + 1) * 2 * KS <= p.depth) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                ra[i] = load16(ga[i] + k0);
+                rb[i] = load16(gb[i] + k0);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                ra[i] = load_frag(ga[i], k0, p.depth);
+                rb[i] = load_frag(gb[i], k0, p.depth);
+            }
+        }
+    };
+    auto put = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int pos = sr + 32 * i, at = pos * 8 + (ch ^ (pos & 7));
+            s_a[buf][at] = ra[i];
+            s_b[buf][at] = rb[i];
+        }
+    };
+    f32x4 acc[4][4] = {};  // [m tile][n tile]
+    if (steps > 0) {
+        fetch(0);
+        put(0);
+    }
+    __syncthreads();
+    for (int s = 0; s < steps; ++s) {
+        if (s + 1 < steps) fetch(s + 1);
+        const int buf = s & 1;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            Frag fa[4], fb[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int am = wm + 16 * i + r, bn = wn + 16 * i + r;
+                fa[i] = s_a[buf][am * 8 + ((4 * h + g) ^ (am & 7))];
+                fb[i] = s_b[buf][bn * 8 + ((4 * h + g) ^ (bn & 7))];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mma(acc[i][j], fb[j], fa[i]);
+        }
+        if (s + 1 < steps) put(buf ^ 1);
+        __syncthreads();
+    }
+#pragma unroll
+    for (int q = 0; q < 4 / TG; ++q) {  // groups of KS outputs
+        const int c0 = n0 + wn + q * KS + E * g;
+        if (c0 >= p.cols) continue;
+        float bias[E] = {};
+        if (p.bias) {
+            const auto f = load_frag(static_cast<const T*>(p.bias), c0, p.cols);
+#pragma unroll
+            for (int j = 0; j < E; ++j) bias[j] = (float)f[j];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t row = m0 + wm + 16 * i + r;
+            if (row >= p.rows) continue;
+            auto other = zero_frag<T>();
+            if (p.other) other = load_frag(static_cast<const T*>(p.other) + row * p.ld_other, c0, p.cols);
+            float v[E];
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] = acc[i][q * TG + j / 4][j % 4] + bias[j];
+            finish_run<T>(p, row, c0, v, other);
+        }
+    }
+}
+
+template <typename T, int SL>
+void launch_narrow(const ProdArgs& p, size_t lds, hipStream_t s) {
+    constexpr int R = SL <= 2 ? 4 : 2;
+    const int threads = lds <= 40960 ? 256 : 512;
+    const int64_t most = 256 * (lds <= 40960 ? 4 : lds <= 81920 ? 2 : 1);
+    const int64_t blocks = cdiv(cdiv(p.rows, 16 * R), threads / 64);
+    hipLaunchKernelGGL((k_prod_narrow<T, SL, R>), dim3((unsigned)(blocks < most ? blocks : most)), dim3(threads), lds,
+                       s, p);
+}
+
+template <typename T>
+void product(const ProdArgs& p, hipStream_t s) {
+    constexpr int KS = Tile<T>::KS;
+    const int groups = (int)cdiv(p.cols, KS), steps = (int)cdiv(p.depth, KS);
+    const int64_t tiles16 = cdiv(p.rows, 16);
+    if (tiles16 * groups <= 2048 && tiles16 <= 65535) {
+        hipLaunchKernelGGL((k_prod_few<T>), dim3(groups, (unsigned)tiles16), dim3(256), 0, s, p);
+        return;
+    }
+    const size_t lds = (size_t)groups * KS * (steps * KS * sizeof(T) + 4);
+    if (lds <= 160 * 1024) {
+        switch (steps) {
+            case 0: case 1: launch_narrow<T, 1>(p, (size_t)groups * KS * (KS * sizeof(T) + 4), s); return;
+            case 2: launch_narrow<T, 2>(p, lds, s); return;
+            case 3: launch_narrow<T, 3>(p, lds, s); return;
+            case 4: launch_narrow<T, 4>(p, lds, s); return;
+            case 5: launch_narrow<T, 5>(p, lds, s); return;
+            case 6: launch_narrow<T, 6>(p, lds, s); return;
+            case 7: launch_narrow<T, 7>(p, lds, s); return;
+            case 8: launch_narrow<T, 8>(p, lds, s); return;
+        }
+    }
+    const int64_t tiles = cdiv(p.cols, kBig) * cdiv(p.rows, kBig);
+    hipLaunchKernelGGL((k_prod_big<T>), dim3((unsigned)(cdiv(tiles, 8) * 8)), dim3(256), 0, s, p);
+}
+
+// part[z](i, j) = sum over the z-th split of the rows m of dz(m, i) x(m, j): one
+// 64 x 64 tile per block.
+template <typename T>
+__global__ __launch_bounds__(256) void k_dw(const T* dz, int64_t ld_dz, const T* x, int64_t ld_x, int64_t rows,
+                                            int32_t n_out, int32_t n_in, int64_t per, float* part) {
     __shared__ float s_a[16][65], s_b[16][65];
-    const T* a = static_cast<const T*>(p.a);
-    const T* b = static_cast<const T*>(p.b);
-    const int64_t i0 = (int64_t)blockIdx.x * 64, j0 = (int64_t)blockIdx.y * 64;
+    const int i0 = blockIdx.x * 64, j0 = blockIdx.y * 64;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     float acc[4][4] = {};
-    const int64_t k_begin = EPI == EPI_PART ? (int64_t)blockIdx.z * p.depth_per : 0;
-    const int64_t k_end = EPI == EPI_PART ? min(p.depth, k_begin + p.depth_per) : p.depth;
-    for (int64_t k0 = k_begin; k0 < k_end; k0 += 16) {
+    const int64_t m_begin = (int64_t)blockIdx.z * per, m_end = min(rows, m_begin + per);
+    for (int64_t m0 = m_begin; m0 < m_end; m0 += 16) {
 #pragma unroll
         for (int e = threadIdx.x; e < 1024; e += 256) {
-            // neighbouring lanes along the contiguous index
-            const int ai = p.sa_k == 1 ? e >> 4 : e & 63, ak = p.sa_k == 1 ? e & 15 : e >> 6;
-            const int bj = p.sb_k == 1 ? e >> 4 : e & 63, bk = p.sb_k == 1 ? e & 15 : e >> 6;
-            s_a[ak][ai] = (i0 + ai < p.rows && k0 + ak < k_end) ? (float)a[(i0 + ai) * p.sa_i + (k0 + ak) * p.sa_k]
-                                                                : 0.f;
-            s_b[bk][bj] = (j0 + bj < p.cols && k0 + bk < k_end) ? (float)b[(k0 + bk) * p.sb_k + (j0 + bj) * p.sb_j]
-                                                                : 0.f;
+            const int c = e & 63, m = e >> 6;
+            const bool in = m0 + m < m_end;
+            s_a[m][c] = in && i0 + c < n_out ? (float)dz[(m0 + m) * ld_dz + i0 + c] : 0.f;
+            s_b[m][c] = in && j0 + c < n_in ? (float)x[(m0 + m) * ld_x + j0 + c] : 0.f;
         }
         __syncthreads();
 #pragma unroll
@@ -83,22 +359,21 @@ __global__ __launch_bounds__(256) void k_tile(TileArgs p) {
     }
     for (int i = 0; i < 4; ++i)
         for (int j = 0; j < 4; ++j) {
-            const int64_t r = i0 + ty + 16 * i, c = j0 + tx + 16 * j;
-            if (r >= p.rows || c >= p.cols) continue;
-            if (EPI == EPI_PART) {
-                static_cast<float*>(p.c)[((int64_t)blockIdx.z * p.rows + r) * p.cols + c] = acc[i][j];
-                continue;
-            }
-            float v = acc[i][j];
-            if (EPI == EPI_FWD || EPI == EPI_DZ)
-                if (p.bias) v += (float)static_cast<const T*>(p.bias)[c];
-            if (EPI == EPI_FWD) {
-                v = act_value<ACT>(v);
-                if (p.other) v += (float)static_cast<const T*>(p.other)[r * p.ld_other + c];
-            }
-            if (EPI == EPI_DZ) v = (float)static_cast<const T*>(p.other)[r * p.ld_other + c] * act_slope<ACT>(v);
-            static_cast<T*>(p.c)[r * p.ld_c + c] = (T)v;
+            const int r = i0 + ty + 16 * i, c = j0 + tx + 16 * j;
+            if (r < n_out && c < n_in) part[((int64_t)blockIdx.z * n_out + r) * n_in + c] = acc[i][j];
         }
+}
+
+// out [cols, rows] = in [rows, cols]^T, 64 x 64 per block.
+template <typename T>
+__global__ __launch_bounds__(256) void k_transpose(const T* in, T* out, int32_t rows, int32_t cols) {
+    __shared__ T s[64][65];
+    const int c0 = blockIdx.x * 64, r0 = blockIdx.y * 64, x = threadIdx.x & 63, y = threadIdx.x >> 6;
+    for (int r = y; r < 64; r += 4)
+        if (r0 + r < rows && c0 + x < cols) s[r][x] = in[(int64_t)(r0 + r) * cols + c0 + x];
+    __syncthreads();
+    for (int c = y; c < 64; c += 4)
+        if (c0 + c < cols && r0 + x < rows) out[(int64_t)(c0 + c) * rows + r0 + x] = s[x][c];
 }
 
 // out[e] = sum over splits of part[s][e], in order.
@@ -123,10 +398,6 @@ __global__ __launch_bounds__(256) void k_colsum(const T* dz, int64_t ld, int64_t
     part[(int64_t)blockIdx.y * cols + c] = acc;
 }
 
-inline int size_of(int32_t dtype) { return dtype == GS_F32 ? 4 : 2; }
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-inline size_t pad256(size_t b) { return (b + 255) & ~(size_t)255; }
-
 inline int check_shape(const gs_linear* d) {
     if (!d || d->rows < 0 || d->n_in < 0 || d->n_out < 0 || d->dtype < GS_F32 || d->dtype > GS_BF16 ||
         d->act < GS_ACT_NONE || d->act > GS_ACT_GELU)
@@ -140,19 +411,24 @@ inline bool element_aligned(const void* p, int32_t dtype) {
 }
 
 struct BwdPlan {
-    size_t dz, dw_part, db_part, bytes;  // offsets in the workspace
+    size_t dz, wt, dw_part, db_part, bytes;  // offsets in the workspace
+    int64_t ld_dz;
     int splits;
     int64_t per;
 };
 
 inline BwdPlan bwd_plan(const gs_linear* d) {
     BwdPlan p{};
+    const int e = 16 / size_of(d->dtype);
     p.splits = (int)(d->rows > 256 ? (d->rows + 255) / 256 : 1);
     if (p.splits > 64) p.splits = 64;
     p.per = cdiv(cdiv(d->rows, p.splits), 16) * 16;
     size_t at = 0;
     p.dz = at;
-    if (d->act != GS_ACT_NONE) at += pad256((size_t)d->rows * d->n_out * size_of(d->dtype));
+    p.ld_dz = cdiv(d->n_out, e) * e;
+    if (d->act != GS_ACT_NONE) at += pad256((size_t)d->rows * p.ld_dz * size_of(d->dtype));
+    p.wt = at;
+    at += pad256((size_t)d->n_out * d->n_in * size_of(d->dtype));
     p.dw_part = at;
     at += pad256((size_t)p.splits * d->n_out * d->n_in * 4);
     p.db_part = at;
@@ -161,22 +437,12 @@ inline BwdPlan bwd_plan(const gs_linear* d) {
     return p;
 }
 
-template <typename T, int EPI>
-void launch_tile(const TileArgs& p, int act, int splits, hipStream_t s) {
-    const dim3 grid((unsigned)cdiv(p.rows, 64), (unsigned)cdiv(p.cols, 64), (unsigned)splits);
-    switch (act) {
-        case GS_ACT_RELU: hipLaunchKernelGGL((k_tile<T, EPI, GS_ACT_RELU>), grid, dim3(256), 0, s, p); break;
-        case GS_ACT_SILU: hipLaunchKernelGGL((k_tile<T, EPI, GS_ACT_SILU>), grid, dim3(256), 0, s, p); break;
-        case GS_ACT_GELU: hipLaunchKernelGGL((k_tile<T, EPI, GS_ACT_GELU>), grid, dim3(256), 0, s, p); break;
-        default: hipLaunchKernelGGL((k_tile<T, EPI, GS_ACT_NONE>), grid, dim3(256), 0, s, p); break;
-    }
-}
-
 template <typename T>
 void fwd(const gs_linear* d, const void* x, const void* w, const void* bias, const void* residual, void* y,
          hipStream_t s) {
-    TileArgs p{x, w, bias, residual, y, d->rows, d->n_out, d->n_in, d->ld_x, 1, 1, d->n_in, d->ld_res, d->ld_y, 0};
-    launch_tile<T, EPI_FWD>(p, d->act, 1, s);
+    ProdArgs p{x, w, bias, residual, y, d->rows, d->ld_x, d->n_in, d->ld_res, d->ld_y, d->n_out, d->n_in, EPI_FWD,
+               d->act};
+    product<T>(p, s);
 }
 
 template <typename T>
@@ -186,21 +452,28 @@ void bwd(const gs_linear* d, const void* x, const void* w, const void* bias, con
     const void* dz = dy;
     int64_t ld_dz = d->ld_y;
     if (d->act != GS_ACT_NONE && d->rows > 0 && d->n_out > 0) {
-        TileArgs p{x, w, bias, dy, ws + plan.dz, d->rows, d->n_out, d->n_in, d->ld_x, 1, 1, d->n_in, d->ld_y,
-                   d->n_out, 0};
-        launch_tile<T, EPI_DZ>(p, d->act, 1, s);
+        ProdArgs p{x, w, bias, dy, ws + plan.dz, d->rows, d->ld_x, d->n_in, d->ld_y, plan.ld_dz, d->n_out, d->n_in,
+                   EPI_DZ, d->act};
+        product<T>(p, s);
         dz = ws + plan.dz;
-        ld_dz = d->n_out;
+        ld_dz = plan.ld_dz;
     }
     if (dx && d->rows > 0 && d->n_in > 0) {
-        TileArgs p{dz, w, nullptr, nullptr, dx, d->rows, d->n_in, d->n_out, ld_dz, 1, d->n_in, 1, 0, d->ld_dx, 0};
-        launch_tile<T, EPI_PLAIN>(p, GS_ACT_NONE, 1, s);
+        T* wt = reinterpret_cast<T*>(ws + plan.wt);
+        if (d->n_out > 0)
+            hipLaunchKernelGGL((k_transpose<T>), dim3((unsigned)cdiv(d->n_in, 64), (unsigned)cdiv(d->n_out, 64)),
+                               dim3(256), 0, s, static_cast<const T*>(w), wt, d->n_out, d->n_in);
+        ProdArgs p{dz, wt, nullptr, nullptr, dx, d->rows, ld_dz, d->n_out, 0, d->ld_dx, d->n_in, d->n_out, EPI_PLAIN,
+                   GS_ACT_NONE};
+        product<T>(p, s);
     }
     float* part = reinterpret_cast<float*>(ws + plan.dw_part);
     const int64_t n_w = (int64_t)d->n_out * d->n_in;
     if (dw && n_w > 0) {
-        TileArgs p{dz, x, nullptr, nullptr, part, d->n_out, d->n_in, d->rows, 1, ld_dz, d->ld_x, 1, 0, 0, plan.per};
-        launch_tile<T, EPI_PART>(p, GS_ACT_NONE, plan.splits, s);
+        hipLaunchKernelGGL((k_dw<T>),
+                           dim3((unsigned)cdiv(d->n_out, 64), (unsigned)cdiv(d->n_in, 64), (unsigned)plan.splits),
+                           dim3(256), 0, s, static_cast<const T*>(dz), ld_dz, static_cast<const T*>(x), d->ld_x,
+                           d->rows, d->n_out, d->n_in, plan.per, part);
         hipLaunchKernelGGL((k_join<T>), dim3((unsigned)cdiv(n_w, 256)), dim3(256), 0, s, part, plan.splits, n_w,
                            static_cast<T*>(dw));
     }

@@ -1,0 +1,187 @@
+// Register tiles of the linear layer's kernels (gfx950 matrix instructions, wave64).
+//
+// A fragment is 16 bytes of a row per lane: lane l holds row l % 16 and, in the
+// lane group g = l / 16, the E = 16 / sizeof(T) elements from E g on.  Sixteen
+// rows and KS = 4 E elements of the summed index make one step: one 16x16x32
+// instruction for the 16-bit types, four 16x16x4 ones for float32 (the j-th
+// takes element j of every lane: the sum's order is free as long as both
+// operands agree).  Both operands are loaded the same way, so rows that are
+// contiguous along the summed index go from memory to the instruction with no
+// transpose.
+//
+// The first operand's rows become the result's rows: lane l then holds rows 4 g
+// .. 4 g + 3 of column l % 16.  The layer computes y^T = w x^T, so that a lane
+// holds consecutive outputs of one row of y.  For the 16-bit types two tiles
+// share a group of KS = 32 outputs with their rows interleaved in fours
+// (out_row), so that a lane's 4 + 4 results are 8 consecutive outputs: a run of
+// 16 bytes, which is also the fragment of that row that a next product over the
+// outputs takes.
+#pragma once
+
+#include "gs_internal.h"
+
+namespace gs {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+template <typename T>
+struct Tile {
+    static constexpr int E = 16 / (int)sizeof(T);  // elements of a fragment, and of a result run
+    static constexpr int KS = 4 * E;               // elements of the summed index per step, outputs per group
+    static constexpr int TG = E / 4;               // 16-row tiles per group of outputs
+    typedef T Frag __attribute__((ext_vector_type(16 / sizeof(T))));
+};
+
+__device__ __forceinline__ void mma(f32x4& c, Tile<float>::Frag a, Tile<float>::Frag b) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
+}
+__device__ __forceinline__ void mma(f32x4& c, Tile<_Float16>::Frag a, Tile<_Float16>::Frag b) {
+    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ void mma(f32x4& c, Tile<__bf16>::Frag a, Tile<__bf16>::Frag b) {
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// Output (within its group of KS) of row r of tile t.
+template <typename T>
+__device__ __forceinline__ int out_row(int t, int r) {
+    return Tile<T>::E * (r >> 2) + 4 * t + (r & 3);
+}
+
+template <typename T>
+__device__ __forceinline__ typename Tile<T>::Frag zero_frag() {
+    typename Tile<T>::Frag f;
+#pragma unroll
+    for (int j = 0; j < Tile<T>::E; ++j) f[j] = (T)0.f;
+    return f;
+}
+
+// 16 bytes at any element alignment (the hardware takes them in one access).
+template <typename T>
+__device__ __forceinline__ typename Tile<T>::Frag load16(const T* p) {
+    typename Tile<T>::Frag f;
+    __builtin_memcpy(&f, p, 16);
+    return f;
+}
+
+// Elements [k0, k0 + E) of a row of `count` elements, zeros from `count` on;
+// reads nothing outside the row.  A fragment that straddles the end is loaded
+// from the row's last 16 bytes and shifted down.
+template <typename T>
+__device__ __forceinline__ typename Tile<T>::Frag load_edge(const T* row, int k0, int count) {
+    constexpr int E = Tile<T>::E;
+    const int last = count - E;
+    union {
+        typename Tile<T>::Frag f;
+        uint64_t q[2];
+    } u;
+    if (last < 0) {  // a row shorter than a fragment
+        u.q[0] = u.q[1] = 0;
+#pragma unroll 1
+        for (int j = 0; k0 + j < count; ++j) {
+            uint64_t b = 0;
+            __builtin_memcpy(&b, row + k0 + j, sizeof(T));
+            const int at = j * 8 * (int)sizeof(T);
+            u.q[0] |= at < 64 ? b << (at & 63) : 0;
+            u.q[1] |= at < 64 ? 0 : b << (at & 63);
+        }
+        return u.f;
+    }
+    u.f = load16(row + (k0 < last ? k0 : last));
+    const int bits = k0 > last ? (k0 - last) * 8 * (int)sizeof(T) : 0;
+    if (bits >= 64) {
+        u.q[0] = bits >= 128 ? 0 : u.q[1] >> (bits - 64);
+        u.q[1] = 0;
+    } else if (bits > 0) {
+        u.q[0] = (u.q[0] >> bits) | (u.q[1] << (64 - bits));
+        u.q[1] >>= bits;
+    }
+    return u.f;
+}
+
+template <typename T>
+__device__ __forceinline__ typename Tile<T>::Frag load_frag(const T* row, int k0, int count) {
+    if (k0 + Tile<T>::E <= count) return load16(row + k0);
+    return load_edge(row, k0, count);
+}
+
+// Stores the run's elements that lie inside a row of `count`.
+template <typename T>
+__device__ __forceinline__ void store_run(T* row, int n0, int count, typename Tile<T>::Frag f) {
+    constexpr int E = Tile<T>::E;
+    if (n0 + E <= count) {
+        __builtin_memcpy(row + n0, &f, 16);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+        if (n0 + j < count) row[n0 + j] = f[j];
+}
+
+// 1 / (1 + exp(-u)).  float32 results take exp's argument to twice the width (the
+// product with log2 e alone is off by |u| 2^-24, which exp multiplies up); the
+// 16-bit types' rounding hides that.
+template <typename T>
+__device__ __forceinline__ float logistic(float u) {
+    const float l2e = 1.44269504f;
+    float t = -u * l2e, e;
+    if (sizeof(T) == 4) {
+        // log2 e = l2e + 1.925963033e-8; the low part of -u log2 e moves exp2 by a factor 1 + lo ln 2
+        const float lo = fmaf(-u, 1.925963033e-8f, fmaf(-u, l2e, -t));
+        const float x = __builtin_amdgcn_exp2f(t);
+        e = x > 0.f && x < 3e38f ? fmaf(x, lo * 0.69314718f, x) : x;  // 0, infinity and NaN stay
+    } else {
+        e = __builtin_amdgcn_exp2f(t);
+    }
+    return __builtin_amdgcn_rcpf(1.f + e);
+}
+
+__device__ __forceinline__ float bounded(float z) {  // beyond 64 every activation is z or 0; NaN stays
+    return z > 64.f ? 64.f : (z < -64.f ? -64.f : z);
+}
+constexpr float kGelu = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+
+// act over a lane's run.
+template <typename T, int N>
+__device__ __forceinline__ void act_run(int act, float (&v)[N]) {
+    if (act == GS_ACT_RELU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = v[j] < 0.f ? 0.f : v[j];
+    } else if (act == GS_ACT_SILU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] *= logistic<T>(v[j]);
+    } else if (act == GS_ACT_GELU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float z = bounded(v[j]);
+            v[j] *= logistic<T>(kGelu * fmaf(0.044715f * z * z, z, z));
+        }
+    }
+}
+
+// v <- g act'(v) over a lane's run.
+template <typename T, int N>
+__device__ __forceinline__ void slope_run(int act, float (&v)[N], const float (&g)[N]) {
+    if (act == GS_ACT_RELU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = v[j] > 0.f ? g[j] : (v[j] <= 0.f ? 0.f : v[j]);
+    } else if (act == GS_ACT_SILU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float z = bounded(v[j]), s = logistic<T>(z);
+            v[j] = g[j] * (s * fmaf(z, 1.f - s, 1.f));
+        }
+    } else if (act == GS_ACT_GELU) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float z = bounded(v[j]), q = z * z, s = logistic<T>(kGelu * fmaf(0.044715f * q, z, z));
+            v[j] = g[j] * (s * fmaf(z * (1.f - s), kGelu * fmaf(0.134145f, q, 1.f), 1.f));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = g[j];
+    }
+}
+
+}  // namespace gs

@@ -144,6 +144,25 @@ def test_backward(size, dtype):
                 check(g, v, tol, (size, act, name))
 
 
+# many rows: every depth a wave holds in registers, odd ones among them, and deeper or wider layers
+MANY = [(33_001, 3, 64), (33_001, 20, 3), (17_003, 63, 59), (17_003, 90, 40), (12_001, 128, 128), (17_000, 150, 33),
+        (16_401, 190, 64), (9_001, 220, 100), (8_200, 256, 256), (17_001, 256, 20), (6_007, 257, 300),
+        (3_001, 700, 520), (33_003, 1000, 5), (5_000, 40, 700), (4_111, 512, 512)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("size", MANY)
+def test_many_rows(size, dtype):
+    k = sum(size) % 4
+    x, w, b, r, dy = inputs(*size, dtype, bias=k != 1, residual=k % 2 == 0, pad=(0, 8, 5)[size[1] % 3])
+    _, y, tol, _ = exact_fwd(x, w, b, r, ACTS[k])
+    check(run_fwd(x, w, b, r, ACTS[k]), y, tol, size)
+    got = run_bwd(dy, x, w, b, ACTS[k])
+    for name, g, (v, tol) in zip(("dx", "dw", "db"), got, exact_bwd(x, w, b, dy, ACTS[k])):
+        if g is not None:
+            check(g, v, tol, (size, name))
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("pad,lead", [(1, 0), (8, 8), (13, 3), (64, 1)])
 def test_strided_and_unaligned(dtype, pad, lead):
