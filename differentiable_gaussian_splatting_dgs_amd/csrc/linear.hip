@@ -330,38 +330,163 @@ void product(const ProdArgs& p, hipStream_t s) {
     hipLaunchKernelGGL((k_prod_big<T>), dim3((unsigned)(cdiv(tiles, 8) * 8)), dim3(256), 0, s, p);
 }
 
-// part[z](i, j) = sum over the z-th split of the rows m of dz(m, i) x(m, j): one
-// 64 x 64 tile per block.
+// Fragments of the transposed operands of dw = dz^T x, whose sum runs down the
+// rows: a step takes KS rows, and lane l needs, of column l % 16, E of them.  The
+// tile lies in LDS in its own row order, 128 columns a row.  16-bit: two
+// transposing reads, each of which hands a group of 16 lanes the 4 x 16 block that
+// its lanes' 8-byte pieces of 4 rows make up (lane i: column i); float32: one
+// 4-byte read for each of the instruction's four 4-row slices.  Rows are rotated
+// by dw_key so that the rows of one access lie in different banks.
 template <typename T>
-__global__ __launch_bounds__(256) void k_dw(const T* dz, int64_t ld_dz, const T* x, int64_t ld_x, int64_t rows,
-                                            int32_t n_out, int32_t n_in, int64_t per, float* part) {
-    __shared__ float s_a[16][65], s_b[16][65];
-    const int i0 = blockIdx.x * 64, j0 = blockIdx.y * 64;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    const int64_t m_begin = (int64_t)blockIdx.z * per, m_end = min(rows, m_begin + per);
-    for (int64_t m0 = m_begin; m0 < m_end; m0 += 16) {
+struct RowsGeom {  // one LDS stage of 16 KB
+    static constexpr int kCols = 128;
+    static constexpr int kRows = 16384 / (kCols * (int)sizeof(T));  // 64 or 32
+    static constexpr int kChunks = kCols / Tile<T>::E;              // 16-byte chunks of a row: 16 or 32
+};
+
+// Byte offset of 16-byte chunk c of row m within a stage.
+template <typename T>
+__device__ __forceinline__ int dw_chunk(int m, int c) {
+    if (sizeof(T) == 2) {  // rotate 32-byte pieces: rows 0-3 and 8-11 of a read apart
+        const int key = (m & 3) | ((m >> 1) & 4);
+        return m * 256 + ((((c >> 1) ^ key) << 1 | (c & 1)) << 4);
+    }
+    return m * 512 + ((((c >> 2) ^ (m & 7)) << 2 | (c & 3)) << 4);  // rotate 64-byte pieces
+}
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Columns [c0, c0 + 16) of rows [m0, m0 + KS) of a stage, transposed.
+template <typename T>
+__device__ __forceinline__ typename Tile<T>::Frag dw_frag(const char* stage, int m0, int c0, int lane) {
+    const int r = lane & 15, g = lane >> 4;
+    if constexpr (sizeof(T) == 2) {
+        union {
+            typename Tile<T>::Frag f;
+            s16x4 h[2];
+        } u;
 #pragma unroll
-        for (int e = threadIdx.x; e < 1024; e += 256) {
-            const int c = e & 63, m = e >> 6;
-            const bool in = m0 + m < m_end;
-            s_a[m][c] = in && i0 + c < n_out ? (float)dz[(m0 + m) * ld_dz + i0 + c] : 0.f;
-            s_b[m][c] = in && j0 + c < n_in ? (float)x[(m0 + m) * ld_x + j0 + c] : 0.f;
+        for (int h = 0; h < 2; ++h) {
+            const int m = m0 + 8 * g + 4 * h + (r >> 2), c = c0 + 4 * (r & 3);
+            const char* at = stage + dw_chunk<T>(m, c >> 3) + (c & 7) * 2;
+            u.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4*)const_cast<char*>(at));
         }
-        __syncthreads();
+        return u.f;
+    } else {
+        typename Tile<T>::Frag f;
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
+        for (int j = 0; j < 4; ++j) {
+            const int m = m0 + 4 * j + g, c = c0 + r;
+            f[j] = *reinterpret_cast<const float*>(stage + dw_chunk<T>(m, c >> 2) + (c & 3) * 4);
+        }
+        return f;
+    }
+}
+
+struct DwArgs {
+    const void* dz;
+    const void* x;
+    float* dw_part;  // [splits][n_out][n_in], NULL: not wanted
+    float* db_part;  // [splits][n_out], NULL: not wanted
+    int64_t rows, ld_dz, ld_x, per;
+    int32_t n_out, n_in;
+};
+
+// One split of the rows for a 128 x 128 tile of dw: 64 x 64 per wave, the next
+// stage's rows on their way while this one's are multiplied.  The blocks of the
+// first column of tiles add up dz's columns as they pass.
+template <typename T>
+__global__ __launch_bounds__(256) void k_dw(DwArgs p) {
+    constexpr int E = Tile<T>::E, KS = Tile<T>::KS;
+    typedef typename Tile<T>::Frag Frag;
+    typedef RowsGeom<T> G;
+    __shared__ __align__(16) char s_dz[2][16384], s_x[2][16384];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wn = (wave & 1) * 64, wk = (wave >> 1) * 64;
+    const int n0 = blockIdx.x * 128, k0 = blockIdx.y * 128;
+    const int64_t m_begin = (int64_t)blockIdx.z * p.per, m_end = min(p.rows, m_begin + p.per);
+    constexpr int kPass = 256 / G::kChunks;  // rows that the block's threads cover at a time
+    const int ch = threadIdx.x % G::kChunks, mr = threadIdx.x / G::kChunks;
+    const T* dz = static_cast<const T*>(p.dz);
+    const T* x = static_cast<const T*>(p.x);
+    Frag rz[4], rx[4];
+    auto fetch = [&](int64_t m0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t m = m0 + mr + i * kPass;
+            rz[i] = rx[i] = zero_frag<T>();
+            if (m < m_end) {
+                rz[i] = load_frag(dz + m * p.ld_dz, n0 + ch * E, p.n_out);
+                rx[i] = load_frag(x + m * p.ld_x, k0 + ch * E, p.n_in);
+            }
+        }
+    };
+    float sum[E] = {};
+    const bool sums = p.db_part && blockIdx.y == 0;
+    auto put = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = dw_chunk<T>(mr + i * kPass, ch);
+            *reinterpret_cast<Frag*>(s_dz[buf] + at) = rz[i];
+            *reinterpret_cast<Frag*>(s_x[buf] + at) = rx[i];
+            if (sums)
+#pragma unroll
+                for (int j = 0; j < E; ++j) sum[j] += (float)rz[i][j];
+        }
+    };
+    f32x4 acc[4][4] = {};  // [n tile][k tile]
+    if (m_begin < m_end) {
+        fetch(m_begin);
+        put(0);
+    }
+    __syncthreads();
+    int buf = 0;
+    for (int64_t m0 = m_begin; m0 < m_end; m0 += G::kRows, buf ^= 1) {
+        const bool more = m0 + G::kRows < m_end;
+        if (more) fetch(m0 + G::kRows);
+#pragma unroll
+        for (int h = 0; h < G::kRows / KS; ++h) {
+            Frag fz[4], fx[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                fz[i] = dw_frag<T>(s_dz[buf], h * KS, wn + 16 * i, lane);
+                fx[i] = dw_frag<T>(s_x[buf], h * KS, wk + 16 * i, lane);
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] += s_a[k][ty + 16 * i] * s_b[k][tx + 16 * j];
+                for (int j = 0; j < 4; ++j) mma(acc[i][j], fz[i], fx[j]);
+        }
+        if (more) put(buf ^ 1);
         __syncthreads();
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int r = i0 + ty + 16 * i, c = j0 + tx + 16 * j;
-            if (r < n_out && c < n_in) part[((int64_t)blockIdx.z * n_out + r) * n_in + c] = acc[i][j];
+    if (p.dw_part) {
+        float* part = p.dw_part + (int64_t)blockIdx.z * p.n_out * p.n_in;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int n = n0 + wn + 16 * i + 4 * g + q;
+                if (n >= p.n_out) continue;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int k = k0 + wk + 16 * j + r;
+                    if (k < p.n_in) part[(int64_t)n * p.n_in + k] = acc[i][j][q];
+                }
+            }
+    }
+    if (sums) {  // the threads of one chunk column, in order
+        float* s_sum = reinterpret_cast<float*>(s_dz[0]);  // [kPass][128]
+#pragma unroll
+        for (int j = 0; j < E; ++j) s_sum[mr * 128 + ch * E + j] = sum[j];
+        __syncthreads();
+        if (threadIdx.x < 128 && n0 + (int)threadIdx.x < p.n_out) {
+            float t = 0.f;
+            for (int i = 0; i < kPass; ++i) t += s_sum[i * 128 + threadIdx.x];
+            p.db_part[(int64_t)blockIdx.z * p.n_out + n0 + threadIdx.x] = t;
         }
+    }
 }
 
 // out [cols, rows] = in [rows, cols]^T, 64 x 64 per block.
@@ -376,26 +501,31 @@ __global__ __launch_bounds__(256) void k_transpose(const T* in, T* out, int32_t 
         if (c0 + c < cols && r0 + x < rows) out[(int64_t)(c0 + c) * rows + r0 + x] = s[x][c];
 }
 
-// out[e] = sum over splits of part[s][e], in order.
+// out[e] = sum over splits of part[s][e]: 256 / lanes elements per block, `lanes`
+// threads taking every lanes-th split each and joining in order.
 template <typename T>
-__global__ __launch_bounds__(256) void k_join(const float* part, int splits, int64_t count, T* out) {
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (e >= count) return;
+__global__ __launch_bounds__(256) void k_join(const float* part, int splits, int64_t count, int lanes, T* out) {
+    __shared__ float s_sum[256];
+    const int width = 256 / lanes, e_in = threadIdx.x % width, l = threadIdx.x / width;
+    const int64_t e = (int64_t)blockIdx.x * width + e_in;
     float acc = 0.f;
-    for (int s = 0; s < splits; ++s) acc += part[(int64_t)s * count + e];
+    if (e < count) {
+#pragma unroll 8
+        for (int s = l; s < splits; s += lanes) acc += part[(int64_t)s * count + e];
+    }
+    s_sum[threadIdx.x] = acc;
+    __syncthreads();
+    if (l != 0 || e >= count) return;
+    for (int i = 1; i < lanes; ++i) acc += s_sum[i * width + e_in];
     out[e] = (T)acc;
 }
 
-// Column sums of dz over one split of the rows (blockIdx.y).
 template <typename T>
-__global__ __launch_bounds__(256) void k_colsum(const T* dz, int64_t ld, int64_t rows, int32_t cols, int64_t per,
-                                                float* part) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= cols) return;
-    const int64_t r0 = (int64_t)blockIdx.y * per, r1 = min(rows, r0 + per);
-    float acc = 0.f;
-    for (int64_t r = r0; r < r1; ++r) acc += (float)dz[r * ld + c];
-    part[(int64_t)blockIdx.y * cols + c] = acc;
+void join(const float* part, int splits, int64_t count, void* out, hipStream_t s) {
+    int lanes = 1;
+    while (lanes < 16 && lanes * 8 <= splits) lanes *= 2;
+    hipLaunchKernelGGL((k_join<T>), dim3((unsigned)cdiv(count, 256 / lanes)), dim3(256), 0, s, part, splits, count,
+                       lanes, static_cast<T*>(out));
 }
 
 inline int check_shape(const gs_linear* d) {
@@ -420,9 +550,13 @@ struct BwdPlan {
 inline BwdPlan bwd_plan(const gs_linear* d) {
     BwdPlan p{};
     const int e = 16 / size_of(d->dtype);
-    p.splits = (int)(d->rows > 256 ? (d->rows + 255) / 256 : 1);
-    if (p.splits > 64) p.splits = 64;
-    p.per = cdiv(cdiv(d->rows, p.splits), 16) * 16;
+    // two blocks per CU between the tiles and the splits of the rows, each split at least 256 rows
+    const int64_t tiles = cdiv(d->n_out, 128) * cdiv(d->n_in > 0 ? d->n_in : 1, 128);
+    int64_t splits = tiles > 0 ? cdiv(512, tiles) : 1;
+    if (splits > cdiv(d->rows, 256)) splits = cdiv(d->rows, 256);
+    if (splits < 1) splits = 1;
+    p.per = cdiv(cdiv(d->rows, splits), 64) * 64;
+    p.splits = (int)(d->rows > 0 ? cdiv(d->rows, p.per) : 1);
     size_t at = 0;
     p.dz = at;
     p.ld_dz = cdiv(d->n_out, e) * e;
@@ -467,23 +601,17 @@ void bwd(const gs_linear* d, const void* x, const void* w, const void* bias, con
                    GS_ACT_NONE};
         product<T>(p, s);
     }
-    float* part = reinterpret_cast<float*>(ws + plan.dw_part);
-    const int64_t n_w = (int64_t)d->n_out * d->n_in;
-    if (dw && n_w > 0) {
-        hipLaunchKernelGGL((k_dw<T>),
-                           dim3((unsigned)cdiv(d->n_out, 64), (unsigned)cdiv(d->n_in, 64), (unsigned)plan.splits),
-                           dim3(256), 0, s, static_cast<const T*>(dz), ld_dz, static_cast<const T*>(x), d->ld_x,
-                           d->rows, d->n_out, d->n_in, plan.per, part);
-        hipLaunchKernelGGL((k_join<T>), dim3((unsigned)cdiv(n_w, 256)), dim3(256), 0, s, part, plan.splits, n_w,
-                           static_cast<T*>(dw));
-    }
-    if (db && d->n_out > 0) {
-        float* dbp = reinterpret_cast<float*>(ws + plan.db_part);
-        hipLaunchKernelGGL((k_colsum<T>), dim3((unsigned)cdiv(d->n_out, 256), plan.splits), dim3(256), 0, s,
-                           static_cast<const T*>(dz), ld_dz, d->rows, d->n_out, plan.per, dbp);
-        hipLaunchKernelGGL((k_join<T>), dim3((unsigned)cdiv(d->n_out, 256)), dim3(256), 0, s, dbp, plan.splits,
-                           (int64_t)d->n_out, static_cast<T*>(db));
-    }
+    const bool want_dw = dw && d->n_out > 0 && d->n_in > 0, want_db = db && d->n_out > 0;
+    if (!want_dw && !want_db) return;
+    DwArgs q{dz, x, nullptr, nullptr, d->rows, ld_dz, d->ld_x, plan.per, d->n_out, want_dw ? d->n_in : 0};
+    if (want_dw) q.dw_part = reinterpret_cast<float*>(ws + plan.dw_part);
+    if (want_db) q.db_part = reinterpret_cast<float*>(ws + plan.db_part);
+    hipLaunchKernelGGL((k_dw<T>),
+                       dim3((unsigned)cdiv(q.n_out, 128), (unsigned)cdiv(q.n_in > 0 ? q.n_in : 1, 128),
+                            (unsigned)plan.splits),
+                       dim3(256), 0, s, q);
+    if (want_dw) join<T>(q.dw_part, plan.splits, (int64_t)d->n_out * d->n_in, dw, s);
+    if (want_db) join<T>(q.db_part, plan.splits, d->n_out, db, s);
 }
 
 }  // namespace
