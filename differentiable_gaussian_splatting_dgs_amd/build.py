@@ -18,7 +18,8 @@ LIB = os.path.join(PKG, "libgs.so")
 MEASURE_LIB = os.path.join(PKG, "libgs_measure.so")
 OBJDIR = os.path.join(PKG, "_build")
 SOURCES = ["api.hip", "preprocess.hip", "binning.hip", "render.hip", "preprocess_bwd.hip", "train.hip",
-           "densify.hip", "debug.hip", "linear.hip", "clip.hip"]
+           "densify.hip", "debug.hip", "linear.hip", "linear_bwd_f32.hip",
+           "linear_bwd_f16.hip", "linear_bwd_bf16.hip", "clip.hip"]
 MEASURE_SOURCES = ["calibrate.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -53,6 +54,7 @@ def build(force=True, verbose=False):
     """Compile every HIP source and link both libraries.  Always rebuilds when force."""
     deps = [os.path.join(CSRC, s) for s in SOURCES + MEASURE_SOURCES] + [
         os.path.join(CSRC, "gs_internal.h"), os.path.join(CSRC, "linear_tile.h"),
+        os.path.join(CSRC, "linear_bwd.h"),
         os.path.join(INCLUDE, "gs.h"), os.path.join(INCLUDE, "gs_measure.h")]
     if (not force and all(os.path.exists(x) for x in (LIB, MEASURE_LIB)) and
             min(os.path.getmtime(LIB), os.path.getmtime(MEASURE_LIB)) >= max(os.path.getmtime(d) for d in deps)):

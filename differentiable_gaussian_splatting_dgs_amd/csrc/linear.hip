@@ -5,7 +5,7 @@
 //
 // Products are summed in float32, the activation runs in float32, and every
 // result is rounded once.
-#include "linear_tile.h"
+#include "linear_bwd.h"
 
 namespace gs {
 namespace {
@@ -330,60 +330,6 @@ void product(const ProdArgs& p, hipStream_t s) {
     hipLaunchKernelGGL((k_prod_big<T>), dim3((unsigned)(cdiv(tiles, 8) * 8)), dim3(256), 0, s, p);
 }
 
-// Fragments of the transposed operands of dw = dz^T x, whose sum runs down the
-// rows: a step takes KS rows, and lane l needs, of column l % 16, E of them.  The
-// tile lies in LDS in its own row order, 128 columns a row.  16-bit: two
-// transposing reads, each of which hands a group of 16 lanes the 4 x 16 block that
-// its lanes' 8-byte pieces of 4 rows make up (lane i: column i); float32: one
-// 4-byte read for each of the instruction's four 4-row slices.  Rows are rotated
-// by dw_key so that the rows of one access lie in different banks.
-template <typename T>
-struct RowsGeom {  // one LDS stage of 16 KB
-    static constexpr int kCols = 128;
-    static constexpr int kRows = 16384 / (kCols * (int)sizeof(T));  // 64 or 32
-    static constexpr int kChunks = kCols / Tile<T>::E;              // 16-byte chunks of a row: 16 or 32
-};
-
-// Byte offset of 16-byte chunk c of row m within a stage.
-template <typename T>
-__device__ __forceinline__ int dw_chunk(int m, int c) {
-    if (sizeof(T) == 2) {  // rotate 32-byte pieces: rows 0-3 and 8-11 of a read apart
-        const int key = (m & 3) | ((m >> 1) & 4);
-        return m * 256 + ((((c >> 1) ^ key) << 1 | (c & 1)) << 4);
-    }
-    return m * 512 + ((((c >> 2) ^ (m & 7)) << 2 | (c & 3)) << 4);  // rotate 64-byte pieces
-}
-
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-
-// Columns [c0, c0 + 16) of rows [m0, m0 + KS) of a stage, transposed.
-template <typename T>
-__device__ __forceinline__ typename Tile<T>::Frag dw_frag(const char* stage, int m0, int c0, int lane) {
-    const int r = lane & 15, g = lane >> 4;
-    if constexpr (sizeof(T) == 2) {
-        union {
-            typename Tile<T>::Frag f;
-            s16x4 h[2];
-        } u;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int m = m0 + 8 * g + 4 * h + (r >> 2), c = c0 + 4 * (r & 3);
-            const char* at = stage + dw_chunk<T>(m, c >> 3) + (c & 7) * 2;
-            u.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4*)const_cast<char*>(at));
-        }
-        return u.f;
-    } else {
-        typename Tile<T>::Frag f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int m = m0 + 4 * j + g, c = c0 + r;
-            f[j] = *reinterpret_cast<const float*>(stage + dw_chunk<T>(m, c >> 2) + (c & 3) * 4);
-        }
-        return f;
-    }
-}
-
 struct DwArgs {
     const void* dz;
     const void* x;
@@ -400,14 +346,15 @@ template <typename T>
 __global__ __launch_bounds__(256) void k_dw(DwArgs p) {
     constexpr int E = Tile<T>::E, KS = Tile<T>::KS;
     typedef typename Tile<T>::Frag Frag;
-    typedef RowsGeom<T> G;
     __shared__ __align__(16) char s_dz[2][16384], s_x[2][16384];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wn = (wave & 1) * 64, wk = (wave >> 1) * 64;
     const int n0 = blockIdx.x * 128, k0 = blockIdx.y * 128;
     const int64_t m_begin = (int64_t)blockIdx.z * p.per, m_end = min(p.rows, m_begin + p.per);
-    constexpr int kPass = 256 / G::kChunks;  // rows that the block's threads cover at a time
-    const int ch = threadIdx.x % G::kChunks, mr = threadIdx.x / G::kChunks;
+    constexpr int kRows = 16384 / (128 * (int)sizeof(T));  // of a stage: 64 or 32
+    constexpr int kChunks = 128 / E;                       // 16-byte chunks of a row
+    constexpr int kPass = 256 / kChunks;  // rows that the block's threads cover at a time
+    const int ch = threadIdx.x % kChunks, mr = threadIdx.x / kChunks;
     const T* dz = static_cast<const T*>(p.dz);
     const T* x = static_cast<const T*>(p.x);
     Frag rz[4], rx[4];
@@ -427,7 +374,7 @@ __global__ __launch_bounds__(256) void k_dw(DwArgs p) {
     auto put = [&](int buf) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int at = dw_chunk<T>(mr + i * kPass, ch);
+            const int at = row_chunk<T, 128>(mr + i * kPass, ch);
             *reinterpret_cast<Frag*>(s_dz[buf] + at) = rz[i];
             *reinterpret_cast<Frag*>(s_x[buf] + at) = rx[i];
             if (sums)
@@ -442,16 +389,16 @@ __global__ __launch_bounds__(256) void k_dw(DwArgs p) {
     }
     __syncthreads();
     int buf = 0;
-    for (int64_t m0 = m_begin; m0 < m_end; m0 += G::kRows, buf ^= 1) {
-        const bool more = m0 + G::kRows < m_end;
-        if (more) fetch(m0 + G::kRows);
+    for (int64_t m0 = m_begin; m0 < m_end; m0 += kRows, buf ^= 1) {
+        const bool more = m0 + kRows < m_end;
+        if (more) fetch(m0 + kRows);
 #pragma unroll
-        for (int h = 0; h < G::kRows / KS; ++h) {
+        for (int h = 0; h < kRows / KS; ++h) {
             Frag fz[4], fx[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                fz[i] = dw_frag<T>(s_dz[buf], h * KS, wn + 16 * i, lane);
-                fx[i] = dw_frag<T>(s_x[buf], h * KS, wk + 16 * i, lane);
+                fz[i] = column_frag<T, 128>(s_dz[buf], h * KS, wn + 16 * i, lane);
+                fx[i] = column_frag<T, 128>(s_x[buf], h * KS, wk + 16 * i, lane);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -541,28 +488,41 @@ inline bool element_aligned(const void* p, int32_t dtype) {
 }
 
 struct BwdPlan {
+    bool narrow;                             // one pass over the rows
     size_t dz, wt, dw_part, db_part, bytes;  // offsets in the workspace
     int64_t ld_dz;
-    int splits;
+    int splits;  // of the rows: partial dw and db
     int64_t per;
 };
 
+template <typename T>
+inline bool plan_narrow(const gs_linear* d, BwdPlan& p) {
+    if (d->rows < 1 || !bwd_narrow_fits<T>(d->n_in, d->n_out)) return false;
+    p.splits = bwd_narrow_blocks<T>(d->rows, d->n_in, d->n_out);
+    return true;
+}
+
 inline BwdPlan bwd_plan(const gs_linear* d) {
     BwdPlan p{};
-    const int e = 16 / size_of(d->dtype);
-    // two blocks per CU between the tiles and the splits of the rows, each split at least 256 rows
-    const int64_t tiles = cdiv(d->n_out, 128) * cdiv(d->n_in > 0 ? d->n_in : 1, 128);
-    int64_t splits = tiles > 0 ? cdiv(512, tiles) : 1;
-    if (splits > cdiv(d->rows, 256)) splits = cdiv(d->rows, 256);
-    if (splits < 1) splits = 1;
-    p.per = cdiv(cdiv(d->rows, splits), 64) * 64;
-    p.splits = (int)(d->rows > 0 ? cdiv(d->rows, p.per) : 1);
     size_t at = 0;
-    p.dz = at;
-    p.ld_dz = cdiv(d->n_out, e) * e;
-    if (d->act != GS_ACT_NONE) at += pad256((size_t)d->rows * p.ld_dz * size_of(d->dtype));
-    p.wt = at;
-    at += pad256((size_t)d->n_out * d->n_in * size_of(d->dtype));
+    p.narrow = d->dtype == GS_F32   ? plan_narrow<float>(d, p)
+               : d->dtype == GS_F16 ? plan_narrow<_Float16>(d, p)
+                                    : plan_narrow<__bf16>(d, p);
+    if (!p.narrow) {
+        // two blocks per CU between the tiles and the splits of the rows, each split at least 256 rows
+        const int64_t tiles = cdiv(d->n_out, 128) * cdiv(d->n_in > 0 ? d->n_in : 1, 128);
+        int64_t splits = tiles > 0 ? cdiv(512, tiles) : 1;
+        if (splits > cdiv(d->rows, 256)) splits = cdiv(d->rows, 256);
+        if (splits < 1) splits = 1;
+        p.per = cdiv(cdiv(d->rows, splits), 64) * 64;
+        p.splits = (int)(d->rows > 0 ? cdiv(d->rows, p.per) : 1);
+        const int e = 16 / size_of(d->dtype);
+        p.ld_dz = cdiv(d->n_out, e) * e;
+        p.dz = at;
+        if (d->act != GS_ACT_NONE) at += pad256((size_t)d->rows * p.ld_dz * size_of(d->dtype));
+        p.wt = at;
+        at += pad256((size_t)d->n_out * d->n_in * size_of(d->dtype));
+    }
     p.dw_part = at;
     at += pad256((size_t)p.splits * d->n_out * d->n_in * 4);
     p.db_part = at;
@@ -583,6 +543,16 @@ template <typename T>
 void bwd(const gs_linear* d, const void* x, const void* w, const void* bias, const void* dy, void* dx, void* dw,
          void* db, char* ws, hipStream_t s) {
     const BwdPlan plan = bwd_plan(d);
+    if (plan.narrow) {
+        BwdArgs q{x, w, bias, dy, dx, nullptr, nullptr, d->rows, d->ld_x, d->ld_y, d->ld_dx, d->n_in, d->n_out,
+                  d->act};
+        if (dw) q.dw_part = reinterpret_cast<float*>(ws + plan.dw_part);
+        if (db) q.db_part = reinterpret_cast<float*>(ws + plan.db_part);
+        launch_bwd_narrow<T>(q, plan.splits, s);
+        if (dw) join<T>(q.dw_part, plan.splits, (int64_t)d->n_out * d->n_in, dw, s);
+        if (db) join<T>(q.db_part, plan.splits, d->n_out, db, s);
+        return;
+    }
     const void* dz = dy;
     int64_t ld_dz = d->ld_y;
     if (d->act != GS_ACT_NONE && d->rows > 0 && d->n_out > 0) {

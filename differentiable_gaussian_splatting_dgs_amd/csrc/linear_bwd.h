@@ -1,0 +1,298 @@
+// The narrow layers' backward in one pass over the rows.
+//
+// A block holds the weights in LDS and walks tiles of 16 rows per wave.  Per tile a
+// wave reads its rows' x and dy once, recomputes z^T = w x^T, turns the result
+// registers into dz, which are at once the fragments of dx^T = w^T dz^T (see
+// linear_tile.h), and writes dx; x and dz go to LDS in the layer's type, where
+// the block's waves share out dw += dz^T x, each keeping its part of dw in registers
+// for the life of the block.  db adds up in the same registers as dz, unrounded.
+// Nothing else touches memory: x and dy are read once, dx is written once, and
+// each block leaves one partial dw and db for the join.
+#pragma once
+
+#include "linear_tile.h"
+
+namespace gs {
+
+struct BwdArgs {
+    const void* x;
+    const void* w;
+    const void* bias;
+    const void* dy;
+    void* dx;        // NULL: not wanted
+    float* dw_part;  // [blocks][n_out][n_in], NULL: not wanted
+    float* db_part;  // [blocks][n_out], NULL: not wanted
+    int64_t rows, ld_x, ld_dy, ld_dx;
+    int32_t n_in, n_out, act;
+};
+
+constexpr int kBwdGroups = 4;  // groups of KS inputs and of KS outputs at most
+
+template <typename T, int SL, int NG>
+struct BwdGeom {
+    static constexpr int KS = Tile<T>::KS, TG = Tile<T>::TG;
+    static constexpr int KP = SL * KS, NP = NG * KS;  // padded inputs and outputs
+    static constexpr int kCopies = sizeof(T) == 4 ? 2 : 1;
+    static constexpr int kWaves = sizeof(T) == 4 || KP * NP <= 64 * 64 ? 4 : 8;
+    static constexpr int kRows = 16 * kWaves;
+    static constexpr int kW = kCopies * KP * NP * (int)sizeof(T);
+    static constexpr int kTiles = kRows * (KP + NP) * (int)sizeof(T);
+    static constexpr int kLds = kW + kTiles + NP * 4;
+    static constexpr int kPerCu = kLds > 80 * 1024 ? 1 : kLds > 53 * 1024 ? 2 : kLds > 40 * 1024 ? 3 : 4;
+    // dw's 16 x 16 tiles, NT by KT, dealt to the waves as TN x TK rectangles
+    static constexpr int NT = NG * TG, KT = SL * TG;
+    static constexpr int split() {
+        int best = 1, cost = 1 << 30;
+        for (int wn = 1; wn <= kWaves; wn *= 2) {
+            const int tn = (NT + wn - 1) / wn, tk = (KT + kWaves / wn - 1) / (kWaves / wn);
+            if (64 * tn * tk + tn + tk < cost) cost = 64 * tn * tk + tn + tk, best = wn;
+        }
+        return best;
+    }
+    static constexpr int WN = split(), WK = kWaves / WN;
+    static constexpr int TN = (NT + WN - 1) / WN, TK = (KT + WK - 1) / WK;
+};
+
+// Slot of lane l's fragment in LDS: the rows of the four lane groups are rotated
+// against each other, so that the transposing reads of w^T find them apart.
+__device__ __forceinline__ int w_slot(int r, int g) { return ((r + 4 * g) & 15) + 16 * g; }
+
+template <typename T, int SL, int NG>
+__global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64)) void k_bwd_narrow(BwdArgs p) {
+    typedef BwdGeom<T, SL, NG> G;
+    constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG;
+    typedef typename Tile<T>::Frag Frag;
+    extern __shared__ __align__(16) char s_mem[];
+    Frag* s_w = reinterpret_cast<Frag*>(s_mem);  // [NG][TG][SL][64], float32: then w^T [SL][NG][64]
+    char* s_dz = s_mem + G::kW;
+    char* s_x = s_dz + G::kRows * G::NP * (int)sizeof(T);
+    float* s_bias = reinterpret_cast<float*>(s_x + G::kRows * G::KP * (int)sizeof(T));
+    const T* w = static_cast<const T*>(p.w);
+    for (int i = threadIdx.x; i < NG * TG * SL * 64; i += blockDim.x) {
+        const int r = i & 15, g = (i >> 4) & 3, f = i >> 6, s = f % SL, n = f / SL / TG * KS + out_row<T>(f / SL % TG, r);
+        s_w[f * 64 + w_slot(r, g)] =
+            n < p.n_out ? load_frag(w + (int64_t)n * p.n_in, s * KS + E * g, p.n_in) : zero_frag<T>();
+    }
+    if constexpr (sizeof(T) == 4) {
+        Frag* s_wt = s_w + NG * SL * 64;
+        for (int i = threadIdx.x; i < NG * SL * 64; i += blockDim.x) {
+            const int r = i & 15, g = (i >> 4) & 3, f = i >> 6, n = f % NG * KS + E * g, k = f / NG * KS + r;
+            Frag v = zero_frag<T>();
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                if (n + j < p.n_out && k < p.n_in) v[j] = w[(int64_t)(n + j) * p.n_in + k];
+            s_wt[i] = v;
+        }
+    }
+    for (int i = threadIdx.x; i < G::NP; i += blockDim.x)
+        s_bias[i] = p.bias && i < p.n_out ? (float)static_cast<const T*>(p.bias)[i] : 0.f;
+    __syncthreads();
+
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tn0 = wave / G::WK * G::TN, tk0 = wave % G::WK * G::TK;
+    const int64_t tiles = (p.rows + G::kRows - 1) / G::kRows;
+    f32x4 dw[G::TN][G::TK] = {};
+    float db[NG][E] = {};
+    Frag x[SL], dy[NG];
+    auto fetch = [&](int64_t tile) {
+        const int64_t row = tile * G::kRows + wave * 16 + r;
+        if (row < p.rows) {
+            const T* xr = static_cast<const T*>(p.x) + row * p.ld_x;
+            const T* yr = static_cast<const T*>(p.dy) + row * p.ld_dy;
+#pragma unroll
+            for (int s = 0; s < SL - 1; ++s) x[s] = load16(xr + s * KS + E * g);
+            x[SL - 1] = load_frag(xr, (SL - 1) * KS + E * g, p.n_in);
+#pragma unroll
+            for (int n = 0; n < NG - 1; ++n) dy[n] = load16(yr + n * KS + E * g);
+            dy[NG - 1] = load_frag(yr, (NG - 1) * KS + E * g, p.n_out);
+        } else {  // rows past the end add nothing: dz = 0, x = 0
+#pragma unroll
+            for (int s = 0; s < SL; ++s) x[s] = zero_frag<T>();
+#pragma unroll
+            for (int n = 0; n < NG; ++n) dy[n] = zero_frag<T>();
+        }
+    };
+    if (blockIdx.x < tiles) fetch(blockIdx.x);
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int64_t row = tile * G::kRows + wave * 16 + r;
+        const int m = wave * 16 + r;
+        Frag dz[NG];
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+            float v[E];
+            if (p.act != GS_ACT_NONE) {
+                f32x4 z[TG];
+#pragma unroll
+                for (int t = 0; t < TG; ++t) z[t] = *reinterpret_cast<f32x4*>(s_bias + n * KS + E * g + 4 * t);
+#pragma unroll
+                for (int s = 0; s < SL; ++s)
+#pragma unroll
+                    for (int t = 0; t < TG; ++t) mma(z[t], s_w[((n * TG + t) * SL + s) * 64 + w_slot(r, g)], x[s]);
+#pragma unroll
+                for (int j = 0; j < E; ++j) v[j] = z[j / 4][j % 4];
+                float d[E];
+#pragma unroll
+                for (int j = 0; j < E; ++j) d[j] = (float)dy[n][j];
+                slope_run<T>(p.act, v, d);
+                if (row >= p.rows)  // the bias can be infinite or NaN there
+#pragma unroll
+                    for (int j = 0; j < E; ++j) v[j] = 0.f;
+            } else {
+#pragma unroll
+                for (int j = 0; j < E; ++j) v[j] = (float)dy[n][j];
+            }
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                db[n][j] += v[j];
+                dz[n][j] = (T)v[j];
+            }
+            *reinterpret_cast<Frag*>(s_dz + row_chunk<T, G::NP>(m, n * 4 + g)) = dz[n];
+        }
+#pragma unroll
+        for (int s = 0; s < SL; ++s) *reinterpret_cast<Frag*>(s_x + row_chunk<T, G::KP>(m, s * 4 + g)) = x[s];
+        if (tile + gridDim.x < tiles) fetch(tile + gridDim.x);
+        if (p.dx) {
+            T* out = static_cast<T*>(p.dx) + row * p.ld_dx;
+#pragma unroll
+            for (int k = 0; k < SL; ++k) {
+                f32x4 acc[TG] = {};
+#pragma unroll
+                for (int n = 0; n < NG; ++n)
+#pragma unroll
+                    for (int t = 0; t < TG; ++t) {
+                        if constexpr (sizeof(T) == 2) {
+                            union {
+                                Frag f;
+                                s16x4 h[2];
+                            } u;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                u.h[h] = read_transposed(
+                                    reinterpret_cast<const char*>(s_w + ((n * TG + h) * SL + k) * 64 +
+                                                                  w_slot(4 * g + (r >> 2), r & 3)) +
+                                    8 * t);
+                            mma(acc[t], u.f, dz[n]);
+                        } else {
+                            mma(acc[t], s_w[(NG * SL + k * NG + n) * 64 + lane], dz[n]);
+                        }
+                    }
+                if (row < p.rows) {
+                    Frag f;
+#pragma unroll
+                    for (int j = 0; j < E; ++j) f[j] = (T)acc[j / 4][j % 4];
+                    store_run(out, k * KS + E * g, p.n_in, f);
+                }
+            }
+        }
+        __syncthreads();
+        if (p.dw_part) {
+#pragma unroll
+            for (int h = 0; h < G::kRows / KS; ++h) {
+                Frag fz[G::TN], fx[G::TK];
+#pragma unroll
+                for (int i = 0; i < G::TN; ++i)
+                    if (tn0 + i < G::NT) fz[i] = column_frag<T, G::NP>(s_dz, h * KS, (tn0 + i) * 16, lane);
+#pragma unroll
+                for (int j = 0; j < G::TK; ++j)
+                    if (tk0 + j < G::KT) fx[j] = column_frag<T, G::KP>(s_x, h * KS, (tk0 + j) * 16, lane);
+#pragma unroll
+                for (int i = 0; i < G::TN; ++i)
+#pragma unroll
+                    for (int j = 0; j < G::TK; ++j)
+                        if (tn0 + i < G::NT && tk0 + j < G::KT) mma(dw[i][j], fz[i], fx[j]);
+            }
+        }
+        __syncthreads();
+    }
+    if (p.dw_part) {
+        float* part = p.dw_part + (int64_t)blockIdx.x * p.n_out * p.n_in;
+#pragma unroll
+        for (int i = 0; i < G::TN; ++i)
+#pragma unroll
+            for (int j = 0; j < G::TK; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int n = (tn0 + i) * 16 + 4 * g + q, k = (tk0 + j) * 16 + r;
+                    if (n < p.n_out && k < p.n_in) part[(int64_t)n * p.n_in + k] = dw[i][j][q];
+                }
+    }
+    if (p.db_part) {  // over the 16 rows of the lanes, then over the waves, in a fixed order
+        float* s_db = reinterpret_cast<float*>(s_dz);  // [waves][NP]
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                float v = db[n][j];
+                for (int o = 1; o < 16; o <<= 1) v += __shfl_xor(v, o, 64);
+                if (r == 0) s_db[wave * G::NP + n * KS + E * g + j] = v;
+            }
+        __syncthreads();
+        for (int n = threadIdx.x; n < p.n_out; n += blockDim.x) {
+            float v = 0.f;
+            for (int i = 0; i < G::kWaves; ++i) v += s_db[i * G::NP + n];
+            p.db_part[(int64_t)blockIdx.x * p.n_out + n] = v;
+        }
+    }
+}
+
+// Whether a layer is narrow enough, the blocks its rows fill, and the launch.
+template <typename T>
+bool bwd_narrow_fits(int32_t n_in, int32_t n_out);
+template <typename T>
+int bwd_narrow_blocks(int64_t rows, int32_t n_in, int32_t n_out);
+template <typename T>
+void launch_bwd_narrow(const BwdArgs& p, int blocks, hipStream_t s);
+
+// Their definitions for one type, for the source that compiles it.
+template <typename T, int SL, int NG>
+inline void bwd_narrow_one(const BwdArgs& p, int64_t rows, int* blocks, hipStream_t s, bool launch) {
+    typedef BwdGeom<T, SL, NG> G;
+    if (!launch) {
+        const int64_t tiles = (rows + G::kRows - 1) / G::kRows, most = 256 * G::kPerCu;
+        *blocks = (int)(tiles < most ? tiles : most);
+        return;
+    }
+    hipLaunchKernelGGL((k_bwd_narrow<T, SL, NG>), dim3(*blocks), dim3(G::kWaves * 64), G::kLds, s, p);
+}
+
+template <typename T, int SL>
+inline void bwd_narrow_out(const BwdArgs& p, int64_t rows, int32_t ng, int* blocks, hipStream_t s, bool launch) {
+    switch (ng) {
+        case 1: bwd_narrow_one<T, SL, 1>(p, rows, blocks, s, launch); break;
+        case 2: bwd_narrow_one<T, SL, 2>(p, rows, blocks, s, launch); break;
+        case 3: bwd_narrow_one<T, SL, 3>(p, rows, blocks, s, launch); break;
+        default: bwd_narrow_one<T, SL, 4>(p, rows, blocks, s, launch); break;
+    }
+}
+
+template <typename T>
+inline void bwd_narrow_any(const BwdArgs& p, int64_t rows, int32_t n_in, int32_t n_out, int* blocks, hipStream_t s,
+                           bool launch) {
+    const int sl = (n_in + Tile<T>::KS - 1) / Tile<T>::KS, ng = (n_out + Tile<T>::KS - 1) / Tile<T>::KS;
+    switch (sl) {
+        case 1: bwd_narrow_out<T, 1>(p, rows, ng, blocks, s, launch); break;
+        case 2: bwd_narrow_out<T, 2>(p, rows, ng, blocks, s, launch); break;
+        case 3: bwd_narrow_out<T, 3>(p, rows, ng, blocks, s, launch); break;
+        default: bwd_narrow_out<T, 4>(p, rows, ng, blocks, s, launch); break;
+    }
+}
+
+#define GS_DEFINE_BWD_NARROW(T)                                                                 \
+    template <>                                                                                 \
+    bool bwd_narrow_fits<T>(int32_t n_in, int32_t n_out) {                                      \
+        constexpr int kMost = kBwdGroups * Tile<T>::KS;                                         \
+        return n_in > 0 && n_out > 0 && n_in <= kMost && n_out <= kMost;                        \
+    }                                                                                           \
+    template <>                                                                                 \
+    int bwd_narrow_blocks<T>(int64_t rows, int32_t n_in, int32_t n_out) {                       \
+        int blocks = 0;                                                                         \
+        bwd_narrow_any<T>(BwdArgs{}, rows, n_in, n_out, &blocks, nullptr, false);               \
+        return blocks;                                                                          \
+    }                                                                                           \
+    template <>                                                                                 \
+    void launch_bwd_narrow<T>(const BwdArgs& p, int blocks, hipStream_t s) {                    \
+        bwd_narrow_any<T>(p, p.rows, p.n_in, p.n_out, &blocks, s, true);                        \
+    }
+
+}  // namespace gs

@@ -184,4 +184,57 @@ __device__ __forceinline__ void slope_run(int act, float (&v)[N], const float (&
     }
 }
 
+// Fragments of the transposed operands of dw = dz^T x, whose sum runs down the
+// rows: a step takes KS rows, and lane l needs, of column l % 16, E of them.  The
+// tile lies in LDS in its own row order, COLS columns a row.  16-bit: two
+// transposing reads, each of which hands a group of 16 lanes the 4 x 16 block that
+// its lanes' 8-byte pieces of 4 rows make up (lane i: column i); float32: one
+// 4-byte read for each of the instruction's four 4-row slices.  The 32-byte (float32:
+// 64-byte) pieces of a row are rotated by the row where rows would otherwise
+// start in the same bank, so that the rows of one access lie apart.
+template <typename T, int COLS>
+__device__ __forceinline__ int row_chunk(int m, int c) {  // byte offset of 16-byte chunk c of row m
+    constexpr int kBytes = COLS * (int)sizeof(T);
+    if constexpr (sizeof(T) == 2) {
+        const int key = kBytes == 256 ? ((m & 3) | ((m >> 1) & 4)) : kBytes == 128 ? ((m >> 1) & 3) : 0;
+        return m * kBytes + ((((c >> 1) ^ key) << 1 | (c & 1)) << 4);
+    } else {
+        const int key = kBytes == 512 ? (m & 7) : kBytes == 256 ? (m & 3) : kBytes == 128 ? ((m >> 1) & 1) : 0;
+        return m * kBytes + ((((c >> 2) ^ key) << 2 | (c & 3)) << 4);
+    }
+}
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ s16x4 read_transposed(const char* lds) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s16x4*)const_cast<char*>(lds));
+}
+
+// Columns [c0, c0 + 16) of rows [m0, m0 + KS), transposed.
+template <typename T, int COLS>
+__device__ __forceinline__ typename Tile<T>::Frag column_frag(const char* tile, int m0, int c0, int lane) {
+    const int r = lane & 15, g = lane >> 4;
+    if constexpr (sizeof(T) == 2) {
+        union {
+            typename Tile<T>::Frag f;
+            s16x4 h[2];
+        } u;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int m = m0 + 8 * g + 4 * h + (r >> 2), c = c0 + 4 * (r & 3);
+            u.h[h] = read_transposed(tile + row_chunk<T, COLS>(m, c >> 3) + (c & 7) * 2);
+        }
+        return u.f;
+    } else {
+        typename Tile<T>::Frag f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int m = m0 + 4 * j + g, c = c0 + r;
+            f[j] = *reinterpret_cast<const float*>(tile + row_chunk<T, COLS>(m, c >> 2) + (c & 3) * 4);
+        }
+        return f;
+    }
+}
+
 }  // namespace gs

@@ -144,6 +144,31 @@ def test_backward(size, dtype):
                 check(g, v, tol, (size, act, name))
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_backward_widths(dtype):
+    """Every number of 16- and 32-wide groups of inputs and outputs up to four, in either dimension."""
+    for n_in in (8, 24, 40, 61, 90, 121):
+        for n_out in (5, 32, 43, 56, 81, 128):
+            act = ACTS[(n_in + n_out) % 4]
+            x, w, b, _, dy = inputs(300, n_in, n_out, dtype)
+            for name, g, (v, tol) in zip(("dx", "dw", "db"), run_bwd(dy, x, w, b, act), exact_bwd(x, w, b, dy, act)):
+                check(g, v, tol, (n_in, n_out, act, name))
+
+
+def test_backward_of_some():
+    """Each gradient alone is what the full call gives, on every path."""
+    from differentiable_gaussian_splatting_dgs_amd import network
+    for dtype in TYPES:
+        for size in ((8, 512, 100), (300, 64, 64), (500, 300, 140)):
+            x, w, b, _, dy = inputs(*size, dtype)
+            print("some", size, dtype, flush=True)
+            full = run_bwd(dy, x, w, b, "silu")
+            for k in range(3):
+                got = network.linear_backward(dy, x, w, b, act="silu", need=[i == k for i in range(3)])
+                assert all((g is None) == (i != k) for i, g in enumerate(got))
+                assert torch.equal(got[k], full[k]), (size, k)
+
+
 # many rows: every depth a wave holds in registers, odd ones among them, and deeper or wider layers
 MANY = [(33_001, 3, 64), (33_001, 20, 3), (17_003, 63, 59), (17_003, 90, 40), (12_001, 128, 128), (17_000, 150, 33),
         (16_401, 190, 64), (9_001, 220, 100), (8_200, 256, 256), (17_001, 256, 20), (6_007, 257, 300),
