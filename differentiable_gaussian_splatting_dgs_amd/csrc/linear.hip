@@ -31,8 +31,8 @@ struct ProdArgs {
 // The epilogue of one run: E consecutive outputs of one row, with the run of the
 // residual or dy already in `other`.
 template <typename T>
-__device__ __forceinline__ void finish_run(const ProdArgs& p, int64_t row, int n0, float (&v)[Tile<T>::E],
-                                           typename Tile<T>::Frag other) {
+__device__ __forceinline__ typename Tile<T>::Frag finish_run(const ProdArgs& p, float (&v)[Tile<T>::E],
+                                                             typename Tile<T>::Frag other) {
     constexpr int E = Tile<T>::E;
     if (p.epi == EPI_FWD) {
         act_run<T>(p.act, v);
@@ -49,7 +49,7 @@ __device__ __forceinline__ void finish_run(const ProdArgs& p, int64_t row, int n
     typename Tile<T>::Frag f;
 #pragma unroll
     for (int j = 0; j < E; ++j) f[j] = (T)v[j];
-    store_run(static_cast<T*>(p.out) + row * p.ld_out, n0, p.cols, f);
+    return f;
 }
 
 // Few outputs or few rows: a block makes one group of KS outputs of 16 rows, its
@@ -111,78 +111,102 @@ __global__ __launch_bounds__(256) void k_prod_few(ProdArgs p) {
     }
     auto other = zero_frag<T>();
     if (p.other) other = load_frag(static_cast<const T*>(p.other) + row * p.ld_other, c0, p.cols);
-    finish_run<T>(p, row, c0, v, other);
+    store_run(static_cast<T*>(p.out) + row * p.ld_out, c0, p.cols, finish_run<T>(p, v, other));
 }
 
 // Narrow layers over many rows: the weights stay in LDS as fragments for the
-// life of the block, and each wave walks tiles of 16 R rows, reading a row's whole
+// life of the block, and each wave walks tiles of 16 rows, reading a row's whole
 // depth (SL steps) into registers once and making all its outputs: x is read once
-// and y written once, with no barrier in the loop.
-constexpr int kNarrowThreads = 512;  // at most
-template <typename T, int SL, int R>
+// and y written once, with no barrier in the loop.  Outputs are made and stored in
+// pairs of groups, 128 bytes of a row at a time: with 64 the lines leave the caches
+// half written (4.0 against 4.5 TB/s).  The next tile's x is on its way meanwhile.
+// Rows whose outputs are not whole 16-byte runs (PACK) are put together in LDS and
+// stored as the one contiguous piece of memory that a tile's rows are.
+constexpr int kNarrowThreads = 1024;  // at most
+template <typename T, int SL, bool PACK>
 __global__ __launch_bounds__(kNarrowThreads) void k_prod_narrow(ProdArgs p) {
-    constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG;
+    constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG, P = 2;
+    constexpr bool kAhead = SL <= 4;
     typedef typename Tile<T>::Frag Frag;
     extern __shared__ __align__(16) char s_mem[];
     const int groups = (p.cols + KS - 1) / KS;
     Frag* s_w = reinterpret_cast<Frag*>(s_mem);                                     // [groups][TG][SL][64]
     f32x4* s_bias = reinterpret_cast<f32x4*>(s_w + (size_t)groups * TG * SL * 64);  // [groups][KS / 4]
-    for (int i = threadIdx.x; i < groups * TG * SL * 64; i += blockDim.x) {
-        const int l = i & 63, sl = (i >> 6) % SL, gt = (i >> 6) / SL;
-        const int n = gt / TG * KS + out_row<T>(gt % TG, l & 15);
-        s_w[i] = n < p.cols ? load_frag(static_cast<const T*>(p.b) + (int64_t)n * p.ld_b, sl * KS + E * (l >> 4), p.depth)
-                            : zero_frag<T>();
+    const int waves = blockDim.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    T* s_out = reinterpret_cast<T*>(s_bias + groups * KS / 4) + wave * 16 * p.cols;  // PACK: [waves][16][cols]
+    const int64_t tiles = (p.rows + 15) / 16, step = (int64_t)gridDim.x * waves;
+    int64_t tile = (int64_t)blockIdx.x * waves + wave;
+    auto row_of = [&](int64_t t) { return min(t * 16 + r, p.rows - 1); };
+    Frag x[SL];
+    auto fetch = [&](int64_t t) {
+        const T* a = static_cast<const T*>(p.a) + row_of(t) * p.ld_a;
+#pragma unroll
+        for (int s = 0; s < SL - 1; ++s) x[s] = load16(a + s * KS + E * g);
+        x[SL - 1] = load_frag(a, (SL - 1) * KS + E * g, p.depth);
+    };
+    if (kAhead && tile < tiles) fetch(tile);
+    for (int i0 = threadIdx.x; i0 < groups * TG * SL * 64; i0 += 4 * blockDim.x) {
+        Frag v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * blockDim.x, l = i & 63, sl = (i >> 6) % SL, gt = (i >> 6) / SL;
+            const int n = gt / TG * KS + out_row<T>(gt % TG, l & 15);
+            v[u] = n < p.cols ? load_frag(static_cast<const T*>(p.b) + (int64_t)n * p.ld_b, sl * KS + E * (l >> 4), p.depth)
+                              : zero_frag<T>();
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (i0 + u * (int)blockDim.x < groups * TG * SL * 64) s_w[i0 + u * blockDim.x] = v[u];
     }
     for (int i = threadIdx.x; i < groups * KS; i += blockDim.x)
         reinterpret_cast<float*>(s_bias)[i] =
             p.bias && i < p.cols ? (float)static_cast<const T*>(p.bias)[i] : 0.f;
     __syncthreads();
-    const int waves = blockDim.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t tiles = (p.rows + 16 * R - 1) / (16 * R);
-    for (int64_t tile = (int64_t)blockIdx.x * waves + wave; tile < tiles; tile += (int64_t)gridDim.x * waves) {
-        const int left = (int)min(p.rows - tile * (16 * R), (int64_t)(16 * R));  // rows of this tile
-        Frag x[R][SL];
-        const T* a = static_cast<const T*>(p.a) + tile * (16 * R) * p.ld_a;
-#pragma unroll
-        for (int q = 0; q < R; ++q) {
-            const T* ar = a + (int64_t)min(16 * q + r, left - 1) * p.ld_a;
-#pragma unroll
-            for (int s = 0; s < SL - 1; ++s) x[q][s] = load16(ar + s * KS + E * g);
-            x[q][SL - 1] = load_frag(ar, (SL - 1) * KS + E * g, p.depth);
-        }
-        const T* o = static_cast<const T*>(p.other) + tile * (16 * R) * p.ld_other;
-        for (int n = 0; n < groups; ++n) {
-            const int c0 = n * KS + E * g;
-            Frag other[R];
+    for (; tile < tiles; tile += step) {
+        const int64_t row = tile * 16 + r;
+        if (!kAhead) fetch(tile);
+        const T* o = static_cast<const T*>(p.other) + row_of(tile) * p.ld_other;
+        T* out = PACK ? s_out + r * p.cols : static_cast<T*>(p.out) + row * p.ld_out;
+        for (int n = 0; n < groups; n += P) {
+            Frag other[P];
             if (p.other) {
 #pragma unroll
-                for (int q = 0; q < R; ++q)
-                    other[q] = load_frag(o + (int64_t)min(16 * q + r, left - 1) * p.ld_other, c0, p.cols);
+                for (int h = 0; h < P; ++h) other[h] = load_frag(o, (n + h) * KS + E * g, p.cols);
             }
-            f32x4 acc[R][TG];
+            f32x4 acc[P][TG];
 #pragma unroll
-            for (int t = 0; t < TG; ++t) {
-                const f32x4 b = s_bias[(n * KS + E * g) / 4 + t];
+            for (int h = 0; h < P; ++h) {
+                if (h > 0 && n + h >= groups) break;
 #pragma unroll
-                for (int q = 0; q < R; ++q) acc[q][t] = b;
+                for (int t = 0; t < TG; ++t) acc[h][t] = s_bias[((n + h) * KS + E * g) / 4 + t];
+#pragma unroll
+                for (int s = 0; s < SL; ++s)
+#pragma unroll
+                    for (int t = 0; t < TG; ++t) mma(acc[h][t], s_w[(((n + h) * TG + t) * SL + s) * 64 + lane], x[s]);
             }
+            if (kAhead && n + P >= groups && tile + step < tiles) fetch(tile + step);
+            Frag f[P];
 #pragma unroll
-            for (int s = 0; s < SL; ++s)
-#pragma unroll
-                for (int t = 0; t < TG; ++t) {
-                    const Frag w = s_w[((n * TG + t) * SL + s) * 64 + lane];
-#pragma unroll
-                    for (int q = 0; q < R; ++q) mma(acc[q][t], w, x[q][s]);
-                }
-#pragma unroll
-            for (int q = 0; q < R; ++q) {
-                if (16 * q + r >= left) continue;
+            for (int h = 0; h < P; ++h) {
                 float v[E];
 #pragma unroll
-                for (int j = 0; j < E; ++j) v[j] = acc[q][j / 4][j % 4];
-                finish_run<T>(p, tile * (16 * R) + 16 * q + r, c0, v, other[q]);
+                for (int j = 0; j < E; ++j) v[j] = acc[h][j / 4][j % 4];
+                f[h] = finish_run<T>(p, v, other[h]);
             }
+            if (PACK || row < p.rows) {
+#pragma unroll
+                for (int h = 0; h < P; ++h) store_run(out, (n + h) * KS + E * g, p.cols, f[h]);
+            }
+        }
+        if (PACK) {
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            const int count = (int)min((int64_t)16, p.rows - tile * 16) * p.cols;
+            T* to = static_cast<T*>(p.out) + tile * 16 * p.cols;
+            for (int i = lane * E; i + E <= count; i += 64 * E)
+                *reinterpret_cast<Frag*>(to + i) = *reinterpret_cast<const Frag*>(s_out + i);
+            for (int i = count / E * E + lane; i < count; i += 64) to[i] = s_out[i];
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         }
     }
 }
@@ -289,19 +313,26 @@ __global__ __launch_bounds__(256) void k_prod_big(ProdArgs p) {
             float v[E];
 #pragma unroll
             for (int j = 0; j < E; ++j) v[j] = acc[i][q * TG + j / 4][j % 4] + bias[j];
-            finish_run<T>(p, row, c0, v, other);
+            store_run(static_cast<T*>(p.out) + row * p.ld_out, c0, p.cols, finish_run<T>(p, v, other));
         }
     }
 }
 
 template <typename T, int SL>
 void launch_narrow(const ProdArgs& p, size_t lds, hipStream_t s) {
-    constexpr int R = SL <= 2 ? 4 : 2;
-    const int threads = lds <= 40960 ? 256 : 512;
-    const int64_t most = 256 * (lds <= 40960 ? 4 : lds <= 81920 ? 2 : 1);
-    const int64_t blocks = cdiv(cdiv(p.rows, 16 * R), threads / 64);
-    hipLaunchKernelGGL((k_prod_narrow<T, SL, R>), dim3((unsigned)(blocks < most ? blocks : most)), dim3(threads), lds,
-                       s, p);
+    constexpr int E = Tile<T>::E;
+    int threads = lds <= 40960 ? 256 : lds <= 81920 ? 512 : 1024;
+    const bool pack = p.ld_out == p.cols && p.cols % E != 0 && aligned16(p.out) &&
+                      lds + (size_t)threads / 4 * p.cols * sizeof(T) <= 160 * 1024;
+    if (pack) lds += (size_t)threads / 4 * p.cols * sizeof(T);
+    int per_cu = (int)(160 * 1024 / lds);
+    if (per_cu > 1024 / threads) per_cu = 1024 / threads;
+    const int64_t blocks = cdiv(cdiv(p.rows, 16), threads / 64);
+    const dim3 grid((unsigned)(blocks < 256 * per_cu ? blocks : 256 * per_cu));
+    if (pack)
+        hipLaunchKernelGGL((k_prod_narrow<T, SL, true>), grid, dim3(threads), lds, s, p);
+    else
+        hipLaunchKernelGGL((k_prod_narrow<T, SL, false>), grid, dim3(threads), lds, s, p);
 }
 
 template <typename T>
