@@ -364,10 +364,10 @@ void product(const ProdArgs& p, hipStream_t s) {
 struct DwArgs {
     const void* dz;
     const void* x;
-    float* dw_part;  // [splits][n_out][n_in], NULL: not wanted
-    float* db_part;  // [splits][n_out], NULL: not wanted
+    float* part;  // [splits][n_out * n_in of dw, then n_out of db], each if wanted
     int64_t rows, ld_dz, ld_x, per;
     int32_t n_out, n_in;
+    int32_t want_dw, want_db;
 };
 
 // One split of the rows for a 128 x 128 tile of dw: 64 x 64 per wave, the next
@@ -401,7 +401,7 @@ __global__ __launch_bounds__(256) void k_dw(DwArgs p) {
         }
     };
     float sum[E] = {};
-    const bool sums = p.db_part && blockIdx.y == 0;
+    const bool sums = p.want_db && blockIdx.y == 0;
     auto put = [&](int buf) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -439,8 +439,9 @@ __global__ __launch_bounds__(256) void k_dw(DwArgs p) {
         if (more) put(buf ^ 1);
         __syncthreads();
     }
-    if (p.dw_part) {
-        float* part = p.dw_part + (int64_t)blockIdx.z * p.n_out * p.n_in;
+    const int64_t n_w = p.want_dw ? (int64_t)p.n_out * p.n_in : 0;
+    float* part = p.part + blockIdx.z * (n_w + (p.want_db ? p.n_out : 0));
+    if (p.want_dw) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -462,7 +463,7 @@ __global__ __launch_bounds__(256) void k_dw(DwArgs p) {
         if (threadIdx.x < 128 && n0 + (int)threadIdx.x < p.n_out) {
             float t = 0.f;
             for (int i = 0; i < kPass; ++i) t += s_sum[i * 128 + threadIdx.x];
-            p.db_part[(int64_t)blockIdx.z * p.n_out + n0 + threadIdx.x] = t;
+            part[n_w + n0 + threadIdx.x] = t;
         }
     }
 }
@@ -479,31 +480,160 @@ __global__ __launch_bounds__(256) void k_transpose(const T* in, T* out, int32_t 
         if (c0 + c < cols && r0 + x < rows) out[(int64_t)(c0 + c) * rows + r0 + x] = s[x][c];
 }
 
-// out[e] = sum over splits of part[s][e]: 256 / lanes elements per block, `lanes`
-// threads taking every lanes-th split each and joining in order.
-template <typename T>
-__global__ __launch_bounds__(256) void k_join(const float* part, int splits, int64_t count, int lanes, T* out) {
-    __shared__ float s_sum[256];
-    const int width = 256 / lanes, e_in = threadIdx.x % width, l = threadIdx.x / width;
-    const int64_t e = (int64_t)blockIdx.x * width + e_in;
-    float acc = 0.f;
-    if (e < count) {
-#pragma unroll 8
-        for (int s = l; s < splits; s += lanes) acc += part[(int64_t)s * count + e];
+// The backward of few rows (views, not Gaussians): one kernel and the join of dx.
+// A block has one group of KS outputs and 256 inputs.  It makes the group's z
+// as k_prod_few does, keeps dz in LDS unrounded, and then every thread has one
+// input: x's column in registers for its column of dw (complete: all rows are
+// here) and the partial dx that this group of outputs gives.  The weights are read
+// twice, the second time from the caches; what bounds it is latency.
+constexpr int kFewRows = 16;
+struct FewArgs {
+    const void* x;
+    const void* w;
+    const void* bias;
+    const void* dy;
+    void* dw;       // NULL: not wanted
+    void* db;       // NULL: not wanted
+    float* dx_part;  // [groups][rows][n_in], NULL: dx not wanted
+    int64_t ld_x, ld_dy;
+    int32_t rows, n_in, n_out, act;
+};
+
+template <typename T, int M>  // M: rows, rounded up
+__global__ __launch_bounds__(256) void k_bwd_few(FewArgs p) {
+    constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG;
+    __shared__ f32x4 s_acc[4][TG][64];
+    __shared__ float s_dz[KS][16];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int n0 = (int)blockIdx.x * KS, c0 = n0 + E * g;
+    const T* x = static_cast<const T*>(p.x);
+    const T* w = static_cast<const T*>(p.w);
+    const int k = (int)blockIdx.y * 256 + threadIdx.x, kc = k < p.n_in ? k : p.n_in - 1;
+    // what the second half needs is on its way during the first
+    float xk[M];
+#pragma unroll
+    for (int m = 0; m < M; ++m) xk[m] = (float)x[(int64_t)(m < p.rows ? m : p.rows - 1) * p.ld_x + kc];
+    f32x4 acc[TG] = {};
+    if (p.act != GS_ACT_NONE) {
+        const T* a = x + (int64_t)(r < p.rows ? r : p.rows - 1) * p.ld_x;
+        const T* b[TG];
+#pragma unroll
+        for (int t = 0; t < TG; ++t) {
+            const int n = n0 + out_row<T>(t, r);
+            b[t] = w + (int64_t)(n < p.n_out ? n : p.n_out - 1) * p.n_in;
+        }
+        for (int s = wave; s * KS < p.n_in; s += 4) {
+            const int k0 = s * KS + E * g;
+            const auto a0 = load_frag(a, k0, p.n_in);
+#pragma unroll
+            for (int t = 0; t < TG; ++t) mma(acc[t], load_frag(b[t], k0, p.n_in), a0);
+        }
     }
-    s_sum[threadIdx.x] = acc;
+#pragma unroll
+    for (int t = 0; t < TG; ++t) s_acc[wave][t][lane] = acc[t];
     __syncthreads();
-    if (l != 0 || e >= count) return;
-    for (int i = 1; i < lanes; ++i) acc += s_sum[i * width + e_in];
-    out[e] = (T)acc;
+    if (wave == 0) {
+        float v[E], d[E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            const int t = j / 4, i = j % 4;
+            v[j] = (s_acc[0][t][lane][i] + s_acc[1][t][lane][i]) + (s_acc[2][t][lane][i] + s_acc[3][t][lane][i]);
+            d[j] = 0.f;
+        }
+        if (p.bias) {
+            const auto bias = load_frag(static_cast<const T*>(p.bias), c0, p.n_out);
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] += (float)bias[j];
+        }
+        if (r < p.rows) {
+            const auto dy = load_frag(static_cast<const T*>(p.dy) + (int64_t)r * p.ld_dy, c0, p.n_out);
+#pragma unroll
+            for (int j = 0; j < E; ++j) d[j] = (float)dy[j];
+        }
+        slope_run<T>(p.act, v, d);
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            if (r >= p.rows || c0 + j >= p.n_out) v[j] = 0.f;
+            s_dz[E * g + j][r] = v[j];
+        }
+    }
+    __syncthreads();
+    if (p.db && blockIdx.y == 0 && threadIdx.x < KS && n0 + (int)threadIdx.x < p.n_out) {
+        float t = 0.f;
+        for (int m = 0; m < p.rows; ++m) t += s_dz[threadIdx.x][m];
+        static_cast<T*>(p.db)[n0 + threadIdx.x] = (T)t;
+    }
+    if (k >= p.n_in) return;
+    float dx[M] = {};
+    const int last = p.n_out - n0 < KS ? p.n_out - n0 : KS;
+#pragma unroll 4
+    for (int n = 0; n < last; ++n) {
+        const float wk = p.dx_part ? (float)w[(int64_t)(n0 + n) * p.n_in + k] : 0.f;
+        float t = 0.f;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            const float dz = s_dz[n][m];
+            // rows past the end have dz = 0, but x there is another row's and may be infinite
+            if (m < p.rows) t = fmaf(dz, xk[m], t);
+            dx[m] = fmaf(dz, wk, dx[m]);
+        }
+        if (p.dw) static_cast<T*>(p.dw)[(int64_t)(n0 + n) * p.n_in + k] = (T)t;
+    }
+    if (p.dx_part)
+        for (int m = 0; m < M; ++m)
+            if (m < p.rows) p.dx_part[((int64_t)blockIdx.x * p.rows + m) * p.n_in + k] = dx[m];
 }
 
 template <typename T>
-void join(const float* part, int splits, int64_t count, void* out, hipStream_t s) {
-    int lanes = 1;
-    while (lanes < 16 && lanes * 8 <= splits) lanes *= 2;
-    hipLaunchKernelGGL((k_join<T>), dim3((unsigned)cdiv(count, 256 / lanes)), dim3(256), 0, s, part, splits, count,
-                       lanes, static_cast<T*>(out));
+void launch_few(const FewArgs& p, hipStream_t s) {
+    const dim3 grid((unsigned)cdiv(p.n_out, Tile<T>::KS), (unsigned)cdiv(p.n_in, 256));
+    if (p.rows <= 1)
+        hipLaunchKernelGGL((k_bwd_few<T, 1>), grid, dim3(256), 0, s, p);
+    else if (p.rows <= 4)
+        hipLaunchKernelGGL((k_bwd_few<T, 4>), grid, dim3(256), 0, s, p);
+    else if (p.rows <= 8)
+        hipLaunchKernelGGL((k_bwd_few<T, 8>), grid, dim3(256), 0, s, p);
+    else
+        hipLaunchKernelGGL((k_bwd_few<T, 16>), grid, dim3(256), 0, s, p);
+}
+
+// The join of partial results: element e of [0, count) is the sum over splits of
+// part[s][e], 256 / lanes elements per block, `lanes` threads taking every lanes-th
+// split each and joining in order.  Elements [0, first) go to out0, rows of `cols`
+// elements ld apart, the rest to out1.
+struct JoinArgs {
+    const float* part;
+    void* out0;
+    void* out1;
+    int64_t count, first, ld;
+    int32_t cols, splits, lanes;
+};
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_join(JoinArgs p) {
+    __shared__ float s_sum[256];
+    const int width = 256 / p.lanes, e_in = threadIdx.x % width, l = threadIdx.x / width;
+    const int64_t e = (int64_t)blockIdx.x * width + e_in;
+    float acc = 0.f;
+    if (e < p.count) {
+#pragma unroll 8
+        for (int s = l; s < p.splits; s += p.lanes) acc += p.part[(int64_t)s * p.count + e];
+    }
+    s_sum[threadIdx.x] = acc;
+    __syncthreads();
+    if (l != 0 || e >= p.count) return;
+    for (int i = 1; i < p.lanes; ++i) acc += s_sum[i * width + e_in];
+    if (e >= p.first)
+        static_cast<T*>(p.out1)[e - p.first] = (T)acc;
+    else
+        static_cast<T*>(p.out0)[p.ld == p.cols ? e : e / p.cols * p.ld + e % p.cols] = (T)acc;
+}
+
+template <typename T>
+void join(JoinArgs p, hipStream_t s) {
+    p.lanes = 1;
+    while (p.lanes < 16 && p.lanes * 8 <= p.splits) p.lanes *= 2;
+    hipLaunchKernelGGL((k_join<T>), dim3((unsigned)cdiv(p.count, 256 / p.lanes)), dim3(256), 0, s, p);
 }
 
 inline int check_shape(const gs_linear* d) {
@@ -519,8 +649,8 @@ inline bool element_aligned(const void* p, int32_t dtype) {
 }
 
 struct BwdPlan {
-    bool narrow;                             // one pass over the rows
-    size_t dz, wt, dw_part, db_part, bytes;  // offsets in the workspace
+    bool few, narrow;            // one kernel for few rows; one pass over the rows
+    size_t dz, wt, part, bytes;  // offsets in the workspace
     int64_t ld_dz;
     int splits;  // of the rows: partial dw and db
     int64_t per;
@@ -536,6 +666,12 @@ inline bool plan_narrow(const gs_linear* d, BwdPlan& p) {
 inline BwdPlan bwd_plan(const gs_linear* d) {
     BwdPlan p{};
     size_t at = 0;
+    p.few = d->rows >= 1 && d->rows <= kFewRows && d->n_in > 0 && d->n_out > 0;
+    if (p.few) {  // a block per group of outputs leaves a partial dx
+        p.splits = (int)cdiv(d->n_out, d->dtype == GS_F32 ? Tile<float>::KS : Tile<_Float16>::KS);
+        p.bytes = pad256((size_t)p.splits * d->rows * d->n_in * 4);
+        return p;
+    }
     p.narrow = d->dtype == GS_F32   ? plan_narrow<float>(d, p)
                : d->dtype == GS_F16 ? plan_narrow<_Float16>(d, p)
                                     : plan_narrow<__bf16>(d, p);
@@ -554,10 +690,8 @@ inline BwdPlan bwd_plan(const gs_linear* d) {
         p.wt = at;
         at += pad256((size_t)d->n_out * d->n_in * size_of(d->dtype));
     }
-    p.dw_part = at;
-    at += pad256((size_t)p.splits * d->n_out * d->n_in * 4);
-    p.db_part = at;
-    at += pad256((size_t)p.splits * d->n_out * 4);
+    p.part = at;
+    at += pad256((size_t)p.splits * d->n_out * ((size_t)d->n_in + 1) * 4);
     p.bytes = at;
     return p;
 }
@@ -574,14 +708,26 @@ template <typename T>
 void bwd(const gs_linear* d, const void* x, const void* w, const void* bias, const void* dy, void* dx, void* dw,
          void* db, char* ws, hipStream_t s) {
     const BwdPlan plan = bwd_plan(d);
-    if (plan.narrow) {
-        BwdArgs q{x, w, bias, dy, dx, nullptr, nullptr, d->rows, d->ld_x, d->ld_y, d->ld_dx, d->n_in, d->n_out,
+    float* part = reinterpret_cast<float*>(ws + plan.part);
+    if (plan.few) {
+        FewArgs q{x, w, bias, dy, dw, db, dx ? part : nullptr, d->ld_x, d->ld_y, (int32_t)d->rows, d->n_in, d->n_out,
                   d->act};
-        if (dw) q.dw_part = reinterpret_cast<float*>(ws + plan.dw_part);
-        if (db) q.db_part = reinterpret_cast<float*>(ws + plan.db_part);
+        launch_few<T>(q, s);
+        if (dx) {
+            const int64_t count = d->rows * d->n_in;
+            join<T>(JoinArgs{part, dx, nullptr, count, count, d->ld_dx, d->n_in, plan.splits, 0}, s);
+        }
+        return;
+    }
+    const bool want_dw = dw && d->n_out > 0 && d->n_in > 0, want_db = db && d->n_out > 0;
+    const int64_t n_w = want_dw ? (int64_t)d->n_out * d->n_in : 0, n_b = want_db ? d->n_out : 0;
+    const JoinArgs sums{part, dw, db, n_w + n_b, n_w, d->n_in, d->n_in, plan.splits, 0};
+    if (plan.narrow) {
+        BwdArgs q{x, w, bias, dy, dx, part, d->rows, d->ld_x, d->ld_y, d->ld_dx, d->n_in, d->n_out, d->act,
+                  want_dw, want_db};
+        if (plan.splits == 1) q.dw = dw, q.db = db;
         launch_bwd_narrow<T>(q, plan.splits, s);
-        if (dw) join<T>(q.dw_part, plan.splits, (int64_t)d->n_out * d->n_in, dw, s);
-        if (db) join<T>(q.db_part, plan.splits, d->n_out, db, s);
+        if (plan.splits > 1 && (want_dw || want_db)) join<T>(sums, s);
         return;
     }
     const void* dz = dy;
@@ -602,17 +748,13 @@ void bwd(const gs_linear* d, const void* x, const void* w, const void* bias, con
                    GS_ACT_NONE};
         product<T>(p, s);
     }
-    const bool want_dw = dw && d->n_out > 0 && d->n_in > 0, want_db = db && d->n_out > 0;
     if (!want_dw && !want_db) return;
-    DwArgs q{dz, x, nullptr, nullptr, d->rows, ld_dz, d->ld_x, plan.per, d->n_out, want_dw ? d->n_in : 0};
-    if (want_dw) q.dw_part = reinterpret_cast<float*>(ws + plan.dw_part);
-    if (want_db) q.db_part = reinterpret_cast<float*>(ws + plan.db_part);
+    DwArgs q{dz, x, part, d->rows, ld_dz, d->ld_x, plan.per, d->n_out, want_dw ? d->n_in : 0, want_dw, want_db};
     hipLaunchKernelGGL((k_dw<T>),
                        dim3((unsigned)cdiv(q.n_out, 128), (unsigned)cdiv(q.n_in > 0 ? q.n_in : 1, 128),
                             (unsigned)plan.splits),
                        dim3(256), 0, s, q);
-    if (want_dw) join<T>(q.dw_part, plan.splits, (int64_t)d->n_out * d->n_in, dw, s);
-    if (want_db) join<T>(q.db_part, plan.splits, d->n_out, db, s);
+    join<T>(sums, s);
 }
 
 }  // namespace

@@ -19,11 +19,13 @@ struct BwdArgs {
     const void* w;
     const void* bias;
     const void* dy;
-    void* dx;        // NULL: not wanted
-    float* dw_part;  // [blocks][n_out][n_in], NULL: not wanted
-    float* db_part;  // [blocks][n_out], NULL: not wanted
+    void* dx;     // NULL: not wanted
+    float* part;  // [blocks][n_out * n_in of dw, then n_out of db], each if wanted
     int64_t rows, ld_x, ld_dy, ld_dx;
     int32_t n_in, n_out, act;
+    int32_t want_dw, want_db;
+    void* dw;  // one block: the results themselves instead of a partial
+    void* db;
 };
 
 constexpr int kBwdGroups = 4;  // groups of KS inputs and of KS outputs at most
@@ -186,7 +188,7 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64)) void k_bwd_narro
             }
         }
         __syncthreads();
-        if (p.dw_part) {
+        if (p.want_dw) {
 #pragma unroll
             for (int h = 0; h < G::kRows / KS; ++h) {
                 Frag fz[G::TN], fx[G::TK];
@@ -205,8 +207,9 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64)) void k_bwd_narro
         }
         __syncthreads();
     }
-    if (p.dw_part) {
-        float* part = p.dw_part + (int64_t)blockIdx.x * p.n_out * p.n_in;
+    const int64_t n_w = p.want_dw ? (int64_t)p.n_out * p.n_in : 0;
+    float* part = p.part + blockIdx.x * (n_w + (p.want_db ? p.n_out : 0));
+    if (p.want_dw) {
 #pragma unroll
         for (int i = 0; i < G::TN; ++i)
 #pragma unroll
@@ -214,10 +217,14 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64)) void k_bwd_narro
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int n = (tn0 + i) * 16 + 4 * g + q, k = (tk0 + j) * 16 + r;
-                    if (n < p.n_out && k < p.n_in) part[(int64_t)n * p.n_in + k] = dw[i][j][q];
+                    if (n >= p.n_out || k >= p.n_in) continue;
+                    if (p.dw)
+                        static_cast<T*>(p.dw)[(int64_t)n * p.n_in + k] = (T)dw[i][j][q];
+                    else
+                        part[(int64_t)n * p.n_in + k] = dw[i][j][q];
                 }
     }
-    if (p.db_part) {  // over the 16 rows of the lanes, then over the waves, in a fixed order
+    if (p.want_db) {  // over the 16 rows of the lanes, then over the waves, in a fixed order
         float* s_db = reinterpret_cast<float*>(s_dz);  // [waves][NP]
 #pragma unroll
         for (int n = 0; n < NG; ++n)
@@ -231,7 +238,10 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64)) void k_bwd_narro
         for (int n = threadIdx.x; n < p.n_out; n += blockDim.x) {
             float v = 0.f;
             for (int i = 0; i < G::kWaves; ++i) v += s_db[i * G::NP + n];
-            p.db_part[(int64_t)blockIdx.x * p.n_out + n] = v;
+            if (p.db)
+                static_cast<T*>(p.db)[n] = (T)v;
+            else
+                part[n_w + n] = v;
         }
     }
 }

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes as C
 import math
 import os
+import struct
 from dataclasses import dataclass, field
 
 import torch
@@ -149,13 +150,14 @@ def load_library(path=LIB_PATH):
     lib.gs_render_fwd_h16.argtypes = [P(GsCamera), P(GsSettings), _i32] + [_vp] * 9 + [_vp]
     lib.gs_render_bwd_h16.argtypes = [P(GsCamera), P(GsSettings), _i32] + [_vp] * 9 + [_i32, _vp]
     lib.gs_count_pairs_h16.argtypes = [P(GsCamera), P(GsSettings), _i32, _vp, _vp, _vp, _vp, _vp, _vp]
-    lib.gs_linear_fwd.argtypes = [P(GsLinear)] + [_vp] * 5 + [_vp]
-    lib.gs_linear_bwd_workspace_size.argtypes = [P(GsLinear), P(C.c_size_t)]
-    lib.gs_linear_bwd.argtypes = [P(GsLinear)] + [_vp] * 7 + [_vp, C.c_size_t, _vp]
+    # the descriptors of the network calls go as pointers to packed bytes or to the structures
+    lib.gs_linear_fwd.argtypes = [_vp] * 7
+    lib.gs_linear_bwd_workspace_size.argtypes = [_vp, P(C.c_size_t)]
+    lib.gs_linear_bwd.argtypes = [_vp] * 9 + [C.c_size_t, _vp]
     lib.gs_grad_workspace_size.argtypes = [_i32, P(C.c_size_t)]
-    lib.gs_grad_norm.argtypes = [_i32, P(GsGradTensor), C.c_float, _vp, _vp, C.c_size_t, _vp]
-    lib.gs_grad_clip.argtypes = [_i32, P(GsGradTensor), C.c_float, _vp, _vp, C.c_size_t, _vp]
-    lib.gs_adam_step_clipped.argtypes = [_i32, P(GsAdamTensor), C.c_float, C.c_float, C.c_float, _i32, _vp, _vp]
+    lib.gs_grad_norm.argtypes = [_i32, _vp, C.c_float, _vp, _vp, C.c_size_t, _vp]
+    lib.gs_grad_clip.argtypes = [_i32, _vp, C.c_float, _vp, _vp, C.c_size_t, _vp]
+    lib.gs_adam_step_clipped.argtypes = [_i32, _vp, C.c_float, C.c_float, C.c_float, _i32, _vp, _vp]
     for name in SYMBOLS:
         if name not in ("gs_error_string",):
             getattr(lib, name).restype = C.c_int
@@ -763,80 +765,124 @@ def gs_count_pairs_views(cams, settings, n, tile_ranges, point_list, splats, cou
 # the clipped Adam step (the classes over them are in network.py).
 # ---------------------------------------------------------------------------
 
+# A layer of a few rows takes a few microseconds on the GPU, so these wrappers keep
+# the host's part as short: one look at each property of a tensor, descriptors
+# packed in one go (gs_linear, gs_grad_tensor and gs_adam_tensor as bytes).
+# ---------------------------------------------------------------------------
+
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 CLIP_STATE_FLOATS = 4
 
+_pack_linear = struct.Struct("=qiiiiqqqq").pack
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
-def _rows(t, shape, dtype, name):
-    """(device pointer, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
+
+def _refuse(t, shape, dtype, name):
+    """Raises what is wrong with a tensor that should be a CUDA tensor of this shape and type."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise GsError(f"{name} must be a CUDA (HIP) tensor")
-    if t.dtype != dtype:
+    if dtype is not None and t.dtype != dtype:
         raise GsError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
+    if t.dtype not in DTYPES:
+        raise GsError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    if shape is not None and t.shape != shape:
         raise GsError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise GsError(f"{name} must be contiguous and on the other tensors' device")
+
+
+def _rows(t, shape, dtype, device, name):
+    """Row stride of a 2-D tensor on that CUDA device whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.get_device() != device:
+        _refuse(t, shape, dtype, name)
     s0, s1 = t.stride()
     if s1 != 1 and shape[1] > 1:
         raise GsError(f"{name} must have contiguous rows")
-    if shape[0] <= 1:
-        s0 = shape[1]
-    return t.data_ptr(), s0
+    return s0 if shape[0] > 1 else shape[1]
 
 
-def _linear_args(x, w, bias, act):
-    """GsLinear of x [rows, n_in] and w [n_out, n_in] with its dtype, and the device pointers of x, w and bias."""
+def _whole(t, shape, dtype, device, name):
+    """Device pointer of a contiguous tensor on that CUDA device (None -> NULL)."""
+    if t is None:
+        return None
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.get_device() != device or
+            not t.is_contiguous()):
+        _refuse(t, shape, dtype, name)
+    return t.data_ptr()
+
+
+def _linear_shape(x, w, act):
+    """(rows, n_in, n_out, type code, activation code, device, ld_x) of x [rows, n_in] and w [n_out, n_in]."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise GsError("x and w must be 2-D tensors")
-    if x.dtype not in DTYPES:
-        raise GsError(f"x must be float32, float16 or bfloat16, got {x.dtype}")
-    if act not in ACTS:
+    code = DTYPES.get(x.dtype)
+    if code is None or not x.is_cuda:
+        _refuse(x, None, None, "x")
+    a = ACTS.get(act)
+    if a is None:
         raise GsError(f"act must be one of {sorted(ACTS)}, got {act!r}")
-    rows, n_in = x.shape
-    n_out = w.shape[0]
-    d = GsLinear(rows, n_in, n_out, DTYPES[x.dtype], ACTS[act])
-    px, d.ld_x = _rows(x, (rows, n_in), x.dtype, "x")
-    if w.shape != (n_out, n_in):
+    shape = x.shape
+    rows, n_in = shape
+    n_out, w_in = w.shape
+    if w_in != n_in:
         raise GsError(f"w must have shape [n_out, {n_in}], got {tuple(w.shape)}")
-    if bias is not None and bias.shape != (n_out,):
-        raise GsError(f"bias must have shape ({n_out},), got {tuple(bias.shape)}")
-    return d, px, _p(w, x.dtype, "w"), _p(bias, x.dtype, "bias")
+    device = x.get_device()
+    return rows, n_in, n_out, code, a, device, _rows(x, shape, x.dtype, device, "x")
+
+
+def linear_fwd_into(x, w, bias, residual, y, act):
+    """gs_linear_fwd; y None: a new [rows, n_out] tensor.  Returns y."""
+    rows, n_in, n_out, code, a, device, ld_x = _linear_shape(x, w, act)
+    dtype, shape = x.dtype, (rows, n_out)
+    if y is None:
+        y, ld_y = torch.empty(shape, dtype=dtype, device=x.device), n_out
+    else:
+        ld_y = _rows(y, shape, dtype, device, "y")
+    pr, ld_res = None, 0
+    if residual is not None:
+        ld_res = _rows(residual, shape, dtype, device, "residual")
+        pr = residual.data_ptr()
+    rc = (_lib or load_library()).gs_linear_fwd(
+        _pack_linear(rows, n_in, n_out, code, a, ld_x, ld_y, ld_res, 0), x.data_ptr(),
+        _whole(w, w.shape, dtype, device, "w"), _whole(bias, (n_out,), dtype, device, "bias"), pr, y.data_ptr(),
+        _raw_stream(_current_device()))
+    if rc:
+        _check(rc, "gs_linear_fwd")
+    return y
 
 
 def gs_linear_fwd(x, w, bias, residual, y, act="none"):
     """y [rows, n_out] = act(x w^T + bias) + residual; bias and residual may be None.  Rows of x, residual and y
     may be strided; a residual with row stride 0 is one row for all."""
-    d, px, pw, pb = _linear_args(x, w, bias, act)
-    shape = (d.rows, d.n_out)
-    pr = None
-    if residual is not None:
-        pr, d.ld_res = _rows(residual, shape, x.dtype, "residual")
-    py, d.ld_y = _rows(y, shape, x.dtype, "y")
-    _check(load_library().gs_linear_fwd(C.byref(d), px, pw, pb, pr, py, _stream()), "gs_linear_fwd")
+    linear_fwd_into(x, w, bias, residual, y, act)
 
 
 def gs_linear_bwd_workspace_size(x, w, act="none"):
-    d, _, _, _ = _linear_args(x, w, None, act)
+    rows, n_in, n_out, code, a, _, _ = _linear_shape(x, w, act)
     b = C.c_size_t()
-    _check(load_library().gs_linear_bwd_workspace_size(C.byref(d), C.byref(b)), "gs_linear_bwd_workspace_size")
+    _check(load_library().gs_linear_bwd_workspace_size(_pack_linear(rows, n_in, n_out, code, a, 0, 0, 0, 0),
+                                                       C.byref(b)), "gs_linear_bwd_workspace_size")
     return b.value
 
 
 def gs_linear_bwd(x, w, bias, dy, dx, dw, db, workspace, act="none"):
     """The layer's gradients from dy [rows, n_out] into dx, dw and db (each may be None: not computed);
     workspace: uint8, gs_linear_bwd_workspace_size bytes, 256-byte aligned."""
-    d, px, pw, pb = _linear_args(x, w, bias, act)
-    pdy, d.ld_y = _rows(dy, (d.rows, d.n_out), x.dtype, "dy")
-    pdx = None
+    rows, n_in, n_out, code, a, device, ld_x = _linear_shape(x, w, act)
+    dtype = x.dtype
+    ld_y = _rows(dy, (rows, n_out), dtype, device, "dy")
+    pdx, ld_dx = None, 0
     if dx is not None:
-        pdx, d.ld_dx = _rows(dx, (d.rows, d.n_in), x.dtype, "dx")
-    if dw is not None and dw.shape != w.shape:
-        raise GsError(f"dw must have shape {tuple(w.shape)}, got {tuple(dw.shape)}")
-    if db is not None and db.shape != (d.n_out,):
-        raise GsError(f"db must have shape ({d.n_out},), got {tuple(db.shape)}")
-    _check(load_library().gs_linear_bwd(C.byref(d), px, pw, pb, pdy, pdx, _p(dw, x.dtype, "dw"),
-                                        _p(db, x.dtype, "db"), _p(workspace, torch.uint8, "workspace"),
-                                        workspace.numel(), _stream()), "gs_linear_bwd")
+        ld_dx = _rows(dx, (rows, n_in), dtype, device, "dx")
+        pdx = dx.data_ptr()
+    rc = (_lib or load_library()).gs_linear_bwd(
+        _pack_linear(rows, n_in, n_out, code, a, ld_x, ld_y, 0, ld_dx), x.data_ptr(),
+        _whole(w, w.shape, dtype, device, "w"), _whole(bias, (n_out,), dtype, device, "bias"), dy.data_ptr(), pdx,
+        _whole(dw, w.shape, dtype, device, "dw"), _whole(db, (n_out,), dtype, device, "db"),
+        _whole(workspace, workspace.shape, torch.uint8, device, "workspace"), workspace.numel(),
+        _raw_stream(_current_device()))
+    if rc:
+        _check(rc, "gs_linear_bwd")
 
 
 def gs_grad_workspace_size(n_tensors):
@@ -845,19 +891,24 @@ def gs_grad_workspace_size(n_tensors):
     return b.value
 
 
-def _grad_array(grads, out):
-    arr = (GsGradTensor * max(len(grads), 1))()
+def _grad_table(grads, out):
+    """The gs_grad_tensor array of a list of gradients, as bytes."""
+    flat = []
+    device = grads[0].get_device() if grads and isinstance(grads[0], torch.Tensor) else -1
     for i, g in enumerate(grads):
-        a = arr[i]
-        a.grad = _p(g, None, f"gradient {i}")
-        if g.dtype not in DTYPES:
-            raise GsError(f"gradient {i} must be float32, float16 or bfloat16, got {g.dtype}")
-        a.count, a.dtype = g.numel(), DTYPES[g.dtype]
-        if out is not None:
-            if out[i].shape != g.shape:
-                raise GsError(f"out {i} must have its gradient's shape")
-            a.out = _p(out[i], g.dtype, f"out {i}")
-    return arr
+        if not isinstance(g, torch.Tensor) or not g.is_contiguous() or g.get_device() != device or device < 0:
+            _refuse(g, None, None, f"gradient {i}")
+        code = DTYPES.get(g.dtype)
+        if code is None:
+            _refuse(g, None, None, f"gradient {i}")
+        p = g.data_ptr()
+        if out is None:
+            flat += (p, 0, g.numel(), code)
+        elif out[i] is g:
+            flat += (p, p, g.numel(), code)
+        else:
+            flat += (p, _whole(out[i], g.shape, g.dtype, device, f"out {i}") or 0, g.numel(), code)
+    return struct.pack("=%dq" % len(flat), *flat)
 
 
 def _clip_state(clip):
@@ -868,8 +919,9 @@ def _clip_state(clip):
 
 def gs_grad_norm(grads, max_norm, clip, workspace):
     """Global norm and clipping coefficient of the list grads into clip [4] float32 (words 0 and 1)."""
-    rc = load_library().gs_grad_norm(len(grads), _grad_array(grads, None), max_norm, _clip_state(clip),
-                                     _p(workspace, torch.uint8, "workspace"), workspace.numel(), _stream())
+    rc = (_lib or load_library()).gs_grad_norm(len(grads), _grad_table(grads, None), max_norm, _clip_state(clip),
+                                               _p(workspace, torch.uint8, "workspace"), workspace.numel(),
+                                               _raw_stream(_current_device()))
     _check(rc, "gs_grad_norm")
 
 
@@ -877,16 +929,18 @@ def gs_grad_clip(grads, out, max_norm, clip, workspace):
     """gs_grad_norm, then out[i] = coefficient * grads[i] (out may be grads itself)."""
     if len(out) != len(grads):
         raise GsError("out needs one tensor for each gradient")
-    rc = load_library().gs_grad_clip(len(grads), _grad_array(grads, out), max_norm, _clip_state(clip),
-                                     _p(workspace, torch.uint8, "workspace"), workspace.numel(), _stream())
+    rc = (_lib or load_library()).gs_grad_clip(len(grads), _grad_table(grads, out), max_norm, _clip_state(clip),
+                                               _p(workspace, torch.uint8, "workspace"), workspace.numel(),
+                                               _raw_stream(_current_device()))
     _check(rc, "gs_grad_clip")
 
 
 def gs_adam_step_clipped(tensors, beta1, beta2, eps, step, clip=None):
     """One Adam step on coefficient * gradient for a ctypes array of GsAdamTensor; clip: the state of
     gs_grad_norm, or None."""
-    rc = load_library().gs_adam_step_clipped(len(tensors), tensors, beta1, beta2, eps, step,
-                                             None if clip is None else _clip_state(clip), _stream())
+    rc = (_lib or load_library()).gs_adam_step_clipped(len(tensors), tensors, beta1, beta2, eps, step,
+                                                       None if clip is None else _clip_state(clip),
+                                                       _raw_stream(_current_device()))
     _check(rc, "gs_adam_step_clipped")
 
 

@@ -24,12 +24,6 @@ def _workspace(nbytes, device):
     return t[off:off + nbytes]
 
 
-def _forward(x, w, bias, residual, act):
-    y = torch.empty((x.shape[0], w.shape[0]), dtype=x.dtype, device=x.device)
-    gs.gs_linear_fwd(x, w, bias, residual, y, act)
-    return y
-
-
 def linear_backward(dy, x, w, bias=None, act="none", need=(True, True, True)):
     """dx, dw, db of y = act(x w^T + bias) from dy = dL/dy (None where need is False; db None without a bias).
     The gradient of a residual added to y is dy itself."""
@@ -47,7 +41,7 @@ class LinearFunction(torch.autograd.Function):
     def forward(ctx, x, w, bias, residual, act):
         ctx.act, ctx.has_bias = act, bias is not None
         ctx.save_for_backward(x, w, bias)
-        return _forward(x, w, bias, residual, act)
+        return gs.linear_fwd_into(x, w, bias, residual, None, act)
 
     @staticmethod
     def backward(ctx, dy):
@@ -73,7 +67,7 @@ def linear(x, w, bias=None, residual=None, act="none"):
     if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad) or
                                     (residual is not None and residual.requires_grad)):
         return LinearFunction.apply(x, w, bias, residual, act)
-    return _forward(x, w, bias, residual, act)
+    return gs.linear_fwd_into(x, w, bias, residual, None, act)
 
 
 class GradClip:
@@ -162,8 +156,7 @@ class Adam:
             if g.shape != self.params[i].shape or g.dtype not in gs.DTYPES:
                 raise GsError(f"gradient {i} must have its parameter's shape and a floating type")
             a = self.table[i]
-            a.grad = gs._p(g, None, f"gradient {i}")
-            a.grad_dtype = gs.DTYPES[g.dtype]
+            a.grad, a.grad_dtype = gs._p(g, None, f"gradient {i}"), gs.DTYPES[g.dtype]
         norm = self.clipper.norm(grads) if self.clipper is not None else None
         self.t += 1
         if self.params:
