@@ -62,7 +62,8 @@ __global__ __launch_bounds__(256) void k_prod_few(ProdArgs p) {
     __shared__ f32x4 s_acc[4][TG][64];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int n0 = (int)blockIdx.x * KS;
-    const int64_t row = (int64_t)blockIdx.y * 16 + r;
+    const int64_t row = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * 16 + r;
+    if (row - r >= p.rows) return;
     const T* a = static_cast<const T*>(p.a) + (row < p.rows ? row : p.rows - 1) * p.ld_a;
     const T* b[TG];
 #pragma unroll
@@ -138,14 +139,15 @@ __global__ __launch_bounds__(kNarrowThreads) void k_prod_narrow(ProdArgs p) {
     const int64_t tiles = (p.rows + 15) / 16, step = (int64_t)gridDim.x * waves;
     int64_t tile = (int64_t)blockIdx.x * waves + wave;
     auto row_of = [&](int64_t t) { return min(t * 16 + r, p.rows - 1); };
-    Frag x[SL];
-    auto fetch = [&](int64_t t) {
-        const T* a = static_cast<const T*>(p.a) + row_of(t) * p.ld_a;
+    const Matrix<T> ma(p.a, p.rows, p.ld_a, p.depth), mo(p.other, p.rows, p.ld_other, p.cols);
+    const bool even_a = p.depth == SL * KS, even_o = p.cols == groups * KS && groups % P == 0;
+    Frag x[SL], next[kAhead ? SL : 1];
+    auto fetch = [&](int64_t t, Frag* to) {
+        const int64_t row = row_of(t);
 #pragma unroll
-        for (int s = 0; s < SL - 1; ++s) x[s] = load16(a + s * KS + E * g);
-        x[SL - 1] = load_frag(a, (SL - 1) * KS + E * g, p.depth);
+        for (int s = 0; s < SL; ++s) to[s] = ma.raw(row, s * KS + E * g);
     };
-    if (kAhead && tile < tiles) fetch(tile);
+    if (kAhead) fetch(tile, next);
     for (int i0 = threadIdx.x; i0 < groups * TG * SL * 64; i0 += 4 * blockDim.x) {
         Frag v[4];
 #pragma unroll
@@ -165,14 +167,21 @@ __global__ __launch_bounds__(kNarrowThreads) void k_prod_narrow(ProdArgs p) {
     __syncthreads();
     for (; tile < tiles; tile += step) {
         const int64_t row = tile * 16 + r;
-        if (!kAhead) fetch(tile);
-        const T* o = static_cast<const T*>(p.other) + row_of(tile) * p.ld_other;
+        if (!kAhead) fetch(tile, x);
+#pragma unroll
+        for (int s = 0; s < SL; ++s)
+            if (kAhead) x[s] = next[s];
+        if (!even_a) {
+#pragma unroll
+            for (int s = 0; s < SL; ++s) x[s] = ma.fixed(x[s], row_of(tile), s * KS + E * g, true);
+        }
+        if (kAhead) fetch(tile + step, next);  // past the end: the last row again
         T* out = PACK ? s_out + r * p.cols : static_cast<T*>(p.out) + row * p.ld_out;
         for (int n = 0; n < groups; n += P) {
             Frag other[P];
             if (p.other) {
 #pragma unroll
-                for (int h = 0; h < P; ++h) other[h] = load_frag(o, (n + h) * KS + E * g, p.cols);
+                for (int h = 0; h < P; ++h) other[h] = mo.raw(row_of(tile), (n + h) * KS + E * g);
             }
             f32x4 acc[P][TG];
 #pragma unroll
@@ -185,7 +194,11 @@ __global__ __launch_bounds__(kNarrowThreads) void k_prod_narrow(ProdArgs p) {
 #pragma unroll
                     for (int t = 0; t < TG; ++t) mma(acc[h][t], s_w[(((n + h) * TG + t) * SL + s) * 64 + lane], x[s]);
             }
-            if (kAhead && n + P >= groups && tile + step < tiles) fetch(tile + step);
+            if (p.other && !even_o) {
+#pragma unroll
+                for (int h = 0; h < P; ++h)
+                    other[h] = mo.fixed(other[h], row_of(tile), (n + h) * KS + E * g, true);
+            }
             Frag f[P];
 #pragma unroll
             for (int h = 0; h < P; ++h) {
@@ -214,10 +227,11 @@ __global__ __launch_bounds__(kNarrowThreads) void k_prod_narrow(ProdArgs p) {
 // Deep or wide layers: 128 x 128 outputs per block, 64 x 64 per wave.  Both
 // operands pass through LDS in rows of 128 bytes (2 steps), their 16-byte chunks
 // rotated by the row so that the fragments' reads meet no bank twice; the next
-// 128 bytes of every row are on their way while these are multiplied.
+// two stages are on their way in registers while one is multiplied: with one, a
+// stage (0.4 us) is shorter than the memory's answer.
 constexpr int kBig = 128;  // rows and outputs of a block
 template <typename T>
-__global__ __launch_bounds__(256) void k_prod_big(ProdArgs p) {
+__global__ __launch_bounds__(256, 2) void k_prod_big(ProdArgs p) {
     constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG;
     typedef typename Tile<T>::Frag Frag;
     __shared__ Frag s_a[2][kBig * 8], s_b[2][kBig * 8];
@@ -233,66 +247,70 @@ __global__ __launch_bounds__(256) void k_prod_big(ProdArgs p) {
     // staging: thread i brings chunk i % 8 of rows i / 8, + 32, + 64, + 96; the weights' rows in the order
     // that interleaves a group's tiles
     const int ch = threadIdx.x & 7, sr = threadIdx.x >> 3;
-    const T *ga[4], *gb[4];
-    Frag ra[4], rb[4];
+    const Matrix<T> ma(p.a, p.rows, p.ld_a, p.depth), mb(p.b, p.cols, p.ld_b, p.depth);
+    int64_t row_a[4];
+    int row_b[4];
+    Frag ra[2][4], rb[2][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int pos = sr + 32 * i;
-        const int64_t m = m0 + pos;
-        const int n = n0 + pos / KS * KS + out_row<T>(pos % KS / 16, pos % 16);
-        ga[i] = static_cast<const T*>(p.a) + (m < p.rows ? m : p.rows - 1) * p.ld_a;
-        gb[i] = static_cast<const T*>(p.b) + (int64_t)(n < p.cols ? n : p.cols - 1) * p.ld_b;
+        const int pos = sr + 32 * i, n = n0 + pos / KS * KS + out_row<T>(pos % KS / 16, pos % 16);
+        row_a[i] = min(m0 + pos, p.rows - 1);
+        row_b[i] = n < p.cols ? n : p.cols - 1;
     }
     const int steps = (p.depth + 2 * KS - 1) / (2 * KS);
-    auto fetch = [&](int s) {
-        const int k0 = s * 2 * KS + E * ch;
-        if ((s + 1) * 2 * KS <= p.depth) {
+    auto fetch = [&](int s, Frag (&a)[4], Frag (&b)[4]) {  // past the end: the matrices' last bytes, not used
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                ra[i] = load16(ga[i] + k0);
-                rb[i] = load16(gb[i] + k0);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                ra[i] = load_frag(ga[i], k0, p.depth);
-                rb[i] = load_frag(gb[i], k0, p.depth);
-            }
+        for (int i = 0; i < 4; ++i) {
+            a[i] = ma.raw(row_a[i], s * 2 * KS + E * ch);
+            b[i] = mb.raw(row_b[i], s * 2 * KS + E * ch);
         }
     };
-    auto put = [&](int buf) {
+    auto put = [&](int s, int buf, Frag (&a)[4], Frag (&b)[4]) {
+        if ((s + 1) * 2 * KS > p.depth) {
+            const int k0 = s * 2 * KS + E * ch;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[i] = ma.fixed(a[i], row_a[i], k0, true);
+                b[i] = mb.fixed(b[i], row_b[i], k0, true);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int pos = sr + 32 * i, at = pos * 8 + (ch ^ (pos & 7));
-            s_a[buf][at] = ra[i];
-            s_b[buf][at] = rb[i];
+            s_a[buf][at] = a[i];
+            s_b[buf][at] = b[i];
         }
     };
     f32x4 acc[4][4] = {};  // [m tile][n tile]
     if (steps > 0) {
-        fetch(0);
-        put(0);
+        fetch(0, ra[0], rb[0]);
+        fetch(1, ra[1], rb[1]);
+        put(0, 0, ra[0], rb[0]);
     }
     __syncthreads();
-    for (int s = 0; s < steps; ++s) {
-        if (s + 1 < steps) fetch(s + 1);
-        const int buf = s & 1;
+    for (int s0 = 0; s0 < steps; s0 += 2) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            Frag fa[4], fb[4];
+        for (int u = 0; u < 2; ++u) {  // stage s0 + u lies in buffer u, the next one in registers
+            const int s = s0 + u;
+            if (s >= steps) break;
+            fetch(s + 2, ra[u], rb[u]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int am = wm + 16 * i + r, bn = wn + 16 * i + r;
-                fa[i] = s_a[buf][am * 8 + ((4 * h + g) ^ (am & 7))];
-                fb[i] = s_b[buf][bn * 8 + ((4 * h + g) ^ (bn & 7))];
+            for (int h = 0; h < 2; ++h) {
+                Frag fa[4], fb[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int am = wm + 16 * i + r, bn = wn + 16 * i + r;
+                    fa[i] = s_a[u][am * 8 + ((4 * h + g) ^ (am & 7))];
+                    fb[i] = s_b[u][bn * 8 + ((4 * h + g) ^ (bn & 7))];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma(acc[i][j], fb[j], fa[i]);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) mma(acc[i][j], fb[j], fa[i]);
+            if (s + 1 < steps) put(s + 1, u ^ 1, ra[u ^ 1], rb[u ^ 1]);
+            __syncthreads();
         }
-        if (s + 1 < steps) put(buf ^ 1);
-        __syncthreads();
     }
 #pragma unroll
     for (int q = 0; q < 4 / TG; ++q) {  // groups of KS outputs
@@ -340,14 +358,18 @@ void product(const ProdArgs& p, hipStream_t s) {
     constexpr int KS = Tile<T>::KS;
     const int groups = (int)cdiv(p.cols, KS), steps = (int)cdiv(p.depth, KS);
     const int64_t tiles16 = cdiv(p.rows, 16);
-    if (tiles16 * groups <= 2048 && tiles16 <= 65535) {
-        hipLaunchKernelGGL((k_prod_few<T>), dim3(groups, (unsigned)tiles16), dim3(256), 0, s, p);
+    // the streaming kernels read 16 bytes at a time: x and the residual have to span them
+    const auto spans = [](int64_t rows, int64_t ld, int32_t count) { return (rows - 1) * ld + count >= Tile<T>::E; };
+    if (tiles16 * groups <= 2048 || p.depth == 0 || !spans(p.rows, p.ld_a, p.depth) ||
+        (p.other && !spans(p.rows, p.ld_other, p.cols))) {
+        const int64_t y = tiles16 < 32768 ? tiles16 : 32768;
+        hipLaunchKernelGGL((k_prod_few<T>), dim3(groups, (unsigned)y, (unsigned)cdiv(tiles16, y)), dim3(256), 0, s, p);
         return;
     }
     const size_t lds = (size_t)groups * KS * (steps * KS * sizeof(T) + 4);
     if (lds <= 160 * 1024) {
         switch (steps) {
-            case 0: case 1: launch_narrow<T, 1>(p, (size_t)groups * KS * (KS * sizeof(T) + 4), s); return;
+            case 1: launch_narrow<T, 1>(p, lds, s); return;
             case 2: launch_narrow<T, 2>(p, lds, s); return;
             case 3: launch_narrow<T, 3>(p, lds, s); return;
             case 4: launch_narrow<T, 4>(p, lds, s); return;
@@ -367,7 +389,7 @@ struct DwArgs {
     float* part;  // [splits][n_out * n_in of dw, then n_out of db], each if wanted
     int64_t rows, ld_dz, ld_x, per;
     int32_t n_out, n_in;
-    int32_t want_dw, want_db;
+    int32_t want_dw, want_db, splits;
 };
 
 // One split of the rows for a 128 x 128 tile of dw: 64 x 64 per wave, the next
@@ -380,29 +402,39 @@ __global__ __launch_bounds__(256) void k_dw(DwArgs p) {
     __shared__ __align__(16) char s_dz[2][16384], s_x[2][16384];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wn = (wave & 1) * 64, wk = (wave >> 1) * 64;
-    const int n0 = blockIdx.x * 128, k0 = blockIdx.y * 128;
-    const int64_t m_begin = (int64_t)blockIdx.z * p.per, m_end = min(p.rows, m_begin + p.per);
+    // the tiles of one split run on one XCD, whose L2 then serves the rows that they share
+    const int tn = (p.n_out + 127) / 128, tiles = tn * (p.n_in > 128 ? (p.n_in + 127) / 128 : 1);
+    const int64_t id = (int64_t)(blockIdx.x & 7) * ((gridDim.x + 7) / 8) + (blockIdx.x >> 3);
+    const int64_t split = id / tiles;
+    if (split >= p.splits) return;
+    const int n0 = (int)(id % tiles) % tn * 128, k0 = (int)(id % tiles) / tn * 128;
+    const int64_t m_begin = split * p.per, m_end = min(p.rows, m_begin + p.per);
     constexpr int kRows = 16384 / (128 * (int)sizeof(T));  // of a stage: 64 or 32
     constexpr int kChunks = 128 / E;                       // 16-byte chunks of a row
     constexpr int kPass = 256 / kChunks;  // rows that the block's threads cover at a time
     const int ch = threadIdx.x % kChunks, mr = threadIdx.x / kChunks;
-    const T* dz = static_cast<const T*>(p.dz);
-    const T* x = static_cast<const T*>(p.x);
+    const Matrix<T> mz(p.dz, p.rows, p.ld_dz, p.n_out), mx(p.x, p.rows, p.ld_x, p.n_in);
+    const bool even = n0 + 128 <= p.n_out && k0 + 128 <= p.n_in;
     Frag rz[4], rx[4];
     auto fetch = [&](int64_t m0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t m = m0 + mr + i * kPass;
-            rz[i] = rx[i] = zero_frag<T>();
-            if (m < m_end) {
-                rz[i] = load_frag(dz + m * p.ld_dz, n0 + ch * E, p.n_out);
-                rx[i] = load_frag(x + m * p.ld_x, k0 + ch * E, p.n_in);
-            }
+            const int64_t m = min(m0 + mr + i * kPass, p.rows - 1);
+            rz[i] = mz.raw(m, n0 + ch * E);
+            if (p.n_in > 0) rx[i] = mx.raw(m, k0 + ch * E);
         }
     };
     float sum[E] = {};
-    const bool sums = p.want_db && blockIdx.y == 0;
-    auto put = [&](int buf) {
+    const bool sums = p.want_db && k0 == 0;
+    auto put = [&](int64_t m0, int buf) {
+        if (!even || m0 + kRows > m_end) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t m = m0 + mr + i * kPass, mc = min(m, p.rows - 1);
+                rz[i] = mz.fixed(rz[i], mc, n0 + ch * E, m < m_end);
+                rx[i] = mx.fixed(rx[i], mc, k0 + ch * E, m < m_end);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int at = row_chunk<T, 128>(mr + i * kPass, ch);
@@ -416,13 +448,13 @@ __global__ __launch_bounds__(256) void k_dw(DwArgs p) {
     f32x4 acc[4][4] = {};  // [n tile][k tile]
     if (m_begin < m_end) {
         fetch(m_begin);
-        put(0);
+        put(m_begin, 0);
     }
     __syncthreads();
     int buf = 0;
     for (int64_t m0 = m_begin; m0 < m_end; m0 += kRows, buf ^= 1) {
         const bool more = m0 + kRows < m_end;
-        if (more) fetch(m0 + kRows);
+        fetch(m0 + kRows);  // past the end: the last row, not used
 #pragma unroll
         for (int h = 0; h < kRows / KS; ++h) {
             Frag fz[4], fx[4];
@@ -436,11 +468,11 @@ __global__ __launch_bounds__(256) void k_dw(DwArgs p) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) mma(acc[i][j], fz[i], fx[j]);
         }
-        if (more) put(buf ^ 1);
+        if (more) put(m0 + kRows, buf ^ 1);
         __syncthreads();
     }
     const int64_t n_w = p.want_dw ? (int64_t)p.n_out * p.n_in : 0;
-    float* part = p.part + blockIdx.z * (n_w + (p.want_db ? p.n_out : 0));
+    float* part = p.part + split * (n_w + (p.want_db ? p.n_out : 0));
     if (p.want_dw) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -508,11 +540,12 @@ __global__ __launch_bounds__(256) void k_bwd_few(FewArgs p) {
     const int n0 = (int)blockIdx.x * KS, c0 = n0 + E * g;
     const T* x = static_cast<const T*>(p.x);
     const T* w = static_cast<const T*>(p.w);
-    const int k = (int)blockIdx.y * 256 + threadIdx.x, kc = k < p.n_in ? k : p.n_in - 1;
+    const int k = (int)blockIdx.y * 256 + threadIdx.x, kc = k < p.n_in ? k : p.n_in - 1;  // -1: no inputs
     // what the second half needs is on its way during the first
-    float xk[M];
+    float xk[M] = {};
 #pragma unroll
-    for (int m = 0; m < M; ++m) xk[m] = (float)x[(int64_t)(m < p.rows ? m : p.rows - 1) * p.ld_x + kc];
+    for (int m = 0; m < M; ++m)
+        if (kc >= 0) xk[m] = (float)x[(int64_t)(m < p.rows ? m : p.rows - 1) * p.ld_x + kc];
     f32x4 acc[TG] = {};
     if (p.act != GS_ACT_NONE) {
         const T* a = x + (int64_t)(r < p.rows ? r : p.rows - 1) * p.ld_x;
@@ -586,7 +619,7 @@ __global__ __launch_bounds__(256) void k_bwd_few(FewArgs p) {
 
 template <typename T>
 void launch_few(const FewArgs& p, hipStream_t s) {
-    const dim3 grid((unsigned)cdiv(p.n_out, Tile<T>::KS), (unsigned)cdiv(p.n_in, 256));
+    const dim3 grid((unsigned)cdiv(p.n_out, Tile<T>::KS), (unsigned)(p.n_in > 0 ? cdiv(p.n_in, 256) : 1));
     if (p.rows <= 1)
         hipLaunchKernelGGL((k_bwd_few<T, 1>), grid, dim3(256), 0, s, p);
     else if (p.rows <= 4)
@@ -658,7 +691,7 @@ struct BwdPlan {
 
 template <typename T>
 inline bool plan_narrow(const gs_linear* d, BwdPlan& p) {
-    if (d->rows < 1 || !bwd_narrow_fits<T>(d->n_in, d->n_out)) return false;
+    if (d->rows <= kFewRows || !bwd_narrow_fits<T>(d->n_in, d->n_out)) return false;
     p.splits = bwd_narrow_blocks<T>(d->rows, d->n_in, d->n_out);
     return true;
 }
@@ -666,7 +699,7 @@ inline bool plan_narrow(const gs_linear* d, BwdPlan& p) {
 inline BwdPlan bwd_plan(const gs_linear* d) {
     BwdPlan p{};
     size_t at = 0;
-    p.few = d->rows >= 1 && d->rows <= kFewRows && d->n_in > 0 && d->n_out > 0;
+    p.few = d->rows >= 1 && d->rows <= kFewRows && d->n_out > 0;
     if (p.few) {  // a block per group of outputs leaves a partial dx
         p.splits = (int)cdiv(d->n_out, d->dtype == GS_F32 ? Tile<float>::KS : Tile<_Float16>::KS);
         p.bytes = pad256((size_t)p.splits * d->rows * d->n_in * 4);
@@ -710,10 +743,10 @@ void bwd(const gs_linear* d, const void* x, const void* w, const void* bias, con
     const BwdPlan plan = bwd_plan(d);
     float* part = reinterpret_cast<float*>(ws + plan.part);
     if (plan.few) {
-        FewArgs q{x, w, bias, dy, dw, db, dx ? part : nullptr, d->ld_x, d->ld_y, (int32_t)d->rows, d->n_in, d->n_out,
+        FewArgs q{x, w, bias, dy, dw, db, dx && d->n_in > 0 ? part : nullptr, d->ld_x, d->ld_y, (int32_t)d->rows, d->n_in, d->n_out,
                   d->act};
         launch_few<T>(q, s);
-        if (dx) {
+        if (q.dx_part) {
             const int64_t count = d->rows * d->n_in;
             join<T>(JoinArgs{part, dx, nullptr, count, count, d->ld_dx, d->n_in, plan.splits, 0}, s);
         }
@@ -749,11 +782,10 @@ void bwd(const gs_linear* d, const void* x, const void* w, const void* bias, con
         product<T>(p, s);
     }
     if (!want_dw && !want_db) return;
-    DwArgs q{dz, x, part, d->rows, ld_dz, d->ld_x, plan.per, d->n_out, want_dw ? d->n_in : 0, want_dw, want_db};
-    hipLaunchKernelGGL((k_dw<T>),
-                       dim3((unsigned)cdiv(q.n_out, 128), (unsigned)cdiv(q.n_in > 0 ? q.n_in : 1, 128),
-                            (unsigned)plan.splits),
-                       dim3(256), 0, s, q);
+    DwArgs q{dz, x, part, d->rows, ld_dz, d->ld_x, plan.per, d->n_out, want_dw ? d->n_in : 0, want_dw, want_db,
+             plan.splits};
+    const int64_t blocks = cdiv(q.n_out, 128) * cdiv(q.n_in > 0 ? q.n_in : 1, 128) * plan.splits;
+    hipLaunchKernelGGL((k_dw<T>), dim3((unsigned)(cdiv(blocks, 8) * 8)), dim3(256), 0, s, q);
     join<T>(sums, s);
 }
 

@@ -96,29 +96,27 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64)) void k_bwd_narro
     const int64_t tiles = (p.rows + G::kRows - 1) / G::kRows;
     f32x4 dw[G::TN][G::TK] = {};
     float db[NG][E] = {};
+    const Matrix<T> mx(p.x, p.rows, p.ld_x, p.n_in), my(p.dy, p.rows, p.ld_dy, p.n_out);
+    const bool even = p.n_in == G::KP && p.n_out == G::NP;
     Frag x[SL], dy[NG];
-    auto fetch = [&](int64_t tile) {
-        const int64_t row = tile * G::kRows + wave * 16 + r;
-        if (row < p.rows) {
-            const T* xr = static_cast<const T*>(p.x) + row * p.ld_x;
-            const T* yr = static_cast<const T*>(p.dy) + row * p.ld_dy;
+    auto fetch = [&](int64_t tile) {  // past the end: the last row again
+        const int64_t row = min(tile * G::kRows + wave * 16 + r, p.rows - 1);
 #pragma unroll
-            for (int s = 0; s < SL - 1; ++s) x[s] = load16(xr + s * KS + E * g);
-            x[SL - 1] = load_frag(xr, (SL - 1) * KS + E * g, p.n_in);
+        for (int s = 0; s < SL; ++s) x[s] = mx.raw(row, s * KS + E * g);
 #pragma unroll
-            for (int n = 0; n < NG - 1; ++n) dy[n] = load16(yr + n * KS + E * g);
-            dy[NG - 1] = load_frag(yr, (NG - 1) * KS + E * g, p.n_out);
-        } else {  // rows past the end add nothing: dz = 0, x = 0
-#pragma unroll
-            for (int s = 0; s < SL; ++s) x[s] = zero_frag<T>();
-#pragma unroll
-            for (int n = 0; n < NG; ++n) dy[n] = zero_frag<T>();
-        }
+        for (int n = 0; n < NG; ++n) dy[n] = my.raw(row, n * KS + E * g);
     };
-    if (blockIdx.x < tiles) fetch(blockIdx.x);
+    fetch(blockIdx.x);
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const int64_t row = tile * G::kRows + wave * 16 + r;
         const int m = wave * 16 + r;
+        if (!even || (tile + 1) * G::kRows > p.rows) {  // rows past the end add nothing: dz = 0, x = 0
+            const int64_t rc = min(row, p.rows - 1);
+#pragma unroll
+            for (int s = 0; s < SL; ++s) x[s] = mx.fixed(x[s], rc, s * KS + E * g, row < p.rows);
+#pragma unroll
+            for (int n = 0; n < NG; ++n) dy[n] = my.fixed(dy[n], rc, n * KS + E * g, row < p.rows);
+        }
         Frag dz[NG];
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
@@ -153,7 +151,7 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64)) void k_bwd_narro
         }
 #pragma unroll
         for (int s = 0; s < SL; ++s) *reinterpret_cast<Frag*>(s_x + row_chunk<T, G::KP>(m, s * 4 + g)) = x[s];
-        if (tile + gridDim.x < tiles) fetch(tile + gridDim.x);
+        fetch(tile + gridDim.x);
         if (p.dx) {
             T* out = static_cast<T*>(p.dx) + row * p.ld_dx;
 #pragma unroll

@@ -106,6 +106,52 @@ __device__ __forceinline__ typename Tile<T>::Frag load_frag(const T* row, int k0
     return load_edge(row, k0, count);
 }
 
+// The same in two steps, for loads that stay in flight while other work is done: a
+// branch between the load and its use would make the compiler wait for the data at
+// the branch's end.  raw() loads 16 bytes from where the fragment starts, or from
+// the matrix's last 16 bytes if that is later (the bytes may belong to the next
+// rows: nothing outside the matrix is read); fixed() then drops what is not the
+// row's.  The matrix spans at least 16 bytes.
+template <typename T>
+struct Matrix {
+    typedef typename Tile<T>::Frag Frag;
+    const T* base;
+    const T* last;  // start of the last 16 bytes
+    int64_t ld;
+    int count;      // elements of a row
+
+    __device__ __forceinline__ Matrix(const void* p, int64_t rows, int64_t ld_, int count_)
+        : base(static_cast<const T*>(p)), last(base + (rows - 1) * ld_ + count_ - Tile<T>::E), ld(ld_), count(count_) {}
+    __device__ __forceinline__ const T* at(int64_t row, int k0) const { return base + row * ld + k0; }
+    __device__ __forceinline__ Frag raw(int64_t row, int k0) const {
+        const T* p = at(row, k0);
+        return load16(p < last ? p : last);
+    }
+    // in: whether the row counts at all (else zeros)
+    __device__ __forceinline__ Frag fixed(Frag f, int64_t row, int k0, bool in) const {
+        constexpr int E = Tile<T>::E, kBits = 8 * (int)sizeof(T);
+        const T* p = at(row, k0);
+        const int64_t over = p - last;
+        const int bits = over > 0 ? (over < E ? (int)over * kBits : 128) : 0;
+        const int keep = !in || k0 >= count ? 0 : (count - k0 < E ? (count - k0) * kBits : 128);
+        union {
+            Frag f;
+            uint64_t q[2];
+        } u;
+        u.f = f;
+        if (bits >= 64) {
+            u.q[0] = bits >= 128 ? 0 : u.q[1] >> (bits - 64);
+            u.q[1] = 0;
+        } else if (bits > 0) {
+            u.q[0] = (u.q[0] >> bits) | (u.q[1] << (64 - bits));
+            u.q[1] >>= bits;
+        }
+        u.q[0] &= keep >= 64 ? ~0ull : (1ull << (keep & 63)) - 1;
+        u.q[1] &= keep >= 128 ? ~0ull : keep > 64 ? (1ull << (keep & 63)) - 1 : 0;
+        return u.f;
+    }
+};
+
 // Stores the run's elements that lie inside a row of `count`.
 template <typename T>
 __device__ __forceinline__ void store_run(T* row, int n0, int count, typename Tile<T>::Frag f) {

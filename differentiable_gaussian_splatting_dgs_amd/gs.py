@@ -865,9 +865,8 @@ def gs_linear_bwd_workspace_size(x, w, act="none"):
     return b.value
 
 
-def gs_linear_bwd(x, w, bias, dy, dx, dw, db, workspace, act="none"):
-    """The layer's gradients from dy [rows, n_out] into dx, dw and db (each may be None: not computed);
-    workspace: uint8, gs_linear_bwd_workspace_size bytes, 256-byte aligned."""
+def linear_bwd_into(x, w, bias, dy, dx, dw, db, workspace, act):
+    """gs_linear_bwd; workspace None: one of the size the call needs."""
     rows, n_in, n_out, code, a, device, ld_x = _linear_shape(x, w, act)
     dtype = x.dtype
     ld_y = _rows(dy, (rows, n_out), dtype, device, "dy")
@@ -875,14 +874,26 @@ def gs_linear_bwd(x, w, bias, dy, dx, dw, db, workspace, act="none"):
     if dx is not None:
         ld_dx = _rows(dx, (rows, n_in), dtype, device, "dx")
         pdx = dx.data_ptr()
-    rc = (_lib or load_library()).gs_linear_bwd(
-        _pack_linear(rows, n_in, n_out, code, a, ld_x, ld_y, 0, ld_dx), x.data_ptr(),
-        _whole(w, w.shape, dtype, device, "w"), _whole(bias, (n_out,), dtype, device, "bias"), dy.data_ptr(), pdx,
-        _whole(dw, w.shape, dtype, device, "dw"), _whole(db, (n_out,), dtype, device, "db"),
+    lib = _lib or load_library()
+    d = _pack_linear(rows, n_in, n_out, code, a, ld_x, ld_y, 0, ld_dx)
+    if workspace is None:
+        b = C.c_size_t()
+        _check(lib.gs_linear_bwd_workspace_size(d, C.byref(b)), "gs_linear_bwd_workspace_size")
+        # torch's device allocations start at multiples of 512 bytes
+        workspace = torch.empty(b.value, dtype=torch.uint8, device=x.device)
+    rc = lib.gs_linear_bwd(
+        d, x.data_ptr(), _whole(w, w.shape, dtype, device, "w"), _whole(bias, (n_out,), dtype, device, "bias"),
+        dy.data_ptr(), pdx, _whole(dw, w.shape, dtype, device, "dw"), _whole(db, (n_out,), dtype, device, "db"),
         _whole(workspace, workspace.shape, torch.uint8, device, "workspace"), workspace.numel(),
         _raw_stream(_current_device()))
     if rc:
         _check(rc, "gs_linear_bwd")
+
+
+def gs_linear_bwd(x, w, bias, dy, dx, dw, db, workspace, act="none"):
+    """The layer's gradients from dy [rows, n_out] into dx, dw and db (each may be None: not computed);
+    workspace: uint8, gs_linear_bwd_workspace_size bytes, 256-byte aligned."""
+    linear_bwd_into(x, w, bias, dy, dx, dw, db, workspace, act)
 
 
 def gs_grad_workspace_size(n_tensors):

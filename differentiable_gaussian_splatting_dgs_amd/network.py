@@ -29,10 +29,9 @@ def linear_backward(dy, x, w, bias=None, act="none", need=(True, True, True)):
     The gradient of a residual added to y is dy itself."""
     need_dx, need_dw, need_db = need
     dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
-    dw = torch.empty(w.shape, dtype=w.dtype, device=x.device) if need_dw else None
-    db = torch.empty(w.shape[:1], dtype=w.dtype, device=x.device) if need_db and bias is not None else None
-    ws = _workspace(gs.gs_linear_bwd_workspace_size(x, w, act), x.device)
-    gs.gs_linear_bwd(x, w, bias, dy, dx, dw, db, ws, act)
+    dw = torch.empty_like(w, memory_format=torch.contiguous_format) if need_dw else None
+    db = torch.empty_like(bias, memory_format=torch.contiguous_format) if need_db and bias is not None else None
+    gs.linear_bwd_into(x, w, bias, dy, dx, dw, db, None, act)
     return dx, dw, db
 
 
