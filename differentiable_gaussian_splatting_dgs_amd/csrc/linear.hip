@@ -312,26 +312,39 @@ __global__ __launch_bounds__(256, 2) void k_prod_big(ProdArgs p) {
             __syncthreads();
         }
     }
+    const Matrix<T> mo(p.other, p.rows, p.ld_other, p.cols);
+    const bool even = n0 + kBig <= p.cols;
+    Frag others[4 / TG][4];
+    if (p.other) {
+#pragma unroll
+        for (int q = 0; q < 4 / TG; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                others[q][i] = mo.raw(min(m0 + wm + 16 * i + r, p.rows - 1), n0 + wn + q * KS + E * g);
+    }
 #pragma unroll
     for (int q = 0; q < 4 / TG; ++q) {  // groups of KS outputs
         const int c0 = n0 + wn + q * KS + E * g;
-        if (c0 >= p.cols) continue;
+        Frag(&other)[4] = others[q];
         float bias[E] = {};
         if (p.bias) {
             const auto f = load_frag(static_cast<const T*>(p.bias), c0, p.cols);
 #pragma unroll
             for (int j = 0; j < E; ++j) bias[j] = (float)f[j];
         }
+        if (p.other && !even) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                other[i] = mo.fixed(other[i], min(m0 + wm + 16 * i + r, p.rows - 1), c0, true);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t row = m0 + wm + 16 * i + r;
-            if (row >= p.rows) continue;
-            auto other = zero_frag<T>();
-            if (p.other) other = load_frag(static_cast<const T*>(p.other) + row * p.ld_other, c0, p.cols);
             float v[E];
 #pragma unroll
             for (int j = 0; j < E; ++j) v[j] = acc[i][q * TG + j / 4][j % 4] + bias[j];
-            store_run(static_cast<T*>(p.out) + row * p.ld_out, c0, p.cols, finish_run<T>(p, v, other));
+            const auto f = finish_run<T>(p, v, other[i]);
+            if (row < p.rows) store_run(static_cast<T*>(p.out) + row * p.ld_out, c0, p.cols, f);
         }
     }
 }
@@ -396,14 +409,14 @@ struct DwArgs {
 // stage's rows on their way while this one's are multiplied.  The blocks of the
 // first column of tiles add up dz's columns as they pass.
 template <typename T>
-__global__ __launch_bounds__(256) void k_dw(DwArgs p) {
+__global__ __launch_bounds__(256, 2) void k_dw(DwArgs p) {
     constexpr int E = Tile<T>::E, KS = Tile<T>::KS;
     typedef typename Tile<T>::Frag Frag;
     __shared__ __align__(16) char s_dz[2][16384], s_x[2][16384];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wn = (wave & 1) * 64, wk = (wave >> 1) * 64;
     // the tiles of one split run on one XCD, whose L2 then serves the rows that they share
-    const int tn = (p.n_out + 127) / 128, tiles = tn * (p.n_in > 128 ? (p.n_in + 127) / 128 : 1);
+    const int tn = (p.n_out + 127) / 128, tiles = tn * ((p.n_in + 127) / 128);
     const int64_t id = (int64_t)(blockIdx.x & 7) * ((gridDim.x + 7) / 8) + (blockIdx.x >> 3);
     const int64_t split = id / tiles;
     if (split >= p.splits) return;
@@ -415,61 +428,65 @@ __global__ __launch_bounds__(256) void k_dw(DwArgs p) {
     const int ch = threadIdx.x % kChunks, mr = threadIdx.x / kChunks;
     const Matrix<T> mz(p.dz, p.rows, p.ld_dz, p.n_out), mx(p.x, p.rows, p.ld_x, p.n_in);
     const bool even = n0 + 128 <= p.n_out && k0 + 128 <= p.n_in;
-    Frag rz[4], rx[4];
-    auto fetch = [&](int64_t m0) {
+    Frag rz[2][4], rx[2][4];
+    auto fetch = [&](int64_t m0, Frag (&z)[4], Frag (&x)[4]) {  // past the end: the last row, not used
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t m = min(m0 + mr + i * kPass, p.rows - 1);
-            rz[i] = mz.raw(m, n0 + ch * E);
-            if (p.n_in > 0) rx[i] = mx.raw(m, k0 + ch * E);
+            z[i] = mz.raw(m, n0 + ch * E);
+            x[i] = mx.raw(m, k0 + ch * E);
         }
     };
     float sum[E] = {};
     const bool sums = p.want_db && k0 == 0;
-    auto put = [&](int64_t m0, int buf) {
+    auto put = [&](int64_t m0, int buf, Frag (&z)[4], Frag (&x)[4]) {
         if (!even || m0 + kRows > m_end) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int64_t m = m0 + mr + i * kPass, mc = min(m, p.rows - 1);
-                rz[i] = mz.fixed(rz[i], mc, n0 + ch * E, m < m_end);
-                rx[i] = mx.fixed(rx[i], mc, k0 + ch * E, m < m_end);
+                z[i] = mz.fixed(z[i], mc, n0 + ch * E, m < m_end);
+                x[i] = mx.fixed(x[i], mc, k0 + ch * E, m < m_end);
             }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int at = row_chunk<T, 128>(mr + i * kPass, ch);
-            *reinterpret_cast<Frag*>(s_dz[buf] + at) = rz[i];
-            *reinterpret_cast<Frag*>(s_x[buf] + at) = rx[i];
+            *reinterpret_cast<Frag*>(s_dz[buf] + at) = z[i];
+            *reinterpret_cast<Frag*>(s_x[buf] + at) = x[i];
             if (sums)
 #pragma unroll
-                for (int j = 0; j < E; ++j) sum[j] += (float)rz[i][j];
+                for (int j = 0; j < E; ++j) sum[j] += (float)z[i][j];
         }
     };
     f32x4 acc[4][4] = {};  // [n tile][k tile]
     if (m_begin < m_end) {
-        fetch(m_begin);
-        put(m_begin, 0);
+        fetch(m_begin, rz[0], rx[0]);
+        fetch(m_begin + kRows, rz[1], rx[1]);
+        put(m_begin, 0, rz[0], rx[0]);
     }
     __syncthreads();
-    int buf = 0;
-    for (int64_t m0 = m_begin; m0 < m_end; m0 += kRows, buf ^= 1) {
-        const bool more = m0 + kRows < m_end;
-        fetch(m0 + kRows);  // past the end: the last row, not used
+    for (int64_t m2 = m_begin; m2 < m_end; m2 += 2 * kRows) {
 #pragma unroll
-        for (int h = 0; h < kRows / KS; ++h) {
-            Frag fz[4], fx[4];
+        for (int u = 0; u < 2; ++u) {  // this stage lies in buffer u, the next one in registers
+            const int64_t m0 = m2 + u * kRows;
+            if (m0 >= m_end) break;
+            fetch(m0 + 2 * kRows, rz[u], rx[u]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                fz[i] = column_frag<T, 128>(s_dz[buf], h * KS, wn + 16 * i, lane);
-                fx[i] = column_frag<T, 128>(s_x[buf], h * KS, wk + 16 * i, lane);
+            for (int h = 0; h < kRows / KS; ++h) {
+                Frag fz[4], fx[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    fz[i] = column_frag<T, 128>(s_dz[u], h * KS, wn + 16 * i, lane);
+                    fx[i] = column_frag<T, 128>(s_x[u], h * KS, wk + 16 * i, lane);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma(acc[i][j], fz[i], fx[j]);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) mma(acc[i][j], fz[i], fx[j]);
+            if (m0 + kRows < m_end) put(m0 + kRows, u ^ 1, rz[u ^ 1], rx[u ^ 1]);
+            __syncthreads();
         }
-        if (more) put(m0 + kRows, buf ^ 1);
-        __syncthreads();
     }
     const int64_t n_w = p.want_dw ? (int64_t)p.n_out * p.n_in : 0;
     float* part = p.part + split * (n_w + (p.want_db ? p.n_out : 0));
@@ -782,9 +799,11 @@ void bwd(const gs_linear* d, const void* x, const void* w, const void* bias, con
         product<T>(p, s);
     }
     if (!want_dw && !want_db) return;
-    DwArgs q{dz, x, part, d->rows, ld_dz, d->ld_x, plan.per, d->n_out, want_dw ? d->n_in : 0, want_dw, want_db,
+    // without dw there is one column of tiles, and its x side reads dz (the product is not stored)
+    DwArgs q{dz, want_dw ? x : dz, part, d->rows, ld_dz, want_dw ? d->ld_x : ld_dz, plan.per, d->n_out,
+             want_dw ? d->n_in : 1, want_dw, want_db,
              plan.splits};
-    const int64_t blocks = cdiv(q.n_out, 128) * cdiv(q.n_in > 0 ? q.n_in : 1, 128) * plan.splits;
+    const int64_t blocks = cdiv(q.n_out, 128) * cdiv(q.n_in, 128) * plan.splits;
     hipLaunchKernelGGL((k_dw<T>), dim3((unsigned)(cdiv(blocks, 8) * 8)), dim3(256), 0, s, q);
     join<T>(sums, s);
 }

@@ -35,7 +35,7 @@ struct BwdGeom {
     static constexpr int KS = Tile<T>::KS, TG = Tile<T>::TG;
     static constexpr int KP = SL * KS, NP = NG * KS;  // padded inputs and outputs
     static constexpr int kCopies = sizeof(T) == 4 ? 2 : 1;
-    static constexpr int kWaves = sizeof(T) == 4 || KP * NP <= 64 * 64 ? 4 : 8;
+    static constexpr int kWaves = 4;
     static constexpr int kRows = 16 * kWaves;
     static constexpr int kW = kCopies * KP * NP * (int)sizeof(T);
     static constexpr int kTiles = kRows * (KP + NP) * (int)sizeof(T);
@@ -60,7 +60,7 @@ struct BwdGeom {
 __device__ __forceinline__ int w_slot(int r, int g) { return ((r + 4 * g) & 15) + 16 * g; }
 
 template <typename T, int SL, int NG>
-__global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64)) void k_bwd_narrow(BwdArgs p) {
+__global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), 2) void k_bwd_narrow(BwdArgs p) {
     typedef BwdGeom<T, SL, NG> G;
     constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG;
     typedef typename Tile<T>::Frag Frag;
@@ -70,26 +70,6 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64)) void k_bwd_narro
     char* s_x = s_dz + G::kRows * G::NP * (int)sizeof(T);
     float* s_bias = reinterpret_cast<float*>(s_x + G::kRows * G::KP * (int)sizeof(T));
     const T* w = static_cast<const T*>(p.w);
-    for (int i = threadIdx.x; i < NG * TG * SL * 64; i += blockDim.x) {
-        const int r = i & 15, g = (i >> 4) & 3, f = i >> 6, s = f % SL, n = f / SL / TG * KS + out_row<T>(f / SL % TG, r);
-        s_w[f * 64 + w_slot(r, g)] =
-            n < p.n_out ? load_frag(w + (int64_t)n * p.n_in, s * KS + E * g, p.n_in) : zero_frag<T>();
-    }
-    if constexpr (sizeof(T) == 4) {
-        Frag* s_wt = s_w + NG * SL * 64;
-        for (int i = threadIdx.x; i < NG * SL * 64; i += blockDim.x) {
-            const int r = i & 15, g = (i >> 4) & 3, f = i >> 6, n = f % NG * KS + E * g, k = f / NG * KS + r;
-            Frag v = zero_frag<T>();
-#pragma unroll
-            for (int j = 0; j < E; ++j)
-                if (n + j < p.n_out && k < p.n_in) v[j] = w[(int64_t)(n + j) * p.n_in + k];
-            s_wt[i] = v;
-        }
-    }
-    for (int i = threadIdx.x; i < G::NP; i += blockDim.x)
-        s_bias[i] = p.bias && i < p.n_out ? (float)static_cast<const T*>(p.bias)[i] : 0.f;
-    __syncthreads();
-
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tn0 = wave / G::WK * G::TN, tk0 = wave % G::WK * G::TK;
@@ -107,6 +87,27 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64)) void k_bwd_narro
         for (int n = 0; n < NG; ++n) dy[n] = my.raw(row, n * KS + E * g);
     };
     fetch(blockIdx.x);
+#pragma unroll
+    for (int f = wave; f < NG * TG * SL; f += G::kWaves) {
+        const int s = f % SL, n = f / SL / TG * KS + out_row<T>(f / SL % TG, r);
+        s_w[f * 64 + w_slot(r, g)] =
+            n < p.n_out ? load_frag(w + (int64_t)n * p.n_in, s * KS + E * g, p.n_in) : zero_frag<T>();
+    }
+    for (int i = threadIdx.x; i < G::NP; i += blockDim.x)
+        s_bias[i] = p.bias && i < p.n_out ? (float)static_cast<const T*>(p.bias)[i] : 0.f;
+    __syncthreads();
+    if constexpr (sizeof(T) == 4) {  // w^T from the copy in LDS: input k of outputs n .. n + 3
+        const float* s_wf = reinterpret_cast<const float*>(s_w);
+#pragma unroll
+        for (int f = wave; f < SL * NG; f += G::kWaves) {
+            const int k = f / NG, n = f % NG;
+            Frag v;
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] = s_wf[((n * SL + k) * 64 + w_slot(4 * g + j, r >> 2)) * 4 + (r & 3)];
+            s_w[(NG * SL + f) * 64 + lane] = v;
+        }
+        __syncthreads();
+    }
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const int64_t row = tile * G::kRows + wave * 16 + r;
         const int m = wave * 16 + r;

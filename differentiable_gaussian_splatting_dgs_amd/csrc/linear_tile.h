@@ -183,7 +183,7 @@ __device__ __forceinline__ float logistic(float u) {
     return __builtin_amdgcn_rcpf(1.f + e);
 }
 
-__device__ __forceinline__ float bounded(float z) {  // beyond 64 every activation is z or 0; NaN stays
+__device__ __forceinline__ float bounded(float z) {  // gelu's cubic; beyond 64 it is z or 0; NaN stays
     return z > 64.f ? 64.f : (z < -64.f ? -64.f : z);
 }
 constexpr float kGelu = 1.5957691216057308f;  // 2 sqrt(2 / pi)
@@ -215,7 +215,7 @@ __device__ __forceinline__ void slope_run(int act, float (&v)[N], const float (&
     } else if (act == GS_ACT_SILU) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const float z = bounded(v[j]), s = logistic<T>(z);
+            const float z = v[j], s = logistic<T>(z);
             v[j] = g[j] * (s * fmaf(z, 1.f - s, 1.f));
         }
     } else if (act == GS_ACT_GELU) {
@@ -235,19 +235,30 @@ __device__ __forceinline__ void slope_run(int act, float (&v)[N], const float (&
 // tile lies in LDS in its own row order, COLS columns a row.  16-bit: two
 // transposing reads, each of which hands a group of 16 lanes the 4 x 16 block that
 // its lanes' 8-byte pieces of 4 rows make up (lane i: column i); float32: one
-// 4-byte read for each of the instruction's four 4-row slices.  The 32-byte (float32:
-// 64-byte) pieces of a row are rotated by the row where rows would otherwise
-// start in the same bank, so that the rows of one access lie apart.
+// 4-byte read for each of the instruction's four 4-row slices.  Chunks of 16 bytes
+// are swapped within a row by a key of the row that serves both accesses: the eight
+// rows that a 16-byte write fills at a time differ in it, and so do the pieces (32
+// bytes of four rows, float32: 64 bytes of two) that one read takes together.
 template <typename T, int COLS>
 __device__ __forceinline__ int row_chunk(int m, int c) {  // byte offset of 16-byte chunk c of row m
-    constexpr int kBytes = COLS * (int)sizeof(T);
+    constexpr int kChunks = COLS * (int)sizeof(T) / 16;
+    int key;
     if constexpr (sizeof(T) == 2) {
-        const int key = kBytes == 256 ? ((m & 3) | ((m >> 1) & 4)) : kBytes == 128 ? ((m >> 1) & 3) : 0;
-        return m * kBytes + ((((c >> 1) ^ key) << 1 | (c & 1)) << 4);
+        if constexpr (kChunks % 16 == 0)
+            key = ((m & 3) << 1) | ((m >> 2) & 1) | (m & 8);
+        else if constexpr (kChunks == 8)
+            key = ((m & 3) << 1) | ((m >> 2) & 1);
+        else  // 4 or 12: rows alternate between the halves of 128 bytes by themselves
+            key = (m & 2) | ((m >> 2) & 1);
     } else {
-        const int key = kBytes == 512 ? (m & 7) : kBytes == 256 ? (m & 3) : kBytes == 128 ? ((m >> 1) & 1) : 0;
-        return m * kBytes + ((((c >> 2) ^ key) << 2 | (c & 3)) << 4);
+        if constexpr (kChunks % 16 == 0)
+            key = ((m & 1) << 2) | ((m >> 1) & 3) | ((m & 2) << 2);
+        else if constexpr (kChunks == 8)
+            key = ((m & 1) << 2) | ((m >> 1) & 3);
+        else
+            key = (m >> 1) & 3;
     }
+    return m * (COLS * (int)sizeof(T)) + ((c ^ key) << 4);
 }
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
