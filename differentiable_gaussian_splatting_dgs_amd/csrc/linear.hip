@@ -28,28 +28,26 @@ struct ProdArgs {
     int32_t cols, depth, epi, act;
 };
 
-// The epilogue of one run: E consecutive outputs of one row, with the run of the
-// residual or dy already in `other`.
-template <typename T>
-__device__ __forceinline__ typename Tile<T>::Frag finish_run(const ProdArgs& p, float (&v)[Tile<T>::E],
-                                                             typename Tile<T>::Frag other) {
+// The epilogue of N runs (E consecutive outputs of one row each), with the runs of
+// the residual or dy already in `other`; one switch over the kinds for all of them.
+template <typename T, int N>
+__device__ __forceinline__ void finish_runs(const ProdArgs& p, float (&v)[N * Tile<T>::E],
+                                            const typename Tile<T>::Frag (&other)[N], typename Tile<T>::Frag (&out)[N]) {
     constexpr int E = Tile<T>::E;
     if (p.epi == EPI_FWD) {
         act_run<T>(p.act, v);
         if (p.other) {
 #pragma unroll
-            for (int j = 0; j < E; ++j) v[j] += (float)other[j];
+            for (int j = 0; j < N * E; ++j) v[j] += (float)other[j / E][j % E];
         }
     } else if (p.epi == EPI_DZ) {
-        float g[E];
+        float g[N * E];
 #pragma unroll
-        for (int j = 0; j < E; ++j) g[j] = (float)other[j];
+        for (int j = 0; j < N * E; ++j) g[j] = (float)other[j / E][j % E];
         slope_run<T>(p.act, v, g);
     }
-    typename Tile<T>::Frag f;
 #pragma unroll
-    for (int j = 0; j < E; ++j) f[j] = (T)v[j];
-    return f;
+    for (int j = 0; j < N * E; ++j) out[j / E][j % E] = (T)v[j];
 }
 
 // Few outputs or few rows: a block makes one group of KS outputs of 16 rows, its
@@ -110,9 +108,10 @@ __global__ __launch_bounds__(256) void k_prod_few(ProdArgs p) {
 #pragma unroll
         for (int j = 0; j < E; ++j) v[j] += (float)bias[j];
     }
-    auto other = zero_frag<T>();
-    if (p.other) other = load_frag(static_cast<const T*>(p.other) + row * p.ld_other, c0, p.cols);
-    store_run(static_cast<T*>(p.out) + row * p.ld_out, c0, p.cols, finish_run<T>(p, v, other));
+    typename Tile<T>::Frag other[1] = {zero_frag<T>()}, f[1];
+    if (p.other) other[0] = load_frag(static_cast<const T*>(p.other) + row * p.ld_other, c0, p.cols);
+    finish_runs<T, 1>(p, v, other, f);
+    store_run(static_cast<T*>(p.out) + row * p.ld_out, c0, p.cols, f[0]);
 }
 
 // Narrow layers over many rows: the weights stay in LDS as fragments for the
@@ -123,11 +122,10 @@ __global__ __launch_bounds__(256) void k_prod_few(ProdArgs p) {
 // half written (4.0 against 4.5 TB/s).  The next tile's x is on its way meanwhile.
 // Rows whose outputs are not whole 16-byte runs (PACK) are put together in LDS and
 // stored as the one contiguous piece of memory that a tile's rows are.
-constexpr int kNarrowThreads = 1024;  // at most
+constexpr int narrow_threads(int sl) { return sl <= 4 ? 1024 : 512; }  // at most: deep rows need 256 registers
 template <typename T, int SL, bool PACK>
-__global__ __launch_bounds__(kNarrowThreads) void k_prod_narrow(ProdArgs p) {
+__global__ __launch_bounds__(narrow_threads(SL)) void k_prod_narrow(ProdArgs p) {
     constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG, P = 2;
-    constexpr bool kAhead = SL <= 4;
     typedef typename Tile<T>::Frag Frag;
     extern __shared__ __align__(16) char s_mem[];
     const int groups = (p.cols + KS - 1) / KS;
@@ -141,13 +139,13 @@ __global__ __launch_bounds__(kNarrowThreads) void k_prod_narrow(ProdArgs p) {
     auto row_of = [&](int64_t t) { return min(t * 16 + r, p.rows - 1); };
     const Matrix<T> ma(p.a, p.rows, p.ld_a, p.depth), mo(p.other, p.rows, p.ld_other, p.cols);
     const bool even_a = p.depth == SL * KS, even_o = p.cols == groups * KS && groups % P == 0;
-    Frag x[SL], next[kAhead ? SL : 1];
-    auto fetch = [&](int64_t t, Frag* to) {
+    Frag x[SL], next[SL];
+    auto fetch = [&](int64_t t) {  // past the end: the last row again
         const int64_t row = row_of(t);
 #pragma unroll
-        for (int s = 0; s < SL; ++s) to[s] = ma.raw(row, s * KS + E * g);
+        for (int s = 0; s < SL; ++s) next[s] = ma.raw(row, s * KS + E * g);
     };
-    if (kAhead) fetch(tile, next);
+    fetch(tile);
     for (int i0 = threadIdx.x; i0 < groups * TG * SL * 64; i0 += 4 * blockDim.x) {
         Frag v[4];
 #pragma unroll
@@ -167,15 +165,13 @@ __global__ __launch_bounds__(kNarrowThreads) void k_prod_narrow(ProdArgs p) {
     __syncthreads();
     for (; tile < tiles; tile += step) {
         const int64_t row = tile * 16 + r;
-        if (!kAhead) fetch(tile, x);
 #pragma unroll
-        for (int s = 0; s < SL; ++s)
-            if (kAhead) x[s] = next[s];
+        for (int s = 0; s < SL; ++s) x[s] = next[s];
         if (!even_a) {
 #pragma unroll
             for (int s = 0; s < SL; ++s) x[s] = ma.fixed(x[s], row_of(tile), s * KS + E * g, true);
         }
-        if (kAhead) fetch(tile + step, next);  // past the end: the last row again
+        fetch(tile + step);
         T* out = PACK ? s_out + r * p.cols : static_cast<T*>(p.out) + row * p.ld_out;
         for (int n = 0; n < groups; n += P) {
             Frag other[P];
@@ -201,11 +197,13 @@ __global__ __launch_bounds__(kNarrowThreads) void k_prod_narrow(ProdArgs p) {
             }
             Frag f[P];
 #pragma unroll
-            for (int h = 0; h < P; ++h) {
+            for (int h = 0; h < P; ++h) {  // one at a time: both together spill registers
                 float v[E];
+                Frag o[1] = {other[h]}, to[1];
 #pragma unroll
                 for (int j = 0; j < E; ++j) v[j] = acc[h][j / 4][j % 4];
-                f[h] = finish_run<T>(p, v, other[h]);
+                finish_runs<T, 1>(p, v, o, to);
+                f[h] = to[0];
             }
             if (PACK || row < p.rows) {
 #pragma unroll
@@ -337,14 +335,15 @@ __global__ __launch_bounds__(256, 2) void k_prod_big(ProdArgs p) {
             for (int i = 0; i < 4; ++i)
                 other[i] = mo.fixed(other[i], min(m0 + wm + 16 * i + r, p.rows - 1), c0, true);
         }
+        float v[4 * E];
+        Frag f[4];
+#pragma unroll
+        for (int j = 0; j < 4 * E; ++j) v[j] = acc[j / E][q * TG + j % E / 4][j % 4] + bias[j % E];
+        finish_runs<T, 4>(p, v, other, f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t row = m0 + wm + 16 * i + r;
-            float v[E];
-#pragma unroll
-            for (int j = 0; j < E; ++j) v[j] = acc[i][q * TG + j / 4][j % 4] + bias[j];
-            const auto f = finish_run<T>(p, v, other[i]);
-            if (row < p.rows) store_run(static_cast<T*>(p.out) + row * p.ld_out, c0, p.cols, f);
+            if (row < p.rows) store_run(static_cast<T*>(p.out) + row * p.ld_out, c0, p.cols, f[i]);
         }
     }
 }
@@ -352,7 +351,7 @@ __global__ __launch_bounds__(256, 2) void k_prod_big(ProdArgs p) {
 template <typename T, int SL>
 void launch_narrow(const ProdArgs& p, size_t lds, hipStream_t s) {
     constexpr int E = Tile<T>::E;
-    int threads = lds <= 40960 ? 256 : lds <= 81920 ? 512 : 1024;
+    const int threads = lds <= 40960 ? 256 : lds <= 81920 || SL > 4 ? 512 : 1024;
     const bool pack = p.ld_out == p.cols && p.cols % E != 0 && aligned16(p.out) &&
                       lds + (size_t)threads / 4 * p.cols * sizeof(T) <= 160 * 1024;
     if (pack) lds += (size_t)threads / 4 * p.cols * sizeof(T);

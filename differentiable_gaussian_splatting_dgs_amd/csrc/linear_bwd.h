@@ -5,7 +5,7 @@
 // registers into dz, which are at once the fragments of dx^T = w^T dz^T (see
 // linear_tile.h), and writes dx; x and dz go to LDS in the layer's type, where
 // the block's waves share out dw += dz^T x, each keeping its part of dw in registers
-// for the life of the block.  db adds up in the same registers as dz, unrounded.
+// for the life of the block; db is dz^T times ones there.
 // Nothing else touches memory: x and dy are read once, dx is written once, and
 // each block leaves one partial dw and db for the join.
 #pragma once
@@ -34,10 +34,9 @@ template <typename T, int SL, int NG>
 struct BwdGeom {
     static constexpr int KS = Tile<T>::KS, TG = Tile<T>::TG;
     static constexpr int KP = SL * KS, NP = NG * KS;  // padded inputs and outputs
-    static constexpr int kCopies = sizeof(T) == 4 ? 2 : 1;
     static constexpr int kWaves = 4;
     static constexpr int kRows = 16 * kWaves;
-    static constexpr int kW = kCopies * KP * NP * (int)sizeof(T);
+    static constexpr int kW = KP * NP * (int)sizeof(T);
     static constexpr int kTiles = kRows * (KP + NP) * (int)sizeof(T);
     static constexpr int kLds = kW + kTiles + NP * 4;
     static constexpr int kPerCu = kLds > 80 * 1024 ? 1 : kLds > 53 * 1024 ? 2 : kLds > 40 * 1024 ? 3 : 4;
@@ -55,17 +54,38 @@ struct BwdGeom {
     static constexpr int TN = (NT + WN - 1) / WN, TK = (KT + WK - 1) / WK;
 };
 
-// Slot of lane l's fragment in LDS: the rows of the four lane groups are rotated
-// against each other, so that the transposing reads of w^T find them apart.
-__device__ __forceinline__ int w_slot(int r, int g) { return ((r + 4 * g) & 15) + 16 * g; }
+// Slot of the fragment of lane (r, g) in LDS.  The rows of the four lane groups are
+// rotated against each other so that the reads of w^T, which take one piece of 16
+// (float32: 64) different fragments at a time, find them in different banks.
+template <typename T>
+__device__ __forceinline__ int w_slot(int r, int g) {
+    return ((r + (sizeof(T) == 2 ? 4 * g : g)) & 15) + 16 * g;
+}
+
+// 16-bit: the pieces are 8 bytes, and two of the 32 that one cycle takes would meet in
+// each 16; fragments of odd lane groups lie with their halves swapped.  The product
+// with x then takes x with its halves swapped there too: the sum's order is free.
+template <typename T>
+__device__ __forceinline__ typename Tile<T>::Frag swap_halves(typename Tile<T>::Frag f, bool swap) {
+    union {
+        typename Tile<T>::Frag f;
+        uint64_t q[2];
+    } u;
+    u.f = f;
+    const uint64_t lo = swap ? u.q[1] : u.q[0], hi = swap ? u.q[0] : u.q[1];
+    u.q[0] = lo;
+    u.q[1] = hi;
+    return u.f;
+}
 
 template <typename T, int SL, int NG>
 __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), 2) void k_bwd_narrow(BwdArgs p) {
     typedef BwdGeom<T, SL, NG> G;
     constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG;
+    constexpr int kPair = sizeof(T) == 2 ? 2 : 1;  // groups of dx stored together: whole 128-byte lines
     typedef typename Tile<T>::Frag Frag;
     extern __shared__ __align__(16) char s_mem[];
-    Frag* s_w = reinterpret_cast<Frag*>(s_mem);  // [NG][TG][SL][64], float32: then w^T [SL][NG][64]
+    Frag* s_w = reinterpret_cast<Frag*>(s_mem);  // [NG][TG][SL][64]
     char* s_dz = s_mem + G::kW;
     char* s_x = s_dz + G::kRows * G::NP * (int)sizeof(T);
     float* s_bias = reinterpret_cast<float*>(s_x + G::kRows * G::KP * (int)sizeof(T));
@@ -75,7 +95,10 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), 2) void k_bwd_na
     const int tn0 = wave / G::WK * G::TN, tk0 = wave % G::WK * G::TK;
     const int64_t tiles = (p.rows + G::kRows - 1) / G::kRows;
     f32x4 dw[G::TN][G::TK] = {};
-    float db[NG][E] = {};
+    f32x4 db[G::TN] = {};
+    Frag ones;
+#pragma unroll
+    for (int j = 0; j < E; ++j) ones[j] = (T)1.f;
     const Matrix<T> mx(p.x, p.rows, p.ld_x, p.n_in), my(p.dy, p.rows, p.ld_dy, p.n_out);
     const bool even = p.n_in == G::KP && p.n_out == G::NP;
     Frag x[SL], dy[NG];
@@ -90,24 +113,13 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), 2) void k_bwd_na
 #pragma unroll
     for (int f = wave; f < NG * TG * SL; f += G::kWaves) {
         const int s = f % SL, n = f / SL / TG * KS + out_row<T>(f / SL % TG, r);
-        s_w[f * 64 + w_slot(r, g)] =
-            n < p.n_out ? load_frag(w + (int64_t)n * p.n_in, s * KS + E * g, p.n_in) : zero_frag<T>();
+        Frag v = zero_frag<T>();
+        if (n < p.n_out) v = load_frag(w + (int64_t)n * p.n_in, s * KS + E * g, p.n_in);
+        s_w[f * 64 + w_slot<T>(r, g)] = sizeof(T) == 2 ? swap_halves<T>(v, g & 1) : v;
     }
     for (int i = threadIdx.x; i < G::NP; i += blockDim.x)
         s_bias[i] = p.bias && i < p.n_out ? (float)static_cast<const T*>(p.bias)[i] : 0.f;
     __syncthreads();
-    if constexpr (sizeof(T) == 4) {  // w^T from the copy in LDS: input k of outputs n .. n + 3
-        const float* s_wf = reinterpret_cast<const float*>(s_w);
-#pragma unroll
-        for (int f = wave; f < SL * NG; f += G::kWaves) {
-            const int k = f / NG, n = f % NG;
-            Frag v;
-#pragma unroll
-            for (int j = 0; j < E; ++j) v[j] = s_wf[((n * SL + k) * 64 + w_slot(4 * g + j, r >> 2)) * 4 + (r & 3)];
-            s_w[(NG * SL + f) * 64 + lane] = v;
-        }
-        __syncthreads();
-    }
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const int64_t row = tile * G::kRows + wave * 16 + r;
         const int m = wave * 16 + r;
@@ -118,90 +130,107 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), 2) void k_bwd_na
 #pragma unroll
             for (int n = 0; n < NG; ++n) dy[n] = my.fixed(dy[n], rc, n * KS + E * g, row < p.rows);
         }
-        Frag dz[NG];
-#pragma unroll
-        for (int n = 0; n < NG; ++n) {
-            float v[E];
-            if (p.act != GS_ACT_NONE) {
-                f32x4 z[TG];
-#pragma unroll
-                for (int t = 0; t < TG; ++t) z[t] = *reinterpret_cast<f32x4*>(s_bias + n * KS + E * g + 4 * t);
-#pragma unroll
-                for (int s = 0; s < SL; ++s)
-#pragma unroll
-                    for (int t = 0; t < TG; ++t) mma(z[t], s_w[((n * TG + t) * SL + s) * 64 + w_slot(r, g)], x[s]);
-#pragma unroll
-                for (int j = 0; j < E; ++j) v[j] = z[j / 4][j % 4];
-                float d[E];
-#pragma unroll
-                for (int j = 0; j < E; ++j) d[j] = (float)dy[n][j];
-                slope_run<T>(p.act, v, d);
-                if (row >= p.rows)  // the bias can be infinite or NaN there
-#pragma unroll
-                    for (int j = 0; j < E; ++j) v[j] = 0.f;
-            } else {
-#pragma unroll
-                for (int j = 0; j < E; ++j) v[j] = (float)dy[n][j];
-            }
-#pragma unroll
-            for (int j = 0; j < E; ++j) {
-                db[n][j] += v[j];
-                dz[n][j] = (T)v[j];
-            }
-            *reinterpret_cast<Frag*>(s_dz + row_chunk<T, G::NP>(m, n * 4 + g)) = dz[n];
-        }
 #pragma unroll
         for (int s = 0; s < SL; ++s) *reinterpret_cast<Frag*>(s_x + row_chunk<T, G::KP>(m, s * 4 + g)) = x[s];
-        fetch(tile + gridDim.x);
-        if (p.dx) {
-            T* out = static_cast<T*>(p.dx) + row * p.ld_dx;
+        if (sizeof(T) == 2) {
 #pragma unroll
-            for (int k = 0; k < SL; ++k) {
-                f32x4 acc[TG] = {};
+            for (int s = 0; s < SL; ++s) x[s] = swap_halves<T>(x[s], g & 1);
+        }
+        // every group's z before the one switch over the activations: branches between the groups would
+        // leave the matrix instructions waiting for each other's operands
+        float v[NG * E], d[NG * E];
+        if (p.act != GS_ACT_NONE) {
+            f32x4 z[NG][TG];
+#pragma unroll
+            for (int n = 0; n < NG; ++n)
+#pragma unroll
+                for (int t = 0; t < TG; ++t) z[n][t] = *reinterpret_cast<f32x4*>(s_bias + n * KS + E * g + 4 * t);
+#pragma unroll
+            for (int s = 0; s < SL; ++s)
 #pragma unroll
                 for (int n = 0; n < NG; ++n)
 #pragma unroll
-                    for (int t = 0; t < TG; ++t) {
-                        if constexpr (sizeof(T) == 2) {
-                            union {
-                                Frag f;
-                                s16x4 h[2];
-                            } u;
+                    for (int t = 0; t < TG; ++t)
+                        mma(z[n][t], s_w[((n * TG + t) * SL + s) * 64 + w_slot<T>(r, g)], x[s]);
 #pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                u.h[h] = read_transposed(
-                                    reinterpret_cast<const char*>(s_w + ((n * TG + h) * SL + k) * 64 +
-                                                                  w_slot(4 * g + (r >> 2), r & 3)) +
-                                    8 * t);
-                            mma(acc[t], u.f, dz[n]);
-                        } else {
-                            mma(acc[t], s_w[(NG * SL + k * NG + n) * 64 + lane], dz[n]);
+            for (int j = 0; j < NG * E; ++j) v[j] = z[j / E][j % E / 4][j % 4];
+        }
+#pragma unroll
+        for (int j = 0; j < NG * E; ++j) d[j] = (float)dy[j / E][j % E];
+        slope_run<T>(p.act, v, d);
+        if ((tile + 1) * G::kRows > p.rows && row >= p.rows) {  // the bias can be infinite or NaN there
+#pragma unroll
+            for (int j = 0; j < NG * E; ++j) v[j] = 0.f;
+        }
+        Frag dz[NG];
+#pragma unroll
+        for (int j = 0; j < NG * E; ++j) dz[j / E][j % E] = (T)v[j];
+#pragma unroll
+        for (int n = 0; n < NG; ++n) *reinterpret_cast<Frag*>(s_dz + row_chunk<T, G::NP>(m, n * 4 + g)) = dz[n];
+        if (p.dx) {
+            T* out = static_cast<T*>(p.dx) + row * p.ld_dx;
+#pragma unroll
+            for (int k0 = 0; k0 < SL; k0 += kPair) {
+                Frag f[kPair];
+#pragma unroll
+                for (int q = 0; q < kPair; ++q) {
+                    const int k = k0 + q;
+                    if (k >= SL) break;
+                    f32x4 acc[TG] = {};
+#pragma unroll
+                    for (int n = 0; n < NG; ++n)
+#pragma unroll
+                        for (int t = 0; t < TG; ++t) {
+                            if constexpr (sizeof(T) == 2) {
+                                union {
+                                    Frag f;
+                                    s16x4 h[2];
+                                } u;
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    u.h[h] = read_transposed(
+                                        reinterpret_cast<const char*>(s_w + ((n * TG + h) * SL + k) * 64 +
+                                                                      w_slot<T>(4 * g + (r >> 2), r & 3)) +
+                                        8 * (t ^ (r & 1)));
+                                mma(acc[t], u.f, dz[n]);
+                            } else {
+                                Frag a;  // input r of outputs 4 g .. 4 g + 3
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    a[j] = reinterpret_cast<const float*>(
+                                        s_w + (n * SL + k) * 64 + w_slot<T>(4 * g + j, r >> 2))[r & 3];
+                                mma(acc[t], a, dz[n]);
+                            }
                         }
-                    }
-                if (row < p.rows) {
-                    Frag f;
 #pragma unroll
-                    for (int j = 0; j < E; ++j) f[j] = (T)acc[j / 4][j % 4];
-                    store_run(out, k * KS + E * g, p.n_in, f);
+                    for (int j = 0; j < E; ++j) f[q][j] = (T)acc[j / 4][j % 4];
+                }
+                if (row < p.rows) {
+#pragma unroll
+                    for (int q = 0; q < kPair; ++q)
+                        if (k0 + q < SL) store_run(out, (k0 + q) * KS + E * g, p.n_in, f[q]);
                 }
             }
         }
+        fetch(tile + gridDim.x);
         __syncthreads();
-        if (p.want_dw) {
+        if (p.want_dw || p.want_db) {
 #pragma unroll
             for (int h = 0; h < G::kRows / KS; ++h) {
+                // a rectangle that reaches past dw's edge repeats the last tiles, which are not stored
                 Frag fz[G::TN], fx[G::TK];
 #pragma unroll
                 for (int i = 0; i < G::TN; ++i)
-                    if (tn0 + i < G::NT) fz[i] = column_frag<T, G::NP>(s_dz, h * KS, (tn0 + i) * 16, lane);
+                    fz[i] = column_frag<T, G::NP>(s_dz, h * KS, min(tn0 + i, G::NT - 1) * 16, lane);
 #pragma unroll
                 for (int j = 0; j < G::TK; ++j)
-                    if (tk0 + j < G::KT) fx[j] = column_frag<T, G::KP>(s_x, h * KS, (tk0 + j) * 16, lane);
+                    fx[j] = column_frag<T, G::KP>(s_x, h * KS, min(tk0 + j, G::KT - 1) * 16, lane);
 #pragma unroll
-                for (int i = 0; i < G::TN; ++i)
+                for (int i = 0; i < G::TN; ++i) {
+                    mma(db[i], fz[i], ones);
 #pragma unroll
-                    for (int j = 0; j < G::TK; ++j)
-                        if (tn0 + i < G::NT && tk0 + j < G::KT) mma(dw[i][j], fz[i], fx[j]);
+                    for (int j = 0; j < G::TK; ++j) mma(dw[i][j], fz[i], fx[j]);
+                }
             }
         }
         __syncthreads();
@@ -223,25 +252,18 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), 2) void k_bwd_na
                         part[(int64_t)n * p.n_in + k] = dw[i][j][q];
                 }
     }
-    if (p.want_db) {  // over the 16 rows of the lanes, then over the waves, in a fixed order
-        float* s_db = reinterpret_cast<float*>(s_dz);  // [waves][NP]
+    if (p.want_db && tk0 == 0 && r == 0) {
 #pragma unroll
-        for (int n = 0; n < NG; ++n)
+        for (int i = 0; i < G::TN; ++i)
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                float v = db[n][j];
-                for (int o = 1; o < 16; o <<= 1) v += __shfl_xor(v, o, 64);
-                if (r == 0) s_db[wave * G::NP + n * KS + E * g + j] = v;
+            for (int q = 0; q < 4; ++q) {
+                const int n = (tn0 + i) * 16 + 4 * g + q;
+                if (n >= p.n_out) continue;
+                if (p.db)
+                    static_cast<T*>(p.db)[n] = (T)db[i][q];
+                else
+                    part[n_w + n] = db[i][q];
             }
-        __syncthreads();
-        for (int n = threadIdx.x; n < p.n_out; n += blockDim.x) {
-            float v = 0.f;
-            for (int i = 0; i < G::kWaves; ++i) v += s_db[i * G::NP + n];
-            if (p.db)
-                static_cast<T*>(p.db)[n] = (T)v;
-            else
-                part[n_w + n] = v;
-        }
     }
 }
 
