@@ -5,7 +5,7 @@
 // registers into dz, which are at once the fragments of dx^T = w^T dz^T (see
 // linear_tile.h), and writes dx; x and dz go to LDS in the layer's type, where
 // the block's waves share out dw += dz^T x, each keeping its part of dw in registers
-// for the life of the block; db is dz^T times ones there.
+// for the life of the block.  db adds up in the registers of dz, before its rounding.
 // Nothing else touches memory: x and dy are read once, dx is written once, and
 // each block leaves one partial dw and db for the join.
 #pragma once
@@ -95,10 +95,7 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), 2) void k_bwd_na
     const int tn0 = wave / G::WK * G::TN, tk0 = wave % G::WK * G::TK;
     const int64_t tiles = (p.rows + G::kRows - 1) / G::kRows;
     f32x4 dw[G::TN][G::TK] = {};
-    f32x4 db[G::TN] = {};
-    Frag ones;
-#pragma unroll
-    for (int j = 0; j < E; ++j) ones[j] = (T)1.f;
+    float db[NG * E] = {};
     const Matrix<T> mx(p.x, p.rows, p.ld_x, p.n_in), my(p.dy, p.rows, p.ld_dy, p.n_out);
     const bool even = p.n_in == G::KP && p.n_out == G::NP;
     Frag x[SL], dy[NG];
@@ -164,7 +161,10 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), 2) void k_bwd_na
         }
         Frag dz[NG];
 #pragma unroll
-        for (int j = 0; j < NG * E; ++j) dz[j / E][j % E] = (T)v[j];
+        for (int j = 0; j < NG * E; ++j) {
+            db[j] += v[j];
+            dz[j / E][j % E] = (T)v[j];
+        }
 #pragma unroll
         for (int n = 0; n < NG; ++n) *reinterpret_cast<Frag*>(s_dz + row_chunk<T, G::NP>(m, n * 4 + g)) = dz[n];
         if (p.dx) {
@@ -214,7 +214,7 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), 2) void k_bwd_na
         }
         fetch(tile + gridDim.x);
         __syncthreads();
-        if (p.want_dw || p.want_db) {
+        if (p.want_dw) {
 #pragma unroll
             for (int h = 0; h < G::kRows / KS; ++h) {
                 // a rectangle that reaches past dw's edge repeats the last tiles, which are not stored
@@ -226,11 +226,9 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), 2) void k_bwd_na
                 for (int j = 0; j < G::TK; ++j)
                     fx[j] = column_frag<T, G::KP>(s_x, h * KS, min(tk0 + j, G::KT - 1) * 16, lane);
 #pragma unroll
-                for (int i = 0; i < G::TN; ++i) {
-                    mma(db[i], fz[i], ones);
+                for (int i = 0; i < G::TN; ++i)
 #pragma unroll
                     for (int j = 0; j < G::TK; ++j) mma(dw[i][j], fz[i], fx[j]);
-                }
             }
         }
         __syncthreads();
@@ -252,18 +250,23 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), 2) void k_bwd_na
                         part[(int64_t)n * p.n_in + k] = dw[i][j][q];
                 }
     }
-    if (p.want_db && tk0 == 0 && r == 0) {
+    if (p.want_db) {  // over the 16 rows of the lanes, then over the waves, in a fixed order
+        float* s_db = reinterpret_cast<float*>(s_dz);  // [waves][NP]
 #pragma unroll
-        for (int i = 0; i < G::TN; ++i)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int n = (tn0 + i) * 16 + 4 * g + q;
-                if (n >= p.n_out) continue;
-                if (p.db)
-                    static_cast<T*>(p.db)[n] = (T)db[i][q];
-                else
-                    part[n_w + n] = db[i][q];
-            }
+        for (int j = 0; j < NG * E; ++j) {
+            float v = db[j];
+            for (int o = 1; o < 16; o <<= 1) v += __shfl_xor(v, o, 64);
+            if (r == 0) s_db[wave * G::NP + j / E * KS + E * g + j % E] = v;
+        }
+        __syncthreads();
+        for (int n = threadIdx.x; n < p.n_out; n += blockDim.x) {
+            float v = 0.f;
+            for (int i = 0; i < G::kWaves; ++i) v += s_db[i * G::NP + n];
+            if (p.db)
+                static_cast<T*>(p.db)[n] = (T)v;
+            else
+                part[n_w + n] = v;
+        }
     }
 }
 
