@@ -904,21 +904,27 @@ def gs_grad_workspace_size(n_tensors):
 
 def _grad_table(grads, out):
     """The gs_grad_tensor array of a list of gradients, as bytes."""
-    flat = []
-    device = grads[0].get_device() if grads and isinstance(grads[0], torch.Tensor) else -1
-    for i, g in enumerate(grads):
-        if not isinstance(g, torch.Tensor) or not g.is_contiguous() or g.get_device() != device or device < 0:
-            _refuse(g, None, None, f"gradient {i}")
-        code = DTYPES.get(g.dtype)
-        if code is None:
-            _refuse(g, None, None, f"gradient {i}")
-        p = g.data_ptr()
-        if out is None:
-            flat += (p, 0, g.numel(), code)
-        elif out[i] is g:
-            flat += (p, p, g.numel(), code)
+    flat, codes = [], DTYPES
+    try:
+        device = grads[0].get_device() if grads else 0
+        if out is None or out is grads:
+            for g in grads:
+                if not g.is_contiguous() or g.get_device() != device:
+                    _refuse(g, None, None, "a gradient")
+                p = g.data_ptr()
+                flat += (p, p if out is grads else 0, g.numel(), codes[g.dtype])
         else:
-            flat += (p, _whole(out[i], g.shape, g.dtype, device, f"out {i}") or 0, g.numel(), code)
+            for g, o in zip(grads, out):
+                n, dtype = g.numel(), g.dtype
+                if not g.is_contiguous() or g.get_device() != device:
+                    _refuse(g, None, None, "a gradient")
+                if not o.is_contiguous() or o.get_device() != device or o.numel() != n or o.dtype != dtype:
+                    _refuse(o, g.shape, dtype, "an output")
+                flat += (g.data_ptr(), o.data_ptr(), n, codes[dtype])
+    except (AttributeError, KeyError):
+        raise GsError("gradients must be float32, float16 or bfloat16 tensors") from None
+    if device < 0:
+        raise GsError("gradients must be CUDA (HIP) tensors")
     return struct.pack("=%dq" % len(flat), *flat)
 
 

@@ -86,7 +86,7 @@ class GradClip:
             raise GsError("no gradients")
         need = gs.gs_grad_workspace_size(len(grads))
         if self.state is None or self.state.device != grads[0].device:
-            self.state = torch.zeros(gs.CLIP_STATE_FLOATS, dtype=torch.float32, device=grads[0].device)
+            self.state = torch.empty(gs.CLIP_STATE_FLOATS, dtype=torch.float32, device=grads[0].device)
             self.value = self.state[0]
             self.workspace = _workspace(need, grads[0].device)
         elif self.workspace.numel() < need:

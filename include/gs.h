@@ -659,9 +659,9 @@ typedef struct gs_grad_tensor {
     int32_t dtype;
 } gs_grad_tensor;
 
-/* The clipping state the next three calls share, device memory of 16 bytes:
-   word 0 the global norm (float32), word 1 the coefficient (float32), words 2
-   and 3 the library's.  Zero it once, before its first use. */
+/* The clipping state the next three calls share, device memory of 16 bytes
+   (16-byte aligned): word 0 the global norm (float32), word 1 the coefficient
+   (float32), words 2 and 3 reserved. */
 #define GS_CLIP_STATE_BYTES 16
 
 /* Bytes of workspace gs_grad_norm and gs_grad_clip need for n_tensors. */
