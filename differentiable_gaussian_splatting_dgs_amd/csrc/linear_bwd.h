@@ -7,7 +7,9 @@
 // the block's waves share out dw += dz^T x, each keeping its part of dw in registers
 // for the life of the block.  db adds up in the registers of dz, before its rounding.
 // Nothing else touches memory: x and dy are read once, dx is written once, and
-// each block leaves one partial dw and db for the join.
+// each block leaves one partial dw and db for the join.  A layer with few inputs and
+// more outputs than a block holds goes through in parts of the outputs (PARTS): dy is
+// still read once, and dx adds up in float32 from part to part.
 #pragma once
 
 #include "linear_tile.h"
@@ -26,9 +28,16 @@ struct BwdArgs {
     int32_t want_dw, want_db;
     void* dw;  // one block: the results themselves instead of a partial
     void* db;
+    // a layer with more outputs, some of them at a time: dx so far [rows][KP] float32, and whether these outputs
+    // are the first and the last
+    float* dx_sum;
+    int32_t first, last;
 };
 
 constexpr int kBwdGroups = 4;  // groups of KS inputs and of KS outputs at most
+// Inputs of a layer that goes through in parts of its outputs, at most.
+template <typename T>
+constexpr int kPartInputs = sizeof(T) == 4 ? kBwdGroups * Tile<T>::KS : Tile<T>::KS;
 
 template <typename T, int SL, int NG>
 struct BwdGeom {
@@ -78,7 +87,7 @@ __device__ __forceinline__ typename Tile<T>::Frag swap_halves(typename Tile<T>::
     return u.f;
 }
 
-template <typename T, int SL, int NG>
+template <typename T, int SL, int NG, bool PARTS>
 __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), 2) void k_bwd_narrow(BwdArgs p) {
     typedef BwdGeom<T, SL, NG> G;
     constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG;
@@ -120,12 +129,20 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), 2) void k_bwd_na
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const int64_t row = tile * G::kRows + wave * 16 + r;
         const int m = wave * 16 + r;
-        if (!even || (tile + 1) * G::kRows > p.rows) {  // rows past the end add nothing: dz = 0, x = 0
+        if ((tile + 1) * G::kRows > p.rows) {  // rows past the end add nothing: dz = 0, x = 0
             const int64_t rc = min(row, p.rows - 1);
 #pragma unroll
             for (int s = 0; s < SL; ++s) x[s] = mx.fixed(x[s], rc, s * KS + E * g, row < p.rows);
 #pragma unroll
             for (int n = 0; n < NG; ++n) dy[n] = my.fixed(dy[n], rc, n * KS + E * g, row < p.rows);
+        } else if (!even) {  // only the last group of a row can reach past its end
+            x[SL - 1] = mx.fixed(x[SL - 1], row, (SL - 1) * KS + E * g, true);
+#pragma unroll
+            for (int n = 0; n < NG; ++n)
+                if (!PARTS && n < NG - 1)
+                    continue;
+                else
+                    dy[n] = my.fixed(dy[n], row, n * KS + E * g, true);
         }
 #pragma unroll
         for (int s = 0; s < SL; ++s) *reinterpret_cast<Frag*>(s_x + row_chunk<T, G::KP>(m, s * 4 + g)) = x[s];
@@ -177,6 +194,11 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), 2) void k_bwd_na
                     const int k = k0 + q;
                     if (k >= SL) break;
                     f32x4 acc[TG] = {};
+                    if (PARTS && !p.first) {
+                        const float* sum = p.dx_sum + min(row, p.rows - 1) * G::KP + k * KS + E * g;
+#pragma unroll
+                        for (int t = 0; t < TG; ++t) acc[t] = *reinterpret_cast<const f32x4*>(sum + 4 * t);
+                    }
 #pragma unroll
                     for (int n = 0; n < NG; ++n)
 #pragma unroll
@@ -202,10 +224,17 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), 2) void k_bwd_na
                                 mma(acc[t], a, dz[n]);
                             }
                         }
+                    if (PARTS && !p.last) {
+                        float* sum = p.dx_sum + row * G::KP + k * KS + E * g;
+                        if (row < p.rows) {
+#pragma unroll
+                            for (int t = 0; t < TG; ++t) *reinterpret_cast<f32x4*>(sum + 4 * t) = acc[t];
+                        }
+                    }
 #pragma unroll
                     for (int j = 0; j < E; ++j) f[q][j] = (T)acc[j / 4][j % 4];
                 }
-                if (row < p.rows) {
+                if ((!PARTS || p.last) && row < p.rows) {
 #pragma unroll
                     for (int q = 0; q < kPair; ++q)
                         if (k0 + q < SL) store_run(out, (k0 + q) * KS + E * g, p.n_in, f[q]);
@@ -287,7 +316,10 @@ inline void bwd_narrow_one(const BwdArgs& p, int64_t rows, int* blocks, hipStrea
         *blocks = (int)(tiles < most ? tiles : most);
         return;
     }
-    hipLaunchKernelGGL((k_bwd_narrow<T, SL, NG>), dim3(*blocks), dim3(G::kWaves * 64), G::kLds, s, p);
+    if (!p.dx_sum)
+        hipLaunchKernelGGL((k_bwd_narrow<T, SL, NG, false>), dim3(*blocks), dim3(G::kWaves * 64), G::kLds, s, p);
+    else if constexpr (NG == kBwdGroups && SL * Tile<T>::KS <= kPartInputs<T>)
+        hipLaunchKernelGGL((k_bwd_narrow<T, SL, NG, true>), dim3(*blocks), dim3(G::kWaves * 64), G::kLds, s, p);
 }
 
 template <typename T, int SL>
@@ -303,7 +335,8 @@ inline void bwd_narrow_out(const BwdArgs& p, int64_t rows, int32_t ng, int* bloc
 template <typename T>
 inline void bwd_narrow_any(const BwdArgs& p, int64_t rows, int32_t n_in, int32_t n_out, int* blocks, hipStream_t s,
                            bool launch) {
-    const int sl = (n_in + Tile<T>::KS - 1) / Tile<T>::KS, ng = (n_out + Tile<T>::KS - 1) / Tile<T>::KS;
+    const int sl = (n_in + Tile<T>::KS - 1) / Tile<T>::KS;
+    const int ng = p.dx_sum ? kBwdGroups : (n_out + Tile<T>::KS - 1) / Tile<T>::KS;
     switch (sl) {
         case 1: bwd_narrow_out<T, 1>(p, rows, ng, blocks, s, launch); break;
         case 2: bwd_narrow_out<T, 2>(p, rows, ng, blocks, s, launch); break;

@@ -172,7 +172,8 @@ def test_backward_of_some():
 # many rows: every depth a wave holds in registers, odd ones among them, and deeper or wider layers
 MANY = [(33_001, 3, 64), (33_001, 20, 3), (17_003, 63, 59), (17_003, 90, 40), (12_001, 128, 128), (17_000, 150, 33),
         (16_401, 190, 64), (9_001, 220, 100), (8_200, 256, 256), (17_001, 256, 20), (6_007, 257, 300),
-        (3_001, 700, 520), (33_003, 1000, 5), (5_000, 40, 700), (4_111, 512, 512)]
+        (3_001, 700, 520), (33_003, 1000, 5), (5_000, 40, 700), (4_111, 512, 512), (65_601, 14, 300), (66_001, 30, 200),
+        (65_536, 60, 257)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
