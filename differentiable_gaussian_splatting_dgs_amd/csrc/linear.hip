@@ -146,18 +146,36 @@ __global__ __launch_bounds__(narrow_threads(SL)) void k_prod_narrow(ProdArgs p) 
         for (int s = 0; s < SL; ++s) next[s] = ma.raw(row, s * KS + E * g);
     };
     fetch(tile);
-    for (int i0 = threadIdx.x; i0 < groups * TG * SL * 64; i0 += 4 * blockDim.x) {
-        Frag v[4];
+    const int frags = groups * TG * SL * 64;
+    auto place = [&](int i, int& n, int& k0) {  // output and first input of fragment i
+        const int l = i & 63, gt = (i >> 6) / SL;
+        n = gt / TG * KS + out_row<T>(gt % TG, l & 15);
+        k0 = (i >> 6) % SL * KS + E * (l >> 4);
+    };
+    if ((p.cols - 1) * p.ld_b + p.depth >= E) {
+        const Matrix<T> mb(p.b, p.cols, p.ld_b, p.depth);
+        for (int i0 = threadIdx.x; i0 < frags; i0 += 8 * blockDim.x) {
+            Frag v[8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int i = i0 + u * blockDim.x, l = i & 63, sl = (i >> 6) % SL, gt = (i >> 6) / SL;
-            const int n = gt / TG * KS + out_row<T>(gt % TG, l & 15);
-            v[u] = n < p.cols ? load_frag(static_cast<const T*>(p.b) + (int64_t)n * p.ld_b, sl * KS + E * (l >> 4), p.depth)
-                              : zero_frag<T>();
+            for (int u = 0; u < 8; ++u) {
+                int n, k0;
+                place(i0 + u * blockDim.x, n, k0);
+                v[u] = mb.raw(min(n, p.cols - 1), k0);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                int n, k0;
+                place(i0 + u * blockDim.x, n, k0);
+                if (i0 + u * (int)blockDim.x < frags)
+                    s_w[i0 + u * blockDim.x] = mb.fixed(v[u], min(n, p.cols - 1), k0, n < p.cols);
+            }
         }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (i0 + u * (int)blockDim.x < groups * TG * SL * 64) s_w[i0 + u * blockDim.x] = v[u];
+    } else {  // fewer weights than a fragment
+        for (int i = threadIdx.x; i < frags; i += blockDim.x) {
+            int n, k0;
+            place(i, n, k0);
+            s_w[i] = n < p.cols ? load_edge(static_cast<const T*>(p.b) + n * p.ld_b, k0, p.depth) : zero_frag<T>();
+        }
     }
     for (int i = threadIdx.x; i < groups * KS; i += blockDim.x)
         reinterpret_cast<float*>(s_bias)[i] =
@@ -195,6 +213,7 @@ __global__ __launch_bounds__(narrow_threads(SL)) void k_prod_narrow(ProdArgs p) 
             Frag f[P];
 #pragma unroll
             for (int h = 0; h < P; ++h) {  // one at a time: both together spill registers
+                if (h > 0 && n + h >= groups) break;
                 float v[E];
                 Frag o[1] = {other[h]}, to[1];
 #pragma unroll
@@ -204,7 +223,10 @@ __global__ __launch_bounds__(narrow_threads(SL)) void k_prod_narrow(ProdArgs p) 
             }
             if (PACK || row < p.rows) {
 #pragma unroll
-                for (int h = 0; h < P; ++h) store_run(out, (n + h) * KS + E * g, p.cols, f[h]);
+                for (int h = 0; h < P; ++h) {
+                    if (h > 0 && n + h >= groups) break;
+                    store_run(out, (n + h) * KS + E * g, p.cols, f[h]);
+                }
             }
         }
         if (PACK) {

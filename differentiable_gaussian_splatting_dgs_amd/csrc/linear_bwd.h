@@ -48,7 +48,10 @@ struct BwdGeom {
     static constexpr int kW = KP * NP * (int)sizeof(T);
     static constexpr int kTiles = kRows * (KP + NP) * (int)sizeof(T);
     static constexpr int kLds = kW + kTiles + NP * 4;
-    static constexpr int kPerCu = kLds > 80 * 1024 ? 1 : kLds > 53 * 1024 ? 2 : kLds > 40 * 1024 ? 3 : 4;
+    // blocks per CU: three where the LDS and 168 registers hold them, else two; the grid counts on it
+    static constexpr bool kManyRegs = sizeof(T) == 2 ? 30 + 40 * NG + 18 * SL > 168 : NG == kBwdGroups;  // by the builds
+    static constexpr int kPerCu = kLds > 53 * 1024 || kManyRegs ? 2 : 3;
+    static_assert(kLds <= 80 * 1024, "two blocks per CU");
     // dw's 16 x 16 tiles, NT by KT, dealt to the waves as TN x TK rectangles
     static constexpr int NT = NG * TG, KT = SL * TG;
     static constexpr int split() {
@@ -88,7 +91,7 @@ __device__ __forceinline__ typename Tile<T>::Frag swap_halves(typename Tile<T>::
 }
 
 template <typename T, int SL, int NG, bool PARTS>
-__global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), 2) void k_bwd_narrow(BwdArgs p) {
+__global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), (BwdGeom<T, SL, NG>::kPerCu)) void k_bwd_narrow(BwdArgs p) {
     typedef BwdGeom<T, SL, NG> G;
     constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG;
     constexpr int kPair = sizeof(T) == 2 ? 2 : 1;  // groups of dx stored together: whole 128-byte lines
@@ -98,7 +101,6 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), 2) void k_bwd_na
     char* s_dz = s_mem + G::kW;
     char* s_x = s_dz + G::kRows * G::NP * (int)sizeof(T);
     float* s_bias = reinterpret_cast<float*>(s_x + G::kRows * G::KP * (int)sizeof(T));
-    const T* w = static_cast<const T*>(p.w);
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tn0 = wave / G::WK * G::TN, tk0 = wave % G::WK * G::TK;
@@ -116,12 +118,37 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), 2) void k_bwd_na
         for (int n = 0; n < NG; ++n) dy[n] = my.raw(row, n * KS + E * g);
     };
     fetch(blockIdx.x);
+    auto place = [&](int f, int& n, int& k0) {  // output and first input of fragment f of this lane
+        n = f / SL / TG * KS + out_row<T>(f / SL % TG, r);
+        k0 = f % SL * KS + E * g;
+    };
+    if ((int64_t)p.n_out * p.n_in >= E) {
+        const Matrix<T> mw(p.w, p.n_out, p.n_in, p.n_in);
+        constexpr int kMine = (NG * TG * SL + G::kWaves - 1) / G::kWaves;
+        Frag v[kMine];
 #pragma unroll
-    for (int f = wave; f < NG * TG * SL; f += G::kWaves) {
-        const int s = f % SL, n = f / SL / TG * KS + out_row<T>(f / SL % TG, r);
-        Frag v = zero_frag<T>();
-        if (n < p.n_out) v = load_frag(w + (int64_t)n * p.n_in, s * KS + E * g, p.n_in);
-        s_w[f * 64 + w_slot<T>(r, g)] = sizeof(T) == 2 ? swap_halves<T>(v, g & 1) : v;
+        for (int u = 0; u < kMine; ++u) {
+            int n, k0;
+            place(min(wave + u * G::kWaves, NG * TG * SL - 1), n, k0);
+            v[u] = mw.raw(min(n, p.n_out - 1), k0);
+        }
+#pragma unroll
+        for (int u = 0; u < kMine; ++u) {
+            const int f = wave + u * G::kWaves;
+            if (f >= NG * TG * SL) break;
+            int n, k0;
+            place(f, n, k0);
+            const Frag w = mw.fixed(v[u], min(n, p.n_out - 1), k0, n < p.n_out);
+            s_w[f * 64 + w_slot<T>(r, g)] = sizeof(T) == 2 ? swap_halves<T>(w, g & 1) : w;
+        }
+    } else {  // fewer weights than a fragment
+        for (int f = wave; f < NG * TG * SL; f += G::kWaves) {
+            int n, k0;
+            place(f, n, k0);
+            Frag w = zero_frag<T>();
+            if (n < p.n_out) w = load_edge(static_cast<const T*>(p.w) + n * p.n_in, k0, p.n_in);
+            s_w[f * 64 + w_slot<T>(r, g)] = sizeof(T) == 2 ? swap_halves<T>(w, g & 1) : w;
+        }
     }
     for (int i = threadIdx.x; i < G::NP; i += blockDim.x)
         s_bias[i] = p.bias && i < p.n_out ? (float)static_cast<const T*>(p.bias)[i] : 0.f;

@@ -936,7 +936,12 @@ def _clip_state(clip):
 
 def gs_grad_norm(grads, max_norm, clip, workspace):
     """Global norm and clipping coefficient of the list grads into clip [4] float32 (words 0 and 1)."""
-    rc = (_lib or load_library()).gs_grad_norm(len(grads), _grad_table(grads, None), max_norm, _clip_state(clip),
+    grad_norm_table(len(grads), _grad_table(grads, None), max_norm, clip, workspace)
+
+
+def grad_norm_table(n, table, max_norm, clip, workspace):
+    """gs_grad_norm of n packed gs_grad_tensor descriptors."""
+    rc = (_lib or load_library()).gs_grad_norm(n, table, max_norm, _clip_state(clip),
                                                _p(workspace, torch.uint8, "workspace"), workspace.numel(),
                                                _raw_stream(_current_device()))
     _check(rc, "gs_grad_norm")
@@ -1257,11 +1262,17 @@ class Trainer:
     restarts), and every `reset_interval` iterations every opacity is scaled by
     `reset_factor` (the opacity's moments restart).
 
+    With max_grad_norm the five gradients are clipped to that global norm first: the
+    2D -> 3D backward writes them (gs_preprocess_bwd), and the Adam step takes the
+    clipping coefficient on the device (gs_grad_norm, gs_adam_step_clipped);
+    clip[0] holds the last norm before clipping.
+
     Plumbing only: buffers and the order of the calls.  params: dict of device
     tensors (updated in place between densifications, replaced at them)."""
 
     def __init__(self, cam, params, sh_degree, target, lr, densify=None, densify_interval=100,
-                 reset_interval=3000, reset_factor=OPACITY_RESET_FACTOR, loss="l1", settings=None):
+                 reset_interval=3000, reset_factor=OPACITY_RESET_FACTOR, loss="l1", settings=None,
+                 max_grad_norm=None):
         self.cam, self.deg, self.lr = cam, int(sh_degree), dict(lr)
         self.target, self.loss_mode = target, loss
         self.densify_params = densify
@@ -1270,6 +1281,9 @@ class Trainer:
         self.p = {k: params[k].contiguous() for k in PARAM_ORDER}
         self.m = {k: torch.zeros_like(v) for k, v in self.p.items()}
         self.v = {k: torch.zeros_like(v) for k, v in self.p.items()}
+        self.max_grad_norm = None if max_grad_norm is None else float(max_grad_norm)
+        if self.max_grad_norm is not None and not self.max_grad_norm >= 0:
+            raise GsError("max_grad_norm must be >= 0")
         self.t = 0
         self.events = []  # (iteration, "densify" | "reset", detail)
         self._rebuild()
@@ -1285,6 +1299,10 @@ class Trainer:
         self.count = torch.zeros(self.n, dtype=torch.int32, device=dev)
         self.dL = torch.empty_like(self.target)
         self.loss = torch.zeros(1 + self.rast.ntiles, dtype=torch.float64, device=dev)
+        if self.max_grad_norm is not None:
+            self.clip = torch.zeros(CLIP_STATE_FLOATS, dtype=torch.float32, device=dev)
+            self.clip_workspace = torch.empty(gs_grad_workspace_size(len(PARAM_ORDER)), dtype=torch.uint8, device=dev)
+            self.grads = {k: torch.empty_like(v) for k, v in self.p.items()}
         self._sized = False
 
     def step(self, dL_hook=None, grads=None, after_update=None):
@@ -1308,15 +1326,37 @@ class Trainer:
             dL_hook(self.dL)
         r.backward_2d(self.dL, accumulate=True)
         self.t += 1
-        gs_preprocess_bwd_adam(self.cam, self.settings, self.deg, self.p, r.tiles_touched, r.clamp, r.grad2d, self.m,
-                               self.v, self.lr, self.t, densify_accum=self.accum, densify_count=self.count,
-                               grads=grads)
+        if self.max_grad_norm is None:
+            gs_preprocess_bwd_adam(self.cam, self.settings, self.deg, self.p, r.tiles_touched, r.clamp, r.grad2d,
+                                   self.m, self.v, self.lr, self.t, densify_accum=self.accum,
+                                   densify_count=self.count, grads=grads)
+        else:
+            self._clipped_update(self.grads if grads is None else grads)
         if after_update is not None:
             after_update(self)
         if self.densify_params is not None and self.densify_interval and self.t % self.densify_interval == 0:
             self.densify()
         if self.reset_interval and self.t % self.reset_interval == 0:
             self.reset_opacity()
+
+    def _clipped_update(self, g):
+        """The 2D -> 3D backward into g, the densification statistic, the global norm and the clipped Adam step."""
+        r, p = self.rast, self.p
+        gs_preprocess_bwd(self.cam, self.settings, self.deg, p["means"], p["log_scales"], p["quats"],
+                          p["opacity_logits"], p["sh"], r.tiles_touched, r.clamp, r.grad2d, *[g[k] for k in PARAM_ORDER])
+        gs_densify_accum(self.n, r.tiles_touched, r.grad2d, self.accum, self.count)
+        gs_grad_norm([g[k] for k in PARAM_ORDER], self.max_grad_norm, self.clip, self.clip_workspace)
+        bands = 3 * (self.deg + 1) ** 2
+        groups = [(k, self.lr[k], 0, None) for k in PARAM_ORDER[:4]] + [("sh", self.lr["sh_dc"], 0, 3)]
+        if bands > 3:
+            groups.append(("sh", self.lr["sh_rest"], 3, bands))
+        table = (GsAdamTensor * len(groups))()
+        for a, (k, lr, c0, c1) in zip(table, groups):
+            a.param, a.grad, a.exp_avg, a.exp_avg_sq = (t[k].data_ptr() for t in (p, g, self.m, self.v))
+            a.rows, a.row_len = self.n, p[k].shape[1:].numel()
+            a.col_begin, a.col_end, a.lr = c0, a.row_len if c1 is None else c1, lr
+            a.normalize_rows = 1 if k == "quats" else 0
+        gs_adam_step_clipped(table, 0.9, 0.999, 1e-8, self.t, self.clip)
 
     def densify(self):
         n0 = self.n

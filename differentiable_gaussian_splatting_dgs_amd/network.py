@@ -11,6 +11,9 @@ from __future__ import annotations
 
 import ctypes as C
 
+import ctypes as C
+
+import numpy as np
 import torch
 
 from . import gs
@@ -92,10 +95,12 @@ class GradClip:
         elif self.workspace.numel() < need:
             self.workspace = _workspace(need, grads[0].device)
 
-    def norm(self, grads):
-        """The global norm of the list; the coefficient is left in state[1] for gs_adam_step_clipped."""
+    def norm(self, grads, table=None):
+        """The global norm of the list; the coefficient is left in state[1] for gs_adam_step_clipped.  table: the
+        list's packed descriptors, if the caller has them."""
         self._prepare(grads)
-        gs.gs_grad_norm(grads, self.max_norm, self.state, self.workspace)
+        gs.grad_norm_table(len(grads), gs._grad_table(grads, None) if table is None else table, self.max_norm,
+                           self.state, self.workspace)
         return self.value
 
     def clip(self, grads, out=None):
@@ -145,18 +150,24 @@ class Adam:
             a.rows = p.numel() // max(a.row_len, 1)
             a.col_end = a.row_len
             a.lr = lrs[i]
+        # the two fields that change from step to step
+        size, field = C.sizeof(gs.GsAdamTensor), gs.GsAdamTensor
+        self._grad_words = np.frombuffer(self.table, dtype=np.int64)[field.grad.offset // 8::size // 8][:n]
+        self._dtype_words = np.frombuffer(self.table, dtype=np.int32)[field.grad_dtype.offset // 4::size // 4][:n]
 
     def step(self, grads):
         """One step with gradients grads (float32 or 16-bit, contiguous).  Returns the global norm before clipping
         as a float32 device scalar (None without max_norm)."""
         if len(grads) != len(self.params):
             raise GsError(f"{len(self.params)} parameters, {len(grads)} gradients")
-        for i, g in enumerate(grads):
-            if g.shape != self.params[i].shape or g.dtype not in gs.DTYPES:
-                raise GsError(f"gradient {i} must have its parameter's shape and a floating type")
-            a = self.table[i]
-            a.grad, a.grad_dtype = gs._p(g, None, f"gradient {i}"), gs.DTYPES[g.dtype]
-        norm = self.clipper.norm(grads) if self.clipper is not None else None
+        packed = gs._grad_table(grads, None)
+        for g, p in zip(grads, self.params):
+            if g.shape != p.shape:
+                raise GsError("a gradient must have its parameter's shape")
+        words = np.frombuffer(packed, dtype=np.int64).reshape(-1, 4)  # grad, out, count, dtype
+        self._grad_words[:] = words[:, 0]
+        self._dtype_words[:] = words[:, 3]
+        norm = self.clipper.norm(grads, packed) if self.clipper is not None and grads else None
         self.t += 1
         if self.params:
             gs.gs_adam_step_clipped(self.table, self.betas[0], self.betas[1], self.eps, self.t,
