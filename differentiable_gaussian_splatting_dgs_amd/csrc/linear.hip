@@ -582,8 +582,7 @@ __global__ __launch_bounds__(256) void k_bwd_few(FewArgs p) {
     const T* x = static_cast<const T*>(p.x);
     const T* w = static_cast<const T*>(p.w);
     const int k = (int)blockIdx.y * 256 + threadIdx.x, kc = k < p.n_in ? k : p.n_in - 1;  // -1: no inputs
-    // what the second half needs is on its way during the first
-    float xk[M] = {};
+    float xk[M] = {};  // on its way during the first half
 #pragma unroll
     for (int m = 0; m < M; ++m)
         if (kc >= 0) xk[m] = (float)x[(int64_t)(m < p.rows ? m : p.rows - 1) * p.ld_x + kc];
@@ -596,7 +595,23 @@ __global__ __launch_bounds__(256) void k_bwd_few(FewArgs p) {
             const int n = n0 + out_row<T>(t, r);
             b[t] = w + (int64_t)(n < p.n_out ? n : p.n_out - 1) * p.n_in;
         }
-        for (int s = wave; s * KS < p.n_in; s += 4) {
+        const int whole = p.n_in / KS;
+        int s = wave;
+        for (; s + 12 < whole; s += 16) {  // four steps' loads in flight
+            typename Tile<T>::Frag fa[4], fb[4][TG];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int k0 = (s + 4 * u) * KS + E * g;
+                fa[u] = load16(a + k0);
+#pragma unroll
+                for (int t = 0; t < TG; ++t) fb[u][t] = load16(b[t] + k0);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int t = 0; t < TG; ++t) mma(acc[t], fb[u][t], fa[u]);
+        }
+        for (; s * KS < p.n_in; s += 4) {
             const int k0 = s * KS + E * g;
             const auto a0 = load_frag(a, k0, p.n_in);
 #pragma unroll
@@ -640,7 +655,7 @@ __global__ __launch_bounds__(256) void k_bwd_few(FewArgs p) {
     if (k >= p.n_in) return;
     float dx[M] = {};
     const int last = p.n_out - n0 < KS ? p.n_out - n0 : KS;
-#pragma unroll 4
+#pragma unroll(M > 8 ? 4 : 8)
     for (int n = 0; n < last; ++n) {
         const float wk = p.dx_part ? (float)w[(int64_t)(n0 + n) * p.n_in + k] : 0.f;
         float t = 0.f;

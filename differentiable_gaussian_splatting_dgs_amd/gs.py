@@ -835,7 +835,7 @@ def linear_fwd_into(x, w, bias, residual, y, act):
     rows, n_in, n_out, code, a, device, ld_x = _linear_shape(x, w, act)
     dtype, shape = x.dtype, (rows, n_out)
     if y is None:
-        y, ld_y = torch.empty(shape, dtype=dtype, device=x.device), n_out
+        y, ld_y = x.new_empty(shape), n_out
     else:
         ld_y = _rows(y, shape, dtype, device, "y")
     pr, ld_res = None, 0

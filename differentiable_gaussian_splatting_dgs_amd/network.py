@@ -11,8 +11,6 @@ from __future__ import annotations
 
 import ctypes as C
 
-import ctypes as C
-
 import numpy as np
 import torch
 
@@ -31,7 +29,7 @@ def linear_backward(dy, x, w, bias=None, act="none", need=(True, True, True)):
     """dx, dw, db of y = act(x w^T + bias) from dy = dL/dy (None where need is False; db None without a bias).
     The gradient of a residual added to y is dy itself."""
     need_dx, need_dw, need_db = need
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None
     dw = torch.empty_like(w, memory_format=torch.contiguous_format) if need_dw else None
     db = torch.empty_like(bias, memory_format=torch.contiguous_format) if need_db and bias is not None else None
     gs.linear_bwd_into(x, w, bias, dy, dx, dw, db, None, act)
