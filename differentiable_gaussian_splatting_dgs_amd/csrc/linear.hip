@@ -124,7 +124,7 @@ __global__ __launch_bounds__(256) void k_prod_few(ProdArgs p) {
 // stored as the one contiguous piece of memory that a tile's rows are.
 constexpr int narrow_threads(int sl) { return sl <= 4 ? 1024 : 512; }  // at most: deep rows need 256 registers
 template <typename T, int SL, bool PACK>
-__global__ __launch_bounds__(narrow_threads(SL)) void k_prod_narrow(ProdArgs p) {
+__global__ __launch_bounds__(narrow_threads(SL), sizeof(T) == 4 ? 4 : 1) void k_prod_narrow(ProdArgs p) {
     constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG, P = 2;
     typedef typename Tile<T>::Frag Frag;
     extern __shared__ __align__(16) char s_mem[];
@@ -389,16 +389,25 @@ void product(const ProdArgs& p, hipStream_t s) {
     constexpr int KS = Tile<T>::KS;
     const int groups = (int)cdiv(p.cols, KS), steps = (int)cdiv(p.depth, KS);
     const int64_t tiles16 = cdiv(p.rows, 16);
+    const size_t lds = (size_t)groups * KS * (steps * KS * sizeof(T) + 4);
+    const bool narrow = lds <= 160 * 1024 && steps <= 8;
+    // Few tiles: a call of ordinary length is its launch, until about 2048 blocks of k_prod_few (500 rows 512 -> 512
+    // bfloat16 8.5 us against 11.2 by k_prod_big, 1000 rows 8.9 against 11.8, 2000 rows 13.8 against 11.9; 16000 rows
+    // 128 -> 128 8.5 by k_prod_narrow against 10.3).  In float32 a wave of k_prod_narrow takes 128 cycles for each of a
+    // tile's groups and steps, and until there are tiles for every wave that is what the call lasts (8000 rows
+    // 128 -> 192 14.6 against 25.2, 63 -> 128 9.6 against 10.6; 16000 rows 128 -> 128 18.1 against 18.9, 128 -> 64
+    // 11.8 against 9.4).
+    const bool few = tiles16 * groups <= 2048 || (sizeof(T) == 4 && narrow && groups > 4 && tiles16 <= 640);
     // the streaming kernels read 16 bytes at a time: x and the residual have to span them
     const auto spans = [](int64_t rows, int64_t ld, int32_t count) { return (rows - 1) * ld + count >= Tile<T>::E; };
-    if (tiles16 * groups <= 2048 || p.depth == 0 || !spans(p.rows, p.ld_a, p.depth) ||
-        (p.other && !spans(p.rows, p.ld_other, p.cols))) {
+    if (few || p.depth == 0 || !spans(p.rows, p.ld_a, p.depth) || (p.other && !spans(p.rows, p.ld_other, p.cols))) {
         const int64_t y = tiles16 < 32768 ? tiles16 : 32768;
         hipLaunchKernelGGL((k_prod_few<T>), dim3(groups, (unsigned)y, (unsigned)cdiv(tiles16, y)), dim3(256), 0, s, p);
         return;
     }
-    const size_t lds = (size_t)groups * KS * (steps * KS * sizeof(T) + 4);
-    if (lds <= 160 * 1024) {
+    // 1M rows 128 -> 128 bfloat16 110 us against 167 by k_prod_big, 256 -> 192 204 against 343, 64 -> 64 float16 52
+    // against 94; 100k rows 63 -> 128 float32 29 against 38
+    if (narrow) {
         switch (steps) {
             case 1: launch_narrow<T, 1>(p, lds, s); return;
             case 2: launch_narrow<T, 2>(p, lds, s); return;
