@@ -397,7 +397,11 @@ void product(const ProdArgs& p, hipStream_t s) {
     // tile's groups and steps, and until there are tiles for every wave that is what the call lasts (8000 rows
     // 128 -> 192 14.6 against 25.2, 63 -> 128 9.6 against 10.6; 16000 rows 128 -> 128 18.1 against 18.9, 128 -> 64
     // 11.8 against 9.4).
-    const bool few = tiles16 * groups <= 2048 || (sizeof(T) == 4 && narrow && groups > 4 && tiles16 <= 640);
+    // Deep float32 rows of one or two groups: k_prod_big's 128 outputs would mostly be multiplied for nothing (150k
+    // rows 417 -> 3 65 us against 174, 417 -> 32 156 against 174, 417 -> 48 224 against 175; bfloat16, whose products
+    // are short, 417 -> 3 56 against 52, 417 -> 32 105 against 60).
+    const bool few = tiles16 * groups <= 2048 || (sizeof(T) == 4 && narrow && groups > 4 && tiles16 <= 640) ||
+                     (sizeof(T) == 4 && !narrow && groups <= 2);
     // the streaming kernels read 16 bytes at a time: x and the residual have to span them
     const auto spans = [](int64_t rows, int64_t ld, int32_t count) { return (rows - 1) * ld + count >= Tile<T>::E; };
     if (few || p.depth == 0 || !spans(p.rows, p.ld_a, p.depth) || (p.other && !spans(p.rows, p.ld_other, p.cols))) {
