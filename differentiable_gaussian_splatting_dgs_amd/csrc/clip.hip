@@ -87,6 +87,9 @@ __device__ __forceinline__ double block_sum(double acc) {
     return (s_part[0] + s_part[1]) + (s_part[2] + s_part[3]);
 }
 
+// Squares and sums in 64 bits: no magnitude of a gradient overflows them, and the
+// arithmetic stays under the loads.  59M float32 43 to 46 us, 5.1 to 5.5 TB/s; 16 tensors of 64 or 4096
+// bfloat16 4.7 us.
 __global__ __launch_bounds__(kThreads) void k_norm(GradArgs a, double* partial) {
     double acc = 0.0;
     const int64_t chunks = a.first_chunk[a.n];
@@ -152,6 +155,7 @@ __device__ __forceinline__ void chunk_scale(const T* g, T* out, int64_t count, i
 
 // back: chunks from the last to the first, which the norm has left in the last-level
 // cache when all of them do not fit (177M float32: 363 against 395 us; 5.9M: 22 against 19).
+// 59M float32 72 us, 6.6 TB/s, since part of the reads are hits there.
 __global__ __launch_bounds__(kThreads) void k_scale(GradArgs a, const double* partial, int parts, float max_norm,
                                                     float* clip, bool write, bool back) {
     const float c0 = coefficient(partial, parts, max_norm, clip, write && blockIdx.x == 0);

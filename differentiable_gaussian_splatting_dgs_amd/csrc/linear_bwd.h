@@ -10,6 +10,13 @@
 // each block leaves one partial dw and db for the join.  A layer with few inputs and
 // more outputs than a block holds goes through in parts of the outputs (PARTS): dy is
 // still read once, and dx adds up in float32 from part to part.
+//
+// 1M rows 128 -> 128 float16 silu: 200 us and 13 for the join, where 770 MB take 147 at
+// the rate of a copy, the matrix units are busy for 49 and the slope's arithmetic for
+// some 90; two waves a SIMD (the weights and the tile fill LDS, dw the registers)
+// overlap them only in part.  One block of eight waves 280 us against 257
+// for two of four; each group's z before its own slope 255 against 209 for all z first.
+// 100k rows 64 -> 64 float32 gelu: 42 us, of which 20 are float32 matrix instructions.
 #pragma once
 
 #include "linear_tile.h"
