@@ -189,6 +189,23 @@ def test_many_rows(size, dtype):
             check(g, v, tol, (size, name))
 
 
+@pytest.mark.parametrize("size", [(10240, 63, 81), (10241, 63, 81), (33000, 200, 3), (33000, 129, 17), (33000, 129, 33)])
+def test_float32_routes(size):
+    """Either side of the sizes at which float32 layers change kernels: 640 tiles of rows, deep rows of two groups."""
+    x, w, b, r, dy = inputs(*size, torch.float32, pad=3)
+    _, y, tol, _ = exact_fwd(x, w, b, r, "silu")
+    check(run_fwd(x, w, b, r, "silu"), y, tol, size)
+    for name, g, (v, t) in zip(("dx", "dw", "db"), run_bwd(dy, x, w, b, "silu"), exact_bwd(x, w, b, dy, "silu")):
+        check(g, v, t, (size, name))
+
+
+def test_deep_rows_past_a_grid_dimension():
+    """Deep rows of few outputs, more tiles of rows than one dimension of the grid takes (32768)."""
+    x, w, b, _, _ = inputs(32768 * 16 + 37, 129, 3, torch.float32, residual=False)
+    _, y, tol, _ = exact_fwd(x, w, b, None, "relu")
+    check(run_fwd(x, w, b, None, "relu"), y, tol, "rows")
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("pad,lead", [(1, 0), (8, 8), (13, 3), (64, 1)])
 def test_strided_and_unaligned(dtype, pad, lead):
