@@ -259,58 +259,58 @@ __global__ __launch_bounds__(narrow_threads(SL), sizeof(T) == 4 ? 4 : 1) void k_
 // 16-bit time; the rest is the barrier of each stage, at two blocks a CU.  256 x 128
 // outputs over eight waves take as long (72 us against 74, 213 against 218).
 constexpr int kBig = 128;  // rows and outputs of a block
-template <typename T>
+template <typename T, int NT>  // NT: tiles of 16 outputs a wave has, 4 (128 outputs a block) or 2 (64)
 __global__ __launch_bounds__(256, 2) void k_prod_big(ProdArgs p) {
     constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG;
     typedef typename Tile<T>::Frag Frag;
-    __shared__ Frag s_a[2][kBig * 8], s_b[2][kBig * 8];
+    __shared__ Frag s_a[2][kBig * 8], s_b[2][32 * NT * 8];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
+    const int wm = (wave & 1) * 64, wn = (wave >> 1) * 16 * NT;
     // blocks of one XCD take neighbouring tiles, outputs first: they share rows of a
-    const int64_t tn = (p.cols + kBig - 1) / kBig, total = (int64_t)gridDim.x, per = (total + 7) / 8;
+    const int64_t tn = (p.cols + 32 * NT - 1) / (32 * NT), total = (int64_t)gridDim.x, per = (total + 7) / 8;
     const int64_t id = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
     const int64_t tiles = tn * ((p.rows + kBig - 1) / kBig);
     if (id >= tiles) return;
     const int64_t m0 = id / tn * kBig;
-    const int n0 = (int)(id % tn) * kBig;
+    const int n0 = (int)(id % tn) * 32 * NT;
     // staging: thread i brings chunk i % 8 of rows i / 8, + 32, + 64, + 96; the weights' rows in the order
     // that interleaves a group's tiles
     const int ch = threadIdx.x & 7, sr = threadIdx.x >> 3;
     const Matrix<T> ma(p.a, p.rows, p.ld_a, p.depth), mb(p.b, p.cols, p.ld_b, p.depth);
     int64_t row_a[4];
-    int row_b[4];
-    Frag ra[2][4], rb[2][4];
+    int row_b[NT];
+    Frag ra[2][4], rb[2][NT];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int pos = sr + 32 * i, n = n0 + pos / KS * KS + out_row<T>(pos % KS / 16, pos % 16);
         row_a[i] = min(m0 + pos, p.rows - 1);
-        row_b[i] = n < p.cols ? n : p.cols - 1;
+        if (i < NT) row_b[i] = n < p.cols ? n : p.cols - 1;
     }
     const int steps = (p.depth + 2 * KS - 1) / (2 * KS);
-    auto fetch = [&](int s, Frag (&a)[4], Frag (&b)[4]) {  // past the end: the matrices' last bytes, not used
+    auto fetch = [&](int s, Frag (&a)[4], Frag (&b)[NT]) {  // past the end: the matrices' last bytes, not used
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             a[i] = ma.raw(row_a[i], s * 2 * KS + E * ch);
-            b[i] = mb.raw(row_b[i], s * 2 * KS + E * ch);
+            if (i < NT) b[i] = mb.raw(row_b[i], s * 2 * KS + E * ch);
         }
     };
-    auto put = [&](int s, int buf, Frag (&a)[4], Frag (&b)[4]) {
+    auto put = [&](int s, int buf, Frag (&a)[4], Frag (&b)[NT]) {
         if ((s + 1) * 2 * KS > p.depth) {
             const int k0 = s * 2 * KS + E * ch;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 a[i] = ma.fixed(a[i], row_a[i], k0, true);
-                b[i] = mb.fixed(b[i], row_b[i], k0, true);
+                if (i < NT) b[i] = mb.fixed(b[i], row_b[i], k0, true);
             }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int pos = sr + 32 * i, at = pos * 8 + (ch ^ (pos & 7));
             s_a[buf][at] = a[i];
-            s_b[buf][at] = b[i];
+            if (i < NT) s_b[buf][at] = b[i];
         }
     };
-    f32x4 acc[4][4] = {};  // [m tile][n tile]
+    f32x4 acc[4][NT] = {};  // [m tile][n tile]
     if (steps > 0) {
         fetch(0, ra[0], rb[0]);
         fetch(1, ra[1], rb[1]);
@@ -320,11 +320,11 @@ __global__ __launch_bounds__(256, 2) void k_prod_big(ProdArgs p) {
     // 16-bit: the residual or dy is on its way during the products (the backward of 65536 rows 512 -> 512 bfloat16
     // 195 us against 205 with it fetched after them); in float32 there are twice the registers of it (920 against 905)
     const Matrix<T> mo(p.other, p.rows, p.ld_other, p.cols);
-    Frag others[4 / TG][4];
+    Frag others[NT / TG][4];
     auto fetch_others = [&]() {
         if (!p.other) return;
 #pragma unroll
-        for (int q = 0; q < 4 / TG; ++q)
+        for (int q = 0; q < NT / TG; ++q)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 others[q][i] = mo.raw(min(m0 + wm + 16 * i + r, p.rows - 1), n0 + wn + q * KS + E * g);
@@ -338,26 +338,26 @@ __global__ __launch_bounds__(256, 2) void k_prod_big(ProdArgs p) {
             fetch(s + 2, ra[u], rb[u]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                Frag fa[4], fb[4];
+                Frag fa[4], fb[NT];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int am = wm + 16 * i + r, bn = wn + 16 * i + r;
                     fa[i] = s_a[u][am * 8 + ((4 * h + g) ^ (am & 7))];
-                    fb[i] = s_b[u][bn * 8 + ((4 * h + g) ^ (bn & 7))];
+                    if (i < NT) fb[i] = s_b[u][bn * 8 + ((4 * h + g) ^ (bn & 7))];
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) mma(acc[i][j], fb[j], fa[i]);
+                    for (int j = 0; j < NT; ++j) mma(acc[i][j], fb[j], fa[i]);
             }
             if (s + 1 < steps) put(s + 1, u ^ 1, ra[u ^ 1], rb[u ^ 1]);
             __syncthreads();
         }
     }
     if (sizeof(T) == 4) fetch_others();
-    const bool even = n0 + kBig <= p.cols;
+    const bool even = n0 + 32 * NT <= p.cols;
 #pragma unroll
-    for (int q = 0; q < 4 / TG; ++q) {  // groups of KS outputs
+    for (int q = 0; q < NT / TG; ++q) {  // groups of KS outputs
         const int c0 = n0 + wn + q * KS + E * g;
         Frag(&other)[4] = others[q];
         float bias[E] = {};
@@ -414,11 +414,11 @@ void product(const ProdArgs& p, hipStream_t s) {
     // tile's groups and steps, and until there are tiles for every wave that is what the call lasts (8000 rows
     // 128 -> 192 14.6 against 25.2, 63 -> 128 9.6 against 10.6; 16000 rows 128 -> 128 18.1 against 18.9, 128 -> 64
     // 11.8 against 9.4).
-    // Deep float32 rows of one or two groups: k_prod_big's 128 outputs would mostly be multiplied for nothing (150k
-    // rows 417 -> 3 65 us against 174, 417 -> 32 156 against 174, 417 -> 48 224 against 175; bfloat16, whose products
-    // are short, 417 -> 3 56 against 52, 417 -> 32 105 against 60).
+    // Deep float32 rows of one group: k_prod_big's outputs would mostly be multiplied for nothing (150k rows 417 -> 3
+    // 65 us against 95, 417 -> 16 93 against 95, 417 -> 32 156 against 96; bfloat16, whose products are short,
+    // 417 -> 3 56 against 52, 417 -> 32 105 against 60).
     const bool few = tiles16 * groups <= 2048 || (sizeof(T) == 4 && narrow && groups > 4 && tiles16 <= 640) ||
-                     (sizeof(T) == 4 && !narrow && groups <= 2);
+                     (sizeof(T) == 4 && !narrow && groups == 1);
     // the streaming kernels read 16 bytes at a time: x and the residual have to span them
     const auto spans = [](int64_t rows, int64_t ld, int32_t count) { return (rows - 1) * ld + count >= Tile<T>::E; };
     if (few || p.depth == 0 || !spans(p.rows, p.ld_a, p.depth) || (p.other && !spans(p.rows, p.ld_other, p.cols))) {
@@ -440,8 +440,16 @@ void product(const ProdArgs& p, hipStream_t s) {
             case 8: launch_narrow<T, 8>(p, lds, s); return;
         }
     }
+    if constexpr (sizeof(T) == 4) {
+        // 150k rows 417 -> 64 106 us against 180 with 128 outputs a block, 150 -> 40 47 against 84
+        if (p.cols <= 64) {
+            const int64_t tiles = cdiv(p.rows, kBig);
+            hipLaunchKernelGGL((k_prod_big<T, 2>), dim3((unsigned)(cdiv(tiles, 8) * 8)), dim3(256), 0, s, p);
+            return;
+        }
+    }
     const int64_t tiles = cdiv(p.cols, kBig) * cdiv(p.rows, kBig);
-    hipLaunchKernelGGL((k_prod_big<T>), dim3((unsigned)(cdiv(tiles, 8) * 8)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((k_prod_big<T, 4>), dim3((unsigned)(cdiv(tiles, 8) * 8)), dim3(256), 0, s, p);
 }
 
 struct DwArgs {
@@ -456,14 +464,17 @@ struct DwArgs {
 // One split of the rows for a 128 x 128 tile of dw: 64 x 64 per wave, the next
 // stage's rows on their way while this one's are multiplied.  The blocks of the
 // first column of tiles add up dz's columns as they pass.  65536 rows 512 -> 512 bfloat16
-// 56 us, 610 TFLOP/s: the stages' barriers bound it, as in k_prod_big.
-template <typename T>
+// 56 us, 610 TFLOP/s: the stages' barriers bound it, as in k_prod_big.  Float32 layers of
+// few outputs have narrower tiles, or the products of nothing would bound them: dx, dw
+// and db of 150k rows 162 -> 9 104 us against 157 with 128 outputs, 417 -> 64 304
+// against 362.
+template <typename T, int NT>  // NT: tiles of 16 outputs a wave has; 1 or 2: a float32 layer of at most 32 or 64
 __global__ __launch_bounds__(256, 2) void k_dw(DwArgs p) {
     constexpr int E = Tile<T>::E, KS = Tile<T>::KS;
     typedef typename Tile<T>::Frag Frag;
     __shared__ __align__(16) char s_dz[2][16384], s_x[2][16384];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    const int wn = (wave & 1) * 64, wk = (wave >> 1) * 64;
+    const int wn = (wave & 1) * 16 * NT, wk = (wave >> 1) * 64;
     // the tiles of one split run on one XCD, whose L2 then serves the rows that they share
     const int tn = (p.n_out + 127) / 128, tiles = tn * ((p.n_in + 127) / 128);
     const int64_t id = (int64_t)(blockIdx.x & 7) * ((gridDim.x + 7) / 8) + (blockIdx.x >> 3);
@@ -513,7 +524,7 @@ __global__ __launch_bounds__(256, 2) void k_dw(DwArgs p) {
                 for (int j = 0; j < E; ++j) sum[j] += (float)z[i][j];
         }
     };
-    f32x4 acc[4][4] = {};  // [n tile][k tile]
+    f32x4 acc[NT][4] = {};  // [n tile][k tile]
     if (m_begin < m_end) {
         fetch(m_begin, rz[0], rx[0]);
         fetch(m_begin + kRows, rz[1], rx[1]);
@@ -528,14 +539,14 @@ __global__ __launch_bounds__(256, 2) void k_dw(DwArgs p) {
             fetch(m0 + 2 * kRows, rz[u], rx[u]);
 #pragma unroll
             for (int h = 0; h < kRows / KS; ++h) {
-                Frag fz[4], fx[4];
+                Frag fz[NT], fx[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    fz[i] = column_frag<T, 128>(s_dz[u], h * KS, wn + 16 * i, lane);
+                    if (i < NT) fz[i] = column_frag<T, 128>(s_dz[u], h * KS, wn + 16 * i, lane);
                     fx[i] = column_frag<T, 128>(s_x[u], h * KS, wk + 16 * i, lane);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < NT; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) mma(acc[i][j], fz[i], fx[j]);
             }
@@ -547,7 +558,7 @@ __global__ __launch_bounds__(256, 2) void k_dw(DwArgs p) {
     float* part = p.part + split * (n_w + (p.want_db ? p.n_out : 0));
     if (p.want_dw) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int n = n0 + wn + 16 * i + 4 * g + q;
@@ -914,7 +925,17 @@ void bwd(const gs_linear* d, const void* x, const void* w, const void* bias, con
              want_dw ? d->n_in : 1, want_dw, want_db,
              plan.splits};
     const int64_t blocks = cdiv(q.n_out, 128) * cdiv(q.n_in, 128) * plan.splits;
-    hipLaunchKernelGGL((k_dw<T>), dim3((unsigned)(cdiv(blocks, 8) * 8)), dim3(256), 0, s, q);
+    const dim3 grid((unsigned)(cdiv(blocks, 8) * 8));
+    if constexpr (sizeof(T) == 4) {
+        if (q.n_out <= 32)
+            hipLaunchKernelGGL((k_dw<T, 1>), grid, dim3(256), 0, s, q);
+        else if (q.n_out <= 64)
+            hipLaunchKernelGGL((k_dw<T, 2>), grid, dim3(256), 0, s, q);
+        else
+            hipLaunchKernelGGL((k_dw<T, 4>), grid, dim3(256), 0, s, q);
+    } else {
+        hipLaunchKernelGGL((k_dw<T, 4>), grid, dim3(256), 0, s, q);
+    }
     join<T>(sums, s);
 }
 

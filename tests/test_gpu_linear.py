@@ -199,6 +199,17 @@ def test_float32_routes(size):
         check(g, v, t, (size, name))
 
 
+@pytest.mark.parametrize("act", ["none", "gelu"])
+@pytest.mark.parametrize("size", [(4100, 300, 32), (4100, 300, 33), (4100, 140, 64), (4100, 140, 65), (3000, 70, 1)])
+def test_float32_tile_widths(size, act):
+    """The float32 layers either side of 32 and 64 outputs, rows that end inside a stage, strided buffers."""
+    x, w, b, r, dy = inputs(*size, torch.float32, pad=5, lead=1)
+    _, y, tol, _ = exact_fwd(x, w, b, r, act)
+    check(run_fwd(x, w, b, r, act), y, tol, size)
+    for name, g, (v, t) in zip(("dx", "dw", "db"), run_bwd(dy, x, w, b, act), exact_bwd(x, w, b, dy, act)):
+        check(g, v, t, (size, name))
+
+
 def test_deep_rows_past_a_grid_dimension():
     """Deep rows of few outputs, more tiles of rows than one dimension of the grid takes (32768)."""
     x, w, b, _, _ = inputs(32768 * 16 + 37, 129, 3, torch.float32, residual=False)
