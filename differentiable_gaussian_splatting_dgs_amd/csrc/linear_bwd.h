@@ -41,6 +41,8 @@ struct BwdArgs {
     int32_t first, last;
 };
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 constexpr int kBwdGroups = 4;  // groups of KS inputs and of KS outputs at most
 // Inputs of a layer that goes through in parts of its outputs, at most.
 template <typename T>
@@ -54,7 +56,7 @@ struct BwdGeom {
     static constexpr int kRows = 16 * kWaves;
     static constexpr int kW = KP * NP * (int)sizeof(T);
     static constexpr int kTiles = kRows * (KP + NP) * (int)sizeof(T);
-    static constexpr int kLds = kW + kTiles + NP * 4;
+    static constexpr int kLds = kW + kTiles + NP * 4 + NG * 64;
     // blocks per CU: three where the LDS and 168 registers hold them, else two; the grid counts on it
     static constexpr bool kManyRegs = sizeof(T) == 2 ? 30 + 40 * NG + 18 * SL > 168 : NG == kBwdGroups;  // by the builds
     static constexpr int kPerCu = kLds > 53 * 1024 || kManyRegs ? 2 : 3;
@@ -108,6 +110,7 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), (BwdGeom<T, SL, 
     char* s_dz = s_mem + G::kW;
     char* s_x = s_dz + G::kRows * G::NP * (int)sizeof(T);
     float* s_bias = reinterpret_cast<float*>(s_x + G::kRows * G::KP * (int)sizeof(T));
+    u32x4* s_live = reinterpret_cast<u32x4*>(s_bias + G::NP);  // [NG][4]: the bits of a fragment that are outputs
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tn0 = wave / G::WK * G::TN, tk0 = wave % G::WK * G::TK;
@@ -159,6 +162,15 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), (BwdGeom<T, SL, 
     }
     for (int i = threadIdx.x; i < G::NP; i += blockDim.x)
         s_bias[i] = p.bias && i < p.n_out ? (float)static_cast<const T*>(p.bias)[i] : 0.f;
+    if (threadIdx.x < NG * 4) {
+        u32x4 live;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int left = (p.n_out - (int)threadIdx.x * E) * (int)sizeof(T) - 4 * q;  // bytes
+            live[q] = left >= 4 ? 0xffffffffu : left == 2 ? 0xffffu : 0u;
+        }
+        s_live[threadIdx.x] = live;
+    }
     __syncthreads();
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const int64_t row = tile * G::kRows + wave * 16 + r;
@@ -215,6 +227,20 @@ __global__ __launch_bounds__((BwdGeom<T, SL, NG>::kWaves * 64), (BwdGeom<T, SL, 
         for (int j = 0; j < NG * E; ++j) {
             db[j] += v[j];
             dz[j / E][j % E] = (T)v[j];
+        }
+        // Past the outputs z is 0 times x, so NaN where x is infinite, and dz with it.  Masks from LDS: 1M rows 128 -> 113
+        // float16 279 us; 297 with them in registers, which then spill, and 300 with a comparison for each element.
+        if (p.n_out < G::NP) {
+#pragma unroll
+            for (int n = PARTS ? 0 : NG - 1; n < NG; ++n) {
+                union {
+                    Frag f;
+                    u32x4 q;
+                } u;
+                u.f = dz[n];
+                u.q &= s_live[n * 4 + g];
+                dz[n] = u.f;
+            }
         }
 #pragma unroll
         for (int n = 0; n < NG; ++n) *reinterpret_cast<Frag*>(s_dz + row_chunk<T, G::NP>(m, n * 4 + g)) = dz[n];

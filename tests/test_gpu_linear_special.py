@@ -1,0 +1,51 @@
+"""Infinite and NaN values through the linear layer's backward, by every kernel that a size can take."""
+import pytest
+import torch
+
+from test_gpu_linear import TINY, TYPES, U, U32, inputs, run_bwd
+
+pytestmark = pytest.mark.gpu
+
+# few rows; one pass with outputs that fill the kernel's groups, that do not, and in parts; separate products
+SIZES = [(9, 64, 59), (150, 64, 64), (150, 64, 59), (150, 30, 5), (150, 128, 97), (300, 300, 59), (65_601, 14, 300),
+         (65_601, 14, 257)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("act", ["relu", "gelu"])
+@pytest.mark.parametrize("size", SIZES)
+def test_infinite_input_has_finite_gradients(size, act, dtype):
+    """One infinite x: z is infinite in that row with the signs of w's column, the slope is 1 or 0 there, and dx of
+    that row and db are sums of finite terms.
+
+    Bounds: dz is dy or 0, exactly.  A sum of n float32 products is within (n + 3) u32 of its terms' magnitudes, and
+    is rounded once.  db's other rows are left out of the comparison by a dy of 0."""
+    x, w, b, _, dy = inputs(*size, dtype)
+    row = size[0] - 2
+    x[row, 0] = float("inf")
+    keep = dy[row].clone()
+    dy.zero_()
+    dy[row] = keep
+    dx, _, db = run_bwd(dy, x, w, b, act)
+    wd = w.cpu().double()
+    dz = keep.cpu().double() * (wd[:, 0] > 0)
+    for name, got, want, terms in (("dx", dx[row], dz @ wd, dz.abs() @ wd.abs()), ("db", db, dz, dz.abs())):
+        got = got.cpu().double()
+        tol = (size[2] + 3) * U32 * terms + U[dtype] * want.abs() + TINY[dtype]
+        bad = ~((got - want).abs() <= tol)
+        assert not bad.any(), (size, name, int(bad.sum()), got[bad][:4])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("size", SIZES)
+def test_nan_input_reaches_its_row(size, dtype):
+    """A NaN in one row of x makes that row of dx NaN and leaves the others' bits alone."""
+    x, w, b, _, dy = inputs(*size, dtype)
+    clean = run_bwd(dy, x, w, b, "relu")[0]
+    row = size[0] - 2
+    x[row, 0] = float("nan")
+    dx = run_bwd(dy, x, w, b, "relu")[0]
+    assert torch.isnan(dx[row]).all()
+    others = torch.ones(size[0], dtype=torch.bool, device="cuda")
+    others[row] = False
+    assert torch.equal(dx[others], clean[others])
