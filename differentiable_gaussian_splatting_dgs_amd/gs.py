@@ -1123,6 +1123,27 @@ class Rasterizer:
         return (c, ev) if per_pixel else c
 
 
+class OnceFunction(torch.autograd.Function):
+    """Hands a gradient on, and raises when it is differentiated itself."""
+
+    @staticmethod
+    def forward(ctx, name, grad, *inputs):
+        ctx.name = name
+        return grad.detach()
+
+    @staticmethod
+    def backward(ctx, _):
+        raise GsError(f"{ctx.name} can be differentiated once: its gradients have no derivatives")
+
+
+def differentiated_once(name, grads, inputs):
+    """grads of a backward that the kernels made, for the autograd graph.  Under create_graph they hang on inputs, the
+    tensors that they depend on, by a node that raises: without it they would be constants in a second derivative."""
+    if not torch.is_grad_enabled():
+        return grads
+    return tuple(g if g is None else OnceFunction.apply(name, g, *inputs) for g in grads)
+
+
 class RasterizeFunction(torch.autograd.Function):
     """image = rasterize(means, log_scales, quats, opacity_logits, sh) for one Rasterizer.
 

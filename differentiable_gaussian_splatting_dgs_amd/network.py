@@ -49,7 +49,8 @@ class LinearFunction(torch.autograd.Function):
         need = ctx.needs_input_grad
         dx = dw = db = None
         if any(need[:3]):
-            dx, dw, db = linear_backward(_plain_rows(dy), x, w, bias, ctx.act, need[:3])
+            grads = linear_backward(_plain_rows(dy), x, w, bias, ctx.act, need[:3])
+            dx, dw, db = gs.differentiated_once("network.linear", grads, (dy, x, w, bias))
         return dx, dw, db, dy if need[3] else None, None
 
 
@@ -60,7 +61,8 @@ def _plain_rows(t):
 
 
 def linear(x, w, bias=None, residual=None, act="none"):
-    """act(x w^T + bias) + residual, differentiable in all four tensors.
+    """act(x w^T + bias) + residual, differentiable in all four tensors, once: a second derivative (a penalty on a
+    gradient) raises GsError, but for the residual's.
 
     x [rows, n_in], w [n_out, n_in], bias [n_out], residual [rows, n_out], all of one type (float32, float16 or
     bfloat16); x and residual may have strided rows.  act: "none", "relu", "silu" or "gelu" (tanh form)."""

@@ -49,3 +49,16 @@ def test_nan_input_reaches_its_row(size, dtype):
     others = torch.ones(size[0], dtype=torch.bool, device="cuda")
     others[row] = False
     assert torch.equal(dx[others], clean[others])
+
+
+def test_second_derivative_raises():
+    from differentiable_gaussian_splatting_dgs_amd import gs, network
+    x, w, b, r, _ = inputs(40, 24, 20, torch.float32)
+    x.requires_grad_()
+    w.requires_grad_()
+    y = network.linear(x, w, b, r, act="silu").sum()
+    print("second derivative", flush=True)
+    g, = torch.autograd.grad(y, x, create_graph=True)
+    assert torch.equal(g, torch.autograd.grad(network.linear(x, w, b, r, act="silu").sum(), x)[0])
+    with pytest.raises(gs.GsError, match="differentiated once"):
+        (y + g.square().sum()).backward()
