@@ -1150,7 +1150,8 @@ class RasterizeFunction(torch.autograd.Function):
     The backward reuses the forward's intermediates (lists, ranges, final_T,
     n_contrib, flags), which the Rasterizer keeps in its own buffers: one
     backward per forward, before the Rasterizer renders again.  A backward after
-    a newer forward on the same Rasterizer raises GsError."""
+    a newer forward on the same Rasterizer raises GsError, and so does a second
+    derivative."""
 
     @staticmethod
     def forward(ctx, rast, means, log_scales, quats, opacity_logits, sh):
@@ -1170,11 +1171,12 @@ class RasterizeFunction(torch.autograd.Function):
         m, s, q, o, c = ctx.saved_tensors
         p = dict(means=m, log_scales=s, quats=q, opacity_logits=o, sh=c)
         g = ctx.rast.backward(p, dL_dimage.contiguous())
-        return None, g["means"], g["log_scales"], g["quats"], g["opacity_logits"], g["sh"]
+        return None, *differentiated_once("rasterize", [g[k] for k in PARAM_ORDER], (dL_dimage, m, s, q, o, c))
 
 
 def rasterize(rast, means, log_scales, quats, opacity_logits, sh):
-    return RasterizeFunction.apply(rast, means, log_scales, quats, opacity_logits, sh)
+    # contiguous out here: a copy that the function makes has no place in the graph
+    return RasterizeFunction.apply(rast, *(t.contiguous() for t in (means, log_scales, quats, opacity_logits, sh)))
 
 
 class RasterizerViews:
