@@ -13,6 +13,7 @@ import ctypes as C
 
 import numpy as np
 import torch
+from torch.autograd import forward_ad
 
 from . import gs
 from .gs import GsError
@@ -62,12 +63,14 @@ def _plain_rows(t):
 
 def linear(x, w, bias=None, residual=None, act="none"):
     """act(x w^T + bias) + residual, differentiable in all four tensors, once: a second derivative (a penalty on a
-    gradient) raises GsError, but for the residual's.
+    gradient) raises GsError, but for the residual's.  Forward mode raises NotImplementedError.
 
     x [rows, n_in], w [n_out, n_in], bias [n_out], residual [rows, n_out], all of one type (float32, float16 or
     bfloat16); x and residual may have strided rows.  act: "none", "relu", "silu" or "gelu" (tanh form)."""
-    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad) or
-                                    (residual is not None and residual.requires_grad)):
+    # under forward mode a tensor with a tangent need not require a gradient: the function raises for it
+    if forward_ad._current_level >= 0 or torch.is_grad_enabled() and (
+            x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad) or
+            (residual is not None and residual.requires_grad)):
         return LinearFunction.apply(x, w, bias, residual, act)
     return gs.linear_fwd_into(x, w, bias, residual, None, act)
 

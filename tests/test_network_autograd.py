@@ -68,3 +68,16 @@ def test_second_derivative_of_the_residual():
     g, = torch.autograd.grad(network.linear(x, w, b, r).pow(3).sum(), r, create_graph=True)
     gg, = torch.autograd.grad(g.sum(), r)
     torch.testing.assert_close(gg, 6 * (formula(x, w, b, "none") + r))
+
+
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("which", range(4))
+def test_forward_mode_raises(which, grad):
+    """A tangent that the layer would drop raises; within a dual level a call without tangents is served."""
+    t = [v.detach() for v in leaves()]
+    with torch.autograd.forward_ad.dual_level(), torch.set_grad_enabled(grad):
+        y = network.linear(*t, act="silu")
+        assert torch.equal(y, formula(*t[:3], "silu") + t[3])
+        t[which] = torch.autograd.forward_ad.make_dual(t[which], torch.ones_like(t[which]))
+        with pytest.raises(NotImplementedError):
+            network.linear(*t, act="silu")
