@@ -120,8 +120,10 @@ class Adam:
     params: float32 device tensors, updated in place.  lr: one rate, or one for each parameter.  copies: for each
     parameter None or a 16-bit tensor of its shape that receives the updated values (the tensor a 16-bit network
     computes with).  normalize_rows: indices of parameters whose rows are renormalised to unit length after the
-    update (quaternions).  exp_avg, exp_avg_sq: the moments, zeros by default.  A step whose norm is not finite
-    changes nothing on the device; it still counts in `t`."""
+    update (quaternions).  exp_avg, exp_avg_sq: the moments, zeros by default.  A step takes what the lists params,
+    exp_avg, exp_avg_sq and copies hold at that time: their entries and the entries' data may be replaced (moments
+    restored, `p.data = ...`).  A step whose norm is not finite changes nothing on the device; it still counts in
+    `t`."""
 
     def __init__(self, params, lr, betas=(0.9, 0.999), eps=1e-8, max_norm=None, copies=None, normalize_rows=(),
                  exp_avg=None, exp_avg_sq=None):
@@ -135,28 +137,53 @@ class Adam:
             raise GsError("lr, copies and the moments need one entry for each parameter")
         self.betas, self.eps, self.t = (float(betas[0]), float(betas[1])), float(eps), 0
         self.clipper = None if max_norm is None else GradClip(max_norm)
+        self.normalize_rows = frozenset(normalize_rows)
         self.table = (gs.GsAdamTensor * max(n, 1))()
-        for i, p in enumerate(self.params):
-            a = self.table[i]
-            a.param = gs._p(p, torch.float32, f"parameter {i}")
-            for t, k in ((self.exp_avg[i], "exp_avg"), (self.exp_avg_sq[i], "exp_avg_sq")):
-                if t.shape != p.shape:
-                    raise GsError(f"{k} {i} must have its parameter's shape")
-                setattr(a, k, gs._p(t, torch.float32, f"{k} {i}"))
-            if self.copies[i] is not None:
-                if self.copies[i].shape != p.shape or self.copies[i].dtype not in gs.DTYPES:
-                    raise GsError(f"copy {i} must have its parameter's shape and a floating type")
-                a.copy = gs._p(self.copies[i], None, f"copy {i}")
-                a.copy_dtype = gs.DTYPES[self.copies[i].dtype]
-            a.normalize_rows = 1 if i in normalize_rows else 0
-            a.row_len = p.shape[-1] if a.normalize_rows else 1
-            a.rows = p.numel() // max(a.row_len, 1)
-            a.col_end = a.row_len
-            a.lr = lrs[i]
+        for a, v in zip(self.table, lrs):
+            a.lr = v
         # the two fields that change from step to step
         size, field = C.sizeof(gs.GsAdamTensor), gs.GsAdamTensor
         self._grad_words = np.frombuffer(self.table, dtype=np.int64)[field.grad.offset // 8::size // 8][:n]
         self._dtype_words = np.frombuffer(self.table, dtype=np.int32)[field.grad_dtype.offset // 4::size // 4][:n]
+        self._describe()
+
+    def _pointers(self):
+        at = torch.Tensor.data_ptr
+        try:
+            return [*map(at, self.params), *map(at, self.exp_avg), *map(at, self.exp_avg_sq),
+                    *[0 if c is None else at(c) for c in self.copies]]
+        except TypeError:
+            raise GsError("parameters, moments and copies must be tensors") from None
+
+    def _describe(self):
+        """Checks parameters, moments and copies and writes their places and sizes into the table.  The detached
+        tensors hold the memory that the table names for as long as it does: a tensor at the same address in a later
+        step is in that memory."""
+        n = len(self.params)
+        if not len(self.exp_avg) == len(self.exp_avg_sq) == len(self.copies) == n == len(self._dtype_words):
+            raise GsError("copies and the moments need one entry for each parameter")
+        described, rows = self._pointers(), []
+        for i, (p, m, v, c) in enumerate(zip(self.params, self.exp_avg, self.exp_avg_sq, self.copies)):
+            at = [gs._p(p, torch.float32, f"parameter {i}")]
+            for t, k in ((m, "exp_avg"), (v, "exp_avg_sq")):
+                at.append(gs._p(t, torch.float32, f"{k} {i}"))
+                if t.shape != p.shape:
+                    raise GsError(f"{k} {i} must have its parameter's shape")
+            at.append(gs._p(c, None, f"copy {i}"))
+            if c is not None and (c.shape != p.shape or c.dtype not in gs.DTYPES):
+                raise GsError(f"copy {i} must have its parameter's shape and a floating type")
+            unit = i in self.normalize_rows
+            if unit and p.dim() == 0:
+                raise GsError(f"parameter {i} has no rows to renormalise")
+            row_len = p.shape[-1] if unit else 1
+            rows.append((at, gs.DTYPES[c.dtype] if c is not None else 0, unit, row_len, p.numel() // max(row_len, 1)))
+        for a, (at, copy_dtype, unit, row_len, count) in zip(self.table, rows):
+            a.param, a.exp_avg, a.exp_avg_sq, a.copy = at
+            a.copy_dtype, a.normalize_rows, a.row_len, a.col_end, a.rows = copy_dtype, unit, row_len, row_len, count
+        self._shapes = [p.shape for p in self.params]
+        self._described = described
+        self._held = [t.detach() for tensors in (self.params, self.exp_avg, self.exp_avg_sq, self.copies)
+                      for t in tensors if t is not None]
 
     def step(self, grads):
         """One step with gradients grads (float32 or 16-bit, contiguous).  Returns the global norm before clipping
@@ -164,9 +191,13 @@ class Adam:
         if len(grads) != len(self.params):
             raise GsError(f"{len(self.params)} parameters, {len(grads)} gradients")
         packed = gs._grad_table(grads, None)
-        for g, p in zip(grads, self.params):
-            if g.shape != p.shape:
-                raise GsError("a gradient must have its parameter's shape")
+        if self._pointers() != self._described or not all(map(torch.Tensor.is_contiguous, self.params)):
+            self._describe()
+        for g, p, shape in zip(grads, self.params, self._shapes):
+            if not g.shape == shape == p.shape:
+                if g.shape != p.shape:
+                    raise GsError("a gradient must have its parameter's shape")
+                self._describe()  # another shape in the same memory
         words = np.frombuffer(packed, dtype=np.int64).reshape(-1, 4)  # grad, out, count, dtype
         self._grad_words[:] = words[:, 0]
         self._dtype_words[:] = words[:, 3]

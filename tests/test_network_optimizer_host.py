@@ -1,0 +1,132 @@
+"""What network.Adam hands to the library, looked at on the CPU: the calls are replaced by recorders."""
+import struct
+
+import pytest
+import torch
+
+from differentiable_gaussian_splatting_dgs_amd import gs, network
+
+FIELDS = ("param", "grad", "exp_avg", "exp_avg_sq", "copy", "rows", "row_len", "copy_dtype", "normalize_rows")
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The descriptors of every gs_adam_step_clipped call."""
+    seen = []
+
+    def pointer(t, dtype=None, name="tensor"):
+        if t is None:
+            return None
+        if not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
+            raise gs.GsError(name)
+        return t.data_ptr()
+
+    def table(grads, out):
+        return struct.pack("=%dq" % (4 * len(grads)),
+                           *[v for g in grads for v in (g.data_ptr(), 0, g.numel(), gs.DTYPES[g.dtype])])
+
+    monkeypatch.setattr(gs, "_p", pointer)
+    monkeypatch.setattr(gs, "_grad_table", table)
+    monkeypatch.setattr(gs, "gs_adam_step_clipped",
+                        lambda t, *a, **k: seen.append([{f: getattr(e, f) for f in FIELDS} for e in t]))
+    return seen
+
+
+def optimizer():
+    p = [torch.randn(6, 4), torch.randn(5)]
+    return network.Adam(p, lr=[1e-3, 2e-3], copies=[p[0].half(), None], normalize_rows=(0,))
+
+
+def expect(opt, grads, got):
+    for i, e in enumerate(got):
+        want = dict(param=opt.params[i], grad=grads[i], exp_avg=opt.exp_avg[i], exp_avg_sq=opt.exp_avg_sq[i],
+                    copy=opt.copies[i])
+        assert {k: e[k] or None for k in want} == {k: None if t is None else t.data_ptr() for k, t in want.items()}
+        assert e["rows"] * e["row_len"] == opt.params[i].numel()
+        assert e["row_len"] == (opt.params[i].shape[-1] if i in (0,) else 1)
+        if opt.copies[i] is not None:
+            assert e["copy_dtype"] == gs.DTYPES[opt.copies[i].dtype]
+
+
+def replace(opt, what):
+    if what == "data":  # what module.to() and loaders do to a parameter
+        opt.params[0].data = torch.randn(6, 4)
+    elif what == "longer":
+        opt.params[1] = torch.randn(9)
+        opt.exp_avg[1], opt.exp_avg_sq[1] = torch.zeros(9), torch.zeros(9)
+    elif what == "moment":
+        opt.exp_avg[0] = torch.ones(6, 4)
+    elif what == "second moment":
+        opt.exp_avg_sq[1].data = torch.ones(5)
+    elif what == "copy":
+        opt.copies[0] = opt.copies[0].bfloat16()
+    elif what == "copy's data":
+        opt.copies[0].data = torch.zeros(6, 4, dtype=torch.float16)
+    elif what == "no copy":
+        opt.copies[0] = None
+    elif what == "new copy":
+        opt.copies[1] = torch.zeros(5, dtype=torch.float16)
+    elif what == "shape":  # other rows in the same memory
+        for t in (opt.params[0], opt.exp_avg[0], opt.exp_avg_sq[0], opt.copies[0]):
+            t.data = t.data.view(3, 8)
+
+
+@pytest.mark.parametrize("what", ["nothing", "data", "longer", "moment", "second moment", "copy", "copy's data", "no copy",
+                                  "new copy", "shape"])
+def test_a_step_takes_what_the_lists_hold(calls, what):
+    opt = optimizer()
+    for k in range(3):
+        if k == 1:
+            replace(opt, what)
+        grads = [torch.randn(p.shape) for p in opt.params]
+        opt.step(grads)
+        expect(opt, grads, calls[-1])
+    assert opt.t == len(calls) == 3
+    assert [e.lr for e in opt.table] == [pytest.approx(1e-3), pytest.approx(2e-3)]
+
+
+def test_the_table_holds_its_memory(calls):
+    """The storages that the table names live until it names others: nothing else can be allocated there."""
+    opt = optimizer()
+    opt.params[0].data = torch.randn(6, 4)
+    freed = opt._held[0].data_ptr()
+    assert opt.table[0].param == freed != opt.params[0].data_ptr()
+    opt.step([torch.randn(p.shape) for p in opt.params])
+    assert opt._held[0].data_ptr() == opt.table[0].param == opt.params[0].data_ptr()
+
+
+@pytest.mark.parametrize("list_name,bad", [("params", torch.zeros(6, 4, dtype=torch.float64)), ("params", torch.zeros(4, 6).t()),
+                                           ("params", None), ("exp_avg", None), ("copies", "half"),
+                                           ("exp_avg", torch.zeros(6, 3)), ("exp_avg_sq", torch.zeros(4, 6).t()),
+                                           ("copies", torch.zeros(24, dtype=torch.float16)),
+                                           ("copies", torch.zeros(6, 4, dtype=torch.int32))])
+def test_replacements_are_checked(calls, list_name, bad):
+    opt = optimizer()
+    grads = [torch.randn(p.shape) for p in opt.params]
+    opt.step(grads)
+    kept = getattr(opt, list_name)[0]
+    getattr(opt, list_name)[0] = bad
+    with pytest.raises(gs.GsError):
+        opt.step(grads)
+    assert len(calls) == 1 and opt.t == 1
+    getattr(opt, list_name)[0] = kept
+    opt.step(grads)
+    expect(opt, grads, calls[-1])
+
+
+def test_a_transposed_view_is_refused(calls):
+    """Same address, same shape, another order."""
+    opt = network.Adam([torch.randn(4, 4)], lr=1e-3)
+    opt.step([torch.randn(4, 4)])
+    opt.params[0].data = opt.params[0].data.t()
+    with pytest.raises(gs.GsError):
+        opt.step([torch.randn(4, 4)])
+
+
+def test_lists_of_another_length(calls):
+    opt = optimizer()
+    opt.exp_avg.append(torch.zeros(5))
+    with pytest.raises(gs.GsError):
+        opt.step([torch.randn(p.shape) for p in opt.params])
+    with pytest.raises(gs.GsError):
+        network.Adam([torch.tensor(1.0)], lr=1e-3, normalize_rows=(0,))
