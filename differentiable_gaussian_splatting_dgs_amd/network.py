@@ -78,25 +78,36 @@ def linear(x, w, bias=None, residual=None, act="none"):
 class GradClip:
     """Clipping of gradient lists to a global norm; owns the clipping state and the workspace.
 
-    norm() and clip() return the norm before clipping as a float32 device scalar (overwritten by the next call);
-    nothing synchronises."""
+    norm() and clip() return the norm before clipping as a float32 device scalar (overwritten by the stream's next
+    call); nothing synchronises.  Every stream has a state and a workspace of its own, so calls on several streams need
+    no order between them, and so has every call that is recorded into a graph: its replays use them for as long as
+    the GradClip lives, which has to be as long as the graph does.  `state` is the last call's."""
 
     def __init__(self, max_norm):
         self.max_norm = float(max_norm)
         if not self.max_norm >= 0:
             raise GsError("max_norm must be >= 0")
         self.state = None
+        self._of_stream = {}  # (device, stream): (state, value, workspace)
+        self._recorded = []
 
     def _prepare(self, grads):
         if not grads:
             raise GsError("no gradients")
-        need = gs.gs_grad_workspace_size(len(grads))
-        if self.state is None or self.state.device != grads[0].device:
-            self.state = torch.empty(gs.CLIP_STATE_FLOATS, dtype=torch.float32, device=grads[0].device)
-            self.value = self.state[0]
-            self.workspace = _workspace(need, grads[0].device)
-        elif self.workspace.numel() < need:
-            self.workspace = _workspace(need, grads[0].device)
+        need, device = gs.gs_grad_workspace_size(len(grads)), grads[0].device
+        recorded = torch.cuda.is_current_stream_capturing()
+        key = device, gs._raw_stream(gs._current_device())
+        held = None if recorded else self._of_stream.get(key)
+        if held is None:
+            state = torch.empty(gs.CLIP_STATE_FLOATS, dtype=torch.float32, device=device)
+            held = state, state[0], _workspace(need, device)
+        elif held[2].numel() < need:  # the old one goes back to this stream, behind the work that uses it
+            held = held[0], held[1], _workspace(need, device)
+        if recorded:
+            self._recorded.append(held)
+        else:
+            self._of_stream[key] = held
+        self.state, self.value, self.workspace = held
 
     def norm(self, grads, table=None):
         """The global norm of the list; the coefficient is left in state[1] for gs_adam_step_clipped.  table: the

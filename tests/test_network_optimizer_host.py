@@ -1,5 +1,7 @@
 """What network.Adam hands to the library, looked at on the CPU: the calls are replaced by recorders."""
+import gc
 import struct
+import weakref
 
 import pytest
 import torch
@@ -130,3 +132,61 @@ def test_lists_of_another_length(calls):
         opt.step([torch.randn(p.shape) for p in opt.params])
     with pytest.raises(gs.GsError):
         network.Adam([torch.tensor(1.0)], lr=1e-3, normalize_rows=(0,))
+
+
+@pytest.fixture
+def clip_calls(monkeypatch):
+    """Every gs_grad_norm call's state and workspace, with the stream and the capture that `at` says."""
+    seen, at = [], dict(stream=1, capturing=False)
+    monkeypatch.setattr(gs, "_grad_table", lambda grads, out: b"")
+    monkeypatch.setattr(gs, "grad_norm_table", lambda n, t, m, state, ws: seen.append((state, ws)))
+    monkeypatch.setattr(gs, "_raw_stream", lambda device: at["stream"])
+    monkeypatch.setattr(gs, "_current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: at["capturing"])
+    return seen, at
+
+
+def shared(a, b):
+    return any(x.data_ptr() == y.data_ptr() for x, y in zip(a, b))
+
+
+def test_recorded_calls_keep_their_buffers(clip_calls):
+    """A longer list, or another recording, neither frees nor uses what a recorded call uses."""
+    seen, at = clip_calls
+    c = network.GradClip(1.0)
+    one, many = [torch.ones(2)], [torch.ones(2)] * 200
+    c.norm(one)
+    for _ in range(2):
+        at["capturing"] = True
+        c.norm(one)
+        at["capturing"] = False
+        c.norm(many)
+        c.norm(one)
+    eager, recorded = [seen[k] for k in (0, 2, 3, 5, 6)], [seen[k] for k in (1, 4)]
+    pointers = [[t.data_ptr() for t in r] for r in recorded]
+    refs = [[weakref.ref(t) for t in r] for r in recorded]
+    assert not shared(*recorded) and not any(shared(r, e) for r in recorded for e in eager)
+    del seen[:], eager, recorded
+    gc.collect()
+    assert [[r().data_ptr() for r in p] for p in refs] == pointers
+
+
+def test_streams_have_their_own_buffers(clip_calls):
+    seen, at = clip_calls
+    c = network.GradClip(1.0)
+    for stream in (1, 2, 1, 2):
+        at["stream"] = stream
+        c.norm([torch.ones(2)])
+        assert c.state is seen[-1][0] and c.workspace is seen[-1][1]
+    assert not shared(seen[0], seen[1])
+    for k in (0, 1):
+        assert all(x is y for x, y in zip(seen[k], seen[k + 2]))
+
+
+def test_a_longer_list_gets_a_longer_workspace(clip_calls):
+    seen, _ = clip_calls
+    c = network.GradClip(1.0)
+    for n in (1, 200, 3, 65):
+        c.norm([torch.ones(2)] * n)
+        assert seen[-1][1].numel() >= gs.gs_grad_workspace_size(n)
+    assert seen[1][1] is seen[2][1] is seen[3][1] and all(s[0] is seen[0][0] for s in seen)
