@@ -767,7 +767,8 @@ def gs_count_pairs_views(cams, settings, n, tile_ranges, point_list, splats, cou
 
 # A layer of a few rows takes a few microseconds on the GPU, so these wrappers keep
 # the host's part as short: one look at each property of a tensor, descriptors
-# packed in one go (gs_linear, gs_grad_tensor and gs_adam_tensor as bytes).
+# packed in one go (gs_linear, gs_grad_tensor and gs_adam_tensor as bytes).  They run on their tensors' device, on the
+# stream that is current there.
 # ---------------------------------------------------------------------------
 
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
@@ -833,6 +834,9 @@ def _linear_shape(x, w, act):
 def linear_fwd_into(x, w, bias, residual, y, act):
     """gs_linear_fwd; y None: a new [rows, n_out] tensor.  Returns y."""
     rows, n_in, n_out, code, a, device, ld_x = _linear_shape(x, w, act)
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return linear_fwd_into(x, w, bias, residual, y, act)
     dtype, shape = x.dtype, (rows, n_out)
     if y is None:
         y, ld_y = x.new_empty(shape), n_out
@@ -845,7 +849,7 @@ def linear_fwd_into(x, w, bias, residual, y, act):
     rc = (_lib or load_library()).gs_linear_fwd(
         _pack_linear(rows, n_in, n_out, code, a, ld_x, ld_y, ld_res, 0), x.data_ptr(),
         _whole(w, w.shape, dtype, device, "w"), _whole(bias, (n_out,), dtype, device, "bias"), pr, y.data_ptr(),
-        _raw_stream(_current_device()))
+        _raw_stream(device))
     if rc:
         _check(rc, "gs_linear_fwd")
     return y
@@ -868,6 +872,9 @@ def gs_linear_bwd_workspace_size(x, w, act="none"):
 def linear_bwd_into(x, w, bias, dy, dx, dw, db, workspace, act):
     """gs_linear_bwd; workspace None: one of the size the call needs."""
     rows, n_in, n_out, code, a, device, ld_x = _linear_shape(x, w, act)
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return linear_bwd_into(x, w, bias, dy, dx, dw, db, workspace, act)
     dtype = x.dtype
     ld_y = _rows(dy, (rows, n_out), dtype, device, "dy")
     pdx, ld_dx = None, 0
@@ -885,7 +892,7 @@ def linear_bwd_into(x, w, bias, dy, dx, dw, db, workspace, act):
         d, x.data_ptr(), _whole(w, w.shape, dtype, device, "w"), _whole(bias, (n_out,), dtype, device, "bias"),
         dy.data_ptr(), pdx, _whole(dw, w.shape, dtype, device, "dw"), _whole(db, (n_out,), dtype, device, "db"),
         _whole(workspace, workspace.shape, torch.uint8, device, "workspace"), workspace.numel(),
-        _raw_stream(_current_device()))
+        _raw_stream(device))
     if rc:
         _check(rc, "gs_linear_bwd")
 
@@ -934,13 +941,26 @@ def _clip_state(clip):
     return _p(clip, torch.float32, "clip")
 
 
+def _clip_device(grads, clip, workspace):
+    """The one device of a clipping call's tensors (each list's tensors are compared with each other in its table)."""
+    _p(clip, None, "clip")
+    device = clip.get_device()
+    if workspace.get_device() != device or (grads and grads[0].get_device() != device):
+        raise GsError("gradients, clipping state and workspace must be on one device")
+    return device
+
+
 def gs_grad_norm(grads, max_norm, clip, workspace):
     """Global norm and clipping coefficient of the list grads into clip [4] float32 (words 0 and 1)."""
-    grad_norm_table(len(grads), _grad_table(grads, None), max_norm, clip, workspace)
+    table, device = _grad_table(grads, None), _clip_device(grads, clip, workspace)
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return grad_norm_table(len(grads), table, max_norm, clip, workspace)
+    grad_norm_table(len(grads), table, max_norm, clip, workspace)
 
 
 def grad_norm_table(n, table, max_norm, clip, workspace):
-    """gs_grad_norm of n packed gs_grad_tensor descriptors."""
+    """gs_grad_norm of n packed gs_grad_tensor descriptors of the current device."""
     rc = (_lib or load_library()).gs_grad_norm(n, table, max_norm, _clip_state(clip),
                                                _p(workspace, torch.uint8, "workspace"), workspace.numel(),
                                                _raw_stream(_current_device()))
@@ -951,6 +971,10 @@ def gs_grad_clip(grads, out, max_norm, clip, workspace):
     """gs_grad_norm, then out[i] = coefficient * grads[i] (out may be grads itself)."""
     if len(out) != len(grads):
         raise GsError("out needs one tensor for each gradient")
+    device = _clip_device(grads, clip, workspace)
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return gs_grad_clip(grads, out, max_norm, clip, workspace)
     rc = (_lib or load_library()).gs_grad_clip(len(grads), _grad_table(grads, out), max_norm, _clip_state(clip),
                                                _p(workspace, torch.uint8, "workspace"), workspace.numel(),
                                                _raw_stream(_current_device()))
@@ -958,8 +982,8 @@ def gs_grad_clip(grads, out, max_norm, clip, workspace):
 
 
 def gs_adam_step_clipped(tensors, beta1, beta2, eps, step, clip=None):
-    """One Adam step on coefficient * gradient for a ctypes array of GsAdamTensor; clip: the state of
-    gs_grad_norm, or None."""
+    """One Adam step on coefficient * gradient for a ctypes array of GsAdamTensor of the current device; clip: the
+    state of gs_grad_norm, or None."""
     rc = (_lib or load_library()).gs_adam_step_clipped(len(tensors), tensors, beta1, beta2, eps, step,
                                                        None if clip is None else _clip_state(clip),
                                                        _raw_stream(_current_device()))

@@ -9,6 +9,7 @@ a time step) or views (an appearance code per camera); its outputs go to
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 
 import numpy as np
@@ -75,6 +76,23 @@ def linear(x, w, bias=None, residual=None, act="none"):
     return gs.linear_fwd_into(x, w, bias, residual, None, act)
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _device_of(grads):
+    """A context in which the gradients' device is the current one."""
+    if not grads:
+        raise GsError("no gradients")
+    if not isinstance(grads[0], torch.Tensor):
+        raise GsError("gradients must be tensors")
+    return _on(grads[0].get_device())
+
+
+def _on(device):
+    """A context in which that device is the current one (-1, the host: nothing; the calls refuse its tensors)."""
+    return _HERE if device < 0 or device == gs._current_device() else torch.cuda.device(device)
+
+
 class GradClip:
     """Clipping of gradient lists to a global norm; owns the clipping state and the workspace.
 
@@ -88,40 +106,42 @@ class GradClip:
         if not self.max_norm >= 0:
             raise GsError("max_norm must be >= 0")
         self.state = None
-        self._of_stream = {}  # (device, stream): (state, value, workspace)
+        self._of_stream = {}  # (device, stream): state, value, workspace, the tensors that it is for
         self._recorded = []
 
     def _prepare(self, grads):
-        if not grads:
-            raise GsError("no gradients")
-        need, device = gs.gs_grad_workspace_size(len(grads)), grads[0].device
+        n, device = len(grads), grads[0].device
         recorded = torch.cuda.is_current_stream_capturing()
         key = device, gs._raw_stream(gs._current_device())
         held = None if recorded else self._of_stream.get(key)
-        if held is None:
-            state = torch.empty(gs.CLIP_STATE_FLOATS, dtype=torch.float32, device=device)
-            held = state, state[0], _workspace(need, device)
-        elif held[2].numel() < need:  # the old one goes back to this stream, behind the work that uses it
-            held = held[0], held[1], _workspace(need, device)
-        if recorded:
-            self._recorded.append(held)
-        else:
-            self._of_stream[key] = held
-        self.state, self.value, self.workspace = held
+        if held is None or held[3] < n:
+            workspace = _workspace(gs.gs_grad_workspace_size(n), device)
+            if held is None:
+                state = torch.empty(gs.CLIP_STATE_FLOATS, dtype=torch.float32, device=device)
+                held = state, state[0], workspace, n
+            else:  # the old workspace goes back to this stream, behind the work that uses it
+                held = held[0], held[1], workspace, n
+            if recorded:
+                self._recorded.append(held)
+            else:
+                self._of_stream[key] = held
+        self.state, self.value, self.workspace, _ = held
 
     def norm(self, grads, table=None):
         """The global norm of the list; the coefficient is left in state[1] for gs_adam_step_clipped.  table: the
         list's packed descriptors, if the caller has them."""
-        self._prepare(grads)
-        gs.grad_norm_table(len(grads), gs._grad_table(grads, None) if table is None else table, self.max_norm,
-                           self.state, self.workspace)
-        return self.value
+        with _device_of(grads):
+            table = gs._grad_table(grads, None) if table is None else table
+            self._prepare(grads)
+            gs.grad_norm_table(len(grads), table, self.max_norm, self.state, self.workspace)
+            return self.value
 
     def clip(self, grads, out=None):
         """Scales the gradients by min(1, max_norm / (norm + 1e-6)), in place or into out."""
-        self._prepare(grads)
-        gs.gs_grad_clip(grads, grads if out is None else out, self.max_norm, self.state, self.workspace)
-        return self.value
+        with _device_of(grads):
+            self._prepare(grads)
+            gs.gs_grad_clip(grads, grads if out is None else out, self.max_norm, self.state, self.workspace)
+            return self.value
 
 
 class Adam:
@@ -183,6 +203,8 @@ class Adam:
             at.append(gs._p(c, None, f"copy {i}"))
             if c is not None and (c.shape != p.shape or c.dtype not in gs.DTYPES):
                 raise GsError(f"copy {i} must have its parameter's shape and a floating type")
+            if any(t is not None and t.get_device() != self.params[0].get_device() for t in (p, m, v, c)):
+                raise GsError("parameters, moments and copies must be on one device")
             unit = i in self.normalize_rows
             if unit and p.dim() == 0:
                 raise GsError(f"parameter {i} has no rows to renormalise")
@@ -209,12 +231,17 @@ class Adam:
                 if g.shape != p.shape:
                     raise GsError("a gradient must have its parameter's shape")
                 self._describe()  # another shape in the same memory
+        if grads and grads[0].get_device() != self.params[0].get_device():
+            raise GsError("gradients must be on their parameters' device")
         words = np.frombuffer(packed, dtype=np.int64).reshape(-1, 4)  # grad, out, count, dtype
         self._grad_words[:] = words[:, 0]
         self._dtype_words[:] = words[:, 3]
-        norm = self.clipper.norm(grads, packed) if self.clipper is not None and grads else None
-        self.t += 1
-        if self.params:
+        if not self.params:
+            self.t += 1
+            return None
+        with _on(self.params[0].get_device()):
+            norm = self.clipper.norm(grads, packed) if self.clipper is not None else None
+            self.t += 1
             gs.gs_adam_step_clipped(self.table, self.betas[0], self.betas[1], self.eps, self.t,
                                     self.clipper.state if self.clipper is not None else None)
         return norm

@@ -93,3 +93,67 @@ def test_clips_on_two_streams():
     torch.cuda.synchronize()
     for out, w in zip(outs, want):
         assert all(torch.equal(a, b) for a, b in zip(out, w))
+
+
+@pytest.fixture
+def elsewhere(monkeypatch):
+    """Another device than the tensors' is the current one, as far as the calls can tell; the devices they enter."""
+    from differentiable_gaussian_splatting_dgs_amd import gs
+    now, entered = [1], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            entered.append(self.index)
+            now.append(self.index)
+
+        def __exit__(self, *a):
+            now.pop()
+
+    monkeypatch.setattr(gs, "_current_device", lambda: now[-1])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    return entered
+
+
+def test_calls_go_to_their_tensors_device(elsewhere):
+    """Each call enters its tensors' device before it takes a stream, once."""
+    from differentiable_gaussian_splatting_dgs_amd import gs, network
+    new = make(3)
+    x, w, b, dy = new(40, 24), new(20, 24), new(20), new(40, 20)
+    grads = [new(30, 3), new(9)]
+    c = network.GradClip(0.5)
+    opt = network.Adam([new(30, 3), new(9)], lr=1e-2, max_norm=0.5)
+    for name, call in (("linear", lambda: network.linear(x, w, b, act="silu")),
+                       ("backward", lambda: network.linear_backward(dy, x, w, b, act="silu")),
+                       ("norm", lambda: c.norm(grads)),
+                       ("clip", lambda: c.clip(grads, out=[torch.empty_like(g) for g in grads])),
+                       ("adam", lambda: opt.step(grads)),
+                       ("gs norm", lambda: gs.gs_grad_norm(grads, 0.5, c.state, c.workspace)),
+                       ("gs clip", lambda: gs.gs_grad_clip(grads, grads, 0.5, c.state, c.workspace))):
+        del elsewhere[:]
+        print(name, flush=True)
+        call()
+        assert elsewhere == [0], name
+
+
+def test_tensors_of_several_devices_are_refused():
+    from differentiable_gaussian_splatting_dgs_amd import gs, network
+    new = make(4)
+    p = [new(5), new(3)]
+    with pytest.raises(gs.GsError):
+        network.Adam(p, lr=1e-3, exp_avg=[torch.zeros(5), torch.zeros(3)])
+    opt = network.Adam(p, lr=1e-3)
+    with pytest.raises(gs.GsError):
+        opt.step([g.cpu() for g in p])
+    c = network.GradClip(1.0)
+    for bad in ([None], [p[0].cpu()], [p[0], p[1].cpu()], []):
+        for call in (c.norm, c.clip):
+            with pytest.raises(gs.GsError):
+                call(bad)
+    c.norm(p)
+    with pytest.raises(gs.GsError):
+        gs.gs_grad_norm(p, 1.0, c.state.cpu(), c.workspace)
+    with pytest.raises(gs.GsError):
+        gs.gs_grad_clip(p, p, 1.0, c.state, c.workspace.cpu())
