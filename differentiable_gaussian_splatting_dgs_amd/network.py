@@ -15,6 +15,7 @@ import ctypes as C
 import numpy as np
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.graph import increment_version
 
 from . import gs
 from .gs import GsError
@@ -140,7 +141,9 @@ class GradClip:
         """Scales the gradients by min(1, max_norm / (norm + 1e-6)), in place or into out."""
         with _device_of(grads):
             self._prepare(grads)
-            gs.gs_grad_clip(grads, grads if out is None else out, self.max_norm, self.state, self.workspace)
+            out = grads if out is None else out
+            gs.gs_grad_clip(grads, out, self.max_norm, self.state, self.workspace)
+            increment_version(out)
             return self.value
 
 
@@ -244,4 +247,6 @@ class Adam:
             self.t += 1
             gs.gs_adam_step_clipped(self.table, self.betas[0], self.betas[1], self.eps, self.t,
                                     self.clipper.state if self.clipper is not None else None)
+            # a graph that saved one of them must not go backward on the new values
+            increment_version(self.params + [c for c in self.copies if c is not None])
         return norm

@@ -157,3 +157,19 @@ def test_tensors_of_several_devices_are_refused():
         gs.gs_grad_norm(p, 1.0, c.state.cpu(), c.workspace)
     with pytest.raises(gs.GsError):
         gs.gs_grad_clip(p, p, 1.0, c.state, c.workspace.cpu())
+
+
+def test_a_backward_after_the_step_is_refused():
+    """The gradients of a layer whose weights a step has changed since would be those of other weights."""
+    from differentiable_gaussian_splatting_dgs_amd import network
+    new = make(5)
+    x, w = new(20, 8), new(6, 8)
+    c = w.to(H).requires_grad_()
+    opt = network.Adam([w], lr=1e-2, max_norm=1.0, copies=[c])
+    y = network.linear(x.to(H).requires_grad_(), c, act="silu").float().sum()
+    opt.step([new(6, 8).to(H)])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    y = network.linear(x.to(H).requires_grad_(), c, act="silu").float().sum()
+    y.backward()
+    opt.step([c.grad])

@@ -190,3 +190,29 @@ def test_a_longer_list_gets_a_longer_workspace(clip_calls):
         c.norm([torch.ones(2)] * n)
         assert seen[-1][1].numel() >= gs.gs_grad_workspace_size(n)
     assert seen[1][1] is seen[2][1] is seen[3][1] and all(s[0] is seen[0][0] for s in seen)
+
+
+def test_a_step_counts_as_a_change(calls):
+    """Autograd knows that a step wrote parameters and copies: a graph that saved them refuses a backward."""
+    opt = optimizer()
+    w, c = opt.params[1].requires_grad_(), opt.copies[0].requires_grad_()
+    loss = w.square().sum() + c.square().sum().float()
+    opt.step([torch.randn(p.shape) for p in opt.params])
+    assert w._version == 1 and c._version == 1
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+@pytest.mark.parametrize("inference", [False, True])
+def test_a_clip_counts_as_a_change(clip_calls, monkeypatch, inference):
+    monkeypatch.setattr(gs, "gs_grad_clip", lambda *a: None)
+    with torch.inference_mode(inference):
+        g, out = [torch.ones(2), torch.ones(3)], [torch.ones(2), torch.ones(3)]
+        c = network.GradClip(1.0)
+        c.norm(g)
+        if not inference:  # tensors made in inference mode have no versions
+            assert [t._version for t in g] == [0, 0]
+        c.clip(g, out=out)
+        c.clip(g)
+        if not inference:
+            assert [t._version for t in g + out] == [1, 1, 1, 1]
