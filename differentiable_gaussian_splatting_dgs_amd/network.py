@@ -157,7 +157,7 @@ class Adam:
     update (quaternions).  exp_avg, exp_avg_sq: the moments, zeros by default.  A step takes what the lists params,
     exp_avg, exp_avg_sq and copies hold at that time: their entries and the entries' data may be replaced (moments
     restored, `p.data = ...`).  A step whose norm is not finite changes nothing on the device; it still counts in
-    `  Recorded into a graph, a step keeps its number: replays correct the moments' bias by it.""""""
+    `t`.  Recorded into a graph, a step keeps its number: replays correct the moments' bias by it."""
 
     def __init__(self, params, lr, betas=(0.9, 0.999), eps=1e-8, max_norm=None, copies=None, normalize_rows=(),
                  exp_avg=None, exp_avg_sq=None):
