@@ -6,8 +6,8 @@
 // Products are summed in float32, the activation runs in float32, and every
 // result is rounded once.  dz enters the two products of the backward rounded to the
 // layer's type: the matrix instructions take no mixed operands, and in float32 they
-// would run at a ninth of the 16-bit rate.  db is summed from dz unrounded where the
-// z is made in the same kernel, and from the rounded dz of the wide layers.
+// would run at a ninth of the 16-bit rate.  db is summed from dz before that rounding,
+// where it is made: sums that cancel would keep the roundings.
 #include "linear_bwd.h"
 
 namespace gs {
@@ -29,6 +29,7 @@ struct ProdArgs {
     void* out;
     int64_t rows, ld_a, ld_b, ld_other, ld_out;
     int32_t cols, depth, epi, act;
+    float* sums;  // DZ: [runs of rows][cols], the sums of dz's rows before its rounding, or NULL
 };
 
 // The epilogue of N runs (E consecutive outputs of one row each), with the runs of
@@ -51,6 +52,15 @@ __device__ __forceinline__ void finish_runs(const ProdArgs& p, float (&v)[N * Ti
     }
 #pragma unroll
     for (int j = 0; j < N * E; ++j) out[j / E][j % E] = (T)v[j];
+}
+
+// Stores the sums of a run's columns over the rows of the lanes: count columns from c0 on, at `to`.
+__device__ __forceinline__ void store_sums(float* to, int c0, int count, const float (&v)[8], int r) {
+    float sum[2];
+    run_sums(v, r, sum);
+    const int c = c0 + pair_of(r);
+    if (r < 4 && c < count) to[c] = sum[0];
+    if (r < 4 && c + 1 < count) to[c + 1] = sum[1];
 }
 
 // Few outputs or few rows: a block makes one group of KS outputs of 16 rows, its
@@ -99,7 +109,8 @@ __global__ __launch_bounds__(256) void k_prod_few(ProdArgs p) {
 #pragma unroll
     for (int t = 0; t < TG; ++t) s_acc[wave][t][lane] = acc[t];
     __syncthreads();
-    if (wave != 0 || row >= p.rows) return;
+    const bool in = row < p.rows;
+    if (wave != 0 || (!in && !p.sums)) return;
     const int c0 = n0 + E * g;
     float v[E];
 #pragma unroll
@@ -113,9 +124,16 @@ __global__ __launch_bounds__(256) void k_prod_few(ProdArgs p) {
         for (int j = 0; j < E; ++j) v[j] += (float)bias[j];
     }
     typename Tile<T>::Frag other[1] = {zero_frag<T>()}, f[1];
-    if (p.other) other[0] = load_frag(static_cast<const T*>(p.other) + row * p.ld_other, c0, p.cols);
+    if (p.other && in) other[0] = load_frag(static_cast<const T*>(p.other) + row * p.ld_other, c0, p.cols);
     finish_runs<T, 1>(p, v, other, f);
-    store_run(static_cast<T*>(p.out) + row * p.ld_out, c0, p.cols, f[0]);
+    if (in) store_run(static_cast<T*>(p.out) + row * p.ld_out, c0, p.cols, f[0]);
+    if constexpr (sizeof(T) == 2) {
+        if (p.sums) {  // a run of 16 rows
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] = in ? v[j] : 0.f;
+            store_sums(p.sums + (row - r) / 16 * p.cols, c0, p.cols, v, r);
+        }
+    }
 }
 
 // Narrow layers over many rows: the weights stay in LDS as fragments for the
@@ -130,8 +148,10 @@ __global__ __launch_bounds__(256) void k_prod_few(ProdArgs p) {
 // 3M rows 64 -> 59 float16 138 us, 5.3 TB/s.  Float32 ones by the matrix rate and, under
 // it, the start: 1M rows 128 -> 128 390 us, 84 TFLOP/s beside 2.6 TB/s; 100k rows
 // 63 -> 128 28 us, of which 11 are products.
+// SUMS: dz for a wide layer's backward, whose rows each wave adds up in LDS on their way
+// (the backward of 1M rows 128 -> 256 float16 635 us against 615 without db's sums).
 constexpr int narrow_threads(int sl) { return sl <= 4 ? 1024 : 512; }  // at most: deep rows need 256 registers
-template <typename T, int SL, bool PACK>
+template <typename T, int SL, bool PACK, bool SUMS>
 __global__ __launch_bounds__(narrow_threads(SL), sizeof(T) == 4 ? 4 : 1) void k_prod_narrow(ProdArgs p) {
     constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG, P = 2;
     typedef typename Tile<T>::Frag Frag;
@@ -142,6 +162,7 @@ __global__ __launch_bounds__(narrow_threads(SL), sizeof(T) == 4 ? 4 : 1) void k_
     const int waves = blockDim.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     T* s_out = reinterpret_cast<T*>(s_bias + groups * KS / 4) + wave * 16 * p.cols;  // PACK: [waves][16][cols]
+    float* s_sum = reinterpret_cast<float*>(s_bias + groups * KS / 4);               // SUMS: [waves][groups * KS]
     const int64_t tiles = (p.rows + 15) / 16, step = (int64_t)gridDim.x * waves;
     int64_t tile = (int64_t)blockIdx.x * waves + wave;
     auto row_of = [&](int64_t t) { return min(t * 16 + r, p.rows - 1); };
@@ -188,6 +209,8 @@ __global__ __launch_bounds__(narrow_threads(SL), sizeof(T) == 4 ? 4 : 1) void k_
     for (int i = threadIdx.x; i < groups * KS; i += blockDim.x)
         reinterpret_cast<float*>(s_bias)[i] =
             p.bias && i < p.cols ? (float)static_cast<const T*>(p.bias)[i] : 0.f;
+    if (SUMS)
+        for (int i = threadIdx.x; i < waves * groups * KS; i += blockDim.x) s_sum[i] = 0.f;
     __syncthreads();
     for (; tile < tiles; tile += step) {
         const int64_t row = tile * 16 + r;
@@ -228,6 +251,14 @@ __global__ __launch_bounds__(narrow_threads(SL), sizeof(T) == 4 ? 4 : 1) void k_
                 for (int j = 0; j < E; ++j) v[j] = acc[h][j / 4][j % 4];
                 finish_runs<T, 1>(p, v, o, to);
                 f[h] = to[0];
+                if constexpr (SUMS) {
+#pragma unroll
+                    for (int j = 0; j < E; ++j) v[j] = row < p.rows ? v[j] : 0.f;
+                    float sum[2];
+                    run_sums(v, r, sum);
+                    float* to = s_sum + (wave * groups + n + h) * KS + E * g + pair_of(r);
+                    if (r < 4) to[0] += sum[0], to[1] += sum[1];
+                }
             }
             if (PACK || row < p.rows) {
 #pragma unroll
@@ -247,6 +278,14 @@ __global__ __launch_bounds__(narrow_threads(SL), sizeof(T) == 4 ? 4 : 1) void k_
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         }
     }
+    if (SUMS) {  // a run is the block's rows
+        __syncthreads();
+        for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
+            float t = 0.f;
+            for (int i = 0; i < waves; ++i) t += s_sum[i * groups * KS + c];
+            p.sums[(int64_t)blockIdx.x * p.cols + c] = t;
+        }
+    }
 }
 
 // Deep or wide layers: 128 x 128 outputs per block, 64 x 64 per wave.  Both
@@ -259,7 +298,7 @@ __global__ __launch_bounds__(narrow_threads(SL), sizeof(T) == 4 ? 4 : 1) void k_
 // 16-bit time; the rest is the barrier of each stage, at two blocks a CU.  256 x 128
 // outputs over eight waves take as long (72 us against 74, 213 against 218).
 constexpr int kBig = 128;  // rows and outputs of a block
-template <typename T, int NT>  // NT: tiles of 16 outputs a wave has, 4 (128 outputs a block) or 2 (64)
+template <typename T, int NT, bool SUMS>  // NT: tiles of 16 outputs a wave has, 4 (128 outputs a block) or 2 (64)
 __global__ __launch_bounds__(256, 2) void k_prod_big(ProdArgs p) {
     constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG;
     typedef typename Tile<T>::Frag Frag;
@@ -381,33 +420,42 @@ __global__ __launch_bounds__(256, 2) void k_prod_big(ProdArgs p) {
             const int64_t row = m0 + wm + 16 * i + r;
             if (row < p.rows) store_run(static_cast<T*>(p.out) + row * p.ld_out, c0, p.cols, f[i]);
         }
+        if constexpr (SUMS) {  // a run is a wave's 64 rows
+            float sum[E] = {};
+#pragma unroll
+            for (int j = 0; j < 4 * E; ++j) sum[j % E] += m0 + wm + 16 * (j / E) + r < p.rows ? v[j] : 0.f;
+            if (m0 + wm < p.rows) store_sums(p.sums + (m0 + wm) / 64 * p.cols, c0, p.cols, sum, r);
+        }
     }
 }
 
-template <typename T, int SL>
-void launch_narrow(const ProdArgs& p, size_t lds, hipStream_t s) {
-    constexpr int E = Tile<T>::E;
-    const int threads = lds <= 40960 ? 256 : lds <= 81920 || SL > 4 ? 512 : 1024;
-    const bool pack = p.ld_out == p.cols && p.cols % E != 0 && aligned16(p.out) &&
-                      lds + (size_t)threads / 4 * p.cols * sizeof(T) <= 160 * 1024;
-    if (pack) lds += (size_t)threads / 4 * p.cols * sizeof(T);
-    int per_cu = (int)(160 * 1024 / lds);
-    if (per_cu > 1024 / threads) per_cu = 1024 / threads;
-    const int64_t blocks = cdiv(cdiv(p.rows, 16), threads / 64);
-    const dim3 grid((unsigned)(blocks < 256 * per_cu ? blocks : 256 * per_cu));
-    if (pack)
-        hipLaunchKernelGGL((k_prod_narrow<T, SL, true>), grid, dim3(threads), lds, s, p);
-    else
-        hipLaunchKernelGGL((k_prod_narrow<T, SL, false>), grid, dim3(threads), lds, s, p);
-}
+constexpr size_t kLdsBytes = 160 * 1024;
 
+// The kernel that a product takes, and the grid of k_prod_narrow.
+struct Route {
+    bool few, narrow;
+    int groups, steps;
+    int threads;
+    size_t lds;
+};
+
+// sums: of dz's rows, for which each wave of k_prod_narrow has LDS of its own.  Eight waves are then taken where
+// sixteen find no room (20000 rows 128 -> 520 bfloat16), and k_prod_big where eight do not (128 -> 600).
 template <typename T>
-void product(const ProdArgs& p, hipStream_t s) {
+Route route(int64_t rows, int32_t cols, int32_t depth, bool sums) {
     constexpr int KS = Tile<T>::KS;
-    const int groups = (int)cdiv(p.cols, KS), steps = (int)cdiv(p.depth, KS);
-    const int64_t tiles16 = cdiv(p.rows, 16);
-    const size_t lds = (size_t)groups * KS * (steps * KS * sizeof(T) + 4);
-    const bool narrow = lds <= 160 * 1024 && steps <= 8;
+    Route q{};
+    q.groups = (int)cdiv(cols, KS), q.steps = (int)cdiv(depth, KS);
+    const int64_t tiles16 = cdiv(rows, 16);
+    q.lds = (size_t)q.groups * KS * (q.steps * KS * sizeof(T) + 4);
+    q.narrow = q.lds <= kLdsBytes && q.steps <= 8;
+    q.threads = q.lds <= 40960 ? 256 : q.lds <= 81920 || q.steps > 4 ? 512 : 1024;
+    if (sums) {
+        const size_t wave = (size_t)q.groups * KS * 4;
+        if (q.threads == 1024 && q.lds + 16 * wave > kLdsBytes) q.threads = 512;
+        q.lds += q.threads / 64 * wave;
+        q.narrow = q.narrow && q.lds <= kLdsBytes;
+    }
     // Few tiles: a call of ordinary length is its launch, until about 2048 blocks of k_prod_few (500 rows 512 -> 512
     // bfloat16 8.5 us against 11.2 by k_prod_big, 1000 rows 8.9 against 11.8, 2000 rows 13.8 against 11.9; 16000 rows
     // 128 -> 128 8.5 by k_prod_narrow against 10.3).  In float32 a wave of k_prod_narrow takes 128 cycles for each of a
@@ -417,39 +465,81 @@ void product(const ProdArgs& p, hipStream_t s) {
     // Deep float32 rows of one group: k_prod_big's outputs would mostly be multiplied for nothing (150k rows 417 -> 3
     // 65 us against 95, 417 -> 16 93 against 95, 417 -> 32 156 against 96; bfloat16, whose products are short,
     // 417 -> 3 56 against 52, 417 -> 32 105 against 60).
-    const bool few = tiles16 * groups <= 2048 || (sizeof(T) == 4 && narrow && groups > 4 && tiles16 <= 640) ||
-                     (sizeof(T) == 4 && !narrow && groups == 1);
+    q.few = tiles16 * q.groups <= 2048 || (sizeof(T) == 4 && q.narrow && q.groups > 4 && tiles16 <= 640) ||
+            (sizeof(T) == 4 && !q.narrow && q.groups == 1) || depth == 0;
+    return q;
+}
+
+inline int64_t narrow_blocks(int64_t rows, const Route& q) {
+    int per_cu = (int)(kLdsBytes / q.lds);
+    if (per_cu > 1024 / q.threads) per_cu = 1024 / q.threads;
+    const int64_t blocks = cdiv(cdiv(rows, 16), q.threads / 64);
+    return blocks < 256 * per_cu ? blocks : 256 * per_cu;
+}
+
+template <typename T, int SL>
+void launch_narrow(const ProdArgs& p, Route q, hipStream_t s) {
+    constexpr int E = Tile<T>::E;
+    const size_t packed = (size_t)q.threads / 4 * p.cols * sizeof(T);
+    const bool pack = !p.sums && p.ld_out == p.cols && p.cols % E != 0 && aligned16(p.out) && q.lds + packed <= kLdsBytes;
+    if (pack) q.lds += packed;
+    const dim3 grid((unsigned)narrow_blocks(p.rows, q));
+    if (pack)
+        hipLaunchKernelGGL((k_prod_narrow<T, SL, true, false>), grid, dim3(q.threads), q.lds, s, p);
+    else if (!p.sums)
+        hipLaunchKernelGGL((k_prod_narrow<T, SL, false, false>), grid, dim3(q.threads), q.lds, s, p);
+    else if constexpr (sizeof(T) == 2)
+        hipLaunchKernelGGL((k_prod_narrow<T, SL, false, true>), grid, dim3(q.threads), q.lds, s, p);
+}
+
+template <typename T>
+void product(const ProdArgs& p, hipStream_t s) {
+    const Route q = route<T>(p.rows, p.cols, p.depth, p.sums != nullptr);
     // the streaming kernels read 16 bytes at a time: x and the residual have to span them
     const auto spans = [](int64_t rows, int64_t ld, int32_t count) { return (rows - 1) * ld + count >= Tile<T>::E; };
-    if (few || p.depth == 0 || !spans(p.rows, p.ld_a, p.depth) || (p.other && !spans(p.rows, p.ld_other, p.cols))) {
-        const int64_t y = tiles16 < 32768 ? tiles16 : 32768;
-        hipLaunchKernelGGL((k_prod_few<T>), dim3(groups, (unsigned)y, (unsigned)cdiv(tiles16, y)), dim3(256), 0, s, p);
+    if (q.few || !spans(p.rows, p.ld_a, p.depth) || (p.other && !spans(p.rows, p.ld_other, p.cols))) {
+        const int64_t tiles16 = cdiv(p.rows, 16), y = tiles16 < 32768 ? tiles16 : 32768;
+        hipLaunchKernelGGL((k_prod_few<T>), dim3(q.groups, (unsigned)y, (unsigned)cdiv(tiles16, y)), dim3(256), 0, s, p);
         return;
     }
     // 1M rows 128 -> 128 bfloat16 110 us against 167 by k_prod_big, 256 -> 192 204 against 343, 64 -> 64 float16 52
     // against 94; 100k rows 63 -> 128 float32 29 against 38
-    if (narrow) {
-        switch (steps) {
-            case 1: launch_narrow<T, 1>(p, lds, s); return;
-            case 2: launch_narrow<T, 2>(p, lds, s); return;
-            case 3: launch_narrow<T, 3>(p, lds, s); return;
-            case 4: launch_narrow<T, 4>(p, lds, s); return;
-            case 5: launch_narrow<T, 5>(p, lds, s); return;
-            case 6: launch_narrow<T, 6>(p, lds, s); return;
-            case 7: launch_narrow<T, 7>(p, lds, s); return;
-            case 8: launch_narrow<T, 8>(p, lds, s); return;
+    if (q.narrow) {
+        switch (q.steps) {
+            case 1: launch_narrow<T, 1>(p, q, s); return;
+            case 2: launch_narrow<T, 2>(p, q, s); return;
+            case 3: launch_narrow<T, 3>(p, q, s); return;
+            case 4: launch_narrow<T, 4>(p, q, s); return;
+            case 5: launch_narrow<T, 5>(p, q, s); return;
+            case 6: launch_narrow<T, 6>(p, q, s); return;
+            case 7: launch_narrow<T, 7>(p, q, s); return;
+            case 8: launch_narrow<T, 8>(p, q, s); return;
         }
     }
     if constexpr (sizeof(T) == 4) {
         // 150k rows 417 -> 64 106 us against 180 with 128 outputs a block, 150 -> 40 47 against 84
         if (p.cols <= 64) {
             const int64_t tiles = cdiv(p.rows, kBig);
-            hipLaunchKernelGGL((k_prod_big<T, 2>), dim3((unsigned)(cdiv(tiles, 8) * 8)), dim3(256), 0, s, p);
+            hipLaunchKernelGGL((k_prod_big<T, 2, false>), dim3((unsigned)(cdiv(tiles, 8) * 8)), dim3(256), 0, s, p);
             return;
         }
     }
     const int64_t tiles = cdiv(p.cols, kBig) * cdiv(p.rows, kBig);
-    hipLaunchKernelGGL((k_prod_big<T, 4>), dim3((unsigned)(cdiv(tiles, 8) * 8)), dim3(256), 0, s, p);
+    const dim3 grid((unsigned)(cdiv(tiles, 8) * 8));
+    if constexpr (sizeof(T) == 2) {
+        if (p.sums) {
+            hipLaunchKernelGGL((k_prod_big<T, 4, true>), grid, dim3(256), 0, s, p);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((k_prod_big<T, 4, false>), grid, dim3(256), 0, s, p);
+}
+
+// Runs of rows whose sums a product for dz leaves.
+template <typename T>
+int64_t sum_runs(int64_t rows, int32_t cols, int32_t depth) {
+    const Route q = route<T>(rows, cols, depth, true);
+    return q.few ? cdiv(rows, 16) : q.narrow ? narrow_blocks(rows, q) : cdiv(rows, 64);
 }
 
 struct DwArgs {
@@ -459,11 +549,14 @@ struct DwArgs {
     int64_t rows, ld_dz, ld_x, per;
     int32_t n_out, n_in;
     int32_t want_dw, want_db, splits;
+    const float* z_sums;  // [runs][n_out]: sums of dz's rows before its rounding; NULL: dz lost nothing by it
+    int64_t runs;
 };
 
 // One split of the rows for a 128 x 128 tile of dw: 64 x 64 per wave, the next
 // stage's rows on their way while this one's are multiplied.  The blocks of the
-// first column of tiles add up dz's columns as they pass.  65536 rows 512 -> 512 bfloat16
+// first column of tiles add up dz's columns as they pass, or the sums that its kernel
+// has left of them where dz was rounded.  65536 rows 512 -> 512 bfloat16
 // 56 us, 610 TFLOP/s: the stages' barriers bound it, as in k_prod_big.  Float32 layers of
 // few outputs have narrower tiles, or the products of nothing would bound them: dx, dw
 // and db of 150k rows 162 -> 9 104 us against 157 with 128 outputs, 417 -> 64 304
@@ -498,7 +591,7 @@ __global__ __launch_bounds__(256, 2) void k_dw(DwArgs p) {
         }
     };
     float sum[E] = {};
-    const bool sums = p.want_db && k0 == 0;
+    const bool sums = p.want_db && k0 == 0, add = sums && !p.z_sums;
     auto put = [&](int64_t m0, int buf, Frag (&z)[4], Frag (&x)[4]) {
         if (!even_z || m0 + kRows > m_end) {
 #pragma unroll
@@ -519,7 +612,7 @@ __global__ __launch_bounds__(256, 2) void k_dw(DwArgs p) {
             const int at = row_chunk<T, 128>(mr + i * kPass, ch);
             *reinterpret_cast<Frag*>(s_dz[buf] + at) = z[i];
             *reinterpret_cast<Frag*>(s_x[buf] + at) = x[i];
-            if (sums)
+            if (add)
 #pragma unroll
                 for (int j = 0; j < E; ++j) sum[j] += (float)z[i][j];
         }
@@ -570,7 +663,19 @@ __global__ __launch_bounds__(256, 2) void k_dw(DwArgs p) {
                 }
             }
     }
-    if (sums) {  // the threads of one chunk column, in order
+    if (sums && p.z_sums) {  // every splits-th run, half of them by each half of the block
+        float* s_sum = reinterpret_cast<float*>(s_dz[0]);  // [256]
+        const int n = n0 + (threadIdx.x & 127);
+        float t = 0.f;
+        if (n < p.n_out) {
+#pragma unroll 8
+            for (int64_t i = split + (int64_t)(threadIdx.x >> 7) * p.splits; i < p.runs; i += 2 * (int64_t)p.splits)
+                t += p.z_sums[i * p.n_out + n];
+        }
+        s_sum[threadIdx.x] = t;
+        __syncthreads();
+        if (threadIdx.x < 128 && n < p.n_out) part[n_w + n] = t + s_sum[threadIdx.x + 128];
+    } else if (sums) {  // the threads of one chunk column, in order
         float* s_sum = reinterpret_cast<float*>(s_dz[0]);  // [kPass][128]
 #pragma unroll
         for (int j = 0; j < E; ++j) s_sum[mr * 128 + ch * E + j] = sum[j];
@@ -788,7 +893,8 @@ inline bool element_aligned(const void* p, int32_t dtype) {
 struct BwdPlan {
     bool few, narrow;            // one kernel for few rows; one pass over the rows
     int32_t outs;                // outputs of a pass (narrow)
-    size_t dz, wt, part, bytes;  // offsets in the workspace
+    size_t dz, sums, wt, part, bytes;  // offsets in the workspace
+    int64_t runs;                      // of rows, whose sums of dz lie at `sums` (0: none)
     int64_t ld_dz;
     int splits;  // of the rows: partial dw and db
     int64_t per;
@@ -834,6 +940,13 @@ inline BwdPlan bwd_plan(const gs_linear* d) {
         p.ld_dz = cdiv(d->n_out, e) * e;
         p.dz = at;
         if (d->act != GS_ACT_NONE) at += pad256((size_t)d->rows * p.ld_dz * size_of(d->dtype));
+        p.sums = at;
+        // relu's dz is dy or 0, which no rounding changes
+        if (d->act != GS_ACT_NONE && d->act != GS_ACT_RELU && d->dtype != GS_F32 && d->rows > 0 && d->n_out > 0) {
+            p.runs = d->dtype == GS_F16 ? sum_runs<_Float16>(d->rows, d->n_out, d->n_in)
+                                        : sum_runs<__bf16>(d->rows, d->n_out, d->n_in);
+            at += pad256((size_t)p.runs * d->n_out * 4);
+        }
         p.wt = at;
         at += pad256((size_t)d->n_out * d->n_in * size_of(d->dtype));
         p.outs = d->n_out;
@@ -852,7 +965,7 @@ template <typename T>
 void fwd(const gs_linear* d, const void* x, const void* w, const void* bias, const void* residual, void* y,
          hipStream_t s) {
     ProdArgs p{x, w, bias, residual, y, d->rows, d->ld_x, d->n_in, d->ld_res, d->ld_y, d->n_out, d->n_in, EPI_FWD,
-               d->act};
+               d->act, nullptr};
     product<T>(p, s);
 }
 
@@ -903,9 +1016,11 @@ void bwd(const gs_linear* d, const void* x, const void* w, const void* bias, con
     const JoinArgs sums{part, dw, db, n_w + n_b, n_w, d->n_in, d->n_in, plan.splits, 0};
     const void* dz = dy;
     int64_t ld_dz = d->ld_y;
+    // made whether db is wanted or not: dz then has the same bits either way
+    float* z_sums = plan.runs > 0 ? reinterpret_cast<float*>(ws + plan.sums) : nullptr;
     if (d->act != GS_ACT_NONE && d->rows > 0 && d->n_out > 0) {
         ProdArgs p{x, w, bias, dy, ws + plan.dz, d->rows, d->ld_x, d->n_in, d->ld_y, plan.ld_dz, d->n_out, d->n_in,
-                   EPI_DZ, d->act};
+                   EPI_DZ, d->act, z_sums};
         product<T>(p, s);
         dz = ws + plan.dz;
         ld_dz = plan.ld_dz;
@@ -916,14 +1031,14 @@ void bwd(const gs_linear* d, const void* x, const void* w, const void* bias, con
             hipLaunchKernelGGL((k_transpose<T>), dim3((unsigned)cdiv(d->n_in, 64), (unsigned)cdiv(d->n_out, 64)),
                                dim3(256), 0, s, static_cast<const T*>(w), wt, d->n_out, d->n_in);
         ProdArgs p{dz, wt, nullptr, nullptr, dx, d->rows, ld_dz, d->n_out, 0, d->ld_dx, d->n_in, d->n_out, EPI_PLAIN,
-                   GS_ACT_NONE};
+                   GS_ACT_NONE, nullptr};
         product<T>(p, s);
     }
     if (!want_dw && !want_db) return;
     // without dw there is one column of tiles, and its x side reads dz (the product is not stored)
     DwArgs q{dz, want_dw ? x : dz, part, d->rows, ld_dz, want_dw ? d->ld_x : ld_dz, plan.per, d->n_out,
              want_dw ? d->n_in : 1, want_dw, want_db,
-             plan.splits};
+             plan.splits, z_sums, plan.runs};
     const int64_t blocks = cdiv(q.n_out, 128) * cdiv(q.n_in, 128) * plan.splits;
     const dim3 grid((unsigned)(cdiv(blocks, 8) * 8));
     if constexpr (sizeof(T) == 4) {

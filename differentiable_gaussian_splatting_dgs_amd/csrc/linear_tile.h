@@ -230,6 +230,29 @@ __device__ __forceinline__ void slope_run(int act, float (&v)[N], const float (&
     }
 }
 
+// v of another lane of the 16 of a lane group.
+template <int CTRL>
+__device__ __forceinline__ float moved(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+
+// Sums of a run's 8 columns over the rows of the 16 lanes r: columns pair_of(r) and the
+// next, the same bits in the four lanes that share them.  Neighbours first halve what
+// each of them has to add: 10 additions and 12 selections where every column's own
+// sum in every lane would take 32 additions.
+__device__ __forceinline__ int pair_of(int r) { return 4 * (r & 1) + (r & 2); }
+__device__ __forceinline__ void run_sums(const float (&v)[8], int r, float (&sum)[2]) {
+    float q[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[j] = (r & 1 ? v[j + 4] : v[j]) + moved<0xb1>(r & 1 ? v[j] : v[j + 4]);  // lanes 1 0 3 2
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        sum[j] = (r & 2 ? q[j + 2] : q[j]) + moved<0x4e>(r & 2 ? q[j] : q[j + 2]);  // lanes 2 3 0 1
+        sum[j] += moved<0x128>(sum[j]);                                             // eight lanes on
+        sum[j] += moved<0x124>(sum[j]);                                             // four lanes on
+    }
+}
+
 // Fragments of the transposed operands of dw = dz^T x, whose sum runs down the
 // rows: a step takes KS rows, and lane l needs, of column l % 16, E of them.  The
 // tile lies in LDS in its own row order, COLS columns a row.  16-bit: two

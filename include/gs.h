@@ -641,8 +641,10 @@ int gs_linear_bwd_workspace_size(const gs_linear* d, size_t* bytes);
  * dx = dz w, dw = dz^T x, db = sum over rows of dz; the residual's gradient is
  * dy itself.  z is recomputed from x, w and bias (the forward keeps nothing).
  * Each of dx, dw and db may be NULL (not computed); a given one is overwritten.
- * dz enters the products rounded to the layer's type; the sums over rows are
- * split and joined in a fixed order, so results are the same from run to run.
+ * dz enters the products dx and dw rounded to the layer's type (for more than 16
+ * rows: with a float16 layer a dz past 65504 is infinite there); db is summed from
+ * it before that rounding.  The sums over rows are split and joined in a fixed
+ * order, so results are the same from run to run.
  * With rows == 0, dw and db are zero.  workspace: gs_linear_bwd_workspace_size()
  * bytes, 256-byte aligned, contents on entry irrelevant.
  */
