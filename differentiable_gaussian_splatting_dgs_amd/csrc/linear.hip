@@ -29,8 +29,11 @@ struct ProdArgs {
     void* out;
     int64_t rows, ld_a, ld_b, ld_other, ld_out;
     int32_t cols, depth, epi, act;
-    float* sums;  // DZ: [runs of rows][cols], the sums of dz's rows before its rounding, or NULL
+    float* sums;  // DZ: [runs of rows][ld_sums(cols)], the sums of dz's rows before its rounding, or NULL
+    int32_t block_runs;  // k_prod_narrow: a run is a block's rows, added up in LDS, else 16 rows
 };
+
+inline __host__ __device__ int64_t ld_sums(int32_t cols) { return ((int64_t)cols + 3) / 4 * 4; }
 
 // The epilogue of N runs (E consecutive outputs of one row each), with the runs of
 // the residual or dy already in `other`; one switch over the kinds for all of them.
@@ -54,13 +57,12 @@ __device__ __forceinline__ void finish_runs(const ProdArgs& p, float (&v)[N * Ti
     for (int j = 0; j < N * E; ++j) out[j / E][j % E] = (T)v[j];
 }
 
-// Stores the sums of a run's columns over the rows of the lanes: count columns from c0 on, at `to`.
+// Stores the sums of columns c0 to c0 + 7 over the rows of the lanes at `to`, a row of ld_sums(count) floats.
 __device__ __forceinline__ void store_sums(float* to, int c0, int count, const float (&v)[8], int r) {
     float sum[2];
     run_sums(v, r, sum);
     const int c = c0 + pair_of(r);
-    if (r < 4 && c < count) to[c] = sum[0];
-    if (r < 4 && c + 1 < count) to[c + 1] = sum[1];
+    if (r < 4 && c < count) *reinterpret_cast<float2*>(to + c) = make_float2(sum[0], sum[1]);
 }
 
 // Few outputs or few rows: a block makes one group of KS outputs of 16 rows, its
@@ -131,7 +133,7 @@ __global__ __launch_bounds__(256) void k_prod_few(ProdArgs p) {
         if (p.sums) {  // a run of 16 rows
 #pragma unroll
             for (int j = 0; j < E; ++j) v[j] = in ? v[j] : 0.f;
-            store_sums(p.sums + (row - r) / 16 * p.cols, c0, p.cols, v, r);
+            store_sums(p.sums + (row - r) / 16 * ld_sums(p.cols), c0, p.cols, v, r);
         }
     }
 }
@@ -148,8 +150,8 @@ __global__ __launch_bounds__(256) void k_prod_few(ProdArgs p) {
 // 3M rows 64 -> 59 float16 138 us, 5.3 TB/s.  Float32 ones by the matrix rate and, under
 // it, the start: 1M rows 128 -> 128 390 us, 84 TFLOP/s beside 2.6 TB/s; 100k rows
 // 63 -> 128 28 us, of which 11 are products.
-// SUMS: dz for a wide layer's backward, whose rows each wave adds up in LDS on their way
-// (the backward of 1M rows 128 -> 256 float16 635 us against 615 without db's sums).
+// SUMS: dz for a wide layer's backward, whose rows are added up on their way (the
+// backward of 300k rows 128 -> 256 bfloat16 202 us against 196 without db's sums).
 constexpr int narrow_threads(int sl) { return sl <= 4 ? 1024 : 512; }  // at most: deep rows need 256 registers
 template <typename T, int SL, bool PACK, bool SUMS>
 __global__ __launch_bounds__(narrow_threads(SL), sizeof(T) == 4 ? 4 : 1) void k_prod_narrow(ProdArgs p) {
@@ -209,7 +211,7 @@ __global__ __launch_bounds__(narrow_threads(SL), sizeof(T) == 4 ? 4 : 1) void k_
     for (int i = threadIdx.x; i < groups * KS; i += blockDim.x)
         reinterpret_cast<float*>(s_bias)[i] =
             p.bias && i < p.cols ? (float)static_cast<const T*>(p.bias)[i] : 0.f;
-    if (SUMS)
+    if (SUMS && p.block_runs)
         for (int i = threadIdx.x; i < waves * groups * KS; i += blockDim.x) s_sum[i] = 0.f;
     __syncthreads();
     for (; tile < tiles; tile += step) {
@@ -254,10 +256,14 @@ __global__ __launch_bounds__(narrow_threads(SL), sizeof(T) == 4 ? 4 : 1) void k_
                 if constexpr (SUMS) {
 #pragma unroll
                     for (int j = 0; j < E; ++j) v[j] = row < p.rows ? v[j] : 0.f;
-                    float sum[2];
-                    run_sums(v, r, sum);
-                    float* to = s_sum + (wave * groups + n + h) * KS + E * g + pair_of(r);
-                    if (r < 4) to[0] += sum[0], to[1] += sum[1];
+                    if (p.block_runs) {
+                        float sum[2];
+                        run_sums(v, r, sum);
+                        float* to = s_sum + (wave * groups + n + h) * KS + E * g + pair_of(r);
+                        if (r < 4) to[0] += sum[0], to[1] += sum[1];
+                    } else {
+                        store_sums(p.sums + tile * ld_sums(p.cols), (n + h) * KS + E * g, p.cols, v, r);
+                    }
                 }
             }
             if (PACK || row < p.rows) {
@@ -278,12 +284,12 @@ __global__ __launch_bounds__(narrow_threads(SL), sizeof(T) == 4 ? 4 : 1) void k_
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         }
     }
-    if (SUMS) {  // a run is the block's rows
+    if (SUMS && p.block_runs) {
         __syncthreads();
         for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
             float t = 0.f;
             for (int i = 0; i < waves; ++i) t += s_sum[i * groups * KS + c];
-            p.sums[(int64_t)blockIdx.x * p.cols + c] = t;
+            p.sums[blockIdx.x * ld_sums(p.cols) + c] = t;
         }
     }
 }
@@ -424,23 +430,36 @@ __global__ __launch_bounds__(256, 2) void k_prod_big(ProdArgs p) {
             float sum[E] = {};
 #pragma unroll
             for (int j = 0; j < 4 * E; ++j) sum[j % E] += m0 + wm + 16 * (j / E) + r < p.rows ? v[j] : 0.f;
-            if (m0 + wm < p.rows) store_sums(p.sums + (m0 + wm) / 64 * p.cols, c0, p.cols, sum, r);
+            if (m0 + wm < p.rows) store_sums(p.sums + (m0 + wm) / 64 * ld_sums(p.cols), c0, p.cols, sum, r);
         }
     }
 }
 
 constexpr size_t kLdsBytes = 160 * 1024;
 
-// The kernel that a product takes, and the grid of k_prod_narrow.
+// The kernel that a product takes, and the block of k_prod_narrow.
 struct Route {
     bool few, narrow;
     int groups, steps;
     int threads;
     size_t lds;
+    bool block_runs;  // sums of dz's rows go through LDS
 };
 
-// sums: of dz's rows, for which each wave of k_prod_narrow has LDS of its own.  Eight waves are then taken where
-// sixteen find no room (20000 rows 128 -> 520 bfloat16), and k_prod_big where eight do not (128 -> 600).
+// Blocks of k_prod_narrow that a CU holds.
+inline int per_cu(size_t lds, int threads) {
+    const int n = (int)(kLdsBytes / lds);
+    return n < 1024 / threads ? n : 1024 / threads;
+}
+inline int64_t narrow_blocks(int64_t rows, const Route& q) {
+    const int64_t blocks = cdiv(cdiv(rows, 16), q.threads / 64), most = 256 * per_cu(q.lds, q.threads);
+    return blocks < most ? blocks : most;
+}
+
+// sums: of dz's rows.  Each wave of k_prod_narrow adds them up in LDS unless the CU then holds fewer blocks, and leaves
+// those of every 16 rows if it does (the backward of 300k rows 128 -> 256 bfloat16 202 us, 212 with every 16 rows;
+// 64 -> 512 354 us, 370 with LDS and fewer blocks).
+
 template <typename T>
 Route route(int64_t rows, int32_t cols, int32_t depth, bool sums) {
     constexpr int KS = Tile<T>::KS;
@@ -450,11 +469,10 @@ Route route(int64_t rows, int32_t cols, int32_t depth, bool sums) {
     q.lds = (size_t)q.groups * KS * (q.steps * KS * sizeof(T) + 4);
     q.narrow = q.lds <= kLdsBytes && q.steps <= 8;
     q.threads = q.lds <= 40960 ? 256 : q.lds <= 81920 || q.steps > 4 ? 512 : 1024;
-    if (sums) {
-        const size_t wave = (size_t)q.groups * KS * 4;
-        if (q.threads == 1024 && q.lds + 16 * wave > kLdsBytes) q.threads = 512;
-        q.lds += q.threads / 64 * wave;
-        q.narrow = q.narrow && q.lds <= kLdsBytes;
+    if (sums && q.narrow) {
+        const size_t lds = q.lds + (size_t)q.threads / 64 * q.groups * KS * 4;
+        q.block_runs = per_cu(lds, q.threads) == per_cu(q.lds, q.threads);
+        if (q.block_runs) q.lds = lds;
     }
     // Few tiles: a call of ordinary length is its launch, until about 2048 blocks of k_prod_few (500 rows 512 -> 512
     // bfloat16 8.5 us against 11.2 by k_prod_big, 1000 rows 8.9 against 11.8, 2000 rows 13.8 against 11.9; 16000 rows
@@ -470,19 +488,13 @@ Route route(int64_t rows, int32_t cols, int32_t depth, bool sums) {
     return q;
 }
 
-inline int64_t narrow_blocks(int64_t rows, const Route& q) {
-    int per_cu = (int)(kLdsBytes / q.lds);
-    if (per_cu > 1024 / q.threads) per_cu = 1024 / q.threads;
-    const int64_t blocks = cdiv(cdiv(rows, 16), q.threads / 64);
-    return blocks < 256 * per_cu ? blocks : 256 * per_cu;
-}
-
 template <typename T, int SL>
-void launch_narrow(const ProdArgs& p, Route q, hipStream_t s) {
+void launch_narrow(ProdArgs p, Route q, hipStream_t s) {
     constexpr int E = Tile<T>::E;
     const size_t packed = (size_t)q.threads / 4 * p.cols * sizeof(T);
     const bool pack = !p.sums && p.ld_out == p.cols && p.cols % E != 0 && aligned16(p.out) && q.lds + packed <= kLdsBytes;
     if (pack) q.lds += packed;
+    p.block_runs = q.block_runs;
     const dim3 grid((unsigned)narrow_blocks(p.rows, q));
     if (pack)
         hipLaunchKernelGGL((k_prod_narrow<T, SL, true, false>), grid, dim3(q.threads), q.lds, s, p);
@@ -539,7 +551,7 @@ void product(const ProdArgs& p, hipStream_t s) {
 template <typename T>
 int64_t sum_runs(int64_t rows, int32_t cols, int32_t depth) {
     const Route q = route<T>(rows, cols, depth, true);
-    return q.few ? cdiv(rows, 16) : q.narrow ? narrow_blocks(rows, q) : cdiv(rows, 64);
+    return !q.few && q.block_runs ? narrow_blocks(rows, q) : cdiv(rows, q.few || q.narrow ? 16 : 64);
 }
 
 struct DwArgs {
@@ -549,7 +561,7 @@ struct DwArgs {
     int64_t rows, ld_dz, ld_x, per;
     int32_t n_out, n_in;
     int32_t want_dw, want_db, splits;
-    const float* z_sums;  // [runs][n_out]: sums of dz's rows before its rounding; NULL: dz lost nothing by it
+    const float* z_sums;  // [runs][ld_sums(n_out)]: sums of dz's rows before its rounding; NULL: dz lost nothing by it
     int64_t runs;
 };
 
@@ -663,18 +675,23 @@ __global__ __launch_bounds__(256, 2) void k_dw(DwArgs p) {
                 }
             }
     }
-    if (sums && p.z_sums) {  // every splits-th run, half of them by each half of the block
-        float* s_sum = reinterpret_cast<float*>(s_dz[0]);  // [256]
-        const int n = n0 + (threadIdx.x & 127);
-        float t = 0.f;
-        if (n < p.n_out) {
+    if (sums && p.z_sums) {  // every splits-th run, an eighth of them by 32 threads with four outputs each
+        float* s_sum = reinterpret_cast<float*>(s_dz[0]);  // [8][128]
+        const int c = (threadIdx.x & 31) * 4, part8 = threadIdx.x >> 5;
+        f32x4 t = {};
+        if (n0 + c < p.n_out) {
+            const float* from = p.z_sums + n0 + c;
 #pragma unroll 8
-            for (int64_t i = split + (int64_t)(threadIdx.x >> 7) * p.splits; i < p.runs; i += 2 * (int64_t)p.splits)
-                t += p.z_sums[i * p.n_out + n];
+            for (int64_t i = split + (int64_t)part8 * p.splits; i < p.runs; i += 8 * (int64_t)p.splits)
+                t += *reinterpret_cast<const f32x4*>(from + i * ld_sums(p.n_out));
         }
-        s_sum[threadIdx.x] = t;
+        *reinterpret_cast<f32x4*>(s_sum + part8 * 128 + c) = t;
         __syncthreads();
-        if (threadIdx.x < 128 && n < p.n_out) part[n_w + n] = t + s_sum[threadIdx.x + 128];
+        if (threadIdx.x < 128 && n0 + (int)threadIdx.x < p.n_out) {
+            float sum_of = 0.f;
+            for (int i = 0; i < 8; ++i) sum_of += s_sum[i * 128 + threadIdx.x];
+            part[n_w + n0 + threadIdx.x] = sum_of;
+        }
     } else if (sums) {  // the threads of one chunk column, in order
         float* s_sum = reinterpret_cast<float*>(s_dz[0]);  // [kPass][128]
 #pragma unroll
@@ -945,7 +962,7 @@ inline BwdPlan bwd_plan(const gs_linear* d) {
         if (d->act != GS_ACT_NONE && d->act != GS_ACT_RELU && d->dtype != GS_F32 && d->rows > 0 && d->n_out > 0) {
             p.runs = d->dtype == GS_F16 ? sum_runs<_Float16>(d->rows, d->n_out, d->n_in)
                                         : sum_runs<__bf16>(d->rows, d->n_out, d->n_in);
-            at += pad256((size_t)p.runs * d->n_out * 4);
+            at += pad256((size_t)p.runs * ld_sums(d->n_out) * 4);
         }
         p.wt = at;
         at += pad256((size_t)d->n_out * d->n_in * size_of(d->dtype));
@@ -965,7 +982,7 @@ template <typename T>
 void fwd(const gs_linear* d, const void* x, const void* w, const void* bias, const void* residual, void* y,
          hipStream_t s) {
     ProdArgs p{x, w, bias, residual, y, d->rows, d->ld_x, d->n_in, d->ld_res, d->ld_y, d->n_out, d->n_in, EPI_FWD,
-               d->act, nullptr};
+               d->act, nullptr, 0};
     product<T>(p, s);
 }
 
@@ -1020,7 +1037,7 @@ void bwd(const gs_linear* d, const void* x, const void* w, const void* bias, con
     float* z_sums = plan.runs > 0 ? reinterpret_cast<float*>(ws + plan.sums) : nullptr;
     if (d->act != GS_ACT_NONE && d->rows > 0 && d->n_out > 0) {
         ProdArgs p{x, w, bias, dy, ws + plan.dz, d->rows, d->ld_x, d->n_in, d->ld_y, plan.ld_dz, d->n_out, d->n_in,
-                   EPI_DZ, d->act, z_sums};
+                   EPI_DZ, d->act, z_sums, 0};
         product<T>(p, s);
         dz = ws + plan.dz;
         ld_dz = plan.ld_dz;
@@ -1031,7 +1048,7 @@ void bwd(const gs_linear* d, const void* x, const void* w, const void* bias, con
             hipLaunchKernelGGL((k_transpose<T>), dim3((unsigned)cdiv(d->n_in, 64), (unsigned)cdiv(d->n_out, 64)),
                                dim3(256), 0, s, static_cast<const T*>(w), wt, d->n_out, d->n_in);
         ProdArgs p{dz, wt, nullptr, nullptr, dx, d->rows, ld_dz, d->n_out, 0, d->ld_dx, d->n_in, d->n_out, EPI_PLAIN,
-                   GS_ACT_NONE, nullptr};
+                   GS_ACT_NONE, nullptr, 0};
         product<T>(p, s);
     }
     if (!want_dw && !want_db) return;
