@@ -725,9 +725,9 @@ __global__ __launch_bounds__(256) void k_transpose(const T* in, T* out, int32_t 
 // here) and the partial dx that this group of outputs gives.  The weights are read
 // twice, the second time from the caches; what bounds it is latency: 8 rows 512 -> 1021
 // float32 11 us and 4 for the join.  Two launches in place of the general path's five,
-// or of a grid that so few rows leave empty: 8 rows 512 -> 1021 float32 17 us a call
-// against 29, 16 rows 256 -> 256 bfloat16 18 against 27; 64 -> 64, which one block of
-// k_bwd_narrow holds, 17 against 15.
+// or of a grid that so few rows leave empty: 8 rows 512 -> 1021 float32 16 us a call
+// against 28, 16 rows 256 -> 256 bfloat16 18 against 25, 128 -> 128 16.6 against 17.1 by
+// one block of k_bwd_narrow; 64 -> 64 16 against 14, which would round dz.
 constexpr int kFewRows = 16;
 struct FewArgs {
     const void* x;
@@ -919,15 +919,19 @@ struct BwdPlan {
 
 // Few inputs, an activation and more outputs than a pass holds: passes over parts of the
 // outputs, so that dz, many times x, makes no trip through memory.  1.76M rows 10 -> 364
-// bfloat16 723 us against 1673 by separate products, 375k rows 63 -> 708 float32 2143
-// against 2455; 300k rows 64 -> 512 bfloat16 349 against 341 and 20k rows 32 -> 512 79
-// against 58, where the parts' dx in float32 and their launches weigh more.
+// bfloat16 691 us against 1836 by separate products, 375k rows 63 -> 708 float32 1580
+// against 2123, 300k rows 64 -> 512 bfloat16 270 against 354.  Where there are few rows,
+// or more inputs, the parts' dx in float32 and their launches weigh more: 20k rows
+// 20 -> 512 80 against 57; of more than 32 16-bit inputs 100k rows take 0.80 to 1.12
+// times as long, 131072 rows 0.79 to 1.08, 200k rows 0.70 to 0.88; 300k rows 90 -> 512
+// 485 against 357.
 template <typename T>
 inline bool plan_narrow(const gs_linear* d, BwdPlan& p) {
     constexpr int kMost = kBwdGroups * Tile<T>::KS;
     if (d->rows <= kFewRows || d->n_out < 1) return false;
     p.outs = d->n_out;
-    if (d->n_out > kMost && d->rows >= 65536 && d->act != GS_ACT_NONE && d->n_in <= kPartInputs<T>) p.outs = kMost;
+    const int64_t least = sizeof(T) == 2 && d->n_in > Tile<T>::KS ? 131072 : 65536;
+    if (d->n_out > kMost && d->rows >= least && d->act != GS_ACT_NONE && d->n_in <= kPartInputs) p.outs = kMost;
     if (!bwd_narrow_fits<T>(d->n_in, p.outs)) return false;
     p.splits = bwd_narrow_blocks<T>(d->rows, d->n_in, p.outs);
     return true;

@@ -44,9 +44,7 @@ struct BwdArgs {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kBwdGroups = 4;  // groups of KS inputs and of KS outputs at most
-// Inputs of a layer that goes through in parts of its outputs, at most.
-template <typename T>
-constexpr int kPartInputs = sizeof(T) == 4 ? kBwdGroups * Tile<T>::KS : Tile<T>::KS;
+constexpr int kPartInputs = 64;  // of a layer that goes through in parts of its outputs, at most
 
 template <typename T, int SL, int NG>
 struct BwdGeom {
@@ -378,7 +376,7 @@ inline void bwd_narrow_one(const BwdArgs& p, int64_t rows, int* blocks, hipStrea
     }
     if (!p.dx_sum)
         hipLaunchKernelGGL((k_bwd_narrow<T, SL, NG, false>), dim3(*blocks), dim3(G::kWaves * 64), G::kLds, s, p);
-    else if constexpr (NG == kBwdGroups && SL * Tile<T>::KS <= kPartInputs<T>)
+    else if constexpr (NG == kBwdGroups && SL * Tile<T>::KS <= kPartInputs)
         hipLaunchKernelGGL((k_bwd_narrow<T, SL, NG, true>), dim3(*blocks), dim3(G::kWaves * 64), G::kLds, s, p);
 }
 

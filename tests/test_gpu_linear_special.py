@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from test_gpu_linear import TINY, TYPES, U, U32, inputs, run_bwd
+from test_gpu_linear import TINY, TYPES, U, U32, check, exact_bwd, inputs, run_bwd
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +62,16 @@ def test_second_derivative_raises():
     assert torch.equal(g, torch.autograd.grad(network.linear(x, w, b, r, act="silu").sum(), x)[0])
     with pytest.raises(gs.GsError, match="differentiated once"):
         (y + g.square().sum()).backward()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("size", [(131_071, 40, 140), (131_072, 40, 140), (131_100, 64, 300), (131_500, 33, 257)])
+def test_parts_of_more_inputs(size, dtype):
+    """Either side of the rows from which layers of 33 to 64 inputs go through in parts of their outputs."""
+    x, w, b, _, dy = inputs(*size, dtype, pad=5)
+    got = run_bwd(dy, x, w, b, "silu")
+    for name, g, (v, tol) in zip(("dx", "dw", "db"), got, exact_bwd(x, w, b, dy, "silu")):
+        check(g, v, tol, (size, name))
+    x[7, 0] = float("inf")
+    dx = run_bwd(dy, x, w, b, "relu")[0]
+    assert torch.isfinite(dx[7]).all()
