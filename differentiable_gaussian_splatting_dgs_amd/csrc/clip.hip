@@ -247,8 +247,8 @@ __device__ __forceinline__ void give4(float* p, f32x4 v) {
 
 // STREAM: for more than the last-level cache holds, parameters and moments pass it by
 // (non-temporal) and blocks run from the last tensor's end, where the norm left the
-// gradients in it: 59M float32 parameters 245 against 305 us (6.7 TB/s); 5.9M, which
-// the cache holds from step to step, 28 against 25.
+// gradients in it: 59M float32 parameters 261 against 314 us (6.4 TB/s); 5.9M, which
+// the cache holds from step to step, 27.4 against 26.5.
 template <bool STREAM>
 __global__ __launch_bounds__(kThreads) void k_adam_clipped(ClipAdamArgs a) {
     const float coef = a.clip ? a.clip[1] : 1.f;
