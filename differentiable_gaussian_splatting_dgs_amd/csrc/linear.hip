@@ -301,7 +301,8 @@ __global__ __launch_bounds__(narrow_threads(SL), sizeof(T) == 4 ? 4 : 1) void k_
 // stage (0.4 us) is shorter than the memory's answer.  65536 rows 512 -> 512 bfloat16
 // 64 us, 530 TFLOP/s, and 54 us, 640 TFLOP/s, without an activation; 1024 -> 1024 218
 // us; float32 512 -> 512 316 us, 109 TFLOP/s.  The matrix units are busy for 40% of the
-// 16-bit time; the rest is the barrier of each stage, at two blocks a CU.  256 x 128
+// 16-bit time, the fragments' reads take as many cycles of LDS, and each stage ends in
+// a barrier, at two blocks a CU.  256 x 128
 // outputs over eight waves take as long (72 us against 74, 213 against 218).
 constexpr int kBig = 128;  // rows and outputs of a block
 template <typename T, int NT, bool SUMS>  // NT: tiles of 16 outputs a wave has, 4 (128 outputs a block) or 2 (64)

@@ -68,7 +68,8 @@ def linear(x, w, bias=None, residual=None, act="none"):
     gradient) raises GsError, but for the residual's.  Forward mode raises NotImplementedError.
 
     x [rows, n_in], w [n_out, n_in], bias [n_out], residual [rows, n_out], all of one type (float32, float16 or
-    bfloat16); x and residual may have strided rows.  act: "none", "relu", "silu" or "gelu" (tanh form)."""
+    bfloat16); x and residual may have strided rows, which must not overlap (but the residual may be one row expanded).
+    act: "none", "relu", "silu" or "gelu" (tanh form)."""
     # under forward mode a tensor with a tangent need not require a gradient: the function raises for it
     if forward_ad._current_level >= 0 or torch.is_grad_enabled() and (
             x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad) or
