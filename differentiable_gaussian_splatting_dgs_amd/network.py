@@ -182,12 +182,16 @@ class Adam:
         self._dtype_words = np.frombuffer(self.table, dtype=np.int32)[field.grad_dtype.offset // 4::size // 4][:n]
         self._describe()
 
-    def _pointers(self):
-        at = torch.Tensor.data_ptr
+    def _places(self):
+        """Where every tensor lies and whether it is contiguous, the copies' types and the lengths of the rows to
+        renormalise: what a step compares with the table."""
+        copies = [c for c in self.copies if c is not None]
+        tensors = [*self.params, *self.exp_avg, *self.exp_avg_sq, *copies]
         try:
-            return [*map(at, self.params), *map(at, self.exp_avg), *map(at, self.exp_avg_sq),
-                    *[0 if c is None else at(c) for c in self.copies]]
-        except TypeError:
+            return ([*map(torch.Tensor.data_ptr, tensors)], all(map(torch.Tensor.is_contiguous, tensors)),
+                    [c if c is None else c.dtype for c in self.copies],
+                    self.normalize_rows and [p.shape for i, p in enumerate(self.params) if i in self.normalize_rows])
+        except (TypeError, AttributeError):
             raise GsError("parameters, moments and copies must be tensors") from None
 
     def _describe(self):
@@ -197,7 +201,7 @@ class Adam:
         n = len(self.params)
         if not len(self.exp_avg) == len(self.exp_avg_sq) == len(self.copies) == n == len(self._dtype_words):
             raise GsError("copies and the moments need one entry for each parameter")
-        described, rows = self._pointers(), []
+        described, rows = self._places(), []
         for i, (p, m, v, c) in enumerate(zip(self.params, self.exp_avg, self.exp_avg_sq, self.copies)):
             at = [gs._p(p, torch.float32, f"parameter {i}")]
             for t, k in ((m, "exp_avg"), (v, "exp_avg_sq")):
@@ -228,10 +232,10 @@ class Adam:
         if len(grads) != len(self.params):
             raise GsError(f"{len(self.params)} parameters, {len(grads)} gradients")
         packed = gs._grad_table(grads, None)
-        if self._pointers() != self._described or not all(map(torch.Tensor.is_contiguous, self.params)):
+        if self._places() != self._described:
             self._describe()
         for g, p, shape in zip(grads, self.params, self._shapes):
-            if not g.shape == shape == p.shape:
+            if g.shape != shape:
                 if g.shape != p.shape:
                     raise GsError("a gradient must have its parameter's shape")
                 self._describe()  # another shape in the same memory

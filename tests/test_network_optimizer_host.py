@@ -216,3 +216,24 @@ def test_a_clip_counts_as_a_change(clip_calls, monkeypatch, inference):
         c.clip(g)
         if not inference:
             assert [t._version for t in g + out] == [1, 1, 1, 1]
+
+
+def test_a_copy_of_another_type_in_the_same_memory(calls):
+    opt = optimizer()
+    grads = [torch.randn(p.shape) for p in opt.params]
+    opt.step(grads)
+    opt.copies[0] = opt.copies[0].view(torch.bfloat16)
+    opt.step(grads)
+    assert calls[0][0]["copy"] == calls[1][0]["copy"]
+    expect(opt, grads, calls[1])
+
+
+@pytest.mark.parametrize("name", ["exp_avg", "exp_avg_sq", "copies"])
+def test_transposed_moments_and_copies_are_refused(calls, name):
+    """The parameter's address, shape and type, another order."""
+    p = torch.randn(4, 4)
+    opt = network.Adam([p], lr=1e-3, copies=[p.half()])
+    opt.step([torch.randn(4, 4)])
+    getattr(opt, name)[0].data = getattr(opt, name)[0].data.t()
+    with pytest.raises(gs.GsError):
+        opt.step([torch.randn(4, 4)])
