@@ -1,0 +1,38 @@
+// What the entry points of cross attention hand to its kernels.
+#pragma once
+
+#include "gs_internal.h"
+
+namespace gs {
+
+struct Div {  // n / d for n < 2^31
+    uint32_t mul, shift;
+};
+
+struct AttnArgs {
+    const void *q, *k, *v, *dout;
+    const uint8_t* mask;                   // [batch] rows of nk, or NULL
+    const int32_t *q_lengths, *k_lengths;  // [batch], or NULL
+    void* out;                             // read by the backward
+    float* lse;                            // [batch, heads, nq]
+    float* delta;                          // the backward's sums of dout * out, like lse
+    void *dq, *dk, *dv;
+    int64_t q_b, q_n, q_h, k_b, k_n, k_h, v_b, v_n, v_h, g_b, g_n, g_h, mask_b;  // strides (g: dout's)
+    int32_t batch, nq, nk, heads, kv_heads, group, d;
+    float scale;
+    Div by_group, by_kv;
+    int32_t tiles;  // of rows or keys of a problem
+};
+
+inline Div div_by(uint32_t d) {
+    uint32_t l = 0;
+    while ((1ull << l) < d) ++l;
+    return Div{(uint32_t)(((1ull << 32) * ((1ull << l) - d)) / d + 1), l};
+}
+
+template <typename T>
+void attn_fwd(const AttnArgs& p, hipStream_t s);
+template <typename T>
+void attn_bwd(const AttnArgs& p, hipStream_t s);
+
+}  // namespace gs

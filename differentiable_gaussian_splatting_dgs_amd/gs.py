@@ -66,6 +66,24 @@ class GsLinear(C.Structure):
                 ("ld_dx", C.c_int64)]
 
 
+class GsAttention(C.Structure):
+    _fields_ = [("batch", C.c_int64), ("nq", C.c_int64), ("nk", C.c_int64), ("heads", C.c_int32),
+                ("kv_heads", C.c_int32), ("d", C.c_int32), ("dtype", C.c_int32), ("q_stride", C.c_int64 * 3),
+                ("k_stride", C.c_int64 * 3), ("v_stride", C.c_int64 * 3), ("dout_stride", C.c_int64 * 3),
+                ("mask_stride", C.c_int64), ("scale", C.c_float)]
+
+
+class GsLayerNorm(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("n", C.c_int32), ("dtype", C.c_int32), ("ld_x", C.c_int64),
+                ("ld_y", C.c_int64), ("ld_dx", C.c_int64), ("eps", C.c_float)]
+
+
+class GsDropoutArgs(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("n", C.c_int32), ("dtype", C.c_int32), ("ld_x", C.c_int64),
+                ("ld_y", C.c_int64), ("ld_res", C.c_int64), ("p", C.c_double), ("seed", C.c_uint64),
+                ("offset", C.c_uint64)]
+
+
 class GsGradTensor(C.Structure):
     _fields_ = [("grad", C.c_void_p), ("out", C.c_void_p), ("count", C.c_int64), ("dtype", C.c_int32)]
 
@@ -88,7 +106,9 @@ SYMBOLS = ["gs_error_string", "gs_version", "gs_tile_grid", "gs_preprocess", "gs
            "gs_preprocess_bwd_adam_views", "gs_count_pairs_views", "gs_count_nonfinite",
            "gs_preprocess_h16", "gs_render_fwd_h16", "gs_render_bwd_h16", "gs_count_pairs_h16",
            "gs_linear_fwd", "gs_linear_bwd_workspace_size", "gs_linear_bwd", "gs_grad_workspace_size", "gs_grad_norm",
-           "gs_grad_clip", "gs_adam_step_clipped"]
+           "gs_grad_clip", "gs_adam_step_clipped",
+           "gs_attention_fwd", "gs_attention_bwd_workspace_size", "gs_attention_bwd", "gs_layer_norm_fwd",
+           "gs_layer_norm_bwd_workspace_size", "gs_layer_norm_bwd", "gs_dropout"]
 MAX_VIEWS = 8
 PARAM_ORDER = ("means", "log_scales", "quats", "opacity_logits", "sh")
 
@@ -157,6 +177,13 @@ def load_library(path=LIB_PATH):
     lib.gs_grad_workspace_size.argtypes = [_i32, P(C.c_size_t)]
     lib.gs_grad_norm.argtypes = [_i32, _vp, C.c_float, _vp, _vp, C.c_size_t, _vp]
     lib.gs_grad_clip.argtypes = [_i32, _vp, C.c_float, _vp, _vp, C.c_size_t, _vp]
+    lib.gs_attention_fwd.argtypes = [_vp] * 10
+    lib.gs_attention_bwd_workspace_size.argtypes = [_vp, P(C.c_size_t)]
+    lib.gs_attention_bwd.argtypes = [_vp] * 14 + [C.c_size_t, _vp]
+    lib.gs_layer_norm_fwd.argtypes = [_vp] * 6
+    lib.gs_layer_norm_bwd_workspace_size.argtypes = [_vp, P(C.c_size_t)]
+    lib.gs_layer_norm_bwd.argtypes = [_vp] * 8 + [C.c_size_t, _vp]
+    lib.gs_dropout.argtypes = [_vp] * 6
     lib.gs_adam_step_clipped.argtypes = [_i32, _vp, C.c_float, C.c_float, C.c_float, _i32, _vp, _vp]
     for name in SYMBOLS:
         if name not in ("gs_error_string",):
@@ -988,6 +1015,256 @@ def gs_adam_step_clipped(tensors, beta1, beta2, eps, step, clip=None):
                                                        None if clip is None else _clip_state(clip),
                                                        _raw_stream(_current_device()))
     _check(rc, "gs_adam_step_clipped")
+
+
+# ---------------------------------------------------------------------------
+# An attention block beside the Gaussians: cross attention, layer norm, dropout
+# (the differentiable functions over them are in network.py).
+# ---------------------------------------------------------------------------
+
+MAX_HEAD_DIM = 256
+_pack_attention = struct.Struct("=3q4i13qf4x").pack
+_pack_layer_norm = struct.Struct("=qii3qf4x").pack
+_pack_dropout = struct.Struct("=qii3qdQQ").pack
+
+
+def _per_head(t, shape, dtype, device, name):
+    """Batch, row and head strides of a 4-D tensor on that CUDA device whose last dimension is contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.get_device() != device:
+        _refuse(t, shape, dtype, name)
+    b, n, h, e = t.stride()
+    if e != 1 and shape[3] > 1:
+        raise GsError(f"{name} must have a contiguous last dimension")
+    return b, n, h
+
+
+def _attention_shape(q, k, scale):
+    """(batch, nq, nk, heads, kv_heads, d, type code, device, scale) of q [batch, nq, heads, d] and k [batch, nk,
+    kv_heads, d]."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4 or not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise GsError("q, k and v must be 4-D tensors")
+    code = DTYPES.get(q.dtype)
+    if code is None or not q.is_cuda:
+        _refuse(q, None, None, "q")
+    batch, nq, heads, d = q.shape
+    b, nk, kv_heads, dk = k.shape
+    if b != batch or dk != d:
+        raise GsError(f"k must have shape [{batch}, nk, kv_heads, {d}], got {tuple(k.shape)}")
+    if kv_heads < 1 or heads < 1 or heads % kv_heads:
+        raise GsError(f"q's heads ({heads}) must be a multiple of k's ({kv_heads})")
+    if d < 1 or d > MAX_HEAD_DIM:
+        raise GsError(f"heads must have 1 to {MAX_HEAD_DIM} elements, got {d}")
+    return batch, nq, nk, heads, kv_heads, d, code, q.get_device(), d ** -0.5 if scale is None else float(scale)
+
+
+def _valid(mask, q_lengths, k_lengths, batch, nk, device):
+    """Pointers of the key mask and the lengths, and the mask's stride."""
+    at = stride = None
+    if mask is not None:
+        if (not isinstance(mask, torch.Tensor) or mask.dtype != torch.bool or mask.shape != (batch, nk) or
+                mask.get_device() != device or (mask.stride(1) != 1 and nk > 1)):
+            raise GsError(f"mask must be a bool tensor [{batch}, {nk}] with contiguous rows on q's device")
+        at, stride = mask.data_ptr(), mask.stride(0)
+    lengths = []
+    for t, name in ((q_lengths, "q_lengths"), (k_lengths, "k_lengths")):
+        if t is not None and (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.shape != (batch,) or
+                              t.get_device() != device or not t.is_contiguous()):
+            raise GsError(f"{name} must be a contiguous int32 tensor [{batch}] on q's device")
+        lengths.append(None if t is None else t.data_ptr())
+    return at, stride or 0, *lengths
+
+
+def attention_fwd_into(q, k, v, mask, q_lengths, k_lengths, out, lse, scale):
+    """gs_attention_fwd; out None: a new tensor.  lse: a tensor, None (not wanted) or True (a new one).  Returns both."""
+    batch, nq, nk, heads, kv_heads, d, code, device, scale = _attention_shape(q, k, scale)
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return attention_fwd_into(q, k, v, mask, q_lengths, k_lengths, out, lse, scale)
+    dtype = q.dtype
+    strides = (*_per_head(q, q.shape, dtype, device, "q"), *_per_head(k, k.shape, dtype, device, "k"),
+               *_per_head(v, k.shape, dtype, device, "v"))
+    pm, mask_stride, pq, pk = _valid(mask, q_lengths, k_lengths, batch, nk, device)
+    if out is None:
+        out = q.new_empty(q.shape)
+        to = out.data_ptr()
+    else:
+        to = _whole(out, q.shape, dtype, device, "out")
+    if lse is True:
+        lse = torch.empty((batch, heads, nq), dtype=torch.float32, device=q.device)
+    rc = (_lib or load_library()).gs_attention_fwd(
+        _pack_attention(batch, nq, nk, heads, kv_heads, d, code, *strides, 0, 0, 0, mask_stride, scale), q.data_ptr(),
+        k.data_ptr(), v.data_ptr(), pm, pq, pk, to, _whole(lse, (batch, heads, nq), torch.float32, device, "lse"),
+        _raw_stream(device))
+    if rc:
+        _check(rc, "gs_attention_fwd")
+    return out, lse
+
+
+def gs_attention_fwd(q, k, v, out, lse=None, mask=None, q_lengths=None, k_lengths=None, scale=None):
+    """out [batch, nq, heads, d] = softmax(scale q k^T) v and lse [batch, heads, nq] float32 (None: not wanted)."""
+    if out is None or lse is True:
+        raise GsError("out and lse are the caller's tensors")
+    attention_fwd_into(q, k, v, mask, q_lengths, k_lengths, out, lse, scale)
+
+
+def gs_attention_bwd_workspace_size(q, k):
+    batch, nq, nk, heads, kv_heads, d, code, _, scale = _attention_shape(q, k, None)
+    b = C.c_size_t()
+    _check(load_library().gs_attention_bwd_workspace_size(
+        _pack_attention(batch, nq, nk, heads, kv_heads, d, code, *[0] * 13, scale), C.byref(b)),
+        "gs_attention_bwd_workspace_size")
+    return b.value
+
+
+def attention_bwd_into(q, k, v, out, lse, dout, dq, dk, dv, workspace, mask, q_lengths, k_lengths, scale):
+    """gs_attention_bwd; workspace None: one of the size the call needs."""
+    batch, nq, nk, heads, kv_heads, d, code, device, scale = _attention_shape(q, k, scale)
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return attention_bwd_into(q, k, v, out, lse, dout, dq, dk, dv, workspace, mask, q_lengths, k_lengths, scale)
+    dtype = q.dtype
+    strides = (*_per_head(q, q.shape, dtype, device, "q"), *_per_head(k, k.shape, dtype, device, "k"),
+               *_per_head(v, k.shape, dtype, device, "v"), *_per_head(dout, q.shape, dtype, device, "dout"))
+    pm, mask_stride, pq, pk = _valid(mask, q_lengths, k_lengths, batch, nk, device)
+    if out is None or lse is None:
+        raise GsError("the backward needs the forward's out and lse")
+    at = (q.data_ptr(), k.data_ptr(), v.data_ptr(), pm, pq, pk, _whole(out, q.shape, dtype, device, "out"),
+          _whole(lse, (batch, heads, nq), torch.float32, device, "lse"), dout.data_ptr(),
+          _whole(dq, q.shape, dtype, device, "dq"), _whole(dk, k.shape, dtype, device, "dk"),
+          _whole(dv, k.shape, dtype, device, "dv"))
+    lib = _lib or load_library()
+    a = _pack_attention(batch, nq, nk, heads, kv_heads, d, code, *strides, mask_stride, scale)
+    if workspace is None:
+        b = C.c_size_t()
+        _check(lib.gs_attention_bwd_workspace_size(a, C.byref(b)), "gs_attention_bwd_workspace_size")
+        # torch's device allocations start at multiples of 512 bytes
+        workspace = torch.empty(b.value, dtype=torch.uint8, device=q.device)
+    rc = lib.gs_attention_bwd(a, *at, _whole(workspace, workspace.shape, torch.uint8, device, "workspace"),
+                              workspace.numel(), _raw_stream(device))
+    if rc:
+        _check(rc, "gs_attention_bwd")
+
+
+def gs_attention_bwd(q, k, v, out, lse, dout, dq, dk, dv, workspace, mask=None, q_lengths=None, k_lengths=None,
+                     scale=None):
+    """The gradients from dout into dq, dk and dv (each may be None: not computed); out and lse: the forward's;
+    workspace: uint8, gs_attention_bwd_workspace_size bytes, 256-byte aligned."""
+    attention_bwd_into(q, k, v, out, lse, dout, dq, dk, dv, workspace, mask, q_lengths, k_lengths, scale)
+
+
+def _row_shape(x, name="x"):
+    """(rows, n, type code, device, row stride) of a 2-D tensor."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise GsError(f"{name} must be a 2-D tensor")
+    code = DTYPES.get(x.dtype)
+    if code is None or not x.is_cuda:
+        _refuse(x, None, None, name)
+    shape, device = x.shape, x.get_device()
+    return *shape, code, device, _rows(x, shape, x.dtype, device, name)
+
+
+def layer_norm_fwd_into(x, w, b, y, eps):
+    """gs_layer_norm_fwd; y None: a new [rows, n] tensor.  Returns y."""
+    rows, n, code, device, ld_x = _row_shape(x)
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return layer_norm_fwd_into(x, w, b, y, eps)
+    dtype = x.dtype
+    if y is None:
+        y, ld_y = x.new_empty((rows, n)), n
+    else:
+        ld_y = _rows(y, (rows, n), dtype, device, "y")
+    rc = (_lib or load_library()).gs_layer_norm_fwd(
+        _pack_layer_norm(rows, n, code, ld_x, ld_y, 0, eps), x.data_ptr(), _whole(w, (n,), dtype, device, "w"),
+        _whole(b, (n,), dtype, device, "b"), y.data_ptr(), _raw_stream(device))
+    if rc:
+        _check(rc, "gs_layer_norm_fwd")
+    return y
+
+
+def gs_layer_norm_fwd(x, w, b, y, eps=1e-5):
+    """y [rows, n] = (x - mean) / sqrt(var + eps) w + b of every row; w and b may be None, y may be x."""
+    if y is None:
+        raise GsError("y is the caller's tensor")
+    layer_norm_fwd_into(x, w, b, y, eps)
+
+
+def gs_layer_norm_bwd_workspace_size(x):
+    rows, n, code, _, ld_x = _row_shape(x)
+    b = C.c_size_t()
+    _check(load_library().gs_layer_norm_bwd_workspace_size(_pack_layer_norm(rows, n, code, ld_x, n, n, 0.0),
+                                                           C.byref(b)), "gs_layer_norm_bwd_workspace_size")
+    return b.value
+
+
+def layer_norm_bwd_into(x, w, dy, dx, dw, db, workspace, eps):
+    """gs_layer_norm_bwd; workspace None: one of the size the call needs."""
+    rows, n, code, device, ld_x = _row_shape(x)
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return layer_norm_bwd_into(x, w, dy, dx, dw, db, workspace, eps)
+    dtype = x.dtype
+    ld_y = _rows(dy, (rows, n), dtype, device, "dy")
+    pdx, ld_dx = None, n
+    if dx is not None:
+        ld_dx = _rows(dx, (rows, n), dtype, device, "dx")
+        pdx = dx.data_ptr()
+    lib = _lib or load_library()
+    d = _pack_layer_norm(rows, n, code, ld_x, ld_y, ld_dx, eps)
+    if workspace is None and (dw is not None or db is not None):
+        size = C.c_size_t()
+        _check(lib.gs_layer_norm_bwd_workspace_size(d, C.byref(size)), "gs_layer_norm_bwd_workspace_size")
+        # torch's device allocations start at multiples of 512 bytes
+        workspace = torch.empty(size.value, dtype=torch.uint8, device=x.device)
+    pw = None if workspace is None else _whole(workspace, workspace.shape, torch.uint8, device, "workspace")
+    rc = lib.gs_layer_norm_bwd(
+        d, x.data_ptr(), _whole(w, (n,), dtype, device, "w"), dy.data_ptr(), pdx, _whole(dw, (n,), dtype, device, "dw"),
+        _whole(db, (n,), dtype, device, "db"), pw, 0 if workspace is None else workspace.numel(), _raw_stream(device))
+    if rc:
+        _check(rc, "gs_layer_norm_bwd")
+
+
+def gs_layer_norm_bwd(x, w, dy, dx, dw, db, workspace, eps=1e-5):
+    """The layer norm's gradients from dy into dx, dw and db (each may be None: not computed); workspace: uint8,
+    gs_layer_norm_bwd_workspace_size bytes, 256-byte aligned (dx alone: may be None)."""
+    layer_norm_bwd_into(x, w, dy, dx, dw, db, workspace, eps)
+
+
+def dropout_into(x, p, seed, offset, residual, y):
+    """gs_dropout; y None: a new [rows, n] tensor.  Returns y."""
+    rows, n, code, device, ld_x = _row_shape(x)
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return dropout_into(x, p, seed, offset, residual, y)
+    dtype, shape = x.dtype, (rows, n)
+    if y is None:
+        y, ld_y = x.new_empty(shape), n
+    else:
+        ld_y = _rows(y, shape, dtype, device, "y")
+    pr, ld_res = None, 0
+    if residual is not None:
+        ld_res = _rows(residual, shape, dtype, device, "residual")
+        pr = residual.data_ptr()
+    state = None
+    if isinstance(seed, torch.Tensor):
+        if seed.dtype != torch.int64 or seed.shape != (2,) or seed.get_device() != device or not seed.is_contiguous():
+            raise GsError("a seed tensor must be int64 [2], contiguous and on x's device")
+        state, seed = seed.data_ptr(), 0
+    if not (isinstance(seed, int) and isinstance(offset, int) and 0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise GsError("seed and offset must be whole numbers from 0 to 2^64 - 1")
+    rc = (_lib or load_library()).gs_dropout(_pack_dropout(rows, n, code, ld_x, ld_y, ld_res, p, seed, offset), state,
+                                             x.data_ptr(), pr, y.data_ptr(), _raw_stream(device))
+    if rc:
+        _check(rc, "gs_dropout")
+    return y
+
+
+def gs_dropout(x, p, seed, offset, residual, y):
+    """y [rows, n] = x keep / (1 - p) + residual (None: none) with keep from seed (a number, or an int64 device tensor
+    of a seed and a number added to offset), offset, row and column; y may be x or residual."""
+    if y is None:
+        raise GsError("y is the caller's tensor")
+    dropout_into(x, p, seed, offset, residual, y)
 
 
 # ---------------------------------------------------------------------------

@@ -1,11 +1,12 @@
-"""Networks beside the Gaussians: the fused linear layer with its gradients, gradient
-clipping by the global norm, and an Adam optimizer that takes the clipping
-coefficient on the device.
+"""Networks beside the Gaussians: the fused linear layer, layer norm, cross attention
+and dropout with their gradients, gradient clipping by the global norm, and an Adam
+optimizer that takes the clipping coefficient on the device.
 
 A network's rows are Gaussians (features decoded to Gaussian parameters, offsets for
-a time step) or views (an appearance code per camera); its outputs go to
-`gs.rasterize` and its gradients come back through it.  Plumbing over the C ABI
-(gs_linear_*, gs_grad_*, gs_adam_step_clipped): buffers and the order of the calls.
+a time step) or views (an appearance code per camera); by cross attention one reads
+the other.  Its outputs go to `gs.rasterize` and its gradients come back through it.
+Plumbing over the C ABI (gs_linear_*, gs_layer_norm_*, gs_attention_*, gs_dropout,
+gs_grad_*, gs_adam_step_clipped): buffers and the order of the calls.
 """
 from __future__ import annotations
 
@@ -76,6 +77,127 @@ def linear(x, w, bias=None, residual=None, act="none"):
             (residual is not None and residual.requires_grad)):
         return LinearFunction.apply(x, w, bias, residual, act)
     return gs.linear_fwd_into(x, w, bias, residual, None, act)
+
+
+def _differentiable(*tensors):
+    """Whether a call on them goes through autograd: under forward mode a tensor with a tangent need not require a
+    gradient, and the function raises for it."""
+    return forward_ad._current_level >= 0 or torch.is_grad_enabled() and any(
+        t is not None and t.requires_grad for t in tensors)
+
+
+def layer_norm_backward(dy, x, w=None, b=None, eps=1e-5, need=(True, True, True)):
+    """dx, dw, db of y = layer_norm(x, w, b, eps) from dy = dL/dy (None where need is False; dw and db None without w
+    and b)."""
+    need_dx, need_dw, need_db = need
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None
+    dw = torch.empty_like(w, memory_format=torch.contiguous_format) if need_dw and w is not None else None
+    db = torch.empty_like(b, memory_format=torch.contiguous_format) if need_db and b is not None else None
+    gs.layer_norm_bwd_into(x, w, dy, dx, dw, db, None, eps)
+    return dx, dw, db
+
+
+class LayerNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, b, eps):
+        ctx.eps = eps
+        ctx.save_for_backward(x, w, b)
+        return gs.layer_norm_fwd_into(x, w, b, None, eps)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, b = ctx.saved_tensors
+        grads = layer_norm_backward(_plain_rows(dy), x, w, b, ctx.eps, ctx.needs_input_grad[:3])
+        return *gs.differentiated_once("network.layer_norm", grads, (dy, x, w)), None
+
+
+def layer_norm(x, w=None, b=None, eps=1e-5):
+    """(x - mean) / sqrt(var + eps) w + b of every row of x [rows, n], differentiable in all three, once.
+
+    w and b [n] (or None) of x's type (float32, float16 or bfloat16); x may have strided rows."""
+    if _differentiable(x, w, b):
+        return LayerNormFunction.apply(x, w, b, eps)
+    return gs.layer_norm_fwd_into(x, w, b, None, eps)
+
+
+class DropoutFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, p, seed, offset):
+        ctx.p, ctx.seed, ctx.offset = p, None if isinstance(seed, torch.Tensor) else seed, offset
+        ctx.save_for_backward(seed if ctx.seed is None else None)
+        return gs.dropout_into(x, p, seed, offset, residual, None)
+
+    @staticmethod
+    def backward(ctx, dy):
+        dx = None
+        if ctx.needs_input_grad[0]:
+            state, = ctx.saved_tensors
+            dx = dropout(_plain_rows(dy), ctx.p, ctx.seed if state is None else state, ctx.offset)
+        return dx, dy if ctx.needs_input_grad[1] else None, None, None, None
+
+
+def dropout(x, p, seed, offset=0, residual=None):
+    """x keep / (1 - p) + residual, differentiable in x and residual.  keep drops an element with probability p, taken
+    to the nearest multiple of 2^-16; it is a function of seed, offset, row and column and is never stored.
+
+    x and residual [rows, n] of one type (float32, float16 or bfloat16), with strided rows that do not overlap (but the
+    residual may be one row expanded).  seed and offset: numbers from 0 to 2^64 - 1; every use in a step takes an
+    offset of its own.  seed may be an int64 device tensor of two, a seed and a number added to offset, which the
+    kernel reads when it runs: a call recorded into a graph draws another mask when the tensor changes between replays.
+    It must hold the same numbers when the gradient is taken."""
+    if _differentiable(x, residual):
+        return DropoutFunction.apply(x, residual, p, seed, offset)
+    return gs.dropout_into(x, p, seed, offset, residual, None)
+
+
+def dropout_backward(dy, p, seed, offset=0):
+    """dx of y = dropout(x, p, seed, offset, residual) from dy; the residual's gradient is dy itself."""
+    return gs.dropout_into(dy, p, seed, offset, None, None)
+
+
+def cross_attention_forward(q, k, v, mask=None, q_lengths=None, k_lengths=None, scale=None):
+    """out of cross_attention and lse [batch, heads, nq] float32, the log of the sums of its softmax (-infinity where
+    nothing counts): what cross_attention_backward takes."""
+    return gs.attention_fwd_into(q, k, v, mask, q_lengths, k_lengths, None, True, scale)
+
+
+def cross_attention_backward(dout, q, k, v, out, lse, mask=None, q_lengths=None, k_lengths=None, scale=None,
+                             need=(True, True, True)):
+    """dq, dk, dv (None where need is False) from dout = dL/dout and the forward's out and lse."""
+    dq, dk, dv = (torch.empty_like(t, memory_format=torch.contiguous_format) if wanted else None
+                  for t, wanted in zip((q, k, v), need))
+    gs.attention_bwd_into(q, k, v, out, lse, dout, dq, dk, dv, None, mask, q_lengths, k_lengths, scale)
+    return dq, dk, dv
+
+
+class CrossAttentionFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, mask, q_lengths, k_lengths, scale):
+        out, lse = cross_attention_forward(q, k, v, mask, q_lengths, k_lengths, scale)
+        ctx.scale = scale
+        ctx.save_for_backward(q, k, v, out, lse, mask, q_lengths, k_lengths)
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        q, k, v, out, lse, *valid = ctx.saved_tensors
+        plain = dout if dout.stride(3) == 1 or dout.shape[3] <= 1 else dout.contiguous()
+        grads = cross_attention_backward(plain, q, k, v, out, lse, *valid, ctx.scale, ctx.needs_input_grad[:3])
+        return *gs.differentiated_once("network.cross_attention", grads, (dout, q, k, v)), None, None, None, None
+
+
+def cross_attention(q, k, v, mask=None, q_lengths=None, k_lengths=None, scale=None):
+    """softmax(scale q k^T) v of every batch item and head, differentiable in q, k and v, once.
+
+    q [batch, nq, heads, d], k and v [batch, nk, kv_heads, d] of one type (float32, float16 or bfloat16); heads is a
+    multiple of kv_heads, head h reads head h // (heads // kv_heads) of k and v; d is at most 256.  Any strides with a
+    contiguous last dimension, expanded ones too: a projection's columns need no copy.  scale: 1 / sqrt(d) if None.
+    mask: bool [batch, nk], the keys that count; q_lengths, k_lengths: int32 [batch], the queries and keys that count,
+    from the first on.  What does not count is not used, whatever it holds, and has a gradient of 0; a query that does
+    not count, or has no key that does, gives 0."""
+    if _differentiable(q, k, v):
+        return CrossAttentionFunction.apply(q, k, v, mask, q_lengths, k_lengths, scale)
+    return gs.attention_fwd_into(q, k, v, mask, q_lengths, k_lengths, None, None, scale)[0]
 
 
 _HERE = contextlib.nullcontext()

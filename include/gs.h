@@ -719,6 +719,113 @@ typedef struct gs_adam_tensor {
 int gs_adam_step_clipped(int32_t n_tensors, const gs_adam_tensor* tensors, float beta1, float beta2, float eps,
                          int32_t step, const float* clip, void* stream);
 
+/*
+ * Cross attention: Gaussians read the tokens of their views, or view codes gather
+ * over Gaussians.  For every batch item b and head h, with head h / (heads /
+ * kv_heads) of k and v:
+ *   s = scale q k^T, out = softmax(s) v, lse = log(sum(exp(s)))
+ * q [batch, nq, heads, d], k and v [batch, nk, kv_heads, d] of one type, with
+ * strides (in elements, >= 0) for batch item, row and head and contiguous d
+ * elements; strides of 0 and overlapping rows are allowed, they are only read.
+ * out, dq like q and dk, dv like k, contiguous; lse [batch, heads, nq] float32.
+ * Element alignment is enough; 16-byte aligned rows are read faster.
+ * mask (NULL: none): bytes, batch items mask_stride apart, nk each: a key whose
+ * byte is 0 does not count.  q_lengths, k_lengths (NULL: all): int32 [batch], the
+ * queries and keys that count, from the first on (clamped to 0 .. nq, nk).  What
+ * does not count is not used, whatever it holds: its gradients are 0.  A query
+ * that does not count, or has no key that does, gives out 0 and lse -infinity.
+ * Products and softmax are summed in float32; the weights, and in the backward
+ * the gradients of s, enter their products rounded to the type (float16: scaled
+ * into its range first).  Results are rounded once.  Sums are split and joined in
+ * a fixed order: results repeat bit for bit.
+ * Limits: d <= GS_MAX_HEAD_DIM; nq heads / kv_heads and nk <= 2^30; 16e6 tiles of
+ * 64 rows or keys over all batch items and heads of keys (GS_ECAPACITY).  scale:
+ * finite and not 0.
+ */
+#define GS_MAX_HEAD_DIM 256
+typedef struct gs_attention {
+    int64_t batch, nq, nk;
+    int32_t heads, kv_heads, d, dtype;
+    int64_t q_stride[3], k_stride[3], v_stride[3];  /* batch item, row, head */
+    int64_t dout_stride[3];                         /* the backward's */
+    int64_t mask_stride;
+    float scale;
+} gs_attention;
+
+/* out and lse (NULL: not wanted); out must not overlap the inputs. */
+int gs_attention_fwd(const gs_attention* a, const void* q, const void* k, const void* v, const uint8_t* mask,
+                     const int32_t* q_lengths, const int32_t* k_lengths, void* out, float* lse, void* stream);
+
+/* Bytes of workspace gs_attention_bwd needs. */
+int gs_attention_bwd_workspace_size(const gs_attention* a, size_t* bytes);
+
+/*
+ * gs_attention_bwd -- dq, dk and dv (each may be NULL: not computed; a given one is
+ * overwritten) from dout = dL/dout and the forward's out and lse.  The softmax is
+ * made again from q and k.  workspace: 256-byte aligned, contents on entry
+ * irrelevant.
+ */
+int gs_attention_bwd(const gs_attention* a, const void* q, const void* k, const void* v, const uint8_t* mask,
+                     const int32_t* q_lengths, const int32_t* k_lengths, const void* out, const float* lse,
+                     const void* dout, void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/*
+ * Layer norm over the n elements of each row: mean and var = mean((x - mean)^2)
+ * in float32, y = (x - mean) / sqrt(var + eps) w + b.
+ * x, y, dy, dx [rows, n] with rows ld_* elements apart (>= n), w, b, dw, db [n]
+ * contiguous, all of one type; element alignment (16-byte aligned rows are read
+ * faster).  w and b may be NULL (1 and 0).  eps >= 0.  y may be x.
+ * Limits: n <= 2^20, rows <= 2^31 - 1 (GS_ECAPACITY).
+ */
+typedef struct gs_layer_norm {
+    int64_t rows;
+    int32_t n, dtype;
+    int64_t ld_x, ld_y, ld_dx; /* ld_y: also dy's */
+    float eps;
+} gs_layer_norm;
+
+int gs_layer_norm_fwd(const gs_layer_norm* d, const void* x, const void* w, const void* b, void* y, void* stream);
+
+/* Bytes of workspace gs_layer_norm_bwd needs. */
+int gs_layer_norm_bwd_workspace_size(const gs_layer_norm* d, size_t* bytes);
+
+/*
+ * gs_layer_norm_bwd -- with xh = (x - mean) / sqrt(var + eps) made again and g = dy w:
+ * dx = (g - mean(g) - xh mean(g xh)) / sqrt(var + eps), dw = sum over rows of dy xh,
+ * db = sum over rows of dy, summed in float32 in a fixed order.  Each of dx, dw and db
+ * may be NULL (not computed); dx may be dy.  With rows == 0, dw and db are zero.
+ * workspace: 256-byte aligned, contents on entry irrelevant.
+ */
+int gs_layer_norm_bwd(const gs_layer_norm* d, const void* x, const void* w, const void* dy, void* dx, void* dw,
+                      void* db, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gs_dropout -- y = x keep / (1 - p) + residual (NULL: none); its gradient is the
+ * same call on dy without a residual, with the same numbers: no mask is stored.
+ * keep(row, column) is 1 where half-word column % 8 (low halves first) of
+ * Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as easy
+ * as 1, 2, 3", 2011) of the counter (column / 8, row, offset low, offset high),
+ * keyed by the seed, is at least t = round(65536 p); the factor is 65536 / (65536 -
+ * t), so that the mean is kept for the p that 16 bits hold.  A dropped element is 0
+ * whatever x holds; p = 1 drops all.  state (NULL: none): two uint64 in device
+ * memory, the seed and a number added to offset, read by the kernel and used for
+ * seed: a captured call draws another mask when they change.
+ * x, y, residual [rows, n] with rows ld_* elements apart, element aligned; y may be
+ * x or residual (same pointer and ld).  ld_res may be 0: one row for all.
+ * 0 <= p <= 1.  Limits: n <= 2^20, rows <= 2^31 - 1 (GS_ECAPACITY).
+ */
+typedef struct gs_dropout_args {
+    int64_t rows;
+    int32_t n, dtype;
+    int64_t ld_x, ld_y, ld_res;
+    double p;
+    uint64_t seed, offset;
+} gs_dropout_args;
+
+int gs_dropout(const gs_dropout_args* d, const uint64_t* state, const void* x, const void* residual, void* y,
+               void* stream);
+
 #ifdef __cplusplus
 }
 #endif

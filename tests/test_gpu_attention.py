@@ -1,0 +1,403 @@
+"""Cross attention on the GPU (gs_attention_fwd, gs_attention_bwd, network.cross_attention) against its definition in
+64 bits.
+
+Bounds.  u is a type's unit roundoff (2^-24, 2^-11, 2^-8), U = 2^-24.  A sum of n float32 products is within (n + 2) U
+of the sum of its terms' magnitudes whatever its order.  A logit s is a sum of d products, scaled (by a factor that is
+itself rounded) and taken relative to a reference: off by es = U ((d + 4) |scale| sum |q||k| + 4 max |s|).  The
+hardware's exp2 is within 2^-22.  So a weight before its division is off by a factor 1 + (es + 2^-21), and so is the
+sum, which adds (nk + 3) U: a weight P is within P r, r = 2 (max es + 2^-21) + (nk + 4) U of exact.  P enters its
+product rounded: u more (16 bits), with a floor of 2^-38 for float16, which holds weights times 2^13 at least.  The
+result is rounded once.  The backward makes P from the log of the sums, itself float32, off by |lse| U more;
+delta = dout . out carries out's error; ds = P (dP - delta) is rounded like P (float16's floor is relative to the
+largest, where that passes 4).  The hardware's exp2 and products give 0 below 2^-126: that is the floor of a weight of
+the other types, and times |dP - delta| of a ds (2^-125 covers both)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+HALF = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+TINY = {torch.float32: 2.0 ** -126, torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -126}
+U = 2.0 ** -24
+TYPES = [torch.float32, torch.float16, torch.bfloat16]
+
+
+def put(a, dtype, order=None, pad=0, lead=0):
+    """A CUDA tensor of these values whose last dimension is contiguous: the others in memory in the given order, rows
+    `pad` elements apart (NaN between them), `lead` elements into its buffer."""
+    order = order or tuple(range(a.ndim - 1))
+    shape = [a.shape[i] for i in order] + [a.shape[-1] + pad]
+    buf = torch.full((lead + math.prod(shape) + 8,), float("nan"), dtype=dtype, device="cuda")
+    view = buf[lead:lead + math.prod(shape)].view(shape)[..., pad:]
+    view = view.permute(*[order.index(i) for i in range(a.ndim - 1)], a.ndim - 1)
+    view.copy_(torch.from_numpy(a.astype(np.float32)).to(dtype))
+    return view
+
+
+def inputs(size, dtype, seed=0, order=None, pad=0, lead=0, q_scale=1.0, dout_scale=0.5):
+    batch, nq, nk, heads, kv_heads, d = size
+    rng = np.random.default_rng(seed + 7 * nq + 13 * nk + d)
+    q = put(rng.standard_normal((batch, nq, heads, d)) * q_scale, dtype, order, pad, lead)
+    k = put(rng.standard_normal((batch, nk, kv_heads, d)) * 1.5, dtype, order, pad, lead)
+    v = put(rng.standard_normal((batch, nk, kv_heads, d)), dtype, order, pad, lead)
+    dout = put(rng.standard_normal((batch, nq, heads, d)) * dout_scale, dtype, order, pad, lead)
+    return q, k, v, dout
+
+
+VALID = ["all", "lengths", "mask", "both", "empty"]
+
+
+def valid_of(kind, size, seed=0):
+    """mask, q_lengths, k_lengths."""
+    batch, nq, nk = size[:3]
+    rng = np.random.default_rng(seed + nq + nk)
+    mask = q_lengths = k_lengths = None
+    if kind in ("lengths", "both"):
+        q_lengths = torch.from_numpy(rng.integers(0, nq + 1, batch).astype(np.int32)).cuda()
+        k_lengths = torch.from_numpy(rng.integers(0, nk + 1, batch).astype(np.int32)).cuda()
+        if batch == 1:
+            k_lengths.clamp_(min=min(1, nk))
+    if kind in ("mask", "both"):
+        mask = torch.from_numpy(rng.random((batch, nk)) < 0.6).cuda()
+        mask[0, 64:192] = False  # a whole tile and more
+    if kind == "empty":
+        mask = torch.zeros(batch, nk, dtype=torch.bool, device="cuda")
+        mask[1:] = True
+    return mask, q_lengths, k_lengths
+
+
+def exact(q, k, v, dout, mask, q_lengths, k_lengths, scale):
+    """out, lse, dq, dk, dv in float64 and their bounds, on the inputs' device."""
+    dtype = q.dtype
+    u, tiny = HALF[dtype], TINY[dtype]
+    rounded = 0.0 if dtype == torch.float32 else u
+    floor = 2.0 ** -38 if dtype == torch.float16 else 2.0 ** -125
+    batch, nq, heads, d = q.shape
+    nk, kv_heads = k.shape[1:3]
+    group = heads // kv_heads
+    rows = torch.arange(nq, device=q.device) < (nq if q_lengths is None else q_lengths.clamp(0, nq)[:, None])
+    keys = torch.arange(nk, device=q.device) < (nk if k_lengths is None else k_lengths.clamp(0, nk)[:, None])
+    keys = keys.expand(batch, nk) if mask is None else keys & mask
+    rows = rows.expand(batch, nq)[:, None, :, None]
+    keys = keys[:, None, None, :]
+
+    def spread(t, count):  # [batch, heads, n, d] in float64, zeros where nothing counts
+        t = t.double().permute(0, 2, 1, 3)
+        if t.shape[1] != heads:
+            t = t.repeat_interleave(group, 1)
+        return torch.where(count, t, 0.0).contiguous()
+
+    col = keys.transpose(2, 3)
+    Q, K, V, G = spread(q, rows), spread(k, col), spread(v, col), spread(dout, rows)
+
+    def t(a):
+        return a.transpose(2, 3).contiguous()
+
+    s = scale * (Q @ t(K))
+    size = abs(scale) * (Q.abs() @ t(K.abs()))
+    s = torch.where(keys, s, -math.inf)
+    lse = torch.logsumexp(s, 3, keepdim=True)
+    some = torch.isfinite(lse) & rows
+    P = torch.where(some, torch.exp(s - torch.where(some, lse, 0.0)), 0.0)
+    big = torch.where(keys, s.abs(), 0.0).amax(3, keepdim=True) if nk else torch.zeros_like(lse)
+    es = U * ((d + 4) * (size.amax(3, keepdim=True) if nk else 0.0) + 4 * big)
+    r = 2 * (es + 2.0 ** -21) + (nk + 4) * U
+    out = P @ V
+    PV = P @ V.abs()
+    out_err = PV * (rounded + r + (nk + 3) * U) + floor * V.abs().sum(2, keepdim=True) + u * out.abs() + tiny
+    lse = torch.where(some, lse, -math.inf)
+    lse_err = torch.where(some, r + 4 * U * (lse.abs() + big), 0.0)
+
+    rb = r + es + 2.0 ** -21 + lse_err
+    rb = torch.where(some, rb, 0.0)
+    dP = G @ t(V)
+    dP_err = (d + 3) * U * (G.abs() @ t(V.abs()))
+    D = (G * out).sum(3, keepdim=True)
+    D_err = (G.abs() * out_err).sum(3, keepdim=True) + (d + 3) * U * (G * out).abs().sum(3, keepdim=True)
+    dS = P * (dP - D)
+    exact_part = P * (rb * (dP - D).abs() + dP_err + D_err + 2 * U * (dP.abs() + D.abs()))
+    size = dS if dtype == torch.float16 else dP - D
+    lost = floor * torch.clamp(size.abs().amax() if nk and nq else torch.zeros((), device=q.device), min=1.0)
+    dS_err = exact_part + rounded * dS.abs() + torch.where(keys & rows, lost, 0.0)
+    P_err = P * (rb + rounded) + torch.where(keys & rows, lost, 0.0)
+    A = dS.abs() + dS_err
+    dq = scale * (dS @ K)
+    dq_err = abs(scale) * (dS_err @ K.abs() + (nk + 4) * U * (A @ K.abs())) + u * dq.abs() + tiny
+
+    def shared(a):
+        return a.view(batch, kv_heads, group, nk, d).sum(2)
+
+    n = nq * group
+    dk = shared(scale * (t(dS) @ Q))
+    dk_err = shared(abs(scale) * (t(dS_err) @ Q.abs() + (n + 4) * U * (t(A) @ Q.abs()))) + u * dk.abs() + tiny
+    dv = shared(t(P) @ G)
+    dv_err = shared(t(P_err) @ G.abs() + (n + 4) * U * (t(P + P_err) @ G.abs())) + u * dv.abs() + tiny
+    back = [a.permute(0, 2, 1, 3) for a in (out, out_err, dq, dq_err, dk, dk_err, dv, dv_err)]
+    return (back[:2], (lse[..., 0], lse_err[..., 0]), back[2:4], back[4:6], back[6:8])
+
+
+def check(got, want, what):
+    got, (value, tol) = got.detach().double(), want
+    assert got.shape == value.shape, what
+    same = got == value  # infinities
+    bad = ~(same | ((got - value).abs() <= tol))
+    if bad.any():
+        i = int(torch.argmax(bad.flatten().int()))
+        raise AssertionError((what, int(bad.sum()), bad.numel(), float(got.flatten()[i]), float(value.flatten()[i]),
+                              float(tol.flatten()[i])))
+
+
+def run(q, k, v, dout, valid, scale=None):
+    from differentiable_gaussian_splatting_dgs_amd import network
+    print("attention", tuple(q.shape), tuple(k.shape), q.dtype, q.stride(), k.stride(),
+          [a is not None for a in valid], scale, flush=True)
+    out, lse = network.cross_attention_forward(q, k, v, *valid, scale)
+    torch.cuda.synchronize()
+    print("backward", flush=True)
+    grads = network.cross_attention_backward(dout, q, k, v, out, lse, *valid, scale)
+    torch.cuda.synchronize()
+    return out, lse, *grads
+
+
+def compare(q, k, v, dout, valid, scale=None):
+    got = run(q, k, v, dout, valid, scale)
+    want = exact(q, k, v, dout, *valid, q.shape[3] ** -0.5 if scale is None else scale)
+    for name, g, w in zip(("out", "lse", "dq", "dk", "dv"), got, want):
+        check(g, w, (name, tuple(q.shape), tuple(k.shape), q.dtype, [a is not None for a in valid]))
+    return got
+
+
+# batch, nq, nk, heads, kv_heads, d: single tokens, tile edges of rows and keys, every padded head, shared heads
+SIZES = [(1, 1, 1, 1, 1, 1), (1, 1, 256, 8, 8, 64), (2, 3, 5, 2, 1, 3), (1, 17, 63, 4, 4, 32), (3, 64, 64, 4, 2, 40),
+         (2, 65, 65, 4, 1, 64), (1, 128, 129, 2, 2, 128), (2, 130, 31, 3, 3, 100), (2, 33, 200, 2, 1, 256),
+         (1, 257, 127, 1, 1, 160), (3, 100, 300, 6, 2, 72), (2, 1000, 77, 2, 2, 33), (2, 2, 5000, 2, 1, 64),
+         (1, 5000, 2, 2, 2, 32), (2, 16, 4097, 4, 1, 128), (1, 600, 600, 2, 2, 64), (2, 9, 1000, 4, 4, 7)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("size", SIZES)
+def test_sizes(size, dtype):
+    for i, kind in enumerate(VALID):
+        compare(*inputs(size, dtype, seed=i), valid_of(kind, size, i))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("pad,lead", [(0, 1), (1, 0), (8, 3), (5, 5)])
+@pytest.mark.parametrize("order", [(0, 1, 2), (0, 2, 1), (2, 0, 1), (1, 0, 2)])
+def test_strides(order, pad, lead, dtype):
+    for size in ((2, 70, 90, 4, 2, 24), (2, 5, 130, 2, 2, 61)):
+        compare(*inputs(size, dtype, order=order, pad=pad, lead=lead), valid_of("both", size))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_broadcast_keys(dtype):
+    """One set of tokens for all batch items and heads, one query for all rows: strides of 0, and their gradients."""
+    from differentiable_gaussian_splatting_dgs_amd import network
+    q, k, v, dout = inputs((3, 40, 70, 4, 2, 32), dtype)
+    k, v, q = k[:1].expand(3, -1, -1, -1), v[:1, :, :1].expand(3, -1, 2, -1), q[:, :1].expand(-1, 40, -1, -1)
+    got = compare(q, k, v, dout, (None, None, None))
+    leaf = v[:1, :, :1].detach().clone().requires_grad_()
+    network.cross_attention(q, k, leaf.expand(3, -1, 2, -1)).backward(dout)
+    whole = got[4].double().sum((0, 2))[None, :, None]
+    assert (leaf.grad.double() - whole).abs().max() <= 6 * HALF[dtype] * got[4].double().abs().sum((0, 2)).max()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_scales(dtype):
+    size = (2, 50, 100, 2, 1, 48)
+    for scale in (0.02, -0.3, 1.0):
+        compare(*inputs(size, dtype), valid_of("both", size), scale)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_far_logits(dtype):
+    """Logits of some hundreds: one key takes nearly all of a row, and references move from tile to tile."""
+    size = (1, 70, 700, 2, 2, 64)
+    q, k, v, dout = inputs(size, dtype, q_scale=20.0)
+    k *= torch.linspace(0.1, 2.0, 700, device="cuda").to(dtype)[None, :, None, None]
+    compare(q, k, v, dout, (None, None, None))
+
+
+def test_large_gradients_in_float16():
+    """ds past float16's largest number once scaled: what is summed so far is scaled down."""
+    size = (1, 80, 300, 2, 1, 64)
+    q, k, v, dout = inputs(size, torch.float16, dout_scale=1.0)
+    dout *= torch.logspace(-2, 2, 80, device="cuda").half()[None, :, None, None]
+    compare(q, k * 0.05, v, dout * 4, (None, None, None), 0.125)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("size", [(2, 70, 200, 4, 2, 40), (2, 3, 900, 2, 1, 64)])
+def test_what_does_not_count_is_not_used(size, dtype):
+    """NaN and infinities in keys, values, queries and gradients that do not count change no bit."""
+    valid = valid_of("both", size, 3)
+    mask, q_lengths, k_lengths = valid
+    q, k, v, dout = inputs(size, dtype)
+    want = run(q, k, v, dout, valid)
+    keys = mask & (torch.arange(size[2], device="cuda") < k_lengths[:, None])
+    rows = torch.arange(size[1], device="cuda") < q_lengths[:, None]
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        for t, count in ((q, rows), (dout, rows), (k, keys), (v, keys)):
+            t.masked_fill_(~count[:, :, None, None], bad)
+        got = run(q, k, v, dout, valid)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_nan_where_it_counts(dtype):
+    """A NaN value reaches its column of every row; a NaN query its own row alone."""
+    q, k, v, dout = inputs((1, 70, 100, 2, 2, 32), dtype)
+    v[0, 5, 1, 3] = float("nan")
+    q[0, 7, 0, 2] = float("nan")
+    out, lse, *_ = run(q, k, v, dout, (None, None, None))
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[0, :, 1, 3] = True
+    bad[0, 7, 0] = True
+    assert torch.equal(out.isnan(), bad)
+
+
+def test_no_keys_and_no_queries():
+    from differentiable_gaussian_splatting_dgs_amd import network
+    for dtype in TYPES:
+        q, k, v, dout = inputs((2, 5, 3, 4, 2, 16), dtype)
+        out, lse, dq, dk, dv = run(q, k[:, :0], v[:, :0], dout, (None, None, None))
+        assert not out.any() and not dq.any() and dk.shape == (2, 0, 2, 16) and torch.isneginf(lse).all()
+        out, lse, dq, dk, dv = run(q[:, :0], k, v, dout[:, :0], (None, None, None))
+        assert out.shape == (2, 0, 4, 16) and not dk.any() and not dv.any()
+        assert network.cross_attention(q[:0], k[:0], v[:0]).shape == (0, 5, 4, 16)
+
+
+def test_lengths_out_of_range_are_clamped():
+    q, k, v, dout = inputs((3, 20, 30, 2, 2, 16), torch.float32)
+    long = torch.tensor([1000, -5, 7], dtype=torch.int32, device="cuda")
+    short = torch.tensor([30, 0, 7], dtype=torch.int32, device="cuda")
+    a, b = run(q, k, v, dout, (None, None, long)), run(q, k, v, dout, (None, None, short))
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("need", [(True, False, False), (False, True, False), (False, False, True), (False, True, True)])
+def test_single_gradients(need):
+    from differentiable_gaussian_splatting_dgs_amd import network
+    for size in ((1, 70, 90, 2, 1, 32), (1, 2, 900, 2, 1, 32)):
+        q, k, v, dout = inputs(size, torch.bfloat16)
+        out, lse, *want = run(q, k, v, dout, (None, None, None))
+        got = network.cross_attention_backward(dout, q, k, v, out, lse, need=need)
+        for g, w, n in zip(got, want, need):
+            assert (g is None) if not n else torch.equal(g, w)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_repeats(dtype):
+    for size in ((1, 3, 20000, 4, 1, 64), (1, 20000, 30, 2, 2, 32), (2, 500, 700, 4, 2, 128)):
+        q, k, v, dout = inputs(size, dtype)
+        first = run(q, k, v, dout, (None, None, None))
+        for _ in range(3):
+            assert all(torch.equal(a, b) for a, b in zip(first, run(q, k, v, dout, (None, None, None))))
+
+
+def test_differences():
+    """Gradients against differences of the forward, in float32."""
+    from differentiable_gaussian_splatting_dgs_amd import network
+    size = (2, 9, 21, 4, 2, 24)
+    q, k, v, dout = inputs(size, torch.float32)
+    valid = valid_of("both", size)
+    leaves = [t.clone().requires_grad_() for t in (q, k, v)]
+    network.cross_attention(*leaves, *valid).backward(dout)
+    rng = np.random.default_rng(0)
+    for i, leaf in enumerate(leaves):
+        step = torch.from_numpy(rng.standard_normal(leaf.shape).astype(np.float32)).cuda()
+        h, values = 2.0 ** -6, []
+        for sign in (1, -1):
+            moved = [t.detach() for t in leaves]
+            moved[i] = moved[i] + sign * h * step
+            values.append(float((network.cross_attention(*moved, *valid).double() * dout.double()).sum()))
+        slope = (values[0] - values[1]) / (2 * h)
+        want = float((leaf.grad.double() * step.double()).sum())
+        # the third derivative leaves h^2 / 6 of the terms' size; they are sums of some thousand terms below 1
+        assert abs(slope - want) <= 2e-3 * float((leaf.grad.double() * step.double()).abs().sum()) + 1e-3, (i, slope, want)
+
+
+def test_autograd():
+    """Through network.cross_attention, with a gradient that is one number expanded, and a leaf that needs none."""
+    from differentiable_gaussian_splatting_dgs_amd import network
+    q, k, v, _ = inputs((2, 30, 40, 4, 2, 16), torch.float32)
+    ones = torch.ones_like(q)
+    _, _, dq, dk, dv = run(q, k, v, ones, (None, None, None))
+    q2, v2 = q.clone().requires_grad_(), v.clone().requires_grad_()
+    network.cross_attention(q2, k, v2).sum().backward()
+    assert torch.equal(q2.grad, dq) and torch.equal(v2.grad, dv)
+    with torch.no_grad():
+        assert not network.cross_attention(q2, k, v2).requires_grad
+
+
+def test_other_stream_and_no_order_between_calls():
+    """Calls on two streams at once share nothing."""
+    from differentiable_gaussian_splatting_dgs_amd import network
+    sets = [inputs(s, torch.bfloat16, seed=i) for i, s in enumerate(((1, 4, 30000, 4, 1, 64), (1, 9000, 60, 4, 4, 32)))]
+    want = [run(*s, (None, None, None)) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i, (stream, (q, k, v, dout)) in enumerate(zip(streams, sets)):
+            with torch.cuda.stream(stream):
+                out, lse = network.cross_attention_forward(q, k, v)
+                got[i].append((out, lse, *network.cross_attention_backward(dout, q, k, v, out, lse)))
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        for g in runs:
+            assert all(torch.equal(a, b) for a, b in zip(w, g))
+
+
+@pytest.mark.parametrize("size", [(1, 2, 9000, 4, 1, 64), (2, 300, 70, 2, 2, 32)])
+def test_graph(size):
+    """Forward and backward recorded and replayed with other inputs and lengths, eager work between the replays."""
+    from differentiable_gaussian_splatting_dgs_amd import network
+    q, k, v, dout = (t.contiguous() for t in inputs(size, torch.bfloat16))
+    k_lengths = torch.full((size[0],), size[2], dtype=torch.int32, device="cuda")
+    valid = (None, None, k_lengths)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(q, k, v, dout, valid)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = network.cross_attention_forward(q, k, v, *valid)
+        grads = network.cross_attention_backward(dout, q, k, v, out, lse, *valid)
+    for i in range(3):
+        for a, b in zip((q, k, v, dout), inputs(size, torch.bfloat16, seed=10 + i)):
+            a.copy_(b)
+        k_lengths.fill_(size[2] - 7 * i)
+        want = run(q, k, v, dout, valid)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, (out, lse, *grads)))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_long(dtype):
+    """Many queries on few keys and few on many, past what one split of the work holds."""
+    for size in ((1, 50_001, 70, 2, 1, 32), (1, 7, 150_001, 2, 1, 32), (2, 1, 60_000, 4, 4, 64)):
+        compare(*inputs(size, dtype), valid_of("mask", size))
+
+
+def test_offsets_past_32_bits():
+    """Keys that lie more than 2^32 elements into their buffer, rows far apart."""
+    stride = 1 << 22
+    buf = torch.empty(1100 * stride + 64, dtype=torch.float16, device="cuda")
+    q, k0, v0, dout = inputs((1, 3, 1100, 1, 1, 32), torch.float16)
+    k = torch.as_strided(buf, (1, 1100, 1, 32), (0, stride, 32, 1))
+    v = torch.as_strided(buf, (1, 1100, 1, 32), (0, stride, 32, 1), 32)
+    k.copy_(k0)
+    v.copy_(v0)
+    got, want = run(q, k, v, dout, (None, None, None)), run(q, k0, v0, dout, (None, None, None))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # and queries
+    got = run(k, k0, v0, v, (None, None, None))
+    want = run(k0, k0, v0, v0, (None, None, None))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
