@@ -7,7 +7,6 @@ namespace gs {
 namespace {
 
 inline int size_of(int32_t dtype) { return dtype == GS_F32 ? 4 : 2; }
-inline size_t pad256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 int check_shape(const gs_attention* a) {
     if (!a || a->batch < 0 || a->nq < 0 || a->nk < 0 || a->heads < 1 || a->kv_heads < 1 || a->d < 1 ||
@@ -43,6 +42,16 @@ AttnArgs args_of(const gs_attention* a, const void* q, const void* k, const void
     return p;
 }
 
+AttnPlan plan_of(const AttnArgs& p, int32_t dtype) {
+    return dtype == GS_F32 ? attn_plan<float>(p) : dtype == GS_F16 ? attn_plan<_Float16>(p) : attn_plan<__bf16>(p);
+}
+
+int check_workspace(const void* workspace, size_t bytes, size_t need) {
+    if (need > 0 && !workspace) return GS_EINVAL;
+    if (bytes < need) return GS_EWORKSPACE;
+    return aligned_to(workspace, 256) ? GS_OK : GS_EALIGN;
+}
+
 }  // namespace
 }  // namespace gs
 
@@ -50,8 +59,8 @@ using namespace gs;
 
 extern "C" int gs_attention_fwd(const gs_attention* a, const void* q, const void* k, const void* v,
                                 const uint8_t* mask, const int32_t* q_lengths, const int32_t* k_lengths, void* out,
-                                float* lse, void* stream) {
-    const int rc = check_shape(a);
+                                float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_shape(a);
     if (rc != GS_OK) return rc;
     if (a->batch == 0 || a->nq == 0) return GS_OK;
     if (!q || !out || (a->nk > 0 && (!k || !v))) return GS_EINVAL;
@@ -61,30 +70,39 @@ extern "C" int gs_attention_fwd(const gs_attention* a, const void* q, const void
         if (!aligned_to(t, 4)) return GS_EALIGN;
     AttnArgs p = args_of(a, q, k, v, mask, q_lengths, k_lengths);
     p.out = out, p.lse = lse;
+    rc = check_workspace(workspace, workspace_bytes, plan_of(p, a->dtype).fwd_bytes);
+    if (rc != GS_OK) return rc;
     hipStream_t s = as_stream(stream);
     if (a->dtype == GS_F32)
-        attn_fwd<float>(p, s);
+        attn_fwd<float>(p, workspace, s);
     else if (a->dtype == GS_F16)
-        attn_fwd<_Float16>(p, s);
+        attn_fwd<_Float16>(p, workspace, s);
     else
-        attn_fwd<__bf16>(p, s);
+        attn_fwd<__bf16>(p, workspace, s);
     return launch_status();
 }
 
-extern "C" int gs_attention_bwd_workspace_size(const gs_attention* a, size_t* bytes) {
+static int workspace_size(const gs_attention* a, size_t AttnPlan::*which, size_t* bytes) {
     const int rc = check_shape(a);
     if (rc != GS_OK) return rc;
     if (!bytes) return GS_EINVAL;
-    *bytes = pad256((size_t)a->batch * a->heads * a->nq * 4);
+    *bytes = plan_of(args_of(a, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr), a->dtype).*which;
     return GS_OK;
+}
+
+extern "C" int gs_attention_fwd_workspace_size(const gs_attention* a, size_t* bytes) {
+    return workspace_size(a, &AttnPlan::fwd_bytes, bytes);
+}
+
+extern "C" int gs_attention_bwd_workspace_size(const gs_attention* a, size_t* bytes) {
+    return workspace_size(a, &AttnPlan::bwd_bytes, bytes);
 }
 
 extern "C" int gs_attention_bwd(const gs_attention* a, const void* q, const void* k, const void* v,
                                 const uint8_t* mask, const int32_t* q_lengths, const int32_t* k_lengths,
                                 const void* out, const float* lse, const void* dout, void* dq, void* dk, void* dv,
                                 void* workspace, size_t workspace_bytes, void* stream) {
-    size_t need = 0;
-    const int rc = gs_attention_bwd_workspace_size(a, &need);
+    int rc = check_shape(a);
     if (rc != GS_OK) return rc;
     if (a->batch == 0 || (a->nq == 0 && a->nk == 0)) return GS_OK;
     if (a->nq > 0 && (!q || !out || !lse || !dout)) return GS_EINVAL;
@@ -93,18 +111,17 @@ extern "C" int gs_attention_bwd(const gs_attention* a, const void* q, const void
         if (!aligned_to(t, size_of(a->dtype))) return GS_EALIGN;
     for (const void* t : {(const void*)q_lengths, (const void*)k_lengths, (const void*)lse})
         if (!aligned_to(t, 4)) return GS_EALIGN;
-    if (need > 0 && !workspace) return GS_EINVAL;
-    if (workspace_bytes < need) return GS_EWORKSPACE;
-    if (!aligned_to(workspace, 256)) return GS_EALIGN;
     AttnArgs p = args_of(a, q, k, v, mask, q_lengths, k_lengths);
     p.out = const_cast<void*>(out), p.lse = const_cast<float*>(lse), p.dout = dout;
-    p.dq = dq, p.dk = dk, p.dv = dv, p.delta = static_cast<float*>(workspace);
+    p.dq = dq, p.dk = dk, p.dv = dv;
+    rc = check_workspace(workspace, workspace_bytes, plan_of(p, a->dtype).bwd_bytes);
+    if (rc != GS_OK) return rc;
     hipStream_t s = as_stream(stream);
     if (a->dtype == GS_F32)
-        attn_bwd<float>(p, s);
+        attn_bwd<float>(p, workspace, s);
     else if (a->dtype == GS_F16)
-        attn_bwd<_Float16>(p, s);
+        attn_bwd<_Float16>(p, workspace, s);
     else
-        attn_bwd<__bf16>(p, s);
+        attn_bwd<__bf16>(p, workspace, s);
     return launch_status();
 }

@@ -21,7 +21,20 @@ struct AttnArgs {
     int32_t batch, nq, nk, heads, kv_heads, group, d;
     float scale;
     Div by_group, by_kv;
-    int32_t tiles;  // of rows or keys of a problem
+    int32_t tiles;   // of rows or keys of a problem
+    int32_t splits;  // of the keys (forward, dq) or of the rows (dk, dv)
+    int32_t per;     // keys or rows of a split
+    // more than one split: [problem][split][row or key][padded d] sums of each, joined by a next launch; the forward's
+    // are relative to the split's reference, which part_stat holds with the sum of the weights: [..][2]
+    float *part, *part_stat;
+};
+
+// How a call shares out its work: the same from sizes alone for the workspace and the launches.
+struct AttnPlan {
+    int few;                   // tiles of 16 rows that a wave takes with all of the keys of its own (0: block tiles)
+    int fwd_qc, dq_qc, dkv_kc; // 16-row tiles a wave
+    int fwd_splits, fwd_per, dq_splits, dq_per, dkv_splits, dkv_per;
+    size_t fwd_bytes, delta_bytes, dq_bytes, bwd_bytes;  // workspaces, and parts of the backward's
 };
 
 inline Div div_by(uint32_t d) {
@@ -31,8 +44,10 @@ inline Div div_by(uint32_t d) {
 }
 
 template <typename T>
-void attn_fwd(const AttnArgs& p, hipStream_t s);
+AttnPlan attn_plan(const AttnArgs& p);
 template <typename T>
-void attn_bwd(const AttnArgs& p, hipStream_t s);
+void attn_fwd(const AttnArgs& p, void* workspace, hipStream_t s);
+template <typename T>
+void attn_bwd(const AttnArgs& p, void* workspace, hipStream_t s);
 
 }  // namespace gs

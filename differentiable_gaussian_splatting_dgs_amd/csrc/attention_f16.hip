@@ -1,5 +1,6 @@
 // The float16 instances of the attention kernels.
 #include "attention.h"
 
-template void gs::attn_fwd<_Float16>(const gs::AttnArgs&, hipStream_t);
-template void gs::attn_bwd<_Float16>(const gs::AttnArgs&, hipStream_t);
+template gs::AttnPlan gs::attn_plan<_Float16>(const gs::AttnArgs&);
+template void gs::attn_fwd<_Float16>(const gs::AttnArgs&, void*, hipStream_t);
+template void gs::attn_bwd<_Float16>(const gs::AttnArgs&, void*, hipStream_t);

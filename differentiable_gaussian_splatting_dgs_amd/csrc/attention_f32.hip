@@ -1,5 +1,6 @@
 // The float32 instances of the attention kernels.
 #include "attention.h"
 
-template void gs::attn_fwd<float>(const gs::AttnArgs&, hipStream_t);
-template void gs::attn_bwd<float>(const gs::AttnArgs&, hipStream_t);
+template gs::AttnPlan gs::attn_plan<float>(const gs::AttnArgs&);
+template void gs::attn_fwd<float>(const gs::AttnArgs&, void*, hipStream_t);
+template void gs::attn_bwd<float>(const gs::AttnArgs&, void*, hipStream_t);

@@ -8,6 +8,7 @@ fallback.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import math
 import os
 import struct
@@ -107,8 +108,8 @@ SYMBOLS = ["gs_error_string", "gs_version", "gs_tile_grid", "gs_preprocess", "gs
            "gs_preprocess_h16", "gs_render_fwd_h16", "gs_render_bwd_h16", "gs_count_pairs_h16",
            "gs_linear_fwd", "gs_linear_bwd_workspace_size", "gs_linear_bwd", "gs_grad_workspace_size", "gs_grad_norm",
            "gs_grad_clip", "gs_adam_step_clipped",
-           "gs_attention_fwd", "gs_attention_bwd_workspace_size", "gs_attention_bwd", "gs_layer_norm_fwd",
-           "gs_layer_norm_bwd_workspace_size", "gs_layer_norm_bwd", "gs_dropout"]
+           "gs_attention_fwd_workspace_size", "gs_attention_fwd", "gs_attention_bwd_workspace_size", "gs_attention_bwd",
+           "gs_layer_norm_fwd", "gs_layer_norm_bwd_workspace_size", "gs_layer_norm_bwd", "gs_dropout"]
 MAX_VIEWS = 8
 PARAM_ORDER = ("means", "log_scales", "quats", "opacity_logits", "sh")
 
@@ -177,7 +178,8 @@ def load_library(path=LIB_PATH):
     lib.gs_grad_workspace_size.argtypes = [_i32, P(C.c_size_t)]
     lib.gs_grad_norm.argtypes = [_i32, _vp, C.c_float, _vp, _vp, C.c_size_t, _vp]
     lib.gs_grad_clip.argtypes = [_i32, _vp, C.c_float, _vp, _vp, C.c_size_t, _vp]
-    lib.gs_attention_fwd.argtypes = [_vp] * 10
+    lib.gs_attention_fwd_workspace_size.argtypes = [_vp, P(C.c_size_t)]
+    lib.gs_attention_fwd.argtypes = [_vp] * 10 + [C.c_size_t, _vp]
     lib.gs_attention_bwd_workspace_size.argtypes = [_vp, P(C.c_size_t)]
     lib.gs_attention_bwd.argtypes = [_vp] * 14 + [C.c_size_t, _vp]
     lib.gs_layer_norm_fwd.argtypes = [_vp] * 6
@@ -1074,12 +1076,22 @@ def _valid(mask, q_lengths, k_lengths, batch, nk, device):
     return at, stride or 0, *lengths
 
 
-def attention_fwd_into(q, k, v, mask, q_lengths, k_lengths, out, lse, scale):
-    """gs_attention_fwd; out None: a new tensor.  lse: a tensor, None (not wanted) or True (a new one).  Returns both."""
+@functools.lru_cache(maxsize=1024)
+def _attention_workspace(name, batch, nq, nk, heads, kv_heads, d, code):
+    """Bytes of workspace of a call on these sizes."""
+    b = C.c_size_t()
+    _check(getattr(load_library(), name)(_pack_attention(batch, nq, nk, heads, kv_heads, d, code, *[0] * 13, 1.0),
+                                         C.byref(b)), name)
+    return b.value
+
+
+def attention_fwd_into(q, k, v, mask, q_lengths, k_lengths, out, lse, workspace, scale):
+    """gs_attention_fwd; out None: a new tensor.  lse: a tensor, None (not wanted) or True (a new one).  workspace None:
+    one of the size the call needs.  Returns out and lse."""
     batch, nq, nk, heads, kv_heads, d, code, device, scale = _attention_shape(q, k, scale)
     if device != _current_device():
         with torch.cuda.device(device):
-            return attention_fwd_into(q, k, v, mask, q_lengths, k_lengths, out, lse, scale)
+            return attention_fwd_into(q, k, v, mask, q_lengths, k_lengths, out, lse, workspace, scale)
     dtype = q.dtype
     strides = (*_per_head(q, q.shape, dtype, device, "q"), *_per_head(k, k.shape, dtype, device, "k"),
                *_per_head(v, k.shape, dtype, device, "v"))
@@ -1091,29 +1103,38 @@ def attention_fwd_into(q, k, v, mask, q_lengths, k_lengths, out, lse, scale):
         to = _whole(out, q.shape, dtype, device, "out")
     if lse is True:
         lse = torch.empty((batch, heads, nq), dtype=torch.float32, device=q.device)
+    size = _attention_workspace("gs_attention_fwd_workspace_size", batch, nq, nk, heads, kv_heads, d, code)
+    if workspace is None and size:
+        # torch's device allocations start at multiples of 512 bytes
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    pw = None
+    if workspace is not None:
+        pw, size = _whole(workspace, workspace.shape, torch.uint8, device, "workspace"), workspace.numel()
     rc = (_lib or load_library()).gs_attention_fwd(
         _pack_attention(batch, nq, nk, heads, kv_heads, d, code, *strides, 0, 0, 0, mask_stride, scale), q.data_ptr(),
         k.data_ptr(), v.data_ptr(), pm, pq, pk, to, _whole(lse, (batch, heads, nq), torch.float32, device, "lse"),
-        _raw_stream(device))
+        pw, size, _raw_stream(device))
     if rc:
         _check(rc, "gs_attention_fwd")
     return out, lse
 
 
-def gs_attention_fwd(q, k, v, out, lse=None, mask=None, q_lengths=None, k_lengths=None, scale=None):
-    """out [batch, nq, heads, d] = softmax(scale q k^T) v and lse [batch, heads, nq] float32 (None: not wanted)."""
+def gs_attention_fwd_workspace_size(q, k):
+    return _attention_workspace("gs_attention_fwd_workspace_size", *_attention_shape(q, k, None)[:7])
+
+
+def gs_attention_fwd(q, k, v, out, lse, workspace, mask=None, q_lengths=None, k_lengths=None, scale=None):
+    """out [batch, nq, heads, d] = softmax(scale q k^T) v and lse [batch, heads, nq] float32 (None: not wanted);
+    workspace: uint8, gs_attention_fwd_workspace_size bytes, 256-byte aligned (None where that is 0)."""
     if out is None or lse is True:
         raise GsError("out and lse are the caller's tensors")
-    attention_fwd_into(q, k, v, mask, q_lengths, k_lengths, out, lse, scale)
+    if workspace is None and gs_attention_fwd_workspace_size(q, k):
+        raise GsError("the call needs a workspace")
+    attention_fwd_into(q, k, v, mask, q_lengths, k_lengths, out, lse, workspace, scale)
 
 
 def gs_attention_bwd_workspace_size(q, k):
-    batch, nq, nk, heads, kv_heads, d, code, _, scale = _attention_shape(q, k, None)
-    b = C.c_size_t()
-    _check(load_library().gs_attention_bwd_workspace_size(
-        _pack_attention(batch, nq, nk, heads, kv_heads, d, code, *[0] * 13, scale), C.byref(b)),
-        "gs_attention_bwd_workspace_size")
-    return b.value
+    return _attention_workspace("gs_attention_bwd_workspace_size", *_attention_shape(q, k, None)[:7])
 
 
 def attention_bwd_into(q, k, v, out, lse, dout, dq, dk, dv, workspace, mask, q_lengths, k_lengths, scale):
@@ -1135,10 +1156,9 @@ def attention_bwd_into(q, k, v, out, lse, dout, dq, dk, dv, workspace, mask, q_l
     lib = _lib or load_library()
     a = _pack_attention(batch, nq, nk, heads, kv_heads, d, code, *strides, mask_stride, scale)
     if workspace is None:
-        b = C.c_size_t()
-        _check(lib.gs_attention_bwd_workspace_size(a, C.byref(b)), "gs_attention_bwd_workspace_size")
+        size = _attention_workspace("gs_attention_bwd_workspace_size", batch, nq, nk, heads, kv_heads, d, code)
         # torch's device allocations start at multiples of 512 bytes
-        workspace = torch.empty(b.value, dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
     rc = lib.gs_attention_bwd(a, *at, _whole(workspace, workspace.shape, torch.uint8, device, "workspace"),
                               workspace.numel(), _raw_stream(device))
     if rc:

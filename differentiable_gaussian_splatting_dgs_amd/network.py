@@ -158,7 +158,7 @@ def dropout_backward(dy, p, seed, offset=0):
 def cross_attention_forward(q, k, v, mask=None, q_lengths=None, k_lengths=None, scale=None):
     """out of cross_attention and lse [batch, heads, nq] float32, the log of the sums of its softmax (-infinity where
     nothing counts): what cross_attention_backward takes."""
-    return gs.attention_fwd_into(q, k, v, mask, q_lengths, k_lengths, None, True, scale)
+    return gs.attention_fwd_into(q, k, v, mask, q_lengths, k_lengths, None, True, None, scale)
 
 
 def cross_attention_backward(dout, q, k, v, out, lse, mask=None, q_lengths=None, k_lengths=None, scale=None,
@@ -197,7 +197,7 @@ def cross_attention(q, k, v, mask=None, q_lengths=None, k_lengths=None, scale=No
     not count, or has no key that does, gives 0."""
     if _differentiable(q, k, v):
         return CrossAttentionFunction.apply(q, k, v, mask, q_lengths, k_lengths, scale)
-    return gs.attention_fwd_into(q, k, v, mask, q_lengths, k_lengths, None, None, scale)[0]
+    return gs.attention_fwd_into(q, k, v, mask, q_lengths, k_lengths, None, None, None, scale)[0]
 
 
 _HERE = contextlib.nullcontext()

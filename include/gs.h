@@ -752,9 +752,14 @@ typedef struct gs_attention {
     float scale;
 } gs_attention;
 
-/* out and lse (NULL: not wanted); out must not overlap the inputs. */
+/* Bytes of workspace gs_attention_fwd needs (0: none; for few queries on many keys). */
+int gs_attention_fwd_workspace_size(const gs_attention* a, size_t* bytes);
+
+/* out and lse (NULL: not wanted); out must not overlap the inputs.  workspace: 256-byte aligned, contents on entry
+   irrelevant. */
 int gs_attention_fwd(const gs_attention* a, const void* q, const void* k, const void* v, const uint8_t* mask,
-                     const int32_t* q_lengths, const int32_t* k_lengths, void* out, float* lse, void* stream);
+                     const int32_t* q_lengths, const int32_t* k_lengths, void* out, float* lse, void* workspace,
+                     size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace gs_attention_bwd needs. */
 int gs_attention_bwd_workspace_size(const gs_attention* a, size_t* bytes);

@@ -29,19 +29,23 @@ BAD = [(dict(batch=-1), -1), (dict(nq=-1), -1), (dict(nk=-1), -1), (dict(heads=0
 @pytest.mark.parametrize("kw,code", BAD)
 def test_attention_shapes(kw, code):
     lib, b, a = gs.load_library(), C.c_size_t(), attention(**kw)
-    assert lib.gs_attention_fwd(C.byref(a), FAKE, FAKE, FAKE, None, None, None, FAKE, None, None) == code
+    assert lib.gs_attention_fwd(C.byref(a), FAKE, FAKE, FAKE, None, None, None, FAKE, None, FAKE, 1 << 40, None) == code
     assert lib.gs_attention_bwd(C.byref(a), FAKE, FAKE, FAKE, None, None, None, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE,
                                 FAKE, 1 << 40, None) == code
-    assert lib.gs_attention_bwd_workspace_size(C.byref(a), C.byref(b)) == code
+    for size in (lib.gs_attention_bwd_workspace_size, lib.gs_attention_fwd_workspace_size):
+        assert size(C.byref(a), C.byref(b)) == code
 
 
 def test_attention_pointers():
     lib = gs.load_library()
 
-    def fwd(q=FAKE, k=FAKE, v=FAKE, mask=None, ql=None, kl=None, out=FAKE, lse=None, **kw):
-        return lib.gs_attention_fwd(C.byref(attention(**kw)), q, k, v, mask, ql, kl, out, lse, None)
+    def fwd(q=FAKE, k=FAKE, v=FAKE, mask=None, ql=None, kl=None, out=FAKE, lse=None, ws=FAKE, size=1 << 30, **kw):
+        return lib.gs_attention_fwd(C.byref(attention(**kw)), q, k, v, mask, ql, kl, out, lse, ws, size, None)
 
-    assert lib.gs_attention_fwd(None, FAKE, FAKE, FAKE, None, None, None, FAKE, None, None) == -1
+    assert lib.gs_attention_fwd(None, FAKE, FAKE, FAKE, None, None, None, FAKE, None, None, 0, None) == -1
+    assert fwd(ws=C.c_void_p((1 << 20) + 64)) == -2
+    long = dict(nq=1, nk=100_000)  # few queries on many keys: the keys are split
+    assert fwd(ws=None, **long) == -1 and fwd(size=64, **long) == -3
     for name in ("q", "k", "v", "out"):
         assert fwd(**{name: None}) == -1 and fwd(**{name: HALF}) == -2 and fwd(dtype=1, **{name: ODD}) == -2, name
     for name in ("ql", "kl", "lse"):
@@ -60,6 +64,8 @@ def test_attention_pointers():
     assert bwd(batch=0) == 0 and bwd(nq=0, nk=0) == 0
     b = C.c_size_t()
     assert lib.gs_attention_bwd_workspace_size(C.byref(attention()), None) == -1
+    assert lib.gs_attention_fwd_workspace_size(C.byref(attention()), None) == -1
+    assert lib.gs_attention_fwd_workspace_size(C.byref(attention()), C.byref(b)) == 0 and b.value == 0
     assert lib.gs_attention_bwd_workspace_size(C.byref(attention()), C.byref(b)) == 0 and b.value % 256 == 0
     assert bwd(size=b.value - 1) == -3
 
@@ -151,7 +157,7 @@ def gradients(function, tensors, outs, upstream):
 
 @pytest.fixture
 def formulas(monkeypatch):
-    def attention_fwd(q, k, v, mask, ql, kl, out, lse, scale):
+    def attention_fwd(q, k, v, mask, ql, kl, out, lse, ws, scale):
         with torch.no_grad():
             return attend(q, k, v, scale).transpose(1, 2), torch.zeros(())
 
