@@ -20,7 +20,8 @@ OBJDIR = os.path.join(PKG, "_build")
 SOURCES = ["api.hip", "preprocess.hip", "binning.hip", "render.hip", "preprocess_bwd.hip", "train.hip",
            "densify.hip", "debug.hip", "linear.hip", "linear_bwd_f32.hip",
            "linear_bwd_f16.hip", "linear_bwd_bf16.hip", "clip.hip", "attention.hip",
-           "attention_f32.hip", "attention_f16.hip", "attention_bf16.hip", "norm.hip", "dropout.hip"]
+           "attention_fwd_f32.hip", "attention_fwd_f16.hip", "attention_fwd_bf16.hip", "attention_bwd_f32.hip",
+           "attention_bwd_f16.hip", "attention_bwd_bf16.hip", "norm.hip", "dropout.hip"]
 MEASURE_SOURCES = ["calibrate.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -56,7 +57,7 @@ def build(force=True, verbose=False):
     deps = [os.path.join(CSRC, s) for s in SOURCES + MEASURE_SOURCES] + [
         os.path.join(CSRC, "gs_internal.h"), os.path.join(CSRC, "linear_tile.h"),
         os.path.join(CSRC, "linear_bwd.h"), os.path.join(CSRC, "attention_args.h"),
-        os.path.join(CSRC, "attention.h"),
+        os.path.join(CSRC, "attention.h"), os.path.join(CSRC, "attention_fwd.h"), os.path.join(CSRC, "attention_bwd.h"),
         os.path.join(INCLUDE, "gs.h"), os.path.join(INCLUDE, "gs_measure.h")]
     if (not force and all(os.path.exists(x) for x in (LIB, MEASURE_LIB)) and
             min(os.path.getmtime(LIB), os.path.getmtime(MEASURE_LIB)) >= max(os.path.getmtime(d) for d in deps)):

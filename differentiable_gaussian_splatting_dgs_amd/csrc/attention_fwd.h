@@ -1,0 +1,423 @@
+// Forward of cross attention (attention.h).
+#pragma once
+
+#include "attention.h"
+
+namespace gs {
+
+// A forward's rows: the results, or those of a split.  o is relative to the reference m.
+template <typename T, int D, int QC>
+__device__ __forceinline__ void forward_rows(const AttnArgs& p, const Place& at, int row0, int live, bool any,
+                                             const float (&m)[QC], const float (&l)[QC],
+                                             const f32x4 (&o)[QC][AttnTile<T, D>::kPairs][Tile<T>::TG], int lane) {
+    constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG;
+    typedef typename Tile<T>::Frag Frag;
+    const int r = lane & 15, g = lane >> 4, rows = p.nq * p.group;
+#pragma unroll
+    for (int c = 0; c < QC; ++c) {
+        const int row = row0 + 16 * c + r;
+        if (row >= rows) continue;
+        if (p.splits > 1) {
+            const int64_t to = at.part(p, rows) + row;
+#pragma unroll
+            for (int e = 0; e < AttnTile<T, D>::kPairs; ++e)
+#pragma unroll
+                for (int u = 0; u < TG; ++u)
+                    *reinterpret_cast<f32x4*>(p.part + to * D + KS * e + E * g + 4 * u) = o[c][e][u];
+            if (g == 0) {
+                p.part_stat[2 * to] = m[c];
+                p.part_stat[2 * to + 1] = any && m[c] == -INFINITY ? NAN : l[c];
+            }
+            continue;
+        }
+        const Row w(p, at.hk, row, true);
+        const bool empty = !any || row >= live;
+        const float inv = 1.f / l[c];
+        T* out = static_cast<T*>(p.out) + w.whole(p, at.b) * p.d;
+#pragma unroll
+        for (int e = 0; e < AttnTile<T, D>::kPairs; ++e) {
+            Frag f;
+#pragma unroll
+            for (int u = 0; u < TG; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[4 * u + j] = empty ? (T)0.f : (T)(o[c][e][u][j] * inv);
+            store_run(out, KS * e + E * g, p.d, f);
+        }
+        if (p.lse && g == 0)
+            p.lse[w.stat(p, at.b)] =
+                empty || m[c] == -INFINITY ? -INFINITY
+                                           : (m[c] + __builtin_amdgcn_logf(l[c]) - Softmax<T>::kShift) * kLn2;
+    }
+}
+
+// The splits' results together: WIDE threads of 4 columns for a row, times SPLITS that share out its splits.
+template <typename T, int D, int SHARE>
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs p) {
+    constexpr int kWide = D / 4, kRows = 256 / (kWide * SHARE);
+    __shared__ f32x4 s_sum[256];
+    __shared__ float s_l[256], s_m[256];
+    const int col = threadIdx.x % kWide, share = threadIdx.x / kWide % SHARE, in = threadIdx.x / (kWide * SHARE);
+    const int rows = p.nq * p.group;
+    const int64_t at = (int64_t)blockIdx.x * kRows + in, total = (int64_t)p.batch * p.kv_heads * rows;
+    const int64_t problem = at < total ? at / rows : 0;
+    const int row = at < total ? (int)(at - problem * rows) : 0;
+    const float* stat = p.part_stat + 2 * (problem * p.splits * rows + row);
+    const float* part = p.part + (problem * p.splits * rows + row) * D + 4 * col;
+    float m = -INFINITY;
+#pragma unroll 4
+    for (int i = threadIdx.x % (kWide * SHARE); i < p.splits; i += kWide * SHARE)
+        m = fmaxf(m, stat[(int64_t)2 * rows * i]);
+    s_m[threadIdx.x] = m;
+    __syncthreads();
+    for (int o = kWide * SHARE / 2; o > 0; o >>= 1) {
+        if (threadIdx.x % (kWide * SHARE) < o) s_m[threadIdx.x] = fmaxf(s_m[threadIdx.x], s_m[threadIdx.x + o]);
+        __syncthreads();
+    }
+    m = s_m[in * (kWide * SHARE)];
+    f32x4 sum = {};
+    float l = 0.f;
+#pragma unroll 4
+    for (int i = share; i < p.splits; i += SHARE) {
+        const float mi = stat[(int64_t)2 * rows * i], li = stat[(int64_t)2 * rows * i + 1];
+        const float w = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mi - m);
+        const f32x4 o = *reinterpret_cast<const f32x4*>(part + (int64_t)rows * D * i);
+        if (mi != -INFINITY || m == -INFINITY) {
+            l = fmaf(w, li, l);
+            sum += o * w;
+        }
+    }
+    s_sum[threadIdx.x] = sum;
+    s_l[threadIdx.x] = l;
+    __syncthreads();
+    if (share > 0 || at >= total) return;
+#pragma unroll
+    for (int i = 1; i < SHARE; ++i) {
+        sum += s_sum[threadIdx.x + i * kWide];
+        l += s_l[threadIdx.x + i * kWide];
+    }
+    const int b = (int)(problem / p.kv_heads), hk = (int)(problem - (int64_t)b * p.kv_heads);
+    const Row w(p, hk, row, true);
+    const bool empty = row >= live_rows(p, b) || (m == -INFINITY && l == 0.f);  // NaN: logits of -infinity
+    const float inv = 1.f / l;
+    T* out = static_cast<T*>(p.out) + w.whole(p, b) * p.d;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (4 * col + j < p.d) out[4 * col + j] = empty ? (T)0.f : (T)(sum[j] * inv);
+    if (p.lse && col == 0)
+        p.lse[w.stat(p, b)] = empty || m == -INFINITY ? -INFINITY : (m + __builtin_amdgcn_logf(l) - Softmax<T>::kShift) * kLn2;
+}
+
+// What a wave's rows have come to: sums relative to a reference, which trails the maximum.
+template <typename T, int D, int QC>
+struct RowState {
+    static constexpr int TG = Tile<T>::TG, E = Tile<T>::E;
+    typedef typename Tile<T>::Frag Frag;
+    f32x4 o[QC][AttnTile<T, D>::kPairs][TG];
+    // l: the lane's part of the weights' sum, before they are rounded (a product with ones would sum them after it);
+    // limit: the reference moves for a logit above it
+    float l[QC], ref[QC], limit[QC];
+    float c2;
+
+    __device__ __forceinline__ explicit RowState(float scale) : o{}, c2(fabsf(scale) * kLog2e) {
+#pragma unroll
+        for (int c = 0; c < QC; ++c) l[c] = 0.f, ref[c] = 0.f, limit[c] = -INFINITY;
+    }
+    __device__ __forceinline__ float reference(int c) const { return limit[c] - Softmax<T>::kSlack; }
+    // the weights of KS keys from their logits, as the next product's fragment
+    __device__ __forceinline__ void weigh(const f32x4 (&s)[QC][TG], Frag (&w)[QC]) {
+        float top[QC];
+        bool over = false;
+#pragma unroll
+        for (int c = 0; c < QC; ++c) {
+            top[c] = s[c][0][0];
+#pragma unroll
+            for (int u = 0; u < TG; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) top[c] = fmaxf(top[c], s[c][u][j]);
+            over |= top[c] * c2 > limit[c];
+        }
+        if (__any(over)) {
+#pragma unroll
+            for (int c = 0; c < QC; ++c) {
+                const float old = reference(c), next = fmaxf(highest(top[c]) * c2, old);
+                if (next != -INFINITY) ref[c] = next - Softmax<T>::kShift;
+                limit[c] = next + Softmax<T>::kSlack;
+                const float by = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(old - next);
+                l[c] *= by;
+#pragma unroll
+                for (int e = 0; e < AttnTile<T, D>::kPairs; ++e)
+#pragma unroll
+                    for (int u = 0; u < TG; ++u) o[c][e][u] *= by;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < QC; ++c) {
+#pragma unroll
+            for (int u = 0; u < TG; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float e = __builtin_amdgcn_exp2f(fmaf(s[c][u][j], c2, -ref[c]));
+                    l[c] += e;
+                    w[c][4 * u + j] = (T)e;
+                }
+        }
+    }
+    // o += w v, values in a tile of LDS from row m0 on
+    __device__ __forceinline__ void add(const char* tile, int m0, const Frag (&w)[QC], int lane) {
+#pragma unroll
+        for (int e = 0; e < AttnTile<T, D>::kPairs; ++e)
+#pragma unroll
+            for (int u = 0; u < TG; ++u) {
+                const Frag a = down_frag<T, D>(tile, m0, e, u, lane);
+#pragma unroll
+                for (int c = 0; c < QC; ++c) mma(o[c][e][u], a, w[c]);
+            }
+    }
+    __device__ __forceinline__ float sum(int c) const { return added(l[c]); }
+};
+
+// Logits of keys that do not count.  bits: the group's, from its first key on.
+template <typename T, int QC>
+__device__ __forceinline__ void without(f32x4 (&s)[QC][Tile<T>::TG], uint64_t bits, int g) {
+#pragma unroll
+    for (int u = 0; u < Tile<T>::TG; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool in = bits >> (Tile<T>::E * g + 4 * u + j) & 1;
+#pragma unroll
+            for (int c = 0; c < QC; ++c) s[c][u][j] = in ? s[c][u][j] : -INFINITY;
+        }
+}
+
+// Forward of few rows: 16 QC of them with all keys of a split, which the four waves of a block share out in tiles of
+// their own.  A wave reads keys and values from memory as fragments, values through LDS of its own to turn them, and
+// nothing but the end waits for another wave: what bounds it is the stream of keys and values.
+template <typename T, int D, int QC, int MODE>
+__global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 512 ? 1 : 2)) void k_attn_few(AttnArgs p) {
+    typedef AttnTile<T, D> A;
+    typedef FewTile<T, D> F;
+    typedef typename Tile<T>::Frag Frag;
+    constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG, KG = F::kGroups, KW = F::kKeys;
+    constexpr int kJoin = 16 * QC * D * 4;
+    __shared__ __align__(16) char s_mem[4 * F::kBytes > kJoin ? 4 * F::kBytes : kJoin];
+    __shared__ float s_m[4][16 * QC], s_l[4][16 * QC];
+    const Place at(p);
+    if (at.none) return;
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Keys keys(p, at.b);
+    const int first = at.split * p.per, last = keys.count - 1;
+    keys.until(first + p.per);
+    const int live = live_rows(p, at.b);
+    char* tv = s_mem + wave * F::kBytes;
+
+    const T* k_base = static_cast<const T*>(p.k) + at.b * p.k_b + at.hk * p.k_h;
+    const T* v_base = static_cast<const T*>(p.v) + at.b * p.v_b + at.hk * p.v_h;
+    Frag k[KG][TG][A::kSteps], v[KG][TG][A::kSteps];
+    int byte = 0;
+    auto fetch = [&](int k0) {
+        byte = lane < KW ? keys.byte(k0, lane) : 0;
+#pragma unroll
+        for (int kg = 0; kg < KG; ++kg)
+#pragma unroll
+            for (int u = 0; u < TG; ++u) {
+                const int in = min(kg * KS + out_row<T>(u, r), last - k0);
+                if constexpr (MODE == ANY) {
+                    raw_frags<T, MODE>(k[kg][u], k_base + (int64_t)(k0 + in) * p.k_n, g, p.d);
+                    raw_frags<T, MODE>(v[kg][u], v_base + (int64_t)(k0 + in) * p.v_n, g, p.d);
+                } else {
+                    raw_frags<T, MODE>(k[kg][u], k_base + k0 * p.k_n + (uint32_t)in * (uint32_t)p.k_n, g, p.d);
+                    raw_frags<T, MODE>(v[kg][u], v_base + k0 * p.v_n + (uint32_t)in * (uint32_t)p.v_n, g, p.d);
+                }
+            }
+    };
+    int k0 = first + wave * KW;
+    if (live == 0) k0 = keys.count;
+    if (k0 < keys.count) fetch(k0);
+    Frag q[QC][A::kSteps];
+    rows_held<T, MODE>(p, at.b, at.hk, 0, live, p.q, p.q_b, p.q_n, p.q_h, p.scale < 0.f, lane, q);
+    RowState<T, D, QC> rows(p.scale);
+    uint64_t any = 0;
+    for (; k0 < keys.count; k0 += 4 * KW) {
+        const uint64_t valid = __ballot(byte != 0);
+        any |= valid;
+        f32x4 s[KG][QC][TG] = {};
+#pragma unroll
+        for (int kg = 0; kg < KG; ++kg)
+#pragma unroll
+            for (int u = 0; u < TG; ++u) {
+                fix_frags<T, MODE>(k[kg][u], g, p.d, true);
+#pragma unroll
+                for (int e = 0; e < A::kSteps; ++e)
+#pragma unroll
+                    for (int c = 0; c < QC; ++c) mma(s[kg][c][u], k[kg][u][e], q[c][e]);
+                const int row = kg * KS + out_row<T>(u, r);
+                fix_frags<T, MODE>(v[kg][u], g, p.d, valid >> row & 1);
+#pragma unroll
+                for (int e = 0; e < A::kSteps; ++e)
+                    *reinterpret_cast<Frag*>(tv + tile_at<T, D>(row, 4 * e + g)) = v[kg][u][e];
+            }
+        if (k0 + 4 * KW < keys.count) fetch(k0 + 4 * KW);
+        wave_sync();
+#pragma unroll
+        for (int kg = 0; kg < KG; ++kg) {
+            if (valid != ~0ull >> (64 - KW)) without<T, QC>(s[kg], valid >> (kg * KS), g);
+            Frag w[QC];
+            rows.weigh(s[kg], w);
+            rows.add(tv, kg * KS, w, lane);
+        }
+        wave_sync();
+    }
+    // the waves' results together, in their order
+    float sum[QC], top[QC];
+#pragma unroll
+    for (int c = 0; c < QC; ++c) {
+        const float own = rows.sum(c);
+        if (g == 0) s_m[wave][16 * c + r] = rows.reference(c), s_l[wave][16 * c + r] = own;
+    }
+    const bool some = __syncthreads_or(any != 0);
+    float* s_o = reinterpret_cast<float*>(s_mem);  // [16 QC][D]
+#pragma unroll
+    for (int c = 0; c < QC; ++c) {
+        const int row = 16 * c + r;
+        const float m = rows.reference(c);
+        top[c] = fmaxf(fmaxf(s_m[0][row], s_m[1][row]), fmaxf(s_m[2][row], s_m[3][row]));
+        sum[c] = 0.f;
+        for (int i = 0; i < 4; ++i)
+            if (s_m[i][row] != -INFINITY) sum[c] = fmaf(__builtin_amdgcn_exp2f(s_m[i][row] - top[c]), s_l[i][row], sum[c]);
+        const float by = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top[c]);
+#pragma unroll
+        for (int e = 0; e < A::kPairs; ++e)
+#pragma unroll
+            for (int u = 0; u < TG; ++u) rows.o[c][e][u] *= by;
+    }
+    for (int i = 0; i < 4; ++i) {
+        if (wave == i) {
+#pragma unroll
+            for (int c = 0; c < QC; ++c)
+#pragma unroll
+                for (int e = 0; e < A::kPairs; ++e)
+#pragma unroll
+                    for (int u = 0; u < TG; ++u) {
+                        f32x4* to = reinterpret_cast<f32x4*>(s_o + (16 * c + r) * D + KS * e + E * g + 4 * u);
+                        if (i > 0) rows.o[c][e][u] += *to;
+                        if (i < 3) *to = rows.o[c][e][u];
+                    }
+        }
+        __syncthreads();
+    }
+    if (wave == 3) forward_rows<T, D, QC>(p, at, 0, live, some, top, sum, rows.o, lane);
+}
+
+// Forward over tiles of 64 QC rows and the keys of a split.
+template <typename T, int D, int QC, int MODE>
+__global__ __launch_bounds__(256, (AttnShape<T, D>::kOccFwd)) void k_attn_fwd(AttnArgs p) {
+    typedef AttnTile<T, D> A;
+    typedef typename Tile<T>::Frag Frag;
+    constexpr int KS = Tile<T>::KS, TG = Tile<T>::TG, KT = A::kRows, NG = A::kGroups;
+    __shared__ __align__(16) char s_k[2][A::kBytes], s_v[2][A::kBytes];
+    const Place at(p);
+    if (at.none) return;
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Keys keys(p, at.b);
+    const int first = at.split * p.per;
+    KeyTiles<T, D, MODE> tile_k(p.k, at.b * p.k_b + at.hk * p.k_h, p.k_n, keys.count, p.d);
+    KeyTiles<T, D, MODE> tile_v(p.v, at.b * p.v_b + at.hk * p.v_h, p.v_n, keys.count, p.d);
+    keys.until(first + p.per);
+    const int live = live_rows(p, at.b);
+    const int row0 = (at.tile * 4 + wave) * 16 * QC;
+    const int tiles = live > at.tile * 64 * QC ? (keys.count - first + KT - 1) / KT : 0;
+    uint64_t valid = 0, any = 0;
+    int byte = 0;
+    if (tiles > 0) {
+        byte = keys.byte(first, lane);
+        tile_k.load(first, p.d);
+        tile_v.load(first, p.d);
+    }
+    Frag q[QC][A::kSteps];
+    rows_held<T, MODE>(p, at.b, at.hk, row0, live, p.q, p.q_b, p.q_n, p.q_h, p.scale < 0.f, lane, q);
+    RowState<T, D, QC> rows(p.scale);
+    if (tiles > 0) {
+        valid = key_bits<KT>(byte);
+        tile_k.move.store(s_k[0], valid, p.d);
+        tile_v.move.store(s_v[0], valid, p.d);
+    }
+    for (int t = 0; t < tiles; ++t) {
+        if (t + 1 < tiles) {
+            const int next = first + (t + 1) * KT;
+            byte = keys.byte(next, lane);
+            tile_k.load(next, p.d);
+            tile_v.load(next, p.d);
+        }
+        __syncthreads();
+        const char* tk = s_k[t & 1];
+        const char* tv = s_v[t & 1];
+        any |= valid;
+#pragma unroll
+        for (int kg = 0; kg < NG; ++kg) {
+            f32x4 s[QC][TG] = {};
+#pragma unroll
+            for (int u = 0; u < TG; ++u)
+#pragma unroll
+                for (int e = 0; e < A::kSteps; ++e) {
+                    const Frag a = row_frag<T, D>(tk, kg * KS + out_row<T>(u, r), e, g);
+#pragma unroll
+                    for (int c = 0; c < QC; ++c) mma(s[c][u], a, q[c][e]);
+                }
+            if (valid != ~0ull >> (64 - KT)) without<T, QC>(s, valid >> (kg * KS), g);
+            Frag w[QC];
+            rows.weigh(s, w);
+            rows.add(tv, kg * KS, w, lane);
+        }
+        if (t + 1 < tiles) {
+            valid = key_bits<KT>(byte);
+            tile_k.move.store(s_k[(t + 1) & 1], valid, p.d);
+            tile_v.move.store(s_v[(t + 1) & 1], valid, p.d);
+        }
+    }
+    float m[QC], l[QC];
+#pragma unroll
+    for (int c = 0; c < QC; ++c) m[c] = rows.reference(c), l[c] = rows.sum(c);
+    forward_rows<T, D, QC>(p, at, row0, live, any != 0, m, l, rows.o, lane);
+}
+
+template <typename T, int D, int MODE>
+void attn_fwd_in(AttnArgs p, void* workspace, hipStream_t s) {
+    const AttnPlan a = plan_at<T, D>(p);
+    constexpr int kFew = MODE == ANY ? 1 : 2, kQc = MODE == ANY ? 1 : AttnShape<T, D>::kFwd;
+    const int64_t rows = (int64_t)p.nq * p.group, problems = (int64_t)p.batch * p.kv_heads;
+    p.splits = a.fwd_splits, p.per = a.fwd_per;
+    p.part = static_cast<float*>(workspace);
+    if (p.splits > 1) p.part_stat = p.part + padded((size_t)problems * rows * D * 4 * p.splits) / 4;
+    if (a.few && a.few <= kFew) {
+        p.tiles = 1;
+        if (a.few == 1) hipLaunchKernelGGL((k_attn_few<T, D, 1, MODE>), grid_of(p), dim3(256), 0, s, p);
+        else hipLaunchKernelGGL((k_attn_few<T, D, kFew, MODE>), grid_of(p), dim3(256), 0, s, p);
+    } else {
+        const int qc = a.fwd_qc < kQc ? a.fwd_qc : kQc;
+        p.tiles = (int32_t)tiles_of(rows, 64 * qc);
+        if (qc == 1) hipLaunchKernelGGL((k_attn_fwd<T, D, 1, MODE>), grid_of(p), dim3(256), 0, s, p);
+        else hipLaunchKernelGGL((k_attn_fwd<T, D, kQc, MODE>), grid_of(p), dim3(256), 0, s, p);
+    }
+    if (p.splits > 1) GS_ATTN_SHARED(k_attn_join, problems * rows);
+}
+
+template <typename T, int D>
+void attn_fwd_at(const AttnArgs& p, void* workspace, hipStream_t s) {
+    const int mode = attn_mode<T, D>(p);
+    if (mode == WHOLE) attn_fwd_in<T, D, WHOLE>(p, workspace, s);
+    else if (mode == PART) attn_fwd_in<T, D, PART>(p, workspace, s);
+    else attn_fwd_in<T, D, ANY>(p, workspace, s);
+}
+
+template <typename T>
+AttnPlan attn_plan(const AttnArgs& p) {
+    return GS_ATTN_BY_HEAD(plan_at)(p);
+}
+template <typename T>
+void attn_fwd(const AttnArgs& p, void* workspace, hipStream_t s) {
+    GS_ATTN_BY_HEAD(attn_fwd_at)(p, workspace, s);
+}
+
+}  // namespace gs
