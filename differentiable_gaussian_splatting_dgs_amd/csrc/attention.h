@@ -11,7 +11,7 @@
 //
 // exp is exp2 of scale log2 e s.  A row's reference m trails its maximum: it moves (and what is summed so far is
 // scaled) only when a logit passes it by more than kSlack, which nothing that is summed in float32 notices.
-// float16 weights are held times 2^kShift: the range from 2^-24 up would lose the small ones of a long row.
+// float16 weights are held times 2^kShift: its steps of 2^-24 would lose the small ones of a long row.
 // A key that its length or mask takes out has weight 0 and is zero in LDS: 0 times infinity or NaN would
 // otherwise reach every row.
 #pragma once
@@ -23,17 +23,21 @@
 
 namespace gs {
 
+constexpr int kThinBlocks = 512;       // that keep their keys: two a CU
+constexpr int kThinTiles = 16;           // tiles of keys that a block keeps in LDS, at most
+constexpr int kThinBytes = 64 * 1024;  // and their bytes: two blocks a CU
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ uint32_t divided(uint32_t n, Div d) { return (__umulhi(n, d.mul) + n) >> d.shift; }
 
+// The forward's reference, in base 2.  float16's largest weight is 2^(kShift + kSlack) < 65504.
 template <typename T>
-struct Softmax {  // base 2
-    static constexpr float kShift = sizeof(T) == 2 ? 0.f : 0.f, kSlack = 8.f;
+struct Softmax {
+    static constexpr float kShift = 0.f, kSlack = 8.f;
 };
 template <>
 struct Softmax<_Float16> {
-    static constexpr float kShift = 13.f, kSlack = 2.f;  // 2^15 < 65504
+    static constexpr float kShift = 7.f, kSlack = 8.f;
 };
 
 // Rows of a tile in LDS, for two buffers of two tiles at two blocks a CU.
@@ -57,6 +61,8 @@ struct AttnShape {
     static constexpr int kFwd = kHalf ? (D <= 64 ? 4 : D <= 128 ? 2 : 1) : D <= 128 ? 2 : 1;
     static constexpr int kDq = kHalf ? (D <= 128 ? 2 : 1) : D <= 64 ? 2 : 1;
     static constexpr int kDkv = kHalf ? (D <= 128 ? 2 : 1) : D <= 64 ? 2 : 1;
+    static constexpr int kThin = D <= 32 ? (kHalf ? 4 : 2) : D <= 128 ? (kHalf ? 2 : 1) : 1;
+    static constexpr int kOccThin = D * (int)sizeof(T) >= 512 ? 1 : 2;
     static constexpr int kOccFwd = D * (int)sizeof(T) >= 512 ? 1 : 2;
     static constexpr int kOccDq = D * (int)sizeof(T) >= 512 ? 1 : 2;
     static constexpr int kOccDkv = D * (int)sizeof(T) >= 256 ? 1 : 2;
@@ -247,16 +253,17 @@ struct Place {
     int b, hk, tile, split;
     uint32_t problem;
     bool none;
-    __device__ __forceinline__ Place(const AttnArgs& p) {
-        const uint32_t problems = (uint32_t)(p.batch * p.kv_heads);
+    // together: the log of how many heads of keys a block takes
+    __device__ __forceinline__ explicit Place(const AttnArgs& p, int together = 0) {
+        const uint32_t problems = (uint32_t)(p.batch * p.kv_heads) >> together;
         const uint32_t id = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
         none = id >= problems * (uint32_t)(p.tiles * p.splits);
         const uint32_t at = id / problems;
         problem = id - at * problems;
         tile = (int)(at / (uint32_t)p.splits);
         split = (int)at - tile * p.splits;
-        b = (int)divided(problem, p.by_kv);
-        hk = (int)problem - b * p.kv_heads;
+        b = (int)divided(problem << together, p.by_kv);
+        hk = (int)(problem << together) - b * p.kv_heads;
     }
     // first row of this split's partial results of `rows` rows
     __device__ __forceinline__ int64_t part(const AttnArgs& p, int rows) const {
@@ -279,6 +286,12 @@ struct Keys {
         return key < count ? mask[key] : 0;
     }
 };
+
+// Whether a tile's group of KS rows holds any that count.
+template <typename T>
+__device__ __forceinline__ bool group_counts(uint64_t valid, int group) {
+    return (valid >> (group * Tile<T>::KS) & ((1ull << Tile<T>::KS) - 1)) != 0;
+}
 
 template <int KEYS>
 __device__ __forceinline__ uint64_t key_bits(int byte) {
@@ -435,6 +448,15 @@ AttnPlan plan_at(const AttnArgs& p) {
     a.dkv_kc = p.nk <= 64 * S::kDkv / 2 ? 1 : S::kDkv;
     if (a.few) split(p.nk, problems, 1024, 512, 4 * FewTile<T, D>::kKeys, a.fwd_splits, a.fwd_per);
     else split(p.nk, problems * tiles_of(rows, 64 * a.fwd_qc), 512, 512, AttnTile<T, D>::kRows, a.fwd_splits, a.fwd_per);
+    // few keys and rows for two tiles a wave: blocks that keep the keys
+    const int64_t key_tiles = tiles_of(p.nk, AttnTile<T, D>::kRows);
+    if (!a.few && a.fwd_splits == 1 && key_tiles <= kThinTiles && key_tiles * 2 * AttnTile<T, D>::kBytes <= kThinBytes) {
+        while (a.together < 2 && p.kv_heads % (2 << a.together) == 0 &&
+               (key_tiles * 4 * AttnTile<T, D>::kBytes << a.together) <= kThinBytes)
+            ++a.together;
+        const int64_t blocks = tiles_of(rows, 64 * S::kThin >> a.together), each = tiles_of(kThinBlocks, problems >> a.together);
+        if (blocks >= 2 * each) a.thin = (int)each;
+    }
     split(p.nk, problems * tiles_of(rows, 64 * a.dq_qc), 512, 256, AttnTile<T, D>::kRows, a.dq_splits, a.dq_per);
     split(rows, problems * tiles_of(p.nk, 64 * a.dkv_kc), 512, 256, AttnTile<T, D>::kRows, a.dkv_splits, a.dkv_per);
     if (a.fwd_splits > 1) a.fwd_bytes = padded(row_part * a.fwd_splits) + padded(row_part / D * 2 * a.fwd_splits);

@@ -24,6 +24,7 @@ struct AttnArgs {
     int32_t tiles;   // of rows or keys of a problem
     int32_t splits;  // of the keys (forward, dq) or of the rows (dk, dv)
     int32_t per;     // keys or rows of a split
+    int32_t together;  // log of the heads of keys that a block takes, where it keeps the keys
     // more than one split: [problem][split][row or key][padded d] sums of each, joined by a next launch; the forward's
     // are relative to the split's reference, which part_stat holds with the sum of the weights: [..][2]
     float *part, *part_stat;
@@ -32,6 +33,8 @@ struct AttnArgs {
 // How a call shares out its work: the same from sizes alone for the workspace and the launches.
 struct AttnPlan {
     int few;                   // tiles of 16 rows that a wave takes with all of the keys of its own (0: block tiles)
+    int thin;                  // blocks that share out a problem's rows and keep its keys (0: not so)
+    int together;              // log of the heads of keys that such a block takes
     int fwd_qc, dq_qc, dkv_kc; // 16-row tiles a wave
     int fwd_splits, fwd_per, dq_splits, dq_per, dkv_splits, dkv_per;
     size_t fwd_bytes, delta_bytes, dq_bytes, bwd_bytes;  // workspaces, and parts of the backward's

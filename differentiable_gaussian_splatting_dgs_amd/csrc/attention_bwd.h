@@ -38,7 +38,7 @@ __global__ __launch_bounds__(256) void k_attn_sum(AttnArgs p) {
 
 // Gradients.  With P = exp(s - lse) and ds = P (dout v^T - delta), delta the row's sum of dout * out:
 // dq = scale ds k, dk = scale ds^T q, dv = P^T dout.  P and ds enter the products rounded to the type.  float16:
-// both are held times 2^kShift and, should a ds not fit then, scaled down with what is summed so far (Shrink).
+// both are held times 2^13 and, should a ds not fit then, scaled down with what is summed so far (Shrink).
 template <typename T>
 struct Shrink {
     static constexpr bool kNeeded = false;
@@ -49,7 +49,7 @@ struct Shrink {
 template <>
 struct Shrink<_Float16> {
     static constexpr bool kNeeded = true;
-    float shift = Softmax<_Float16>::kShift;
+    float shift = 13.f;
     // most: the lane's largest |ds| of this step; over(f) scales what the wave holds by f
     template <typename Over>
     __device__ __forceinline__ void operator()(float most, Over over) {
@@ -132,6 +132,7 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDq)) void k_attn_dq(Attn
         const char* tv = s_v[t & 1];
 #pragma unroll
         for (int kg = 0; kg < NG; ++kg) {
+            if (!group_counts<T>(valid, kg)) continue;
             f32x4 s[QC][TG] = {}, dp[QC][TG] = {};
 #pragma unroll
             for (int u = 0; u < TG; ++u)
@@ -309,6 +310,7 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDkv)) void k_attn_dkv(At
         const char* tg = s_g[t & 1];
 #pragma unroll
         for (int rg = 0; rg < NG; ++rg) {
+            if (!group_counts<T>(valid, rg)) continue;
             f32x4 s[KC][TG] = {}, dp[KC][TG] = {};
 #pragma unroll
             for (int u = 0; u < TG; ++u)

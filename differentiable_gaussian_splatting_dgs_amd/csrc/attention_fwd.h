@@ -32,7 +32,7 @@ __device__ __forceinline__ void forward_rows(const AttnArgs& p, const Place& at,
         }
         const Row w(p, at.hk, row, true);
         const bool empty = !any || row >= live;
-        const float inv = 1.f / l[c];
+        const float inv = __builtin_amdgcn_rcpf(l[c]);
         T* out = static_cast<T*>(p.out) + w.whole(p, at.b) * p.d;
 #pragma unroll
         for (int e = 0; e < AttnTile<T, D>::kPairs; ++e) {
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p) {
     const int b = (int)(problem / p.kv_heads), hk = (int)(problem - (int64_t)b * p.kv_heads);
     const Row w(p, hk, row, true);
     const bool empty = row >= live_rows(p, b) || (m == -INFINITY && l == 0.f);  // NaN: logits of -infinity
-    const float inv = 1.f / l;
+    const float inv = __builtin_amdgcn_rcpf(l);
     T* out = static_cast<T*>(p.out) + w.whole(p, b) * p.d;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -356,6 +356,7 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccFwd)) void k_attn_fwd(At
         any |= valid;
 #pragma unroll
         for (int kg = 0; kg < NG; ++kg) {
+            if (!group_counts<T>(valid, kg)) continue;
             f32x4 s[QC][TG] = {};
 #pragma unroll
             for (int u = 0; u < TG; ++u)
@@ -382,6 +383,127 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccFwd)) void k_attn_fwd(At
     forward_rows<T, D, QC>(p, at, row0, live, any != 0, m, l, rows.o, lane);
 }
 
+// Forward of many rows on few keys: the keys and values of a problem stay in LDS for the life of a block, and each
+// wave walks tiles of 16 QC rows with the next tile's queries in flight and no barrier.
+template <typename T, int D, int QC, int MODE>
+__global__ __launch_bounds__(256, (AttnShape<T, D>::kOccThin)) void k_attn_thin(AttnArgs p) {
+    typedef AttnTile<T, D> A;
+    typedef typename Tile<T>::Frag Frag;
+    constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG, KT = A::kRows, NG = A::kGroups;
+    extern __shared__ __align__(16) char s_mem[];  // [tiles of keys][keys, values]
+    __shared__ uint64_t s_valid[kThinTiles];
+    Place at(p, p.together);  // tile: the block's share of the rows
+    if (at.none) return;
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Keys keys(p, at.b);
+    const int rows = p.nq * p.group, live = live_rows(p, at.b);
+    // the waves of a block take the same rows of its heads, which are neighbours in memory
+    const int heads = 1 << p.together, step = p.tiles * (64 * QC >> p.together);
+    int row0 = (at.tile * (4 >> p.together) + (wave >> p.together)) * 16 * QC;
+    const int own = wave & (heads - 1), first_head = at.hk;
+    at.hk += own;
+    const T* q_base = static_cast<const T*>(p.q) + at.b * p.q_b;
+    // one head for each head of keys: a lane's places in a whole tile of rows are the same from tile to tile
+    const uint32_t out_n = (uint32_t)(p.heads * p.d);
+    uint32_t q_at[QC], out_at[QC];
+#pragma unroll
+    for (int c = 0; c < QC; ++c) {
+        q_at[c] = (uint32_t)(16 * c + r) * (uint32_t)p.q_n;
+        out_at[c] = (uint32_t)(16 * c + r) * out_n;
+    }
+    Frag next[QC][A::kSteps];
+    auto fetch = [&](int from) {
+        if (p.group == 1 && from + 16 * QC <= live) {
+            const T* tile = q_base + from * p.q_n + at.hk * p.q_h;
+#pragma unroll
+            for (int c = 0; c < QC; ++c) raw_frags<T, MODE>(next[c], tile + q_at[c], g, p.d);
+            return;
+        }
+#pragma unroll
+        for (int c = 0; c < QC; ++c) {
+            const Row w(p, at.hk, from + 16 * c + r, from + 16 * c + r < live);
+            raw_frags<T, MODE>(next[c], q_base + w.query * p.q_n + w.head * p.q_h, g, p.d);
+        }
+    };
+    fetch(row0);
+    const int tiles = (keys.count + KT - 1) / KT;
+    uint64_t any = 0;
+    for (int h = 0; h < heads; ++h) {
+        KeyTiles<T, D, MODE> tile_k(p.k, at.b * p.k_b + (first_head + h) * p.k_h, p.k_n, keys.count, p.d);
+        KeyTiles<T, D, MODE> tile_v(p.v, at.b * p.v_b + (first_head + h) * p.v_h, p.v_n, keys.count, p.d);
+        char* to = s_mem + 2 * h * tiles * A::kBytes;
+        for (int t = 0; t < tiles; ++t) {
+            const int byte = keys.byte(t * KT, lane);
+            tile_k.load(t * KT, p.d);
+            tile_v.load(t * KT, p.d);
+            const uint64_t valid = key_bits<KT>(byte);
+            any |= valid;
+            tile_k.move.store(to + 2 * t * A::kBytes, valid, p.d);
+            tile_v.move.store(to + (2 * t + 1) * A::kBytes, valid, p.d);
+            if (threadIdx.x == 0) s_valid[t] = valid;
+        }
+    }
+    __syncthreads();
+    for (; row0 < rows; row0 += step) {
+        Frag q[QC][A::kSteps];
+#pragma unroll
+        for (int c = 0; c < QC; ++c) {
+#pragma unroll
+            for (int e = 0; e < A::kSteps; ++e) q[c][e] = next[c][e];
+            fix_frags<T, MODE>(q[c], g, p.d, row0 + 16 * c + r < live);
+            if (p.scale < 0.f)
+#pragma unroll
+                for (int e = 0; e < A::kSteps; ++e) q[c][e] = -q[c][e];
+        }
+        if (row0 + step < rows) fetch(row0 + step);
+        RowState<T, D, QC> state(p.scale);
+        for (int t = 0; t < tiles; ++t) {
+            const char* tk = s_mem + 2 * (own * tiles + t) * A::kBytes;
+            const char* tv = tk + A::kBytes;
+            const uint64_t valid = s_valid[t];
+#pragma unroll
+            for (int kg = 0; kg < NG; ++kg) {
+                if (!group_counts<T>(valid, kg)) continue;
+                f32x4 s[QC][TG] = {};
+#pragma unroll
+                for (int u = 0; u < TG; ++u)
+#pragma unroll
+                    for (int e = 0; e < A::kSteps; ++e) {
+                        const Frag a = row_frag<T, D>(tk, kg * KS + out_row<T>(u, r), e, g);
+#pragma unroll
+                        for (int c = 0; c < QC; ++c) mma(s[c][u], a, q[c][e]);
+                    }
+                if (valid != ~0ull >> (64 - KT)) without<T, QC>(s, valid >> (kg * KS), g);
+                Frag w[QC];
+                state.weigh(s, w);
+                state.add(tv, kg * KS, w, lane);
+            }
+        }
+        float m[QC], l[QC];
+#pragma unroll
+        for (int c = 0; c < QC; ++c) m[c] = state.reference(c), l[c] = state.sum(c);
+        if (!(p.group == 1 && row0 + 16 * QC <= live && any) || p.lse) {
+            forward_rows<T, D, QC>(p, at, row0, live, any != 0, m, l, state.o, lane);
+            continue;
+        }
+        T* out = static_cast<T*>(p.out) + ((int64_t)at.b * p.nq + row0) * out_n + at.hk * p.d;
+#pragma unroll
+        for (int c = 0; c < QC; ++c) {
+            const float inv = __builtin_amdgcn_rcpf(l[c]);
+#pragma unroll
+            for (int e = 0; e < A::kPairs; ++e) {
+                Frag f;
+#pragma unroll
+                for (int u = 0; u < TG; ++u)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) f[4 * u + j] = (T)(state.o[c][e][u][j] * inv);
+                store_run(out + out_at[c], KS * e + E * g, p.d, f);
+            }
+        }
+    }
+}
+
 template <typename T, int D, int MODE>
 void attn_fwd_in(AttnArgs p, void* workspace, hipStream_t s) {
     const AttnPlan a = plan_at<T, D>(p);
@@ -394,6 +516,13 @@ void attn_fwd_in(AttnArgs p, void* workspace, hipStream_t s) {
         p.tiles = 1;
         if (a.few == 1) hipLaunchKernelGGL((k_attn_few<T, D, 1, MODE>), grid_of(p), dim3(256), 0, s, p);
         else hipLaunchKernelGGL((k_attn_few<T, D, kFew, MODE>), grid_of(p), dim3(256), 0, s, p);
+    } else if (a.thin && MODE != ANY) {
+        constexpr int kThin = AttnShape<T, D>::kThin;
+        p.tiles = a.thin, p.together = a.together;
+        const int64_t lds = tiles_of(p.nk, AttnTile<T, D>::kRows) * 2 * AttnTile<T, D>::kBytes << a.together;
+        const int64_t blocks = (problems >> a.together) * p.tiles;
+        hipLaunchKernelGGL((k_attn_thin<T, D, kThin, MODE == ANY ? PART : MODE>),
+                           dim3((unsigned)(tiles_of(blocks, 8) * 8)), dim3(256), (unsigned)lds, s, p);
     } else {
         const int qc = a.fwd_qc < kQc ? a.fwd_qc : kQc;
         p.tiles = (int32_t)tiles_of(rows, 64 * qc);

@@ -6,10 +6,10 @@ of the sum of its terms' magnitudes whatever its order.  A logit s is a sum of d
 itself rounded) and taken relative to a reference: off by es = U ((d + 4) |scale| sum |q||k| + 4 max |s|).  The
 hardware's exp2 is within 2^-22.  So a weight before its division is off by a factor 1 + (es + 2^-21), and so is the
 sum, which adds (nk + 3) U: a weight P is within P r, r = 2 (max es + 2^-21) + (nk + 4) U of exact.  P enters its
-product rounded: u more (16 bits), with a floor of 2^-38 for float16, which holds weights times 2^13 at least.  The
-result is rounded once.  The backward makes P from the log of the sums, itself float32, off by |lse| U more;
-delta = dout . out carries out's error; ds = P (dP - delta) is rounded like P (float16's floor is relative to the
-largest, where that passes 4).  The hardware's exp2 and products give 0 below 2^-126: that is the floor of a weight of
+product rounded: u more (16 bits), with a floor of 2^-32 for float16, which holds weights times 2^7 at least and whose
+half step is 2^-25.  The result is rounded once.  The backward makes P from the log of the sums, itself float32, off by
+|lse| U more; delta = dout . out carries out's error; ds = P (dP - delta) is rounded like P (float16's floor: 2^-38,
+for both are held times 2^13, and relative to the largest where that passes 4).  The hardware's exp2 and products give 0 below 2^-126: that is the floor of a weight of
 the other types, and times |dP - delta| of a ds (2^-125 covers both)."""
 import math
 
@@ -107,7 +107,7 @@ def exact(q, k, v, dout, mask, q_lengths, k_lengths, scale):
     r = 2 * (es + 2.0 ** -21) + (nk + 4) * U
     out = P @ V
     PV = P @ V.abs()
-    out_err = PV * (rounded + r + (nk + 3) * U) + floor * V.abs().sum(2, keepdim=True) + u * out.abs() + tiny
+    out_err = PV * (rounded + r + (nk + 3) * U) + 64 * floor * V.abs().sum(2, keepdim=True) + u * out.abs() + tiny
     lse = torch.where(some, lse, -math.inf)
     lse_err = torch.where(some, r + 4 * U * (lse.abs() + big), 0.0)
 
