@@ -65,6 +65,9 @@ struct AttnShape {
     static constexpr int kOccThin = D * (int)sizeof(T) >= 512 ? 1 : 2;
     static constexpr int kOccFwd = D * (int)sizeof(T) >= 512 ? 1 : 2;
     static constexpr int kOccDq = D * (int)sizeof(T) >= 512 ? 1 : 2;
+    static constexpr int kHeld = kHalf ? (D <= 64 ? 4 : D <= 128 ? 2 : 1) : D <= 32 ? 4 : D <= 64 ? 2 : 1;
+    // by the registers of keys, values, their gradients and a step's logits; the rest takes some 130
+    static constexpr int occ_held(int kc) { return kc * (kHalf ? D / 2 + D / 4 + 16 : D + 8) <= 110 ? 2 : 1; }
     static constexpr int kOccDkv = D * (int)sizeof(T) >= 256 ? 1 : 2;
 };
 
@@ -83,7 +86,7 @@ __device__ __forceinline__ int tile_at(int m, int c) {
     if constexpr (sizeof(T) == 2) {
         return row_chunk<T, D>(m, c);
     } else {
-        constexpr int kMask = D * 4 / 16 >= 16 ? 15 : 7;
+        constexpr int kMask = D * 4 / 16 >= 16 ? 15 : D * 4 / 16 - 1;
         return m * (D * 4) + ((c ^ (m & kMask)) << 4);
     }
 }
@@ -459,12 +462,22 @@ AttnPlan plan_at(const AttnArgs& p) {
     }
     split(p.nk, problems * tiles_of(rows, 64 * a.dq_qc), 512, 256, AttnTile<T, D>::kRows, a.dq_splits, a.dq_per);
     split(rows, problems * tiles_of(p.nk, 64 * a.dkv_kc), 512, 256, AttnTile<T, D>::kRows, a.dkv_splits, a.dkv_per);
+    a.few_back = a.few == 2 && sizeof(T) == 4 && D == 256 ? 0 : a.few;  // their tiles fill LDS
+    split(p.nk, problems, 1024, 256, 4 * Tile<T>::KS, a.few_splits, a.few_per);
+    a.held = p.nk < 1 || a.few_back ? 0 : p.nk <= 64 ? 1 : p.nk <= 128 ? 2 : p.nk <= 256 ? 4 : 0;
+    if (a.held > S::kHeld) a.held = 0;
+    split(rows, problems, 512, 4 * AttnTile<T, D>::kRows, AttnTile<T, D>::kRows, a.held_splits, a.held_per);
     if (a.fwd_splits > 1) a.fwd_bytes = padded(row_part * a.fwd_splits) + padded(row_part / D * 2 * a.fwd_splits);
     a.delta_bytes = padded((size_t)problems * rows * 4);
-    if (a.dq_splits > 1) a.dq_bytes = padded(row_part * a.dq_splits);
     // dq's partials are joined before those of dk and dv are made
+    size_t most = a.dq_splits > 1 ? padded(row_part * a.dq_splits) : 0;
     const size_t kv = a.dkv_splits > 1 ? padded(2 * key_part * a.dkv_splits) : 0;
-    a.bwd_bytes = a.delta_bytes + (a.dq_bytes > kv ? a.dq_bytes : kv);
+    most = kv > most ? kv : most;
+    const size_t few = a.few_back && a.few_splits > 1 ? padded(row_part * a.few_splits) : 0;
+    most = few > most ? few : most;
+    const size_t held = a.held && a.held_splits > 1 ? padded(2 * key_part * a.held_splits) : 0;
+    most = held > most ? held : most;
+    a.bwd_bytes = a.delta_bytes + most;
     return a;
 }
 

@@ -36,8 +36,11 @@ struct AttnPlan {
     int thin;                  // blocks that share out a problem's rows and keep its keys (0: not so)
     int together;              // log of the heads of keys that such a block takes
     int fwd_qc, dq_qc, dkv_kc; // 16-row tiles a wave
+    int held;                  // 16-key tiles a wave where a block holds all keys in the backward (0: it does not)
+    int few_back;              // few, where the backward has it
+    int few_splits, few_per, held_splits, held_per;  // of the backward
     int fwd_splits, fwd_per, dq_splits, dq_per, dkv_splits, dkv_per;
-    size_t fwd_bytes, delta_bytes, dq_bytes, bwd_bytes;  // workspaces, and parts of the backward's
+    size_t fwd_bytes, delta_bytes, bwd_bytes;  // workspaces, and parts of the backward's
 };
 
 inline Div div_by(uint32_t d) {

@@ -235,6 +235,43 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDq)) void k_attn_dq(Attn
     }
 }
 
+// The gradients of a lane's key: the results, or those of a split.
+template <typename T, int D>
+__device__ __forceinline__ void keys_out(const AttnArgs& p, const Place& at, int key, bool counts, float by,
+                                         const f32x4 (&dk)[AttnTile<T, D>::kPairs][Tile<T>::TG],
+                                         const f32x4 (&dv)[AttnTile<T, D>::kPairs][Tile<T>::TG], int lane) {
+    constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG;
+    const int g = lane >> 4;
+    if (key >= p.nk) return;
+    if (p.splits > 1) {
+        float* to = p.part + (at.part(p, p.nk) + key) * D;
+        float* to_v = to + (int64_t)p.batch * p.kv_heads * p.splits * p.nk * D;
+#pragma unroll
+        for (int e = 0; e < AttnTile<T, D>::kPairs; ++e)
+#pragma unroll
+            for (int u = 0; u < TG; ++u) {
+                const int k = KS * e + E * g + 4 * u;
+                *reinterpret_cast<f32x4*>(to + k) = counts ? dk[e][u] * (by * p.scale) : f32x4{};
+                *reinterpret_cast<f32x4*>(to_v + k) = counts ? dv[e][u] * by : f32x4{};
+            }
+        return;
+    }
+    const int64_t row = (((int64_t)at.b * p.nk + key) * p.kv_heads + at.hk) * p.d;
+#pragma unroll
+    for (int e = 0; e < AttnTile<T, D>::kPairs; ++e) {
+        typename Tile<T>::Frag a, b;
+#pragma unroll
+        for (int u = 0; u < TG; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                a[4 * u + j] = counts ? (T)(dk[e][u][j] * (by * p.scale)) : (T)0.f;
+                b[4 * u + j] = counts ? (T)(dv[e][u][j] * by) : (T)0.f;
+            }
+        if (p.dk) store_run(static_cast<T*>(p.dk) + row, KS * e + E * g, p.d, a);
+        if (p.dv) store_run(static_cast<T*>(p.dv) + row, KS * e + E * g, p.d, b);
+    }
+}
+
 // dk and dv over tiles of 64 KC keys and the rows of a split.  Here a lane holds consecutive rows of one key: s = q k^T.
 template <typename T, int D, int KC, int MODE>
 __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDkv)) void k_attn_dkv(AttnArgs p) {
@@ -395,36 +432,542 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDkv)) void k_attn_dkv(At
     }
     const float by = __builtin_amdgcn_exp2f(-shrink.shift);
 #pragma unroll
+    for (int c = 0; c < KC; ++c) keys_out<T, D>(p, at, key0 + 16 * c + r, counts[c], by, dk[c], dv[c], lane);
+}
+
+// Columns [c0, c0 + 16) of keys [m0, m0 + KS) of a tile of keys down and RT rows across: lane (r, g) has row c0 + r,
+// keys m0 + E g on.
+template <typename T, int RT>
+__device__ __forceinline__ typename Tile<T>::Frag across_frag(const char* tile, int m0, int c0, int lane) {
+    const int r = lane & 15, g = lane >> 4;
+    if constexpr (sizeof(T) == 2) {
+        union {
+            typename Tile<T>::Frag f;
+            s16x4 h[2];
+        } u;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int m = m0 + 8 * g + 4 * h + (r >> 2), c = c0 + 4 * (r & 3);
+            u.h[h] = read_transposed(tile + tile_at<T, RT>(m, c >> 3) + (c & 7) * 2);
+        }
+        return u.f;
+    } else {
+        typename Tile<T>::Frag f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            f[j] = *reinterpret_cast<const float*>(tile + tile_at<T, RT>(m0 + 4 * g + j, (c0 + r) >> 2) + (r & 3) * 4);
+        return f;
+    }
+}
+
+// The gradients where a block holds all keys of a problem (64 KC of them at most), 16 KC a wave, and walks the rows of
+// its split.  ds goes through LDS, keys down and rows across, and comes back as the fragments of dq: s, P and ds are
+// made once, q, dout and out are read once and dq is written once.  delta is made where out passes by.
+template <typename T, int D, int KC>
+struct HeldTile {
+    static constexpr int kRows = AttnTile<T, D>::kRows, kKeys = 64 * KC;
+    static constexpr int kDs = kKeys * kRows * (int)sizeof(T), kKeyBytes = kKeys * D * (int)sizeof(T);
+    static constexpr int kBytes = 2 * AttnTile<T, D>::kBytes + kDs + kKeyBytes + 2 * kRows * 4;
+};
+
+template <typename T, int D, int KC, int MODE>
+__global__ __launch_bounds__(256, (AttnShape<T, D>::occ_held(KC))) void k_attn_held(AttnArgs p) {
+    typedef AttnTile<T, D> A;
+    typedef HeldTile<T, D, KC> H;
+    typedef typename Tile<T>::Frag Frag;
+    constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG, RT = A::kRows, NG = A::kGroups;
+    extern __shared__ __align__(16) char s_mem[];
+    char *s_q = s_mem, *s_g = s_q + A::kBytes, *s_k = s_g + A::kBytes, *s_ds = s_k + H::kKeyBytes;
+    float *s_lse = reinterpret_cast<float*>(s_ds + H::kDs), *s_delta = s_lse + RT;
+    const Place at(p);
+    if (at.none) return;
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Keys keys(p, at.b);
+    const int rows = p.nq * p.group, first = at.split * p.per, end = min(rows, first + p.per);
+    const int live = min(live_rows(p, at.b), end);
+    const float c2 = fabsf(p.scale) * kLog2e;
+    const int64_t d = p.d;
+    RowTiles<T, D, MODE> tile_q(p, at.b, at.hk, p.q, p.q_b, p.q_n, p.q_h);
+    RowTiles<T, D, MODE> tile_g(p, at.b, at.hk, p.dout, p.g_b, p.g_n, p.g_h);
+    RowTiles<T, D, MODE> tile_o(p, at.b, at.hk, p.out, d * p.heads * p.nq, d * p.heads, d);
+    float next_lse = 0.f;
+    auto fetch = [&](int row0) {
+        tile_q.load(p, row0, live);
+        tile_g.load(p, row0, live);
+        tile_o.load(p, row0, live);
+        if (threadIdx.x < RT) {
+            const int row = row0 + (int)threadIdx.x;
+            next_lse = p.lse[Row(p, at.hk, row, row < live).stat(p, at.b)];
+        }
+    };
+    const int tiles = keys.count > 0 ? (live - first + RT - 1) / RT : 0;
+    if (tiles > 0) fetch(first);
+
+    Frag k[KC][A::kSteps], v[KC][A::kSteps];
+    bool counts[KC];
+#pragma unroll
     for (int c = 0; c < KC; ++c) {
-        const int key = key0 + 16 * c + r;
-        if (key >= p.nk) continue;
-        if (p.splits > 1) {
-            float* to = p.part + (at.part(p, p.nk) + key) * D;
-            float* to_v = to + (int64_t)p.batch * p.kv_heads * p.splits * p.nk * D;
+        const int key = (wave * KC + c) * 16 + r;
+        counts[c] = key < keys.count && (!keys.mask || keys.mask[key]);
+        const int64_t from = counts[c] ? key : 0;
+        raw_frags<T, MODE>(k[c], static_cast<const T*>(p.k) + at.b * p.k_b + from * p.k_n + at.hk * p.k_h, g, p.d);
+        raw_frags<T, MODE>(v[c], static_cast<const T*>(p.v) + at.b * p.v_b + from * p.v_n + at.hk * p.v_h, g, p.d);
+    }
+#pragma unroll
+    for (int c = 0; c < KC; ++c) {
+        fix_frags<T, MODE>(k[c], g, p.d, counts[c]);
+        fix_frags<T, MODE>(v[c], g, p.d, counts[c]);
+#pragma unroll
+        for (int e = 0; e < A::kSteps; ++e)
+            *reinterpret_cast<Frag*>(s_k + tile_at<T, D>((wave * KC + c) * 16 + r, 4 * e + g)) = k[c][e];
+        if (p.scale < 0.f)
+#pragma unroll
+            for (int s = 0; s < A::kSteps; ++s) k[c][s] = -k[c][s];
+    }
+
+    f32x4 dk[KC][A::kPairs][TG] = {}, dv[KC][A::kPairs][TG] = {};
+    Shrink<T> shrink;
+    __shared__ float s_shift[4];
+    // the lane's ds of the tile's first groups
+    auto rescale = [&](float f, int groups) {
+        for (int rg = 0; rg < groups; ++rg)
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                Frag* at_ds = reinterpret_cast<Frag*>(s_ds + tile_at<T, RT>((wave * KC + c) * 16 + r, 4 * rg + g));
+                Frag v = *at_ds;
+#pragma unroll
+                for (int j = 0; j < E; ++j) v[j] = (T)((float)v[j] * f);
+                *at_ds = v;
+            }
+    };
+    for (int t = 0; t < tiles; ++t) {
+        const int row0 = first + t * RT;
+        const uint64_t valid = ~0ull >> (64 - min(RT, live - row0));
+        tile_q.move.store(s_q, valid, p.d);
+        tile_g.move.store(s_g, valid, p.d);
+        {  // delta: a thread's chunks, then the threads of a row
+            const Chunk<T> ch(tile_o.move.first(), p.d);
+#pragma unroll
+            for (int i = 0; i < A::kEach; ++i) {
+                const Frag a = chunk_fixed<T, MODE>(tile_o.move.f[i], ch, p.d, true);
+                const Frag b = chunk_fixed<T, MODE>(tile_g.move.f[i], ch, p.d, true);
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < E; ++j) sum = fmaf((float)a[j], (float)b[j], sum);
+#pragma unroll
+                for (int o = 1; o < A::kChunks; o <<= 1) sum += __shfl_xor(sum, o, 64);
+                if (threadIdx.x % A::kChunks == 0) s_delta[tile_o.move.row(i)] = sum;
+            }
+            if (threadIdx.x < RT) s_lse[threadIdx.x] = next_lse * kLog2e;
+        }
+        __syncthreads();
+        if (t + 1 < tiles) fetch(row0 + RT);
+#pragma unroll
+        for (int rg = 0; rg < NG; ++rg) {
+            f32x4 s[KC][TG] = {}, dp[KC][TG] = {};
+#pragma unroll
+            for (int u = 0; u < TG; ++u)
+#pragma unroll
+                for (int e = 0; e < A::kSteps; ++e) {
+                    const Frag a = row_frag<T, D>(s_q, rg * KS + out_row<T>(u, r), e, g);
+                    const Frag b = row_frag<T, D>(s_g, rg * KS + out_row<T>(u, r), e, g);
+#pragma unroll
+                    for (int c = 0; c < KC; ++c) {
+                        mma(s[c][u], a, k[c][e]);
+                        mma(dp[c][u], b, v[c][e]);
+                    }
+                }
+#pragma unroll
+            for (int u = 0; u < TG; ++u) {
+                const f32x4 lse = *reinterpret_cast<const f32x4*>(&s_lse[rg * KS + E * g + 4 * u]);
+                const f32x4 delta = *reinterpret_cast<const f32x4*>(&s_delta[rg * KS + E * g + 4 * u]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int c = 0; c < KC; ++c) {
+                        const float w = __builtin_amdgcn_exp2f(fmaf(s[c][u][j], c2, shrink.shift - lse[j]));
+                        s[c][u][j] = w;
+                        dp[c][u][j] = w * (dp[c][u][j] - delta[j]);
+                    }
+            }
+            // rows and keys that do not count
+#pragma unroll
+            for (int c = 0; c < KC; ++c)
+                if (__any(valid != ~0ull >> (64 - RT) || !counts[c]))
+#pragma unroll
+                    for (int u = 0; u < TG; ++u)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const bool in = counts[c] && (valid >> (rg * KS + E * g + 4 * u + j) & 1);
+                            s[c][u][j] = in ? s[c][u][j] : 0.f;
+                            dp[c][u][j] = in ? dp[c][u][j] : 0.f;
+                        }
+            float most = 0.f;
+            if constexpr (Shrink<T>::kNeeded)
+#pragma unroll
+                for (int c = 0; c < KC; ++c)
+#pragma unroll
+                    for (int u = 0; u < TG; ++u)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) most = fmaxf(most, fabsf(dp[c][u][j]));
+            shrink(most, [&](float f) {
+#pragma unroll
+                for (int c = 0; c < KC; ++c) {
+#pragma unroll
+                    for (int u = 0; u < TG; ++u) s[c][u] *= f, dp[c][u] *= f;
+#pragma unroll
+                    for (int e = 0; e < A::kPairs; ++e)
+#pragma unroll
+                        for (int u = 0; u < TG; ++u) dk[c][e][u] *= f, dv[c][e][u] *= f;
+                }
+                rescale(f, rg);  // what this tile's earlier groups have left for dq
+            });
+            Frag w[KC], ds[KC];
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+#pragma unroll
+                for (int u = 0; u < TG; ++u)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[c][4 * u + j] = (T)s[c][u][j], ds[c][4 * u + j] = (T)dp[c][u][j];
+                *reinterpret_cast<Frag*>(s_ds + tile_at<T, RT>((wave * KC + c) * 16 + r, 4 * rg + g)) = ds[c];
+            }
 #pragma unroll
             for (int e = 0; e < A::kPairs; ++e)
 #pragma unroll
                 for (int u = 0; u < TG; ++u) {
-                    const int k = KS * e + E * g + 4 * u;
-                    *reinterpret_cast<f32x4*>(to + k) = counts[c] ? dk[c][e][u] * (by * p.scale) : f32x4{};
-                    *reinterpret_cast<f32x4*>(to_v + k) = counts[c] ? dv[c][e][u] * by : f32x4{};
+                    const Frag a = down_frag<T, D>(s_g, rg * KS, e, u, lane);
+                    const Frag b = down_frag<T, D>(s_q, rg * KS, e, u, lane);
+#pragma unroll
+                    for (int c = 0; c < KC; ++c) {
+                        mma(dv[c][e][u], a, w[c]);
+                        mma(dk[c][e][u], b, ds[c]);
+                    }
                 }
-            continue;
         }
-        const int64_t row = (((int64_t)at.b * p.nk + key) * p.kv_heads + at.hk) * p.d;
+        if (Shrink<T>::kNeeded && lane == 0) s_shift[wave] = shrink.shift;
+        __syncthreads();
+        if constexpr (Shrink<T>::kNeeded) {  // all waves' ds to one scale
+            const float low = fminf(fminf(s_shift[0], s_shift[1]), fminf(s_shift[2], s_shift[3]));
+            if (low != s_shift[0] || low != s_shift[1] || low != s_shift[2] || low != s_shift[3]) {
+                const float f = __builtin_amdgcn_exp2f(low - shrink.shift);
+                if (f != 1.f) {
+                    rescale(f, NG);
 #pragma unroll
-        for (int e = 0; e < A::kPairs; ++e) {
-            Frag a, b;
+                    for (int c = 0; c < KC; ++c)
 #pragma unroll
-            for (int u = 0; u < TG; ++u)
+                        for (int e = 0; e < A::kPairs; ++e)
+#pragma unroll
+                            for (int u = 0; u < TG; ++u) dk[c][e][u] *= f, dv[c][e][u] *= f;
+                    shrink.shift = low;
+                }
+                __syncthreads();
+            }
+        }
+        if (p.dq) {
+            // 16 rows a wave, or fewer columns of them where a tile has fewer rows
+            constexpr int kRowTiles = RT / 16, kShare = 4 / kRowTiles;
+            constexpr int kParts = (A::kPairs + kShare - 1) / kShare;
+            const int tile = wave % kRowTiles, e0 = wave / kRowTiles * kParts;
+            f32x4 dq[kParts][TG] = {};
+#pragma unroll
+            for (int key0 = 0; key0 < H::kKeys; key0 += KS) {
+                if (key0 >= keys.count) break;
+                const Frag ds = across_frag<T, RT>(s_ds, key0, tile * 16, lane);
+#pragma unroll
+                for (int e = 0; e < kParts; ++e)
+#pragma unroll
+                    for (int u = 0; u < TG; ++u) mma(dq[e][u], down_frag<T, D>(s_k, key0, e0 + e, u, lane), ds);
+            }
+            const float by = p.scale * __builtin_amdgcn_exp2f(-shrink.shift);
+            const int row = row0 + tile * 16 + r;
+            if (row < live) {
+                T* to = static_cast<T*>(p.dq) + Row(p, at.hk, row, true).whole(p, at.b) * d;
+#pragma unroll
+                for (int e = 0; e < kParts; ++e) {
+                    Frag f;
+#pragma unroll
+                    for (int u = 0; u < TG; ++u)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) f[4 * u + j] = (T)(dq[e][u][j] * by);
+                    store_run(to, KS * (e0 + e) + E * g, p.d, f);
+                }
+            }
+        }
+    }
+    if (p.dq) {  // rows that do not count, or have no key that does
+        const int64_t none = keys.count > 0 ? max(live, first) : first;
+        for (int64_t i = none * p.d + threadIdx.x; i < (int64_t)end * p.d; i += 256) {
+            const int row = (int)(i / p.d);
+            static_cast<T*>(p.dq)[Row(p, at.hk, row, true).whole(p, at.b) * d + (i - (int64_t)row * p.d)] = (T)0.f;
+        }
+    }
+    const float by = __builtin_amdgcn_exp2f(-shrink.shift);
+#pragma unroll
+    for (int c = 0; c < KC; ++c) keys_out<T, D>(p, at, (wave * KC + c) * 16 + r, counts[c], by, dk[c], dv[c], lane);
+}
+
+// The gradients of few rows: 16 QC of them, with all keys of a split, in tiles that the waves of a block share out.
+// A wave reads its keys and values once, writes their gradients, which are whole since it has all rows, and adds up dq.
+// Keys and ds go through LDS of the wave's own to come back as fragments down the keys.
+template <typename T, int D, int QC>
+struct FewBack {
+    static constexpr int kParts = sizeof(T) == 2 ? 1 : QC;  // steps of a sum over the rows
+    static constexpr int kFixed = D / 16 * kParts * 1024;   // fragments down the rows of q, and of dout
+    static constexpr int kPitch = 16 * QC * (int)sizeof(T);
+    static constexpr int kWave = Tile<T>::KS * (D * (int)sizeof(T) + kPitch);
+    static constexpr int kJoin = 16 * QC * D * 4;
+    static constexpr int kBytes = 2 * kFixed + (4 * kWave > kJoin ? 4 * kWave : kJoin);
+};
+
+template <typename T, int D, int QC, int MODE>
+__global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_attn_few_bwd(AttnArgs p) {
+    typedef AttnTile<T, D> A;
+    typedef FewBack<T, D, QC> F;
+    typedef typename Tile<T>::Frag Frag;
+    constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG;
+    extern __shared__ __align__(16) char s_mem[];
+    __shared__ float s_lse[16 * QC], s_delta[16 * QC];
+    const Place at(p);
+    if (at.none) return;
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Keys keys(p, at.b);
+    const int first = at.split * p.per, last = keys.count - 1;
+    keys.until(first + p.per);
+    const int rows = p.nq * p.group, live = live_rows(p, at.b), whole_end = min(p.nk, first + p.per);
+    const float c2 = fabsf(p.scale) * kLog2e;
+    Frag* s_qt = reinterpret_cast<Frag*>(s_mem);
+    Frag* s_gt = reinterpret_cast<Frag*>(s_mem + F::kFixed);
+    char* tk = s_mem + 2 * F::kFixed + wave * F::kWave;
+    char* tds = tk + KS * D * (int)sizeof(T);
+
+    const T* k_base = static_cast<const T*>(p.k) + at.b * p.k_b + at.hk * p.k_h;
+    const T* v_base = static_cast<const T*>(p.v) + at.b * p.v_b + at.hk * p.v_h;
+    Frag k[TG][A::kSteps], v[TG][A::kSteps];
+    int byte = 0;
+    auto fetch = [&](int k0) {
+        byte = lane < KS ? keys.byte(k0, lane) : 0;
+#pragma unroll
+        for (int u = 0; u < TG; ++u) {
+            const int in = min(16 * u + r, last - k0);
+            if constexpr (MODE == ANY) {
+                raw_frags<T, MODE>(k[u], k_base + (int64_t)(k0 + in) * p.k_n, g, p.d);
+                raw_frags<T, MODE>(v[u], v_base + (int64_t)(k0 + in) * p.v_n, g, p.d);
+            } else {
+                raw_frags<T, MODE>(k[u], k_base + k0 * p.k_n + (uint32_t)in * (uint32_t)p.k_n, g, p.d);
+                raw_frags<T, MODE>(v[u], v_base + k0 * p.v_n + (uint32_t)in * (uint32_t)p.v_n, g, p.d);
+            }
+        }
+    };
+    int k0 = first + wave * KS;
+    const int end = live > 0 ? keys.count : 0;
+    if (k0 < end) fetch(k0);
+    // fragments down the rows: element 4 c + j (float32: j of part c) is row 16 c + 4 g + j
+    for (int i = threadIdx.x; i < 2 * D / 16 * F::kParts * 64; i += 256) {
+        const int l = i & 63, part = (i >> 6) % F::kParts, tile = (i >> 6) / F::kParts % (D / 16);
+        const bool is_q = i < D / 16 * F::kParts * 64;
+        const int col = KS * (tile / TG) + out_row<T>(tile % TG, l & 15);
+        Frag f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int row = 16 * (sizeof(T) == 2 ? e >> 2 : part) + 4 * (l >> 4) + (e & 3);
+            const bool in = row < live && row < 16 * QC && col < p.d;
+            const Row w(p, at.hk, row, in);
+            const T* from = is_q ? static_cast<const T*>(p.q) + at.b * p.q_b + w.query * p.q_n + w.head * p.q_h
+                                 : static_cast<const T*>(p.dout) + at.b * p.g_b + w.query * p.g_n + w.head * p.g_h;
+            f[e] = in ? from[col] : (T)0.f;
+        }
+        (is_q ? s_qt : s_gt)[(tile * F::kParts + part) * 64 + l] = f;
+    }
+    Frag q[QC][A::kSteps], dout[QC][A::kSteps];
+    rows_held<T, MODE>(p, at.b, at.hk, 0, live, p.q, p.q_b, p.q_n, p.q_h, p.scale < 0.f, lane, q);
+    rows_held<T, MODE>(p, at.b, at.hk, 0, live, p.dout, p.g_b, p.g_n, p.g_h, false, lane, dout);
+    if (wave == 0) {
+        Frag out[QC][A::kSteps];
+        const int64_t row = p.d, query = row * p.heads;
+        rows_held<T, MODE>(p, at.b, at.hk, 0, live, p.out, query * p.nq, query, row, false, lane, out);
+#pragma unroll
+        for (int c = 0; c < QC; ++c) {
+            const bool in = 16 * c + r < live;
+            float sum = 0.f;
+#pragma unroll
+            for (int s = 0; s < A::kSteps; ++s)
+#pragma unroll
+                for (int j = 0; j < E; ++j) sum = fmaf((float)dout[c][s][j], (float)out[c][s][j], sum);
+            sum = added(sum);
+            if (g == 0) {
+                s_lse[16 * c + r] = in ? p.lse[Row(p, at.hk, 16 * c + r, in).stat(p, at.b)] * kLog2e : 0.f;
+                s_delta[16 * c + r] = sum;
+            }
+        }
+    }
+    __syncthreads();
+    f32x4 lse[QC], delta[QC];
+#pragma unroll
+    for (int c = 0; c < QC; ++c) {
+        lse[c] = *reinterpret_cast<const f32x4*>(&s_lse[16 * c + 4 * g]);
+        delta[c] = *reinterpret_cast<const f32x4*>(&s_delta[16 * c + 4 * g]);
+    }
+    f32x4 dq[QC][A::kPairs][TG] = {};
+    Shrink<T> shrink;
+    const int64_t out_n = (int64_t)p.kv_heads * p.d;
+    T* dk_base = static_cast<T*>(p.dk) + (int64_t)at.b * p.nk * out_n + at.hk * p.d;
+    T* dv_base = static_cast<T*>(p.dv) + (int64_t)at.b * p.nk * out_n + at.hk * p.d;
+    for (; k0 < end; k0 += 4 * KS) {
+        const uint64_t valid = __ballot(byte != 0);
+        f32x4 s[TG][QC] = {}, dp[TG][QC] = {};
+#pragma unroll
+        for (int u = 0; u < TG; ++u) {
+            const bool in = valid >> (16 * u + r) & 1;
+            fix_frags<T, MODE>(k[u], g, p.d, in);
+            fix_frags<T, MODE>(v[u], g, p.d, in);
+#pragma unroll
+            for (int e = 0; e < A::kSteps; ++e) {
+                *reinterpret_cast<Frag*>(tk + tile_at<T, D>(16 * u + r, 4 * e + g)) = k[u][e];
+#pragma unroll
+                for (int c = 0; c < QC; ++c) {
+                    mma(s[u][c], q[c][e], k[u][e]);
+                    mma(dp[u][c], dout[c][e], v[u][e]);
+                }
+            }
+        }
+        if (k0 + 4 * KS < end) fetch(k0 + 4 * KS);
+        float most = 0.f;
+#pragma unroll
+        for (int u = 0; u < TG; ++u) {
+            const bool key_in = valid >> (16 * u + r) & 1;
+#pragma unroll
+            for (int c = 0; c < QC; ++c)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    a[4 * u + j] = counts[c] ? (T)(dk[c][e][u][j] * (by * p.scale)) : (T)0.f;
-                    b[4 * u + j] = counts[c] ? (T)(dv[c][e][u][j] * by) : (T)0.f;
+                    const bool in = key_in && 16 * c + 4 * g + j < live;
+                    const float w = in ? __builtin_amdgcn_exp2f(fmaf(s[u][c][j], c2, shrink.shift - lse[c][j])) : 0.f;
+                    s[u][c][j] = w;
+                    dp[u][c][j] = in ? w * (dp[u][c][j] - delta[c][j]) : 0.f;
+                    if (Shrink<T>::kNeeded) most = fmaxf(most, fabsf(dp[u][c][j]));
                 }
-            if (p.dk) store_run(static_cast<T*>(p.dk) + row, KS * e + E * g, p.d, a);
-            if (p.dv) store_run(static_cast<T*>(p.dv) + row, KS * e + E * g, p.d, b);
         }
+        shrink(most, [&](float f) {
+#pragma unroll
+            for (int c = 0; c < QC; ++c) {
+#pragma unroll
+                for (int u = 0; u < TG; ++u) s[u][c] *= f, dp[u][c] *= f;
+#pragma unroll
+                for (int e = 0; e < A::kPairs; ++e)
+#pragma unroll
+                    for (int u = 0; u < TG; ++u) dq[c][e][u] *= f;
+            }
+        });
+        Frag w[TG][F::kParts], ds[TG][F::kParts];
+#pragma unroll
+        for (int u = 0; u < TG; ++u)
+#pragma unroll
+            for (int i = 0; i < F::kParts; ++i)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int c = sizeof(T) == 2 ? e >> 2 : i;
+                    w[u][i][e] = c < QC ? (T)s[u][c < QC ? c : 0][e & 3] : (T)0.f;
+                    ds[u][i][e] = c < QC ? (T)dp[u][c < QC ? c : 0][e & 3] : (T)0.f;
+                }
+#pragma unroll
+        for (int u = 0; u < TG; ++u)
+#pragma unroll
+            for (int c = 0; c < QC; ++c) {
+                typedef T Quad __attribute__((ext_vector_type(4)));
+                Quad quad;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) quad[j] = sizeof(T) == 2 ? ds[u][0][(4 * c + j) % E] : ds[u][c % F::kParts][j];
+                *reinterpret_cast<Quad*>(tds + (16 * u + r) * F::kPitch + (16 * c + 4 * g) * (int)sizeof(T)) = quad;
+            }
+        wave_sync();
+        const float by = __builtin_amdgcn_exp2f(-shrink.shift);
+#pragma unroll
+        for (int e = 0; e < A::kPairs; ++e) {
+            f32x4 gk[TG][TG] = {}, gv[TG][TG] = {};  // of key tile, column tile
+#pragma unroll
+            for (int t = 0; t < TG; ++t)
+#pragma unroll
+                for (int i = 0; i < F::kParts; ++i) {
+                    const Frag a = s_qt[((TG * e + t) * F::kParts + i) * 64 + lane];
+                    const Frag b = s_gt[((TG * e + t) * F::kParts + i) * 64 + lane];
+#pragma unroll
+                    for (int u = 0; u < TG; ++u) {
+                        mma(gk[u][t], a, ds[u][i]);
+                        mma(gv[u][t], b, w[u][i]);
+                    }
+                }
+#pragma unroll
+            for (int u = 0; u < TG; ++u) {
+                const int key = k0 + 16 * u + r;
+                Frag a, b;
+#pragma unroll
+                for (int t = 0; t < TG; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        a[4 * t + j] = (T)(gk[u][t][j] * (by * p.scale));
+                        b[4 * t + j] = (T)(gv[u][t][j] * by);
+                    }
+                if (key < whole_end) {
+                    if (p.dk) store_run(dk_base + key * out_n, KS * e + E * g, p.d, a);
+                    if (p.dv) store_run(dv_base + key * out_n, KS * e + E * g, p.d, b);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < TG; ++t) {
+                const Frag a = down_frag<T, D>(tk, 0, e, t, lane);
+#pragma unroll
+                for (int c = 0; c < QC; ++c) {
+                    union {
+                        Frag f;
+                        s16x4 h[2];
+                    } b;
+                    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            b.h[h] = read_transposed(tds + (8 * g + 4 * h + (r >> 2)) * F::kPitch +
+                                                     (16 * c + 4 * (r & 3)) * 2);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            b.f[j] = *reinterpret_cast<const T*>(tds + (4 * g + j) * F::kPitch + (16 * c + r) * 4);
+                    }
+                    mma(dq[c][e][t], a, b.f);
+                }
+            }
+        }
+        wave_sync();
+    }
+    // keys of the split past the length
+    for (int64_t i = (int64_t)max(end, first) * p.d + threadIdx.x; i < (int64_t)whole_end * p.d; i += 256) {
+        const int64_t key = i / p.d, to = key * out_n + (i - key * p.d);
+        if (p.dk) dk_base[to] = (T)0.f;
+        if (p.dv) dv_base[to] = (T)0.f;
+    }
+    if (!p.dq) return;
+    __syncthreads();
+    float* s_dq = reinterpret_cast<float*>(s_mem + 2 * F::kFixed);  // [16 QC][D], the waves in their order
+    const float by = p.scale * __builtin_amdgcn_exp2f(-shrink.shift);
+    for (int i = 0; i < 4; ++i) {
+        if (wave == i)
+#pragma unroll
+            for (int c = 0; c < QC; ++c)
+#pragma unroll
+                for (int e = 0; e < A::kPairs; ++e)
+#pragma unroll
+                    for (int t = 0; t < TG; ++t) {
+                        f32x4* to = reinterpret_cast<f32x4*>(s_dq + (16 * c + r) * D + KS * e + E * g + 4 * t);
+                        const f32x4 own = dq[c][e][t] * by;
+                        *to = i > 0 ? *to + own : own;
+                    }
+        __syncthreads();
+    }
+    for (int i = threadIdx.x; i < min(rows, 16 * QC) * D; i += 256) {
+        const int row = i / D, col = i % D;
+        if (p.splits > 1)
+            p.part[at.part(p, rows) * D + i] = row < live ? s_dq[i] : 0.f;
+        else if (col < p.d)
+            static_cast<T*>(p.dq)[Row(p, at.hk, row, true).whole(p, at.b) * p.d + col] = row < live ? (T)s_dq[i] : (T)0.f;
     }
 }
 
@@ -435,6 +978,27 @@ void attn_bwd_in(AttnArgs p, void* workspace, hipStream_t s) {
     const int64_t rows = (int64_t)p.nq * p.group, problems = (int64_t)p.batch * p.kv_heads;
     p.delta = static_cast<float*>(workspace);
     p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + a.delta_bytes);
+    if (a.few_back && p.nq > 0 && p.nk > 0 && (a.few_back == 1 || MODE != ANY)) {
+        constexpr int kFew = MODE == ANY || (sizeof(T) == 4 && D == 256) ? 1 : 2;
+        p.splits = a.few_splits, p.per = a.few_per, p.tiles = 1;
+        if (a.few_back == 1) {
+            hipLaunchKernelGGL((k_attn_few_bwd<T, D, 1, MODE>), grid_of(p), dim3(256), (FewBack<T, D, 1>::kBytes), s, p);
+        } else {
+            hipLaunchKernelGGL((k_attn_few_bwd<T, D, kFew, MODE>), grid_of(p), dim3(256), (FewBack<T, D, kFew>::kBytes), s,
+                               p);
+        }
+        if (p.splits > 1 && p.dq) GS_ATTN_SHARED(k_attn_sum, problems * rows, , false);
+        return;
+    }
+    if (a.held && p.nq > 0 && MODE != ANY) {
+        constexpr int kMost = AttnShape<T, D>::kHeld, kMode = MODE == ANY ? PART : MODE;
+        p.splits = a.held_splits, p.per = a.held_per, p.tiles = 1;
+        if (a.held == 1) hipLaunchKernelGGL((k_attn_held<T, D, 1, kMode>), grid_of(p), dim3(256), (HeldTile<T, D, 1>::kBytes), s, p);
+        else if (a.held == 2) hipLaunchKernelGGL((k_attn_held<T, D, (kMost < 2 ? kMost : 2), kMode>), grid_of(p), dim3(256), (HeldTile<T, D, (kMost < 2 ? kMost : 2)>::kBytes), s, p);
+        else hipLaunchKernelGGL((k_attn_held<T, D, kMost, kMode>), grid_of(p), dim3(256), (HeldTile<T, D, kMost>::kBytes), s, p);
+        if (p.splits > 1 && (p.dk || p.dv)) GS_ATTN_SHARED(k_attn_sum, 2 * problems * p.nk, , true);
+        return;
+    }
     if (p.nq > 0) {
         const int qc = a.dq_qc < kQc ? a.dq_qc : kQc;
         p.splits = p.dq ? a.dq_splits : 1, p.per = p.dq ? a.dq_per : 0;
