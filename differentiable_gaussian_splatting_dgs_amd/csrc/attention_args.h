@@ -33,6 +33,7 @@ struct AttnArgs {
 // How a call shares out its work: the same from sizes alone for the workspace and the launches.
 struct AttnPlan {
     int few;                   // tiles of 16 rows that a wave takes with all of the keys of its own (0: block tiles)
+    int few_heads;             // log of the heads that a block of few rows takes in the backward
     int thin;                  // blocks that share out a problem's rows and keep its keys (0: not so)
     int together;              // log of the heads of keys that such a block takes
     int fwd_qc, dq_qc, dkv_kc; // 16-row tiles a wave

@@ -717,7 +717,10 @@ struct FewBack {
     static constexpr int kPitch = 16 * QC * (int)sizeof(T);
     static constexpr int kWave = Tile<T>::KS * (D * (int)sizeof(T) + kPitch);
     static constexpr int kJoin = 16 * QC * D * 4;
-    static constexpr int kBytes = 2 * kFixed + (4 * kWave > kJoin ? 4 * kWave : kJoin);
+    static int bytes(int heads) {
+        const int join = heads * kJoin;
+        return 2 * heads * kFixed + (4 * kWave > join ? 4 * kWave : join);
+    }
 };
 
 template <typename T, int D, int QC, int MODE>
@@ -727,19 +730,23 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_at
     typedef typename Tile<T>::Frag Frag;
     constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG;
     extern __shared__ __align__(16) char s_mem[];
-    __shared__ float s_lse[16 * QC], s_delta[16 * QC];
-    const Place at(p);
+    __shared__ __align__(16) float s_lse[4][16 * QC], s_delta[4][16 * QC];
+    Place at(p, p.together);
     if (at.none) return;
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int heads = 1 << p.together, own = wave & (heads - 1), part = wave >> p.together, parts = 4 >> p.together;
+    const int first_head = at.hk;
+    at.hk += own;
+    at.problem = (at.problem << p.together) + own;
     Keys keys(p, at.b);
     const int first = at.split * p.per, last = keys.count - 1;
     keys.until(first + p.per);
     const int rows = p.nq * p.group, live = live_rows(p, at.b), whole_end = min(p.nk, first + p.per);
     const float c2 = fabsf(p.scale) * kLog2e;
-    Frag* s_qt = reinterpret_cast<Frag*>(s_mem);
-    Frag* s_gt = reinterpret_cast<Frag*>(s_mem + F::kFixed);
-    char* tk = s_mem + 2 * F::kFixed + wave * F::kWave;
+    Frag* s_qt = reinterpret_cast<Frag*>(s_mem + 2 * own * F::kFixed);
+    Frag* s_gt = reinterpret_cast<Frag*>(s_mem + (2 * own + 1) * F::kFixed);
+    char* tk = s_mem + 2 * heads * F::kFixed + wave * F::kWave;
     char* tds = tk + KS * D * (int)sizeof(T);
 
     const T* k_base = static_cast<const T*>(p.k) + at.b * p.k_b + at.hk * p.k_h;
@@ -760,30 +767,31 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_at
             }
         }
     };
-    int k0 = first + wave * KS;
+    int k0 = first + part * KS;
     const int end = live > 0 ? keys.count : 0;
     if (k0 < end) fetch(k0);
     // fragments down the rows: element 4 c + j (float32: j of part c) is row 16 c + 4 g + j
-    for (int i = threadIdx.x; i < 2 * D / 16 * F::kParts * 64; i += 256) {
-        const int l = i & 63, part = (i >> 6) % F::kParts, tile = (i >> 6) / F::kParts % (D / 16);
-        const bool is_q = i < D / 16 * F::kParts * 64;
+    for (int i = threadIdx.x; i < heads * 2 * (D / 16) * F::kParts * 64; i += 256) {
+        const int l = i & 63, step = (i >> 6) % F::kParts, tile = (i >> 6) / F::kParts % (D / 16);
+        const int which = i / (D / 16 * F::kParts * 64), head = first_head + (which >> 1);
+        const bool is_q = (which & 1) == 0;
         const int col = KS * (tile / TG) + out_row<T>(tile % TG, l & 15);
         Frag f;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int row = 16 * (sizeof(T) == 2 ? e >> 2 : part) + 4 * (l >> 4) + (e & 3);
+            const int row = 16 * (sizeof(T) == 2 ? e >> 2 : step) + 4 * (l >> 4) + (e & 3);
             const bool in = row < live && row < 16 * QC && col < p.d;
-            const Row w(p, at.hk, row, in);
+            const Row w(p, head, row, in);
             const T* from = is_q ? static_cast<const T*>(p.q) + at.b * p.q_b + w.query * p.q_n + w.head * p.q_h
                                  : static_cast<const T*>(p.dout) + at.b * p.g_b + w.query * p.g_n + w.head * p.g_h;
             f[e] = in ? from[col] : (T)0.f;
         }
-        (is_q ? s_qt : s_gt)[(tile * F::kParts + part) * 64 + l] = f;
+        reinterpret_cast<Frag*>(s_mem + which * F::kFixed)[(tile * F::kParts + step) * 64 + l] = f;
     }
     Frag q[QC][A::kSteps], dout[QC][A::kSteps];
     rows_held<T, MODE>(p, at.b, at.hk, 0, live, p.q, p.q_b, p.q_n, p.q_h, p.scale < 0.f, lane, q);
     rows_held<T, MODE>(p, at.b, at.hk, 0, live, p.dout, p.g_b, p.g_n, p.g_h, false, lane, dout);
-    if (wave == 0) {
+    if (part == 0) {
         Frag out[QC][A::kSteps];
         const int64_t row = p.d, query = row * p.heads;
         rows_held<T, MODE>(p, at.b, at.hk, 0, live, p.out, query * p.nq, query, row, false, lane, out);
@@ -797,8 +805,8 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_at
                 for (int j = 0; j < E; ++j) sum = fmaf((float)dout[c][s][j], (float)out[c][s][j], sum);
             sum = added(sum);
             if (g == 0) {
-                s_lse[16 * c + r] = in ? p.lse[Row(p, at.hk, 16 * c + r, in).stat(p, at.b)] * kLog2e : 0.f;
-                s_delta[16 * c + r] = sum;
+                s_lse[own][16 * c + r] = in ? p.lse[Row(p, at.hk, 16 * c + r, in).stat(p, at.b)] * kLog2e : 0.f;
+                s_delta[own][16 * c + r] = sum;
             }
         }
     }
@@ -806,15 +814,15 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_at
     f32x4 lse[QC], delta[QC];
 #pragma unroll
     for (int c = 0; c < QC; ++c) {
-        lse[c] = *reinterpret_cast<const f32x4*>(&s_lse[16 * c + 4 * g]);
-        delta[c] = *reinterpret_cast<const f32x4*>(&s_delta[16 * c + 4 * g]);
+        lse[c] = *reinterpret_cast<const f32x4*>(&s_lse[own][16 * c + 4 * g]);
+        delta[c] = *reinterpret_cast<const f32x4*>(&s_delta[own][16 * c + 4 * g]);
     }
     f32x4 dq[QC][A::kPairs][TG] = {};
     Shrink<T> shrink;
     const int64_t out_n = (int64_t)p.kv_heads * p.d;
     T* dk_base = static_cast<T*>(p.dk) + (int64_t)at.b * p.nk * out_n + at.hk * p.d;
     T* dv_base = static_cast<T*>(p.dv) + (int64_t)at.b * p.nk * out_n + at.hk * p.d;
-    for (; k0 < end; k0 += 4 * KS) {
+    for (; k0 < end; k0 += parts * KS) {
         const uint64_t valid = __ballot(byte != 0);
         f32x4 s[TG][QC] = {}, dp[TG][QC] = {};
 #pragma unroll
@@ -832,7 +840,7 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_at
                 }
             }
         }
-        if (k0 + 4 * KS < end) fetch(k0 + 4 * KS);
+        if (k0 + parts * KS < end) fetch(k0 + parts * KS);
         float most = 0.f;
 #pragma unroll
         for (int u = 0; u < TG; ++u) {
@@ -939,17 +947,18 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_at
         wave_sync();
     }
     // keys of the split past the length
-    for (int64_t i = (int64_t)max(end, first) * p.d + threadIdx.x; i < (int64_t)whole_end * p.d; i += 256) {
+    for (int64_t i = (int64_t)max(end, first) * p.d + part * 64 + lane; i < (int64_t)whole_end * p.d; i += parts * 64) {
         const int64_t key = i / p.d, to = key * out_n + (i - key * p.d);
         if (p.dk) dk_base[to] = (T)0.f;
         if (p.dv) dv_base[to] = (T)0.f;
     }
     if (!p.dq) return;
     __syncthreads();
-    float* s_dq = reinterpret_cast<float*>(s_mem + 2 * F::kFixed);  // [16 QC][D], the waves in their order
+    // [16 QC][D] of each head, its waves in their order
+    float* s_dq = reinterpret_cast<float*>(s_mem + 2 * heads * F::kFixed) + own * (16 * QC * D);
     const float by = p.scale * __builtin_amdgcn_exp2f(-shrink.shift);
-    for (int i = 0; i < 4; ++i) {
-        if (wave == i)
+    for (int i = 0; i < parts; ++i) {
+        if (part == i)
 #pragma unroll
             for (int c = 0; c < QC; ++c)
 #pragma unroll
@@ -962,7 +971,7 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_at
                     }
         __syncthreads();
     }
-    for (int i = threadIdx.x; i < min(rows, 16 * QC) * D; i += 256) {
+    for (int i = part * 64 + lane; i < min(rows, 16 * QC) * D; i += parts * 64) {
         const int row = i / D, col = i % D;
         if (p.splits > 1)
             p.part[at.part(p, rows) * D + i] = row < live ? s_dq[i] : 0.f;
@@ -980,12 +989,14 @@ void attn_bwd_in(AttnArgs p, void* workspace, hipStream_t s) {
     p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + a.delta_bytes);
     if (a.few_back && p.nq > 0 && p.nk > 0 && (a.few_back == 1 || MODE != ANY)) {
         constexpr int kFew = MODE == ANY || (sizeof(T) == 4 && D == 256) ? 1 : 2;
-        p.splits = a.few_splits, p.per = a.few_per, p.tiles = 1;
+        p.splits = a.few_splits, p.per = a.few_per, p.tiles = 1, p.together = a.few_heads;
+        const int heads = 1 << p.together;
         if (a.few_back == 1) {
-            hipLaunchKernelGGL((k_attn_few_bwd<T, D, 1, MODE>), grid_of(p), dim3(256), (FewBack<T, D, 1>::kBytes), s, p);
+            const unsigned lds = (unsigned)FewBack<T, D, 1>::bytes(heads);
+            hipLaunchKernelGGL((k_attn_few_bwd<T, D, 1, MODE>), grid_of(p), dim3(256), lds, s, p);
         } else {
-            hipLaunchKernelGGL((k_attn_few_bwd<T, D, kFew, MODE>), grid_of(p), dim3(256), (FewBack<T, D, kFew>::kBytes), s,
-                               p);
+            const unsigned lds = (unsigned)FewBack<T, D, kFew>::bytes(heads);
+            hipLaunchKernelGGL((k_attn_few_bwd<T, D, kFew, MODE>), grid_of(p), dim3(256), lds, s, p);
         }
         if (p.splits > 1 && p.dq) GS_ATTN_SHARED(k_attn_sum, problems * rows, , false);
         return;

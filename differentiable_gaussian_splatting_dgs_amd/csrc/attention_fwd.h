@@ -520,9 +520,8 @@ void attn_fwd_in(AttnArgs p, void* workspace, hipStream_t s) {
         constexpr int kThin = AttnShape<T, D>::kThin;
         p.tiles = a.thin, p.together = a.together;
         const int64_t lds = tiles_of(p.nk, AttnTile<T, D>::kRows) * 2 * AttnTile<T, D>::kBytes << a.together;
-        const int64_t blocks = (problems >> a.together) * p.tiles;
-        hipLaunchKernelGGL((k_attn_thin<T, D, kThin, MODE == ANY ? PART : MODE>),
-                           dim3((unsigned)(tiles_of(blocks, 8) * 8)), dim3(256), (unsigned)lds, s, p);
+        hipLaunchKernelGGL((k_attn_thin<T, D, kThin, MODE == ANY ? PART : MODE>), grid_of(p), dim3(256), (unsigned)lds, s,
+                           p);
     } else {
         const int qc = a.fwd_qc < kQc ? a.fwd_qc : kQc;
         p.tiles = (int32_t)tiles_of(rows, 64 * qc);
