@@ -9,8 +9,8 @@
 // sum are numbers of its lane, the same in the four lane groups.  Fragments down the rows of a tile in LDS (v^T)
 // come from transposing reads.
 //
-// exp is exp2 of scale log2 e s.  A row's reference m trails its maximum: it moves (and what is summed so far is
-// scaled) only when a logit passes it by more than kSlack, which nothing that is summed in float32 notices.
+// exp is exp2 of scale log2 e s.  A row's reference trails its maximum: it moves (and what is summed so far is scaled)
+// only when weights grow past 2^8, which nothing that is summed in float32 notices.
 // float16 weights are held times 2^kShift: its steps of 2^-24 would lose the small ones of a long row.
 // A key that its length or mask takes out has weight 0 and is zero in LDS: 0 times infinity or NaN would
 // otherwise reach every row.
@@ -31,14 +31,14 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ uint32_t divided(uint32_t n, Div d) { return (__umulhi(n, d.mul) + n) >> d.shift; }
 
-// The forward's reference, in base 2.  float16's largest weight is 2^(kShift + kSlack) < 65504.
+// The forward's weights are relative to 2^(reference - kShift); past kMost, in the sum of a lane's, it moves.
 template <typename T>
 struct Softmax {
-    static constexpr float kShift = 0.f, kSlack = 8.f;
+    static constexpr float kShift = 0.f, kMost = 256.f;
 };
 template <>
 struct Softmax<_Float16> {
-    static constexpr float kShift = 7.f, kSlack = 8.f;
+    static constexpr float kShift = 7.f, kMost = 32768.f;
 };
 
 // Rows of a tile in LDS, for two buffers of two tiles at two blocks a CU.
@@ -60,7 +60,7 @@ template <typename T, int D>
 struct AttnShape {
     static constexpr bool kHalf = sizeof(T) == 2;
     static constexpr int kFwd = kHalf ? (D <= 64 ? 4 : D <= 128 ? 2 : 1) : D <= 128 ? 2 : 1;
-    static constexpr int kDq = kHalf ? (D <= 128 ? 2 : 1) : D <= 64 ? 2 : 1;
+    static constexpr int kDq = kHalf ? (D <= 64 ? 2 : 1) : D <= 64 ? 2 : 1;
     static constexpr int kDkv = kHalf ? (D <= 128 ? 2 : 1) : D <= 64 ? 2 : 1;
     static constexpr int kThin = D <= 32 ? (kHalf ? 4 : 2) : D <= 128 ? (kHalf ? 2 : 1) : 1;
     static constexpr int kOccThin = D * (int)sizeof(T) >= 512 ? 1 : 2;
@@ -80,16 +80,22 @@ struct FewTile {
     static constexpr int kBytes = kKeys * D * (int)sizeof(T);
 };
 
-// Byte offset of 16-byte chunk c of row m.  float32: reads of a row's chunks take sixteen rows at a time, reads
-// down the columns four rows that lie four apart, and the key tells both apart.
+// Byte offset of 16-byte chunk c of row m.  LDS hands out 256 bytes a cycle: 16 chunks, which for a row fragment are
+// two neighbouring ones of 8 rows, four and four of 16 (out_row).  So the key tells rows apart by bits 0, 1 and 3 and
+// leaves a chunk's lowest bit alone.  16-bit reads down the columns take
+// the same half of four neighbouring chunks of 8 rows at a time and meet every bank twice at best, which is what they do
+// here: 4 cycles a fragment by rows, 8 down the columns.  Shorter rows share the 256 bytes and need less of the key.
 template <typename T, int D>
 __device__ __forceinline__ int tile_at(int m, int c) {
+    constexpr int kChunks = D * (int)sizeof(T) / 16;
+    int key;
     if constexpr (sizeof(T) == 2) {
-        return row_chunk<T, D>(m, c);
+        const int x = (m >> 3 ^ m >> 2) & 1;
+        key = kChunks >= 16 ? (m & 3) << 1 | x << 3 : kChunks == 8 ? (m & 2) << 1 | x << 1 : x << 1;
     } else {
-        constexpr int kMask = D * 4 / 16 >= 16 ? 15 : D * 4 / 16 - 1;
-        return m * (D * 4) + ((c ^ (m & kMask)) << 4);
+        key = m & (kChunks >= 16 ? 15 : kChunks - 1);
     }
+    return m * (D * (int)sizeof(T)) + ((c ^ key) << 4);
 }
 
 // Fragment of row m, step s: the first operand of a product over the columns.

@@ -107,59 +107,71 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p) {
         p.lse[w.stat(p, b)] = empty || m == -INFINITY ? -INFINITY : (m + __builtin_amdgcn_logf(l) - Softmax<T>::kShift) * kLn2;
 }
 
-// What a wave's rows have come to: sums relative to a reference, which trails the maximum.
+// What a wave's rows have come to: sums relative to a reference, which trails the maximum.  Whether it has to move is
+// seen from the weights themselves: the lane's sum of a step's weights, which is needed anyway, passes a limit if one
+// of them does (a maximum of the logits for every step would be a sixth of the arithmetic).
 template <typename T, int D, int QC>
 struct RowState {
     static constexpr int TG = Tile<T>::TG, E = Tile<T>::E;
     typedef typename Tile<T>::Frag Frag;
     f32x4 o[QC][AttnTile<T, D>::kPairs][TG];
-    // l: the lane's part of the weights' sum, before they are rounded (a product with ones would sum them after it);
-    // limit: the reference moves for a logit above it
-    float l[QC], ref[QC], limit[QC];
+    float l[QC];    // the lane's part of the weights' sum, before they are rounded (a product with ones would sum after)
+    float ref[QC];  // what logits are relative to, less kShift; 0 until a key counts
+    float most[QC]; // of a step's weights, or -1 until a key counts
     float c2;
 
     __device__ __forceinline__ explicit RowState(float scale) : o{}, c2(fabsf(scale) * kLog2e) {
 #pragma unroll
-        for (int c = 0; c < QC; ++c) l[c] = 0.f, ref[c] = 0.f, limit[c] = -INFINITY;
+        for (int c = 0; c < QC; ++c) l[c] = 0.f, ref[c] = 0.f, most[c] = -1.f;
     }
-    __device__ __forceinline__ float reference(int c) const { return limit[c] - Softmax<T>::kSlack; }
-    // the weights of KS keys from their logits, as the next product's fragment
-    __device__ __forceinline__ void weigh(const f32x4 (&s)[QC][TG], Frag (&w)[QC]) {
-        float top[QC];
-        bool over = false;
+    __device__ __forceinline__ float reference(int c) const {
+        return most[c] < 0.f ? -INFINITY : ref[c] + Softmax<T>::kShift;
+    }
+    // takes the highest logit of a step for the reference, where that is higher
+    __device__ __forceinline__ void move(const f32x4 (&s)[QC][TG]) {
 #pragma unroll
         for (int c = 0; c < QC; ++c) {
-            top[c] = s[c][0][0];
+            float top = s[c][0][0];
 #pragma unroll
-            for (int u = 0; u < TG; ++u)
+            for (int j = 1; j < E; ++j) top = fmaxf(top, s[c][j >> 2][j & 3]);
+            const float old = reference(c), next = fmaxf(highest(top) * c2, old);
+            if (next == -INFINITY) continue;  // none above it yet
+            const float by = __builtin_amdgcn_exp2f(old - next);
+            ref[c] = next - Softmax<T>::kShift;
+            most[c] = Softmax<T>::kMost;
+            l[c] *= by;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) top[c] = fmaxf(top[c], s[c][u][j]);
-            over |= top[c] * c2 > limit[c];
+            for (int p = 0; p < AttnTile<T, D>::kPairs; ++p)
+#pragma unroll
+                for (int u = 0; u < TG; ++u) o[c][p][u] *= by;
         }
-        if (__any(over)) {
+    }
+    // the weights of KS keys from their logits, as the next product's fragment; first: of the wave's first keys
+    __device__ __forceinline__ void weigh(const f32x4 (&s)[QC][TG], Frag (&w)[QC], bool first) {
+        float e[QC][E], sum[QC];
+        auto weights = [&]() {
+            bool over = false;
 #pragma unroll
             for (int c = 0; c < QC; ++c) {
-                const float old = reference(c), next = fmaxf(highest(top[c]) * c2, old);
-                if (next != -INFINITY) ref[c] = next - Softmax<T>::kShift;
-                limit[c] = next + Softmax<T>::kSlack;
-                const float by = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(old - next);
-                l[c] *= by;
 #pragma unroll
-                for (int e = 0; e < AttnTile<T, D>::kPairs; ++e)
-#pragma unroll
-                    for (int u = 0; u < TG; ++u) o[c][e][u] *= by;
+                for (int j = 0; j < E; ++j) {
+                    e[c][j] = __builtin_amdgcn_exp2f(fmaf(s[c][j >> 2][j & 3], c2, -ref[c]));
+                    sum[c] = j == 0 ? e[c][0] : sum[c] + e[c][j];
+                }
+                over |= sum[c] > most[c];
             }
+            return over;
+        };
+        if (first) move(s);
+        if (__any(weights())) {
+            move(s);
+            weights();
         }
 #pragma unroll
         for (int c = 0; c < QC; ++c) {
+            l[c] += sum[c];
 #pragma unroll
-            for (int u = 0; u < TG; ++u)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float e = __builtin_amdgcn_exp2f(fmaf(s[c][u][j], c2, -ref[c]));
-                    l[c] += e;
-                    w[c][4 * u + j] = (T)e;
-                }
+            for (int j = 0; j < E; ++j) w[c][j] = (T)e[c][j];
         }
     }
     // o += w v, values in a tile of LDS from row m0 on
@@ -237,6 +249,7 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 512 ? 1 : 2)) void k_at
     Frag q[QC][A::kSteps];
     rows_held<T, MODE>(p, at.b, at.hk, 0, live, p.q, p.q_b, p.q_n, p.q_h, p.scale < 0.f, lane, q);
     RowState<T, D, QC> rows(p.scale);
+    bool first_keys = true;
     uint64_t any = 0;
     for (; k0 < keys.count; k0 += 4 * KW) {
         const uint64_t valid = __ballot(byte != 0);
@@ -261,9 +274,11 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 512 ? 1 : 2)) void k_at
         wave_sync();
 #pragma unroll
         for (int kg = 0; kg < KG; ++kg) {
+            if (!group_counts<T>(valid, kg)) continue;
             if (valid != ~0ull >> (64 - KW)) without<T, QC>(s[kg], valid >> (kg * KS), g);
             Frag w[QC];
-            rows.weigh(s[kg], w);
+            rows.weigh(s[kg], w, first_keys);
+            first_keys = false;
             rows.add(tv, kg * KS, w, lane);
         }
         wave_sync();
@@ -338,6 +353,7 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccFwd)) void k_attn_fwd(At
     Frag q[QC][A::kSteps];
     rows_held<T, MODE>(p, at.b, at.hk, row0, live, p.q, p.q_b, p.q_n, p.q_h, p.scale < 0.f, lane, q);
     RowState<T, D, QC> rows(p.scale);
+    bool first_keys = true;
     if (tiles > 0) {
         valid = key_bits<KT>(byte);
         tile_k.move.store(s_k[0], valid, p.d);
@@ -368,7 +384,8 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccFwd)) void k_attn_fwd(At
                 }
             if (valid != ~0ull >> (64 - KT)) without<T, QC>(s, valid >> (kg * KS), g);
             Frag w[QC];
-            rows.weigh(s, w);
+            rows.weigh(s, w, first_keys);
+            first_keys = false;
             rows.add(tv, kg * KS, w, lane);
         }
         if (t + 1 < tiles) {
@@ -458,6 +475,7 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccThin)) void k_attn_thin(
         }
         if (row0 + step < rows) fetch(row0 + step);
         RowState<T, D, QC> state(p.scale);
+        bool first_keys = true;
         for (int t = 0; t < tiles; ++t) {
             const char* tk = s_mem + 2 * (own * tiles + t) * A::kBytes;
             const char* tv = tk + A::kBytes;
@@ -476,7 +494,8 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccThin)) void k_attn_thin(
                     }
                 if (valid != ~0ull >> (64 - KT)) without<T, QC>(s, valid >> (kg * KS), g);
                 Frag w[QC];
-                state.weigh(s, w);
+                state.weigh(s, w, first_keys);
+                first_keys = false;
                 state.add(tv, kg * KS, w, lane);
             }
         }
