@@ -41,17 +41,20 @@ struct Softmax<_Float16> {
     static constexpr float kShift = 7.f, kMost = 32768.f;
 };
 
-// Rows of a tile in LDS, for two buffers of two tiles at two blocks a CU.
+// Rows of a tile in LDS, for two buffers of two tiles at two blocks a CU.  D columns take part in products, a multiple
+// of KS; rows lie a power of two apart.
+constexpr int pitch_of(int d) { return d <= 32 ? 32 : d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 template <typename T, int D>
 struct AttnTile {
-    static constexpr int kRows = 16384 / (D * (int)sizeof(T)) < 64 ? 16384 / (D * (int)sizeof(T)) : 64;
-    static constexpr int kBytes = kRows * D * (int)sizeof(T);
-    static constexpr int kChunks = D / Tile<T>::E;           // of 16 bytes, in a row
+    static constexpr int kPitch = pitch_of(D);
+    static constexpr int kRows = 16384 / (kPitch * (int)sizeof(T)) < 64 ? 16384 / (kPitch * (int)sizeof(T)) : 64;
+    static constexpr int kBytes = kRows * kPitch * (int)sizeof(T);
+    static constexpr int kChunks = kPitch / Tile<T>::E;      // of 16 bytes, in a row
     static constexpr int kEach = kRows * kChunks / 256;      // that a thread moves
     static constexpr int kGroups = kRows / Tile<T>::KS;      // of KS rows: the steps of a sum over the rows
     static constexpr int kSteps = D / Tile<T>::KS;           // of a sum over a row
     static constexpr int kPairs = D / 16 / Tile<T>::TG;      // groups of TG result tiles over the columns
-    static_assert(kEach >= 1 && kGroups >= 1 && 256 % kChunks == 0, "tile");
+    static_assert(kEach >= 1 && kGroups >= 1 && 256 % kChunks == 0 && D % Tile<T>::KS == 0, "tile");
 };
 
 // 16-row tiles of queries, and of keys, that a wave holds: each more is one more use of what a wave reads from LDS,
@@ -68,8 +71,8 @@ struct AttnShape {
     static constexpr int kOccDq = D * (int)sizeof(T) >= 512 ? 1 : 2;
     static constexpr int kHeld = kHalf ? (D <= 64 ? 4 : D <= 128 ? 2 : 1) : D <= 32 ? 4 : D <= 64 ? 2 : 1;
     // by the registers of keys, values, their gradients and a step's logits; the rest takes some 130
-    static constexpr int occ_held(int kc) { return kc * (kHalf ? D / 2 + D / 4 + 16 : D + 8) <= 110 ? 2 : 1; }
-    static constexpr int kOccDkv = D * (int)sizeof(T) >= 256 ? 1 : 2;
+    static constexpr int occ_held(int kc) { return kc * (kHalf ? D / 2 + D / 4 + 16 : D + 8) <= 80 ? 2 : 1; }
+    static constexpr int kOccDkv = D * (int)sizeof(T) >= (kHalf ? 192 : 256) ? 1 : 2;
 };
 
 // Keys that a wave takes at a time where rows are few: what 32 registers hold of them.
@@ -77,7 +80,7 @@ template <typename T, int D>
 struct FewTile {
     static constexpr int kGroups = AttnTile<T, D>::kSteps * Tile<T>::TG * 4 <= 16 ? 2 : 1;
     static constexpr int kKeys = kGroups * Tile<T>::KS;
-    static constexpr int kBytes = kKeys * D * (int)sizeof(T);
+    static constexpr int kBytes = kKeys * pitch_of(D) * (int)sizeof(T);
 };
 
 // Byte offset of 16-byte chunk c of row m.  LDS hands out 256 bytes a cycle: 16 chunks, which for a row fragment are
@@ -87,7 +90,7 @@ struct FewTile {
 // here: 4 cycles a fragment by rows, 8 down the columns.  Shorter rows share the 256 bytes and need less of the key.
 template <typename T, int D>
 __device__ __forceinline__ int tile_at(int m, int c) {
-    constexpr int kChunks = D * (int)sizeof(T) / 16;
+    constexpr int kBytes = D < 32 ? D * (int)sizeof(T) : pitch_of(D) * (int)sizeof(T), kChunks = kBytes / 16;
     int key;
     if constexpr (sizeof(T) == 2) {
         const int x = (m >> 3 ^ m >> 2) & 1;
@@ -95,7 +98,7 @@ __device__ __forceinline__ int tile_at(int m, int c) {
     } else {
         key = m & (kChunks >= 16 ? 15 : kChunks - 1);
     }
-    return m * (D * (int)sizeof(T)) + ((c ^ key) << 4);
+    return m * kBytes + ((c ^ key) << 4);
 }
 
 // Fragment of row m, step s: the first operand of a product over the columns.
@@ -141,7 +144,7 @@ struct Chunk {
     }
 };
 
-// How a kernel reads rows.  WHOLE: d fills the padded row.  PART: rows end inside or before a chunk, which is loaded
+// How a kernel reads rows.  WHOLE: d fills the padded row, a power of two.  PART: rows end inside or before a chunk, which is loaded
 // from the row's last 16 bytes and shifted.  Both take 32-bit offsets from a tile's first row.  ANY: rows shorter than
 // a chunk, read element by element, and offsets of 64 bits.
 enum { WHOLE, PART, ANY };
@@ -433,17 +436,20 @@ inline void split(int64_t n, int64_t blocks, int64_t want, int64_t least, int64_
     splits = (int)(n > 0 ? tiles_of(n, per) : 1);
 }
 
-// The way to read rows: 32-bit offsets reach a tile of 64 keys or rows, and the heads of a group.
-template <typename T, int D>
-int attn_mode(const AttnArgs& p) {
+// Whether rows need more than 32-bit offsets from a tile of 64 keys or rows and the heads of a group, or are short.
+template <typename T>
+bool attn_any(const AttnArgs& p) {
     const int64_t most = ((int64_t)1 << 31) / (int64_t)sizeof(T);
     int64_t far = 64 * (p.k_n > p.v_n ? p.k_n : p.v_n);
     for (const auto& s : {std::pair<int64_t, int64_t>{p.q_n, p.q_h}, {p.g_n, p.g_h}}) {
         const int64_t reach = (64 / p.group + 2) * s.first + (p.group > 1 ? p.group * s.second : 0);
         far = reach > far ? reach : far;
     }
-    if (far >= most || p.d < Tile<T>::E) return ANY;
-    return p.d == D ? WHOLE : PART;
+    return far >= most || p.d < Tile<T>::E;
+}
+template <typename T, int D>
+int attn_mode(const AttnArgs& p) {
+    return attn_any<T>(p) ? ANY : p.d == pitch_of(D) ? WHOLE : PART;
 }
 
 template <typename T, int D>
@@ -451,7 +457,7 @@ AttnPlan plan_at(const AttnArgs& p) {
     typedef AttnShape<T, D> S;
     AttnPlan a{};
     const int64_t problems = (int64_t)p.batch * p.kv_heads, rows = (int64_t)p.nq * p.group;
-    const size_t row_part = (size_t)problems * rows * D * 4, key_part = (size_t)problems * p.nk * D * 4;
+    const size_t row_part = (size_t)problems * rows * pitch_of(D) * 4, key_part = (size_t)problems * p.nk * pitch_of(D) * 4;
     a.few = rows <= 16 ? 1 : rows <= 32 ? 2 : 0;
     a.fwd_qc = rows <= 64 * S::kFwd / 2 ? 1 : S::kFwd;
     a.dq_qc = rows <= 64 * S::kDq / 2 ? 1 : S::kDq;
@@ -469,7 +475,7 @@ AttnPlan plan_at(const AttnArgs& p) {
     }
     split(p.nk, problems * tiles_of(rows, 64 * a.dq_qc), 512, 256, AttnTile<T, D>::kRows, a.dq_splits, a.dq_per);
     split(rows, problems * tiles_of(p.nk, 64 * a.dkv_kc), 512, 256, AttnTile<T, D>::kRows, a.dkv_splits, a.dkv_per);
-    a.few_back = a.few == 2 && sizeof(T) == 4 && D == 256 ? 0 : a.few;  // their tiles fill LDS
+    a.few_back = a.few == 2 && sizeof(T) == 4 && D > 128 ? 0 : a.few;  // their tiles fill LDS
     // heads of at most a line of memory: a wave each.  1M keys of 8 heads of 32 bfloat16 848 us against 896 (forward
     // and backward), 200k of 4 of 64 162 against 175; of 128 326 against 335, and its tiles in LDS leave room for less
     if (D * sizeof(T) <= 128 && p.nk >= kHeadsApart)
@@ -479,7 +485,7 @@ AttnPlan plan_at(const AttnArgs& p) {
     a.held = p.nk < 1 || a.few_back ? 0 : p.nk <= 64 ? 1 : p.nk <= 128 ? 2 : p.nk <= 256 ? 4 : 0;
     if (a.held > S::kHeld) a.held = 0;
     split(rows, problems, 512, 4 * AttnTile<T, D>::kRows, AttnTile<T, D>::kRows, a.held_splits, a.held_per);
-    if (a.fwd_splits > 1) a.fwd_bytes = padded(row_part * a.fwd_splits) + padded(row_part / D * 2 * a.fwd_splits);
+    if (a.fwd_splits > 1) a.fwd_bytes = padded(row_part * a.fwd_splits) + padded(row_part / pitch_of(D) * 2 * a.fwd_splits);
     a.delta_bytes = padded((size_t)problems * rows * 4);
     // dq's partials are joined before those of dk and dv are made
     size_t most = a.dq_splits > 1 ? padded(row_part * a.dq_splits) : 0;
@@ -493,26 +499,31 @@ AttnPlan plan_at(const AttnArgs& p) {
     return a;
 }
 
-// A kernel with D / 4 threads for a row's columns and, with many splits, more of them to share the splits out.
+// A kernel with a thread for every 4 of a row's columns and, with many splits, more of them to share the splits out.
 #define GS_ATTN_SHARED(KERNEL, ROWS, ...)                                                                              \
     do {                                                                                                               \
-        constexpr int kMost = 1024 / D, kFull = kMost < 16 ? kMost : 16;                                               \
+        constexpr int kP = pitch_of(D), kMost = 1024 / kP, kFull = kMost < 16 ? kMost : 16;                            \
         const int64_t rows_ = (ROWS);                                                                                  \
         if (p.splits <= 2)                                                                                             \
-            hipLaunchKernelGGL((KERNEL<T, D, 1 __VA_ARGS__>), dim3((unsigned)tiles_of(rows_, kMost)), dim3(256), 0, s, \
-                               p);                                                                                     \
+            hipLaunchKernelGGL((KERNEL<T, kP, 1 __VA_ARGS__>), dim3((unsigned)tiles_of(rows_, kMost)), dim3(256), 0,   \
+                               s, p);                                                                                  \
         else if (p.splits <= 16)                                                                                       \
-            hipLaunchKernelGGL((KERNEL<T, D, 4 __VA_ARGS__>), dim3((unsigned)tiles_of(rows_, kMost / 4)), dim3(256),   \
+            hipLaunchKernelGGL((KERNEL<T, kP, 4 __VA_ARGS__>), dim3((unsigned)tiles_of(rows_, kMost / 4)), dim3(256),  \
                                0, s, p);                                                                               \
         else                                                                                                           \
-            hipLaunchKernelGGL((KERNEL<T, D, kFull __VA_ARGS__>), dim3((unsigned)tiles_of(rows_, kMost / kFull)),      \
+            hipLaunchKernelGGL((KERNEL<T, kP, kFull __VA_ARGS__>), dim3((unsigned)tiles_of(rows_, kMost / kFull)),     \
                                dim3(256), 0, s, p);                                                                    \
     } while (0)
 
-#define GS_ATTN_BY_HEAD(CALL)   \
-    (p.d <= 32    ? CALL<T, 32>  \
-     : p.d <= 64  ? CALL<T, 64>  \
-     : p.d <= 128 ? CALL<T, 128> \
-                  : CALL<T, 256>)
+// CALL of the columns that products take: between the powers of two one more, and 48 for float32, whose products are
+// what takes the time.  Those read rows as PART; ANY takes powers of two.
+#define GS_ATTN_BY_HEAD(CALL, D_, ANY_)                                                    \
+    ((D_) <= 32                             ? CALL<T, 32>                                  \
+     : (D_) <= 48 && sizeof(T) == 4 && !(ANY_) ? CALL<T, sizeof(T) == 4 ? 48 : 64>         \
+     : (D_) <= 64                           ? CALL<T, 64>                                  \
+     : (D_) <= 96 && !(ANY_)                ? CALL<T, 96>                                  \
+     : (D_) <= 128                          ? CALL<T, 128>                                 \
+     : (D_) <= 192 && !(ANY_)               ? CALL<T, 192>                                 \
+                                            : CALL<T, 256>)
 
 }  // namespace gs

@@ -42,8 +42,8 @@ AttnArgs args_of(const gs_attention* a, const void* q, const void* k, const void
     return p;
 }
 
-AttnPlan plan_of(const AttnArgs& p, int32_t dtype) {
-    return dtype == GS_F32 ? attn_plan<float>(p) : dtype == GS_F16 ? attn_plan<_Float16>(p) : attn_plan<__bf16>(p);
+AttnBytes bytes_of(const AttnArgs& p, int32_t dtype) {
+    return dtype == GS_F32 ? attn_bytes<float>(p) : dtype == GS_F16 ? attn_bytes<_Float16>(p) : attn_bytes<__bf16>(p);
 }
 
 int check_workspace(const void* workspace, size_t bytes, size_t need) {
@@ -70,7 +70,7 @@ extern "C" int gs_attention_fwd(const gs_attention* a, const void* q, const void
         if (!aligned_to(t, 4)) return GS_EALIGN;
     AttnArgs p = args_of(a, q, k, v, mask, q_lengths, k_lengths);
     p.out = out, p.lse = lse;
-    rc = check_workspace(workspace, workspace_bytes, plan_of(p, a->dtype).fwd_bytes);
+    rc = check_workspace(workspace, workspace_bytes, bytes_of(p, a->dtype).fwd);
     if (rc != GS_OK) return rc;
     hipStream_t s = as_stream(stream);
     if (a->dtype == GS_F32)
@@ -82,20 +82,20 @@ extern "C" int gs_attention_fwd(const gs_attention* a, const void* q, const void
     return launch_status();
 }
 
-static int workspace_size(const gs_attention* a, size_t AttnPlan::*which, size_t* bytes) {
+static int workspace_size(const gs_attention* a, size_t AttnBytes::*which, size_t* bytes) {
     const int rc = check_shape(a);
     if (rc != GS_OK) return rc;
     if (!bytes) return GS_EINVAL;
-    *bytes = plan_of(args_of(a, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr), a->dtype).*which;
+    *bytes = bytes_of(args_of(a, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr), a->dtype).*which;
     return GS_OK;
 }
 
 extern "C" int gs_attention_fwd_workspace_size(const gs_attention* a, size_t* bytes) {
-    return workspace_size(a, &AttnPlan::fwd_bytes, bytes);
+    return workspace_size(a, &AttnBytes::fwd, bytes);
 }
 
 extern "C" int gs_attention_bwd_workspace_size(const gs_attention* a, size_t* bytes) {
-    return workspace_size(a, &AttnPlan::bwd_bytes, bytes);
+    return workspace_size(a, &AttnBytes::bwd, bytes);
 }
 
 extern "C" int gs_attention_bwd(const gs_attention* a, const void* q, const void* k, const void* v,
@@ -114,7 +114,7 @@ extern "C" int gs_attention_bwd(const gs_attention* a, const void* q, const void
     AttnArgs p = args_of(a, q, k, v, mask, q_lengths, k_lengths);
     p.out = const_cast<void*>(out), p.lse = const_cast<float*>(lse), p.dout = dout;
     p.dq = dq, p.dk = dk, p.dv = dv;
-    rc = check_workspace(workspace, workspace_bytes, plan_of(p, a->dtype).bwd_bytes);
+    rc = check_workspace(workspace, workspace_bytes, bytes_of(p, a->dtype).bwd);
     if (rc != GS_OK) return rc;
     hipStream_t s = as_stream(stream);
     if (a->dtype == GS_F32)

@@ -50,8 +50,12 @@ inline Div div_by(uint32_t d) {
     return Div{(uint32_t)(((1ull << 32) * ((1ull << l) - d)) / d + 1), l};
 }
 
+struct AttnBytes {
+    size_t fwd, bwd;
+};
+
 template <typename T>
-AttnPlan attn_plan(const AttnArgs& p);
+AttnBytes attn_bytes(const AttnArgs& p);
 template <typename T>
 void attn_fwd(const AttnArgs& p, void* workspace, hipStream_t s);
 template <typename T>

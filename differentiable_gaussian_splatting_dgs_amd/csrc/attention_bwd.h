@@ -214,7 +214,7 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDq)) void k_attn_dq(Attn
         const int row = row0 + 16 * c + r;
         if (row >= rows) continue;
         if (p.splits > 1) {
-            float* to = p.part + (at.part(p, rows) + row) * D;
+            float* to = p.part + (at.part(p, rows) + row) * pitch_of(D);
 #pragma unroll
             for (int e = 0; e < A::kPairs; ++e)
 #pragma unroll
@@ -244,8 +244,8 @@ __device__ __forceinline__ void keys_out(const AttnArgs& p, const Place& at, int
     const int g = lane >> 4;
     if (key >= p.nk) return;
     if (p.splits > 1) {
-        float* to = p.part + (at.part(p, p.nk) + key) * D;
-        float* to_v = to + (int64_t)p.batch * p.kv_heads * p.splits * p.nk * D;
+        float* to = p.part + (at.part(p, p.nk) + key) * pitch_of(D);
+        float* to_v = to + (int64_t)p.batch * p.kv_heads * p.splits * p.nk * pitch_of(D);
 #pragma unroll
         for (int e = 0; e < AttnTile<T, D>::kPairs; ++e)
 #pragma unroll
@@ -466,7 +466,7 @@ __device__ __forceinline__ typename Tile<T>::Frag across_frag(const char* tile, 
 template <typename T, int D, int KC>
 struct HeldTile {
     static constexpr int kRows = AttnTile<T, D>::kRows, kKeys = 64 * KC;
-    static constexpr int kDs = kKeys * kRows * (int)sizeof(T), kKeyBytes = kKeys * D * (int)sizeof(T);
+    static constexpr int kDs = kKeys * kRows * (int)sizeof(T), kKeyBytes = kKeys * pitch_of(D) * (int)sizeof(T);
     static constexpr int kBytes = 2 * AttnTile<T, D>::kBytes + kDs + kKeyBytes + 2 * kRows * 4;
 };
 
@@ -715,7 +715,7 @@ struct FewBack {
     static constexpr int kParts = sizeof(T) == 2 ? 1 : QC;  // steps of a sum over the rows
     static constexpr int kFixed = D / 16 * kParts * 1024;   // fragments down the rows of q, and of dout
     static constexpr int kPitch = 16 * QC * (int)sizeof(T);
-    static constexpr int kWave = Tile<T>::KS * (D * (int)sizeof(T) + kPitch);
+    static constexpr int kWave = Tile<T>::KS * (pitch_of(D) * (int)sizeof(T) + kPitch);
     static constexpr int kJoin = 16 * QC * D * 4;
     static int bytes(int heads) {
         const int join = heads * kJoin;
@@ -747,7 +747,7 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_at
     Frag* s_qt = reinterpret_cast<Frag*>(s_mem + 2 * own * F::kFixed);
     Frag* s_gt = reinterpret_cast<Frag*>(s_mem + (2 * own + 1) * F::kFixed);
     char* tk = s_mem + 2 * heads * F::kFixed + wave * F::kWave;
-    char* tds = tk + KS * D * (int)sizeof(T);
+    char* tds = tk + KS * pitch_of(D) * (int)sizeof(T);
 
     const T* k_base = static_cast<const T*>(p.k) + at.b * p.k_b + at.hk * p.k_h;
     const T* v_base = static_cast<const T*>(p.v) + at.b * p.v_b + at.hk * p.v_h;
@@ -974,7 +974,7 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_at
     for (int i = part * 64 + lane; i < min(rows, 16 * QC) * D; i += parts * 64) {
         const int row = i / D, col = i % D;
         if (p.splits > 1)
-            p.part[at.part(p, rows) * D + i] = row < live ? s_dq[i] : 0.f;
+            p.part[(at.part(p, rows) + row) * pitch_of(D) + col] = row < live ? s_dq[i] : 0.f;
         else if (col < p.d)
             static_cast<T*>(p.dq)[Row(p, at.hk, row, true).whole(p, at.b) * p.d + col] = row < live ? (T)s_dq[i] : (T)0.f;
     }
@@ -988,7 +988,7 @@ void attn_bwd_in(AttnArgs p, void* workspace, hipStream_t s) {
     p.delta = static_cast<float*>(workspace);
     p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + a.delta_bytes);
     if (a.few_back && p.nq > 0 && p.nk > 0 && (a.few_back == 1 || MODE != ANY)) {
-        constexpr int kFew = MODE == ANY || (sizeof(T) == 4 && D == 256) ? 1 : 2;
+        constexpr int kFew = MODE == ANY || (sizeof(T) == 4 && D > 128) ? 1 : 2;
         p.splits = a.few_splits, p.per = a.few_per, p.tiles = 1, p.together = a.few_heads;
         const int heads = 1 << p.together;
         if (a.few_back == 1) {
@@ -1031,14 +1031,16 @@ void attn_bwd_in(AttnArgs p, void* workspace, hipStream_t s) {
 template <typename T, int D>
 void attn_bwd_at(const AttnArgs& p, void* workspace, hipStream_t s) {
     const int mode = attn_mode<T, D>(p);
-    if (mode == WHOLE) attn_bwd_in<T, D, WHOLE>(p, workspace, s);
-    else if (mode == PART) attn_bwd_in<T, D, PART>(p, workspace, s);
-    else attn_bwd_in<T, D, ANY>(p, workspace, s);
+    if constexpr (D == pitch_of(D)) {
+        if (mode == WHOLE) attn_bwd_in<T, D, WHOLE>(p, workspace, s);
+        else if (mode == ANY) attn_bwd_in<T, D, ANY>(p, workspace, s);
+    }
+    if (mode == PART) attn_bwd_in<T, D, PART>(p, workspace, s);
 }
 
 template <typename T>
 void attn_bwd(const AttnArgs& p, void* workspace, hipStream_t s) {
-    GS_ATTN_BY_HEAD(attn_bwd_at)(p, workspace, s);
+    GS_ATTN_BY_HEAD(attn_bwd_at, p.d, attn_any<T>(p))(p, workspace, s);
 }
 
 }  // namespace gs

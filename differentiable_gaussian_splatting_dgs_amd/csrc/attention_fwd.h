@@ -23,7 +23,7 @@ __device__ __forceinline__ void forward_rows(const AttnArgs& p, const Place& at,
             for (int e = 0; e < AttnTile<T, D>::kPairs; ++e)
 #pragma unroll
                 for (int u = 0; u < TG; ++u)
-                    *reinterpret_cast<f32x4*>(p.part + to * D + KS * e + E * g + 4 * u) = o[c][e][u];
+                    *reinterpret_cast<f32x4*>(p.part + to * pitch_of(D) + KS * e + E * g + 4 * u) = o[c][e][u];
             if (g == 0) {
                 p.part_stat[2 * to] = m[c];
                 p.part_stat[2 * to + 1] = any && m[c] == -INFINITY ? NAN : l[c];
@@ -530,7 +530,7 @@ void attn_fwd_in(AttnArgs p, void* workspace, hipStream_t s) {
     const int64_t rows = (int64_t)p.nq * p.group, problems = (int64_t)p.batch * p.kv_heads;
     p.splits = a.fwd_splits, p.per = a.fwd_per;
     p.part = static_cast<float*>(workspace);
-    if (p.splits > 1) p.part_stat = p.part + padded((size_t)problems * rows * D * 4 * p.splits) / 4;
+    if (p.splits > 1) p.part_stat = p.part + padded((size_t)problems * rows * pitch_of(D) * 4 * p.splits) / 4;
     if (a.few && a.few <= kFew) {
         p.tiles = 1;
         if (a.few == 1) hipLaunchKernelGGL((k_attn_few<T, D, 1, MODE>), grid_of(p), dim3(256), 0, s, p);
@@ -553,18 +553,23 @@ void attn_fwd_in(AttnArgs p, void* workspace, hipStream_t s) {
 template <typename T, int D>
 void attn_fwd_at(const AttnArgs& p, void* workspace, hipStream_t s) {
     const int mode = attn_mode<T, D>(p);
-    if (mode == WHOLE) attn_fwd_in<T, D, WHOLE>(p, workspace, s);
-    else if (mode == PART) attn_fwd_in<T, D, PART>(p, workspace, s);
-    else attn_fwd_in<T, D, ANY>(p, workspace, s);
+    if constexpr (D == pitch_of(D)) {
+        if (mode == WHOLE) attn_fwd_in<T, D, WHOLE>(p, workspace, s);
+        else if (mode == ANY) attn_fwd_in<T, D, ANY>(p, workspace, s);
+    }
+    if (mode == PART) attn_fwd_in<T, D, PART>(p, workspace, s);
 }
 
+// Bytes of workspace, by sizes alone: what either way to read the rows asks for.
 template <typename T>
-AttnPlan attn_plan(const AttnArgs& p) {
-    return GS_ATTN_BY_HEAD(plan_at)(p);
+AttnBytes attn_bytes(const AttnArgs& p) {
+    const AttnPlan a = GS_ATTN_BY_HEAD(plan_at, p.d, false)(p), b = GS_ATTN_BY_HEAD(plan_at, p.d, true)(p);
+    return AttnBytes{a.fwd_bytes > b.fwd_bytes ? a.fwd_bytes : b.fwd_bytes,
+                     a.bwd_bytes > b.bwd_bytes ? a.bwd_bytes : b.bwd_bytes};
 }
 template <typename T>
 void attn_fwd(const AttnArgs& p, void* workspace, hipStream_t s) {
-    GS_ATTN_BY_HEAD(attn_fwd_at)(p, workspace, s);
+    GS_ATTN_BY_HEAD(attn_fwd_at, p.d, attn_any<T>(p))(p, workspace, s);
 }
 
 }  // namespace gs

@@ -1,5 +1,5 @@
 // The bfloat16 instances of attention's forward.
 #include "attention_fwd.h"
 
-template gs::AttnPlan gs::attn_plan<__bf16>(const gs::AttnArgs&);
+template gs::AttnBytes gs::attn_bytes<__bf16>(const gs::AttnArgs&);
 template void gs::attn_fwd<__bf16>(const gs::AttnArgs&, void*, hipStream_t);

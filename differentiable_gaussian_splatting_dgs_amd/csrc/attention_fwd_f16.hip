@@ -1,5 +1,5 @@
 // The float16 instances of attention's forward.
 #include "attention_fwd.h"
 
-template gs::AttnPlan gs::attn_plan<_Float16>(const gs::AttnArgs&);
+template gs::AttnBytes gs::attn_bytes<_Float16>(const gs::AttnArgs&);
 template void gs::attn_fwd<_Float16>(const gs::AttnArgs&, void*, hipStream_t);

@@ -1,5 +1,5 @@
 // The float32 instances of attention's forward.
 #include "attention_fwd.h"
 
-template gs::AttnPlan gs::attn_plan<float>(const gs::AttnArgs&);
+template gs::AttnBytes gs::attn_bytes<float>(const gs::AttnArgs&);
 template void gs::attn_fwd<float>(const gs::AttnArgs&, void*, hipStream_t);

@@ -173,7 +173,7 @@ def compare(q, k, v, dout, valid, scale=None):
 # batch, nq, nk, heads, kv_heads, d: single tokens, tile edges of rows and keys, every padded head, shared heads
 SIZES = [(1, 1, 1, 1, 1, 1), (1, 1, 256, 8, 8, 64), (2, 3, 5, 2, 1, 3), (1, 17, 63, 4, 4, 32), (3, 64, 64, 4, 2, 40),
          (2, 65, 65, 4, 1, 64), (1, 128, 129, 2, 2, 128), (2, 130, 31, 3, 3, 100), (2, 33, 200, 2, 1, 256),
-         (1, 257, 127, 1, 1, 160), (3, 100, 300, 6, 2, 72), (2, 1000, 77, 2, 2, 33), (2, 2, 5000, 2, 1, 64),
+         (1, 257, 127, 1, 1, 160), (2, 70, 300, 2, 1, 48), (1, 90, 280, 2, 2, 96), (1, 40, 150, 1, 1, 192), (3, 100, 300, 6, 2, 72), (2, 1000, 77, 2, 2, 33), (2, 2, 5000, 2, 1, 64),
          (1, 5000, 2, 2, 2, 32), (2, 16, 4097, 4, 1, 128), (1, 600, 600, 2, 2, 64), (2, 9, 1000, 4, 4, 7)]
 
 
