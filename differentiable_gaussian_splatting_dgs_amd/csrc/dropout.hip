@@ -71,7 +71,7 @@ __global__ __launch_bounds__(256) void k_dropout(DropArgs p) {
                 const float v = half >= p.least ? (float)f[i][j] * p.factor : 0.f;
                 f[i][j] = (T)(RES ? v + (float)r[i][j] : v);
             }
-            store_run(static_cast<T*>(p.y) + row * p.ld_y, block * 8 + i * E, p.n, f[i]);
+            store_part(static_cast<T*>(p.y) + row * p.ld_y, block * 8 + i * E, p.n, f[i]);
         }
         row += row_step, block += block_step;
         if (block >= p.blocks) block -= p.blocks, ++row;

@@ -165,6 +165,33 @@ __device__ __forceinline__ void store_run(T* row, int n0, int count, typename Ti
         if (n0 + j < count) row[n0 + j] = f[j];
 }
 
+// The same with at most three stores for the row's last elements, 8, 4 and 2 (float32: 8 and 4) bytes of them.
+template <typename T>
+__device__ __forceinline__ void store_part(T* row, int n0, int count, typename Tile<T>::Frag f) {
+    constexpr int E = Tile<T>::E, kBits = 8 * (int)sizeof(T);
+    if (n0 + E <= count) {
+        __builtin_memcpy(row + n0, &f, 16);
+        return;
+    }
+    uint64_t q[2];
+    __builtin_memcpy(q, &f, 16);
+    T* to = row + n0;
+    const int left = count - n0;  // may be negative: nothing
+    if (left <= 0) return;
+    if (left & (E / 2)) {
+        __builtin_memcpy(to, q, 8);
+        to += E / 2;
+        q[0] = q[1];
+    }
+    if constexpr (E == 8)
+        if (left & 2) {
+            __builtin_memcpy(to, q, 4);
+            to += 2;
+            q[0] >>= 2 * kBits;
+        }
+    if (left & 1) __builtin_memcpy(to, q, sizeof(T));
+}
+
 // 1 / (1 + exp(-u)).  float32 results take exp's argument to twice the width (the
 // product with log2 e alone is off by |u| 2^-24, which exp multiplies up); the
 // 16-bit types' rounding hides that.

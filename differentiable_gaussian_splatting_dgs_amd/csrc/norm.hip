@@ -6,7 +6,8 @@
 // Both directions are bound by memory: a row is read once and stays in registers while its moments are taken (the
 // mean first, then the squares about it: no cancellation).  A row is spread over G lanes of a wave with U chunks of
 // 16 bytes each, so a wave takes 64 / G rows at a time and a row's sums need log2 G exchanges; longer rows take a
-// block, and rows past its registers are read again for each pass (they lie in L2 by then).  The backward's sums
+// block, and rows past its registers are read again for each pass (they lie in L2 by then).  A row's last chunk is its
+// last 16 bytes: what it shares with the chunk before it counts there, and is written by both, the same bits.  The backward's sums
 // over the rows stay in the registers of the lane that has the columns; each block leaves one partial of them, which
 // a second launch adds in a fixed order.
 #include "linear_tile.h"
@@ -18,13 +19,14 @@ struct NormArgs {
     const void *x, *w, *b, *dy;
     void *y, *dx;
     float* part;  // [blocks][2][n]: dw and db
+    void *dw, *db;  // one block: the results themselves
     int64_t rows, ld_x, ld_y, ld_dx;
     int32_t n;
     float eps;
 };
 
-constexpr int kMostChunks = 512;  // of a row that a wave holds
-constexpr int kBlockU = 8;        // chunks a lane of a block's row
+constexpr int kMostChunks = 256;  // of a row that a wave holds: 4 a lane
+constexpr int kBlockU = 8;        // chunks a lane of a block's row, at most
 constexpr int kSumBlocks = 1024;  // partials of the backward at most
 
 // sum / n: the product with inv = 1 / n, and what it leaves.  A row of one value has that value for its mean.
@@ -41,197 +43,201 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// The same over the 256 threads of a block.
-__device__ __forceinline__ float block_sum(float v, float* s_sum) {
-    v = row_sum<64>(v);
-    __syncthreads();  // the last sum has been read
-    if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = v;
+// The same of K sums over the 256 threads of a block.
+template <int K>
+__device__ __forceinline__ void block_sums(float (&v)[K], float (*s_sum)[K]) {
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] = row_sum<64>(v[i]);
+    __syncthreads();  // the last sums have been read
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+        for (int i = 0; i < K; ++i) s_sum[threadIdx.x >> 6][i] = v[i];
     __syncthreads();
-    return (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] = (s_sum[0][i] + s_sum[1][i]) + (s_sum[2][i] + s_sum[3][i]);
+}
+__device__ __forceinline__ float block_sum(float v, float (*s_sum)[1]) {
+    float one[1] = {v};
+    block_sums(one, s_sum);
+    return one[0];
 }
 
-// A lane's chunks of a row, whose c-th is chunk first + c * step, as float32.  Elements past the row are 0; `count`
-// of each chunk's elements are the row's.
-template <typename T, int U>
-struct Chunks {
-    static constexpr int E = Tile<T>::E;
-    typename Tile<T>::Frag f[U];
+template <int G, int K>
+__device__ __forceinline__ void row_sums(float (&v)[K], float (*s_sum)[K]) {
+    if constexpr (G == 256) {
+        block_sums(v, s_sum);
+    } else {
+#pragma unroll
+        for (int i = 0; i < K; ++i) v[i] = row_sum<G>(v[i]);
+    }
+}
 
-    // n >= E
-    __device__ __forceinline__ void load(const T* row, int first, int step, int n) {
+// A lane's chunks of a row of n >= E elements: chunk u of lane `at` of G is that of number at + u G.  FULL: all lanes
+// have all of their chunks whole.
+template <typename T, int G, int U, bool FULL>
+struct Lane {
+    static constexpr int E = Tile<T>::E;
+    typedef typename Tile<T>::Frag Frag;
+    int from[U];  // where the chunk lies
+    int skip[U];  // how many of its elements belong to the chunk before (E: all, there is no such chunk)
+    __device__ __forceinline__ Lane(int at, int n) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int k0 = (first + u * step) * E;
-            f[u] = load16(row + max(min(k0, n - E), 0));
+            const int k = (at + u * G) * E;
+            from[u] = FULL ? k : min(k, n - E);
+            skip[u] = FULL ? 0 : min(k - from[u], E);
         }
     }
-    __device__ __forceinline__ void fix(int first, int step, int n, bool in) {
+    __device__ __forceinline__ void load(const T* row, Frag (&f)[U]) const {
+#pragma unroll
+        for (int u = 0; u < U; ++u) f[u] = load16(row + from[u]);
+    }
+    __device__ __forceinline__ bool counts(int u, int j) const { return FULL || j >= skip[u]; }
+    __device__ __forceinline__ void store(T* row, int u, Frag f) const {
+        if (FULL || skip[u] < E) __builtin_memcpy(row + from[u], &f, 16);
+    }
+    // elements of a vector of n, or `missing` without one
+    __device__ __forceinline__ void vector(const void* p, float missing, float (&v)[U][E]) const {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int k0 = (first + u * step) * E, drop = in ? min(max(k0 - (n - E), 0), E) * 8 * (int)sizeof(T) : 128;
-            union {
-                typename Tile<T>::Frag f;
-                uint64_t q[2];
-            } v;
-            v.f = f[u];
-            if (drop >= 64) {
-                v.q[0] = drop >= 128 ? 0 : v.q[1] >> (drop - 64);
-                v.q[1] = 0;
-            } else if (drop > 0) {
-                v.q[0] = (v.q[0] >> drop) | (v.q[1] << (64 - drop));
-                v.q[1] >>= drop;
-            }
-            f[u] = v.f;
+            Frag f;
+            if (p) f = load16(static_cast<const T*>(p) + from[u]);
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[u][j] = p ? (float)f[j] : missing;
         }
     }
-    __device__ __forceinline__ float at(int u, int j) const { return (float)f[u][j]; }
 };
 
 // Forward, G lanes a row (of a wave; G == 256: of a block), U chunks a lane.
-template <typename T, int G, int U>
+template <typename T, int G, int U, bool FULL>
 __global__ __launch_bounds__(256) void k_norm_fwd(NormArgs p) {
     constexpr int E = Tile<T>::E, kRows = 256 / G;  // rows a block takes at a time
-    __shared__ float s_sum[4];
-    const int at = threadIdx.x % G;
-    auto total = [&](float v) {
-        if constexpr (G == 256) return block_sum(v, s_sum);
-        else return row_sum<G>(v);
-    };
+    __shared__ float s_sum[4][1];
+    const Lane<T, G, U, FULL> lane(threadIdx.x % G, p.n);
     float w[U][E], b[U][E];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-            const int k = min((at + u * G) * E + j, p.n - 1);
-            w[u][j] = p.w ? (float)static_cast<const T*>(p.w)[k] : 1.f;
-            b[u][j] = p.b ? (float)static_cast<const T*>(p.b)[k] : 0.f;
-        }
+    lane.vector(p.w, 1.f, w);
+    lane.vector(p.b, 0.f, b);
     const float inv = 1.f / (float)p.n;
     const int64_t step = (int64_t)gridDim.x * kRows;
     int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / G;
     // rows of the same block end together: G == 256 meets at its barriers
     const int64_t sets = (p.rows + kRows - 1) / kRows;
-    Chunks<T, U> next;
-    if (blockIdx.x < sets) next.load(static_cast<const T*>(p.x) + (row < p.rows ? row : 0) * p.ld_x, at, G, p.n);
+    const T* x = static_cast<const T*>(p.x);
+    typename Tile<T>::Frag next[U];
+    if (blockIdx.x < sets) lane.load(x + (row < p.rows ? row : 0) * p.ld_x, next);
     for (int64_t set = blockIdx.x; set < sets; set += gridDim.x, row += step) {
-        const bool in = row < p.rows;
-        Chunks<T, U> x = next;
-        if (set + gridDim.x < sets) {
-            const int64_t to = row + step;
-            next.load(static_cast<const T*>(p.x) + (to < p.rows ? to : 0) * p.ld_x, at, G, p.n);
-        }
-        x.fix(at, G, p.n, in);
-        float sum = 0.f;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int j = 0; j < E; ++j) sum += x.at(u, j);
-        const float mean = mean_of(total(sum), inv, p.n);
-        float squares = 0.f;
+        float v[U][E], sum[1] = {0.f};
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int j = 0; j < E; ++j) {
-                const float d = (at + u * G) * E + j < p.n ? x.at(u, j) - mean : 0.f;
-                squares = fmaf(d, d, squares);
+                v[u][j] = (float)next[u][j];
+                sum[0] += lane.counts(u, j) ? v[u][j] : 0.f;
             }
-        const float r = 1.f / sqrtf(total(squares) * inv + p.eps);
-        if (!in) continue;
+        if (set + gridDim.x < sets) lane.load(x + (row + step < p.rows ? row + step : 0) * p.ld_x, next);
+        row_sums<G>(sum, s_sum);
+        const float mean = mean_of(sum[0], inv, p.n);
+        float squares[1] = {0.f};
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                v[u][j] -= mean;
+                const float d = lane.counts(u, j) ? v[u][j] : 0.f;
+                squares[0] = fmaf(d, d, squares[0]);
+            }
+        row_sums<G>(squares, s_sum);
+        const float r = 1.f / sqrtf(squares[0] * inv + p.eps);
+        if (row >= p.rows) continue;
         T* y = static_cast<T*>(p.y) + row * p.ld_y;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             typename Tile<T>::Frag f;
 #pragma unroll
-            for (int j = 0; j < E; ++j) f[j] = (T)fmaf((x.at(u, j) - mean) * r, w[u][j], b[u][j]);
-            store_run(y, (at + u * G) * E, p.n, f);
+            for (int j = 0; j < E; ++j) f[j] = (T)fmaf(v[u][j] * r, w[u][j], b[u][j]);
+            lane.store(y, u, f);
         }
     }
 }
 
 // Backward, the same way.
-template <typename T, int G, int U>
+template <typename T, int G, int U, bool FULL>
 __global__ __launch_bounds__(256) void k_norm_bwd(NormArgs p) {
     constexpr int E = Tile<T>::E, kRows = 256 / G;
-    __shared__ float s_sum[4];
+    __shared__ float s_sum[4][1], s_sums[4][3];
     extern __shared__ float s_part[];  // [kRows][G * U * E], one of dw and db at a time
     const int at = threadIdx.x % G;
-    auto total = [&](float v) {
-        if constexpr (G == 256) return block_sum(v, s_sum);
-        else return row_sum<G>(v);
-    };
-    float w[U][E], dw[U][E], db[U][E];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-            const int k = (at + u * G) * E + j;
-            w[u][j] = k >= p.n ? 0.f : p.w ? (float)static_cast<const T*>(p.w)[k] : 1.f;
-            dw[u][j] = db[u][j] = 0.f;
-        }
+    const Lane<T, G, U, FULL> lane(at, p.n);
+    float w[U][E], dw[U][E] = {}, db[U][E] = {};
+    lane.vector(p.w, 1.f, w);
     const float inv = 1.f / (float)p.n;
     const int64_t step = (int64_t)gridDim.x * kRows, sets = (p.rows + kRows - 1) / kRows;
     int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / G;
-    Chunks<T, U> next_x, next_g;
+    typename Tile<T>::Frag next_x[U], next_g[U];
     auto fetch = [&](int64_t to) {
         to = to < p.rows ? to : 0;
-        next_x.load(static_cast<const T*>(p.x) + to * p.ld_x, at, G, p.n);
-        next_g.load(static_cast<const T*>(p.dy) + to * p.ld_y, at, G, p.n);
+        lane.load(static_cast<const T*>(p.x) + to * p.ld_x, next_x);
+        lane.load(static_cast<const T*>(p.dy) + to * p.ld_y, next_g);
     };
     if (blockIdx.x < sets) fetch(row);
     for (int64_t set = blockIdx.x; set < sets; set += gridDim.x, row += step) {
-        const bool in = row < p.rows;
-        Chunks<T, U> x = next_x, g = next_g;
-        if (set + gridDim.x < sets) fetch(row + step);
-        x.fix(at, G, p.n, in);
-        g.fix(at, G, p.n, in);
-        float sum = 0.f;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int j = 0; j < E; ++j) sum += x.at(u, j);
-        const float mean = mean_of(total(sum), inv, p.n);
-        float squares = 0.f, along = 0.f, flat = 0.f;
+        float x[U][E], g[U][E], sum[1] = {0.f};
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int j = 0; j < E; ++j) {
-                const float d = (at + u * G) * E + j < p.n ? x.at(u, j) - mean : 0.f, gw = g.at(u, j) * w[u][j];
-                squares = fmaf(d, d, squares);
-                along = fmaf(gw, d, along);
-                flat += gw;
+                x[u][j] = (float)next_x[u][j], g[u][j] = (float)next_g[u][j];
+                sum[0] += lane.counts(u, j) ? x[u][j] : 0.f;
             }
-        const float r = 1.f / sqrtf(total(squares) * inv + p.eps);
-        along = total(along) * inv * r * r, flat = total(flat) * inv;
-        if (in) {
+        if (set + gridDim.x < sets) fetch(row + step);
+        row_sums<G>(sum, s_sum);
+        const float mean = mean_of(sum[0], inv, p.n);
+        float sums[3] = {0.f, 0.f, 0.f};  // of squares, of g xh, of g
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                typename Tile<T>::Frag f;
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int j = 0; j < E; ++j) {
-                    const float d = x.at(u, j) - mean, dy = g.at(u, j);
-                    f[j] = (T)(r * (fmaf(dy, w[u][j], -flat) - d * along));
-                    dw[u][j] = fmaf(dy, d * r, dw[u][j]);
-                    db[u][j] += dy;
-                }
-                if (p.dx) store_run(static_cast<T*>(p.dx) + row * p.ld_dx, (at + u * G) * E, p.n, f);
+            for (int j = 0; j < E; ++j) {
+                x[u][j] -= mean;
+                const bool in = lane.counts(u, j);
+                const float d = in ? x[u][j] : 0.f, gw = in ? g[u][j] * w[u][j] : 0.f;
+                sums[0] = fmaf(d, d, sums[0]);
+                sums[1] = fmaf(gw, d, sums[1]);
+                sums[2] += gw;
             }
+        row_sums<G>(sums, s_sums);
+        const float r = 1.f / sqrtf(sums[0] * inv + p.eps);
+        const float along = sums[1] * inv * r * r, flat = sums[2] * inv;
+        if (row >= p.rows) continue;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            typename Tile<T>::Frag f;
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                f[j] = (T)(r * (fmaf(g[u][j], w[u][j], -flat) - x[u][j] * along));
+                dw[u][j] = fmaf(g[u][j], x[u][j] * r, dw[u][j]);
+                db[u][j] += g[u][j];
+            }
+            if (p.dx) lane.store(static_cast<T*>(p.dx) + row * p.ld_dx, u, f);
         }
     }
     if (!p.part) return;
     // the block's rows join in LDS
     for (int which = 0; which < 2; ++which) {
         float* part = p.part + ((int64_t)blockIdx.x * 2 + which) * p.n;
+        T* out = static_cast<T*>(which ? p.db : p.dw);
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int j = 0; j < E; ++j)
-                s_part[threadIdx.x / G * (G * U * E) + (at + u * G) * E + j] = which ? db[u][j] : dw[u][j];
+                if (lane.counts(u, j))
+                    s_part[threadIdx.x / G * (G * U * E) + lane.from[u] + j] = which ? db[u][j] : dw[u][j];
         __syncthreads();
         for (int k = threadIdx.x; k < p.n; k += 256) {
             float sum = 0.f;
             for (int i = 0; i < kRows; ++i) sum += s_part[i * (G * U * E) + k];
-            part[k] = sum;
+            if (gridDim.x > 1) part[k] = sum;
+            else if (out) out[k] = (T)sum;
         }
     }
 }
@@ -294,8 +300,12 @@ __global__ __launch_bounds__(256) void k_norm_short(NormArgs p) {
 #pragma unroll
                 for (int j = 0; j < E; ++j) s_part[threadIdx.x][j] += s_part[threadIdx.x + o][j];
         }
+        T* out = static_cast<T*>(which ? p.db : p.dw);
         if (threadIdx.x == 0)
-            for (int j = 0; j < p.n; ++j) p.part[((int64_t)blockIdx.x * 2 + which) * p.n + j] = s_part[0][j];
+            for (int j = 0; j < p.n; ++j) {
+                if (gridDim.x > 1) p.part[((int64_t)blockIdx.x * 2 + which) * p.n + j] = s_part[0][j];
+                else if (out) out[j] = (T)s_part[0][j];
+            }
     }
 }
 
@@ -303,7 +313,7 @@ __global__ __launch_bounds__(256) void k_norm_short(NormArgs p) {
 // add up in the block's partial in memory, each column by one thread.
 template <typename T>
 __global__ __launch_bounds__(256) void k_norm_long(NormArgs p) {
-    __shared__ float s_sum[4];
+    __shared__ float s_sum[4][1];
     const T *w = static_cast<const T*>(p.w), *b = static_cast<const T*>(p.b);
     const float inv = 1.f / (float)p.n;
     float* part = p.part ? p.part + (int64_t)blockIdx.x * 2 * p.n : nullptr;
@@ -369,14 +379,17 @@ __global__ __launch_bounds__(256) void k_norm_join(const float* part, int parts,
 inline int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int size_of(int32_t dtype) { return dtype == GS_F32 ? 4 : 2; }
 
-enum { NORM_SHORT, NORM_WAVE, NORM_BLOCK, NORM_LONG };
+enum { NORM_SHORT, NORM_WAVE, NORM_LONG };
 
 struct NormPlan {
     int kind, lanes, chunks;  // lanes a row and chunks a lane
+    bool full;                // which the row fills
     int64_t sets;             // of rows that a block takes at a time
 };
 
-// Lanes of a row: the fewest that hold it a chunk each, up to a wave; then more chunks a lane, then a block.
+// Lanes of a row: the fewest that hold it a chunk each, up to a wave; then up to 4 chunks a lane, then a block.
+// 400 MB of bfloat16 rows of 2100: by a wave of 8 chunks a lane forward 454 us, backward 521, by a block of 2 180 and
+// 364; of 1500 by 4 chunks a lane 205 and 262, by 3 153 and 249.
 NormPlan plan_of(const gs_layer_norm* d) {
     const int e = 16 / size_of(d->dtype);
     const int64_t chunks = cdiv64(d->n, e);
@@ -384,20 +397,24 @@ NormPlan plan_of(const gs_layer_norm* d) {
     if (d->n < e) {
         p.kind = NORM_SHORT, p.sets = cdiv64(d->rows, 256);
     } else if (chunks <= kMostChunks) {
-        p.kind = NORM_WAVE, p.lanes = 1, p.chunks = 1;
+        p.kind = NORM_WAVE, p.lanes = 1;
         while (p.lanes < 64 && p.lanes < chunks) p.lanes *= 2;
-        while (p.lanes * p.chunks < chunks) p.chunks *= 2;
+        p.chunks = (int)cdiv64(chunks, p.lanes);
         p.sets = cdiv64(d->rows, 256 / p.lanes);
     } else if (chunks <= 256 * kBlockU) {
-        p.kind = NORM_BLOCK, p.lanes = 256, p.chunks = chunks <= 256 * 4 ? 4 : 8, p.sets = d->rows;
+        p.kind = NORM_WAVE, p.lanes = 256, p.chunks = (int)cdiv64(chunks, 256), p.sets = d->rows;
+        if (p.chunks > 4) p.chunks = 8;
     } else {
         p.kind = NORM_LONG, p.sets = d->rows;
     }
+    p.full = d->n == (int64_t)p.lanes * p.chunks * e;
     return p;
 }
 
-// Blocks of the backward: a partial of 8 n bytes each, so no more than a tenth of the rows' bytes asks for.
+// Blocks of the backward: a partial of 8 n bytes each, so no more than a tenth of the rows' bytes asks for.  A few sets
+// of rows go to one block, which needs no second launch (but for rows that a block reads again).
 int bwd_blocks(const gs_layer_norm* d, const NormPlan& plan) {
+    if (plan.kind != NORM_LONG && plan.sets <= 4) return 1;
     const int64_t most = d->rows * size_of(d->dtype) / 80;
     int64_t blocks = plan.sets < kSumBlocks ? plan.sets : kSumBlocks;
     const int64_t least = plan.sets < 256 ? plan.sets : 256;
@@ -406,13 +423,18 @@ int bwd_blocks(const gs_layer_norm* d, const NormPlan& plan) {
     return (int)blocks;
 }
 
-template <typename T, int G, int U>
+template <typename T, int G, int U, bool FULL>
 void norm_launch(const NormArgs& p, int blocks, bool back, hipStream_t s) {
     if (back)
-        hipLaunchKernelGGL((k_norm_bwd<T, G, U>), dim3(blocks), dim3(256),
+        hipLaunchKernelGGL((k_norm_bwd<T, G, U, FULL>), dim3(blocks), dim3(256),
                            p.part ? (256 / G) * G * U * Tile<T>::E * 4 : 0, s, p);
     else
-        hipLaunchKernelGGL((k_norm_fwd<T, G, U>), dim3(blocks), dim3(256), 0, s, p);
+        hipLaunchKernelGGL((k_norm_fwd<T, G, U, FULL>), dim3(blocks), dim3(256), 0, s, p);
+}
+template <typename T, int G, int U>
+void norm_any(const NormArgs& p, const NormPlan& plan, int blocks, bool back, hipStream_t s) {
+    if (plan.full) norm_launch<T, G, U, true>(p, blocks, back, s);
+    else norm_launch<T, G, U, false>(p, blocks, back, s);
 }
 
 template <typename T>
@@ -421,24 +443,22 @@ void norm_run(const NormArgs& p, const NormPlan& plan, int blocks, bool back, hi
         hipLaunchKernelGGL(k_norm_short<T>, dim3(blocks), dim3(256), 0, s, p);
     } else if (plan.kind == NORM_LONG) {
         hipLaunchKernelGGL(k_norm_long<T>, dim3(blocks), dim3(256), 0, s, p);
-    } else if (plan.kind == NORM_BLOCK) {
-        if (plan.chunks == 4) norm_launch<T, 256, 4>(p, blocks, back, s);
-        else norm_launch<T, 256, 8>(p, blocks, back, s);
-    } else if (plan.lanes == 64) {
-        switch (plan.chunks) {
-            case 1: norm_launch<T, 64, 1>(p, blocks, back, s); break;
-            case 2: norm_launch<T, 64, 2>(p, blocks, back, s); break;
-            case 4: norm_launch<T, 64, 4>(p, blocks, back, s); break;
-            default: norm_launch<T, 64, 8>(p, blocks, back, s); break;
-        }
     } else {
-        switch (plan.lanes) {
-            case 1: norm_launch<T, 1, 1>(p, blocks, back, s); break;
-            case 2: norm_launch<T, 2, 1>(p, blocks, back, s); break;
-            case 4: norm_launch<T, 4, 1>(p, blocks, back, s); break;
-            case 8: norm_launch<T, 8, 1>(p, blocks, back, s); break;
-            case 16: norm_launch<T, 16, 1>(p, blocks, back, s); break;
-            default: norm_launch<T, 32, 1>(p, blocks, back, s); break;
+        switch (plan.lanes < 64 ? plan.lanes : plan.lanes * 10 + plan.chunks) {
+            case 1: norm_any<T, 1, 1>(p, plan, blocks, back, s); break;
+            case 2: norm_any<T, 2, 1>(p, plan, blocks, back, s); break;
+            case 4: norm_any<T, 4, 1>(p, plan, blocks, back, s); break;
+            case 8: norm_any<T, 8, 1>(p, plan, blocks, back, s); break;
+            case 16: norm_any<T, 16, 1>(p, plan, blocks, back, s); break;
+            case 32: norm_any<T, 32, 1>(p, plan, blocks, back, s); break;
+            case 641: norm_any<T, 64, 1>(p, plan, blocks, back, s); break;
+            case 642: norm_any<T, 64, 2>(p, plan, blocks, back, s); break;
+            case 643: norm_any<T, 64, 3>(p, plan, blocks, back, s); break;
+            case 644: norm_any<T, 64, 4>(p, plan, blocks, back, s); break;
+            case 2562: norm_any<T, 256, 2>(p, plan, blocks, back, s); break;
+            case 2563: norm_any<T, 256, 3>(p, plan, blocks, back, s); break;
+            case 2564: norm_any<T, 256, 4>(p, plan, blocks, back, s); break;
+            default: norm_any<T, 256, 8>(p, plan, blocks, back, s); break;
         }
     }
 }
@@ -466,13 +486,10 @@ void fwd(const gs_layer_norm* d, NormArgs& p, hipStream_t s) {
 
 template <typename T>
 void bwd(const gs_layer_norm* d, NormArgs& p, void* dw, void* db, hipStream_t s) {
-    int blocks = 0;
-    if (d->rows > 0) {
-        const NormPlan plan = plan_of(d);
-        blocks = bwd_blocks(d, plan);
-        norm_run<T>(p, plan, blocks, true, s);
-    }
-    if (dw || db)
+    const NormPlan plan = plan_of(d);
+    const int blocks = d->rows > 0 ? bwd_blocks(d, plan) : 0;
+    if (blocks > 0) norm_run<T>(p, plan, blocks, true, s);
+    if ((dw || db) && (blocks != 1 || plan.kind == NORM_LONG))
         hipLaunchKernelGGL(k_norm_join<T>, dim3((unsigned)cdiv64(2 * (int64_t)d->n, 16)), dim3(256), 0, s, p.part, blocks,
                            d->n, static_cast<T*>(dw), static_cast<T*>(db));
 }
@@ -490,7 +507,7 @@ extern "C" int gs_layer_norm_fwd(const gs_layer_norm* d, const void* x, const vo
     if (!x || !y || d->ld_x < d->n || d->ld_y < d->n) return GS_EINVAL;
     for (const void* t : {x, w, b, (const void*)y})
         if (!element_aligned(t, d->dtype)) return GS_EALIGN;
-    NormArgs p{x, w, b, nullptr, y, nullptr, nullptr, d->rows, d->ld_x, d->ld_y, 0, d->n, d->eps};
+    NormArgs p{x, w, b, nullptr, y, nullptr, nullptr, nullptr, nullptr, d->rows, d->ld_x, d->ld_y, 0, d->n, d->eps};
     hipStream_t s = as_stream(stream);
     if (d->dtype == GS_F32)
         fwd<float>(d, p, s);
@@ -520,8 +537,8 @@ extern "C" int gs_layer_norm_bwd(const gs_layer_norm* d, const void* x, const vo
     if ((dw || db) && !workspace) return GS_EINVAL;
     if ((dw || db) && workspace_bytes < workspace_of(d)) return GS_EWORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return GS_EALIGN;
-    NormArgs p{x, w, nullptr, dy, nullptr, dx, dw || db ? static_cast<float*>(workspace) : nullptr, d->rows, d->ld_x,
-               d->ld_y, d->ld_dx, d->n, d->eps};
+    NormArgs p{x, w, nullptr, dy, nullptr, dx, dw || db ? static_cast<float*>(workspace) : nullptr, dw, db, d->rows,
+               d->ld_x, d->ld_y, d->ld_dx, d->n, d->eps};
     hipStream_t s = as_stream(stream);
     if (d->dtype == GS_F32)
         bwd<float>(d, p, dw, db, s);

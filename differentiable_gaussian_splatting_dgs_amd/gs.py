@@ -1183,6 +1183,15 @@ def _row_shape(x, name="x"):
     return *shape, code, device, _rows(x, shape, x.dtype, device, name)
 
 
+@functools.lru_cache(maxsize=1024)
+def _layer_norm_workspace(rows, n, code):
+    """Bytes of workspace of a backward on these sizes."""
+    b = C.c_size_t()
+    _check(load_library().gs_layer_norm_bwd_workspace_size(_pack_layer_norm(rows, n, code, n, n, n, 0.0), C.byref(b)),
+           "gs_layer_norm_bwd_workspace_size")
+    return b.value
+
+
 def layer_norm_fwd_into(x, w, b, y, eps):
     """gs_layer_norm_fwd; y None: a new [rows, n] tensor.  Returns y."""
     rows, n, code, device, ld_x = _row_shape(x)
@@ -1210,11 +1219,7 @@ def gs_layer_norm_fwd(x, w, b, y, eps=1e-5):
 
 
 def gs_layer_norm_bwd_workspace_size(x):
-    rows, n, code, _, ld_x = _row_shape(x)
-    b = C.c_size_t()
-    _check(load_library().gs_layer_norm_bwd_workspace_size(_pack_layer_norm(rows, n, code, ld_x, n, n, 0.0),
-                                                           C.byref(b)), "gs_layer_norm_bwd_workspace_size")
-    return b.value
+    return _layer_norm_workspace(*_row_shape(x)[:3])
 
 
 def layer_norm_bwd_into(x, w, dy, dx, dw, db, workspace, eps):
@@ -1232,10 +1237,8 @@ def layer_norm_bwd_into(x, w, dy, dx, dw, db, workspace, eps):
     lib = _lib or load_library()
     d = _pack_layer_norm(rows, n, code, ld_x, ld_y, ld_dx, eps)
     if workspace is None and (dw is not None or db is not None):
-        size = C.c_size_t()
-        _check(lib.gs_layer_norm_bwd_workspace_size(d, C.byref(size)), "gs_layer_norm_bwd_workspace_size")
         # torch's device allocations start at multiples of 512 bytes
-        workspace = torch.empty(size.value, dtype=torch.uint8, device=x.device)
+        workspace = torch.empty(_layer_norm_workspace(rows, n, code), dtype=torch.uint8, device=x.device)
     pw = None if workspace is None else _whole(workspace, workspace.shape, torch.uint8, device, "workspace")
     rc = lib.gs_layer_norm_bwd(
         d, x.data_ptr(), _whole(w, (n,), dtype, device, "w"), dy.data_ptr(), pdx, _whole(dw, (n,), dtype, device, "dw"),
