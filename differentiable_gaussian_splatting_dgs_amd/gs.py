@@ -1040,23 +1040,28 @@ def _per_head(t, shape, dtype, device, name):
     return b, n, h
 
 
-def _attention_shape(q, k, scale):
-    """(batch, nq, nk, heads, kv_heads, d, type code, device, scale) of q [batch, nq, heads, d] and k [batch, nk,
-    kv_heads, d]."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 4 or not isinstance(k, torch.Tensor) or k.dim() != 4:
-        raise GsError("q, k and v must be 4-D tensors")
-    code = DTYPES.get(q.dtype)
-    if code is None or not q.is_cuda:
+def _attention_shape(q, k, v, scale):
+    """(q's shape, k's shape, type code, device, scale, strides of q, k and v) of q [batch, nq, heads, d] and k, v
+    [batch, nk, kv_heads, d]."""
+    try:
+        shape, k_shape, dtype = q.shape, k.shape, q.dtype
+        batch, _, heads, d = shape
+        k_batch, _, kv_heads, k_d = k_shape
+        device = q.get_device()
+    except (AttributeError, ValueError, TypeError):
+        raise GsError("q, k and v must be 4-D tensors") from None
+    code = DTYPES.get(dtype)
+    if code is None or device < 0:
         _refuse(q, None, None, "q")
-    batch, nq, heads, d = q.shape
-    b, nk, kv_heads, dk = k.shape
-    if b != batch or dk != d:
-        raise GsError(f"k must have shape [{batch}, nk, kv_heads, {d}], got {tuple(k.shape)}")
+    if k_batch != batch or k_d != d:
+        raise GsError(f"k must have shape [{batch}, nk, kv_heads, {d}], got {tuple(k_shape)}")
     if kv_heads < 1 or heads < 1 or heads % kv_heads:
         raise GsError(f"q's heads ({heads}) must be a multiple of k's ({kv_heads})")
     if d < 1 or d > MAX_HEAD_DIM:
         raise GsError(f"heads must have 1 to {MAX_HEAD_DIM} elements, got {d}")
-    return batch, nq, nk, heads, kv_heads, d, code, q.get_device(), d ** -0.5 if scale is None else float(scale)
+    strides = (*_per_head(q, shape, dtype, device, "q"), *_per_head(k, k_shape, dtype, device, "k"),
+               *_per_head(v, k_shape, dtype, device, "v"))
+    return shape, k_shape, code, device, d ** -0.5 if scale is None else float(scale), strides
 
 
 def _valid(mask, q_lengths, k_lengths, batch, nk, device):
@@ -1076,6 +1081,9 @@ def _valid(mask, q_lengths, k_lengths, batch, nk, device):
     return at, stride or 0, *lengths
 
 
+_ALL_VALID = None, 0, None, None
+
+
 @functools.lru_cache(maxsize=1024)
 def _attention_workspace(name, batch, nq, nk, heads, kv_heads, d, code):
     """Bytes of workspace of a call on these sizes."""
@@ -1088,39 +1096,47 @@ def _attention_workspace(name, batch, nq, nk, heads, kv_heads, d, code):
 def attention_fwd_into(q, k, v, mask, q_lengths, k_lengths, out, lse, workspace, scale):
     """gs_attention_fwd; out None: a new tensor.  lse: a tensor, None (not wanted) or True (a new one).  workspace None:
     one of the size the call needs.  Returns out and lse."""
-    batch, nq, nk, heads, kv_heads, d, code, device, scale = _attention_shape(q, k, scale)
+    shape, k_shape, code, device, scale, strides = _attention_shape(q, k, v, scale)
     if device != _current_device():
         with torch.cuda.device(device):
             return attention_fwd_into(q, k, v, mask, q_lengths, k_lengths, out, lse, workspace, scale)
-    dtype = q.dtype
-    strides = (*_per_head(q, q.shape, dtype, device, "q"), *_per_head(k, k.shape, dtype, device, "k"),
-               *_per_head(v, k.shape, dtype, device, "v"))
-    pm, mask_stride, pq, pk = _valid(mask, q_lengths, k_lengths, batch, nk, device)
+    (batch, nq, heads, d), (_, nk, kv_heads, _) = shape, k_shape
+    pm, mask_stride, pq, pk = (_ALL_VALID if mask is q_lengths is k_lengths is None else
+                               _valid(mask, q_lengths, k_lengths, batch, nk, device))
     if out is None:
-        out = q.new_empty(q.shape)
+        out = q.new_empty(shape)
         to = out.data_ptr()
     else:
-        to = _whole(out, q.shape, dtype, device, "out")
+        to = _whole(out, shape, q.dtype, device, "out")
+    pl = None
     if lse is True:
-        lse = torch.empty((batch, heads, nq), dtype=torch.float32, device=q.device)
-    size = _attention_workspace("gs_attention_fwd_workspace_size", batch, nq, nk, heads, kv_heads, d, code)
-    if workspace is None and size:
-        # torch's device allocations start at multiples of 512 bytes
-        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-    pw = None
+        lse = q.new_empty((batch, heads, nq), dtype=torch.float32)
+        pl = lse.data_ptr()
+    elif lse is not None:
+        pl = _whole(lse, (batch, heads, nq), torch.float32, device, "lse")
+    size, pw = _attention_workspace("gs_attention_fwd_workspace_size", batch, nq, nk, heads, kv_heads, d, code), None
     if workspace is not None:
         pw, size = _whole(workspace, workspace.shape, torch.uint8, device, "workspace"), workspace.numel()
+    elif size:
+        # torch's device allocations start at multiples of 512 bytes
+        workspace = q.new_empty(size, dtype=torch.uint8)
+        pw = workspace.data_ptr()
     rc = (_lib or load_library()).gs_attention_fwd(
         _pack_attention(batch, nq, nk, heads, kv_heads, d, code, *strides, 0, 0, 0, mask_stride, scale), q.data_ptr(),
-        k.data_ptr(), v.data_ptr(), pm, pq, pk, to, _whole(lse, (batch, heads, nq), torch.float32, device, "lse"),
-        pw, size, _raw_stream(device))
+        k.data_ptr(), v.data_ptr(), pm, pq, pk, to, pl, pw, size, _raw_stream(device))
     if rc:
         _check(rc, "gs_attention_fwd")
     return out, lse
 
 
+def _attention_sizes(q, k):
+    """The sizes that a workspace follows from."""
+    shape, k_shape, code, *_ = _attention_shape(q, k, k, None)
+    return shape[0], shape[1], k_shape[1], shape[2], k_shape[2], shape[3], code
+
+
 def gs_attention_fwd_workspace_size(q, k):
-    return _attention_workspace("gs_attention_fwd_workspace_size", *_attention_shape(q, k, None)[:7])
+    return _attention_workspace("gs_attention_fwd_workspace_size", *_attention_sizes(q, k))
 
 
 def gs_attention_fwd(q, k, v, out, lse, workspace, mask=None, q_lengths=None, k_lengths=None, scale=None):
@@ -1134,33 +1150,35 @@ def gs_attention_fwd(q, k, v, out, lse, workspace, mask=None, q_lengths=None, k_
 
 
 def gs_attention_bwd_workspace_size(q, k):
-    return _attention_workspace("gs_attention_bwd_workspace_size", *_attention_shape(q, k, None)[:7])
+    return _attention_workspace("gs_attention_bwd_workspace_size", *_attention_sizes(q, k))
 
 
 def attention_bwd_into(q, k, v, out, lse, dout, dq, dk, dv, workspace, mask, q_lengths, k_lengths, scale):
     """gs_attention_bwd; workspace None: one of the size the call needs."""
-    batch, nq, nk, heads, kv_heads, d, code, device, scale = _attention_shape(q, k, scale)
+    shape, k_shape, code, device, scale, strides = _attention_shape(q, k, v, scale)
     if device != _current_device():
         with torch.cuda.device(device):
             return attention_bwd_into(q, k, v, out, lse, dout, dq, dk, dv, workspace, mask, q_lengths, k_lengths, scale)
-    dtype = q.dtype
-    strides = (*_per_head(q, q.shape, dtype, device, "q"), *_per_head(k, k.shape, dtype, device, "k"),
-               *_per_head(v, k.shape, dtype, device, "v"), *_per_head(dout, q.shape, dtype, device, "dout"))
-    pm, mask_stride, pq, pk = _valid(mask, q_lengths, k_lengths, batch, nk, device)
+    (batch, nq, heads, d), (_, nk, kv_heads, _), dtype = shape, k_shape, q.dtype
+    of_dout = _per_head(dout, shape, dtype, device, "dout")
+    pm, mask_stride, pq, pk = (_ALL_VALID if mask is q_lengths is k_lengths is None else
+                               _valid(mask, q_lengths, k_lengths, batch, nk, device))
     if out is None or lse is None:
         raise GsError("the backward needs the forward's out and lse")
-    at = (q.data_ptr(), k.data_ptr(), v.data_ptr(), pm, pq, pk, _whole(out, q.shape, dtype, device, "out"),
+    at = (q.data_ptr(), k.data_ptr(), v.data_ptr(), pm, pq, pk, _whole(out, shape, dtype, device, "out"),
           _whole(lse, (batch, heads, nq), torch.float32, device, "lse"), dout.data_ptr(),
-          _whole(dq, q.shape, dtype, device, "dq"), _whole(dk, k.shape, dtype, device, "dk"),
-          _whole(dv, k.shape, dtype, device, "dv"))
-    lib = _lib or load_library()
-    a = _pack_attention(batch, nq, nk, heads, kv_heads, d, code, *strides, mask_stride, scale)
+          _whole(dq, shape, dtype, device, "dq"), _whole(dk, k_shape, dtype, device, "dk"),
+          _whole(dv, k_shape, dtype, device, "dv"))
     if workspace is None:
         size = _attention_workspace("gs_attention_bwd_workspace_size", batch, nq, nk, heads, kv_heads, d, code)
         # torch's device allocations start at multiples of 512 bytes
-        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-    rc = lib.gs_attention_bwd(a, *at, _whole(workspace, workspace.shape, torch.uint8, device, "workspace"),
-                              workspace.numel(), _raw_stream(device))
+        workspace = q.new_empty(size, dtype=torch.uint8)
+        pw = workspace.data_ptr()
+    else:
+        pw, size = _whole(workspace, workspace.shape, torch.uint8, device, "workspace"), workspace.numel()
+    rc = (_lib or load_library()).gs_attention_bwd(
+        _pack_attention(batch, nq, nk, heads, kv_heads, d, code, *strides, *of_dout, mask_stride, scale), *at, pw, size,
+        _raw_stream(device))
     if rc:
         _check(rc, "gs_attention_bwd")
 

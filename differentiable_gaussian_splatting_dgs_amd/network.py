@@ -79,13 +79,6 @@ def linear(x, w, bias=None, residual=None, act="none"):
     return gs.linear_fwd_into(x, w, bias, residual, None, act)
 
 
-def _differentiable(*tensors):
-    """Whether a call on them goes through autograd: under forward mode a tensor with a tangent need not require a
-    gradient, and the function raises for it."""
-    return forward_ad._current_level >= 0 or torch.is_grad_enabled() and any(
-        t is not None and t.requires_grad for t in tensors)
-
-
 def layer_norm_backward(dy, x, w=None, b=None, eps=1e-5, need=(True, True, True)):
     """dx, dw, db of y = layer_norm(x, w, b, eps) from dy = dL/dy (None where need is False; dw and db None without w
     and b)."""
@@ -115,7 +108,8 @@ def layer_norm(x, w=None, b=None, eps=1e-5):
     """(x - mean) / sqrt(var + eps) w + b of every row of x [rows, n], differentiable in all three, once.
 
     w and b [n] (or None) of x's type (float32, float16 or bfloat16); x may have strided rows."""
-    if _differentiable(x, w, b):
+    if forward_ad._current_level >= 0 or torch.is_grad_enabled() and (
+            x.requires_grad or (w is not None and w.requires_grad) or (b is not None and b.requires_grad)):
         return LayerNormFunction.apply(x, w, b, eps)
     return gs.layer_norm_fwd_into(x, w, b, None, eps)
 
@@ -145,7 +139,8 @@ def dropout(x, p, seed, offset=0, residual=None):
     offset of its own.  seed may be an int64 device tensor of two, a seed and a number added to offset, which the
     kernel reads when it runs: a call recorded into a graph draws another mask when the tensor changes between replays.
     It must hold the same numbers when the gradient is taken."""
-    if _differentiable(x, residual):
+    if forward_ad._current_level >= 0 or torch.is_grad_enabled() and (
+            x.requires_grad or (residual is not None and residual.requires_grad)):
         return DropoutFunction.apply(x, residual, p, seed, offset)
     return gs.dropout_into(x, p, seed, offset, residual, None)
 
@@ -164,8 +159,8 @@ def cross_attention_forward(q, k, v, mask=None, q_lengths=None, k_lengths=None, 
 def cross_attention_backward(dout, q, k, v, out, lse, mask=None, q_lengths=None, k_lengths=None, scale=None,
                              need=(True, True, True)):
     """dq, dk, dv (None where need is False) from dout = dL/dout and the forward's out and lse."""
-    dq, dk, dv = (torch.empty_like(t, memory_format=torch.contiguous_format) if wanted else None
-                  for t, wanted in zip((q, k, v), need))
+    dq, dk, dv = [torch.empty_like(t, memory_format=torch.contiguous_format) if wanted else None
+                  for t, wanted in zip((q, k, v), need)]
     gs.attention_bwd_into(q, k, v, out, lse, dout, dq, dk, dv, None, mask, q_lengths, k_lengths, scale)
     return dq, dk, dv
 
@@ -195,7 +190,12 @@ def cross_attention(q, k, v, mask=None, q_lengths=None, k_lengths=None, scale=No
     mask: bool [batch, nk], the keys that count; q_lengths, k_lengths: int32 [batch], the queries and keys that count,
     from the first on.  What does not count is not used, whatever it holds, and has a gradient of 0; a query that does
     not count, or has no key that does, gives 0."""
-    if _differentiable(q, k, v):
+    try:
+        through = forward_ad._current_level >= 0 or torch.is_grad_enabled() and (
+            q.requires_grad or k.requires_grad or v.requires_grad)
+    except AttributeError:
+        raise GsError("q, k and v must be 4-D tensors") from None
+    if through:
         return CrossAttentionFunction.apply(q, k, v, mask, q_lengths, k_lengths, scale)
     return gs.attention_fwd_into(q, k, v, mask, q_lengths, k_lengths, None, None, None, scale)[0]
 
