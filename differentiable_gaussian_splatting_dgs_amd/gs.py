@@ -1025,6 +1025,7 @@ def gs_adam_step_clipped(tensors, beta1, beta2, eps, step, clip=None):
 # ---------------------------------------------------------------------------
 
 MAX_HEAD_DIM = 256
+_like, _contiguous = torch.empty_like, torch.contiguous_format  # the quickest way to a new tensor
 _pack_attention = struct.Struct("=3q4i13qf4x").pack
 _pack_layer_norm = struct.Struct("=qii3qf4x").pack
 _pack_dropout = struct.Struct("=qii3qdQQ").pack
@@ -1104,7 +1105,7 @@ def attention_fwd_into(q, k, v, mask, q_lengths, k_lengths, out, lse, workspace,
     pm, mask_stride, pq, pk = (_ALL_VALID if mask is q_lengths is k_lengths is None else
                                _valid(mask, q_lengths, k_lengths, batch, nk, device))
     if out is None:
-        out = q.new_empty(shape)
+        out = _like(q, memory_format=_contiguous)
         to = out.data_ptr()
     else:
         to = _whole(out, shape, q.dtype, device, "out")
@@ -1218,7 +1219,7 @@ def layer_norm_fwd_into(x, w, b, y, eps):
             return layer_norm_fwd_into(x, w, b, y, eps)
     dtype = x.dtype
     if y is None:
-        y, ld_y = x.new_empty((rows, n)), n
+        y, ld_y = _like(x, memory_format=_contiguous), n
     else:
         ld_y = _rows(y, (rows, n), dtype, device, "y")
     rc = (_lib or load_library()).gs_layer_norm_fwd(
@@ -1279,7 +1280,7 @@ def dropout_into(x, p, seed, offset, residual, y):
             return dropout_into(x, p, seed, offset, residual, y)
     dtype, shape = x.dtype, (rows, n)
     if y is None:
-        y, ld_y = x.new_empty(shape), n
+        y, ld_y = _like(x, memory_format=_contiguous), n
     else:
         ld_y = _rows(y, shape, dtype, device, "y")
     pr, ld_res = None, 0
