@@ -441,7 +441,8 @@ template <typename T>
 bool attn_any(const AttnArgs& p) {
     const int64_t most = ((int64_t)1 << 31) / (int64_t)sizeof(T);
     int64_t far = 64 * (p.k_n > p.v_n ? p.k_n : p.v_n);
-    for (const auto& s : {std::pair<int64_t, int64_t>{p.q_n, p.q_h}, {p.g_n, p.g_h}}) {
+    const int64_t d = p.d;  // out's rows are whole, also where q is one head expanded
+    for (const auto& s : {std::pair<int64_t, int64_t>{p.q_n, p.q_h}, {p.g_n, p.g_h}, {p.heads * d, d}}) {
         const int64_t reach = (64 / p.group + 2) * s.first + (p.group > 1 ? p.group * s.second : 0);
         far = reach > far ? reach : far;
     }

@@ -401,3 +401,30 @@ def test_offsets_past_32_bits():
     got = run(k, k0, v0, v, (None, None, None))
     want = run(k0, k0, v0, v0, (None, None, None))
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("nq,nk,group", [(200, 20, 1), (200, 20, 8), (40, 20, 1), (10, 20, 1)])
+def test_many_heads_of_one_row(nq, nk, group):
+    """Inputs of one head expanded to so many that the rows of out, which are whole, lie 2^26 elements apart: the first
+    head of keys' results are right, and the other heads' are the same."""
+    from differentiable_gaussian_splatting_dgs_amd import network
+    heads, d = (1 << 26) // 32, 32
+    print("heads", heads, nq, nk, group, flush=True)
+    q, k, v, dout = inputs((1, nq, nk, 1, 1, d), torch.bfloat16)
+
+    def expanded(heads):
+        return [t.expand(-1, -1, n, -1) for t, n in zip((q, k, v, dout), (heads, heads // group, heads // group, heads))]
+
+    want = exact(*expanded(group), None, None, None, d ** -0.5)
+    q_, k_, v_, dout_ = expanded(heads)
+    out, lse = network.cross_attention_forward(q_, k_, v_)
+    got = (out, lse, *network.cross_attention_backward(dout_, q_, k_, v_, out, lse))
+    torch.cuda.synchronize()
+    for i, (a, b) in enumerate(zip(got, want)):
+        if i != 1:
+            a = a.transpose(1, 2)  # [1, heads, rows, d]
+            b = [t.transpose(1, 2) for t in b]
+        first = a[:, :b[0].shape[1]]
+        check(first, b, (i, nq, group))
+        for part in a.split(1 << 18, 1):
+            assert torch.equal(part, first[:, :1].expand_as(part)), (i, nq, group)
