@@ -63,7 +63,7 @@ template <typename T, int D>
 struct AttnShape {
     static constexpr bool kHalf = sizeof(T) == 2;
     static constexpr int kFwd = kHalf ? (D <= 64 ? 4 : D <= 128 ? 2 : 1) : D <= 128 ? 2 : 1;
-    static constexpr int kDq = kHalf ? (D <= 64 ? 2 : 1) : D <= 64 ? 2 : 1;
+    static constexpr int kDq = kHalf ? (D <= 128 ? 2 : 1) : D <= 64 ? 2 : 1;
     static constexpr int kDkv = kHalf ? (D <= 128 ? 2 : 1) : D <= 64 ? 2 : 1;
     static constexpr int kThin = D <= 32 ? (kHalf ? 4 : 2) : D <= 128 ? (kHalf ? 2 : 1) : 1;
     static constexpr int kOccThin = D * (int)sizeof(T) >= 512 ? 1 : 2;
@@ -176,13 +176,16 @@ __device__ __forceinline__ typename Tile<T>::Frag chunk_fixed(typename Tile<T>::
     return u.f;
 }
 
-// Rows of a matrix in memory on their way into a tile of LDS: each thread moves the same chunk of kEach rows.  at
-// holds the offsets of its loads from the tile's first row (bytes), or the rows' addresses (ANY).
-template <typename T, int D, int MODE>
+// Rows of a matrix in memory on their way into a tile of LDS: each thread moves a chunk of kEach rows.  at holds the
+// offsets of its loads from the tile's first row (bytes).  DIRECT (of WHOLE rows): the loads write LDS themselves, lane
+// l of a wave the l-th 16 bytes of the wave's run, so that a lane reads the chunk that tile_at has there; they hold
+// no registers on their way.  Loads in flight are the caller's to wait for: place() does, before a barrier.
+template <typename T, int D, int MODE, bool DIRECT = false>
 struct Mover {
     typedef AttnTile<T, D> A;
     typedef typename Tile<T>::Frag Frag;
-    Frag f[A::kEach];
+    static_assert(!DIRECT || MODE == WHOLE, "direct loads");
+    Frag f[DIRECT ? 1 : A::kEach];
     uint32_t at[MODE == ANY ? 1 : A::kEach];
 
     static __device__ __forceinline__ int row(int i) { return i * (256 / A::kChunks) + threadIdx.x / A::kChunks; }
@@ -191,16 +194,29 @@ struct Mover {
     template <typename Of>
     __device__ __forceinline__ void aim(Of of, int d) {
         if constexpr (MODE != ANY) {
-            const uint32_t start = MODE == WHOLE ? first() : Chunk<T>(first(), d).start;
+            uint32_t start = MODE == WHOLE ? first() : Chunk<T>(first(), d).start;
 #pragma unroll
-            for (int i = 0; i < A::kEach; ++i) at[i] = ((uint32_t)of(row(i)) + start) * (uint32_t)sizeof(T);
+            for (int i = 0; i < A::kEach; ++i) {
+                if (DIRECT) start = ((tile_at<T, D>(row(i), threadIdx.x % A::kChunks) >> 4) - row(i) * A::kChunks) * Tile<T>::E;
+                at[i] = ((uint32_t)of(row(i)) + start) * (uint32_t)sizeof(T);
+            }
         }
     }
-    // tile: its first row in memory, the same for all lanes
-    __device__ __forceinline__ void load(const T* tile) {
+    // from: the tile's first row in memory, the same for all lanes; to: the tile in LDS, which nobody reads now (DIRECT)
+    __device__ __forceinline__ void load(const T* from, char* to) {
+        if constexpr (DIRECT) {
+            const uint32_t run = __builtin_amdgcn_readfirstlane(
+                (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)to + (threadIdx.x >> 6) * 1024);
 #pragma unroll
-        for (int i = 0; i < A::kEach; ++i)
-            f[i] = load16(reinterpret_cast<const T*>(reinterpret_cast<const char*>(tile) + at[i]));
+            for (int i = 0; i < A::kEach; ++i)
+                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(run + i * 4096),
+                             "v"(at[i]), "s"(from)
+                             : "memory");
+        } else {
+#pragma unroll
+            for (int i = 0; i < A::kEach; ++i)
+                f[i] = load16(reinterpret_cast<const T*>(reinterpret_cast<const char*>(from) + at[i]));
+        }
     }
     // where(i): the tile's row i in memory
     template <typename Where>
@@ -209,25 +225,34 @@ struct Mover {
 #pragma unroll
         for (int i = 0; i < A::kEach; ++i) f[i] = chunk_load<T, ANY>(where(row(i)), c, first(), d);
     }
-    __device__ __forceinline__ void store(char* tile, uint64_t valid, int d) const {
+    // the loaded tile in LDS, zeros in rows that do not count
+    __device__ __forceinline__ void place(char* tile, uint64_t valid, int d) const {
+        if constexpr (DIRECT) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            if (valid == ~0ull >> (64 - A::kRows)) return;
+#pragma unroll
+            for (int i = 0; i < A::kEach; ++i)
+                if (!(valid >> row(i) & 1)) *reinterpret_cast<Frag*>(tile + (i * 256 + (int)threadIdx.x) * 16) = Frag{};
+            return;
+        }
         const int ch = threadIdx.x % A::kChunks;
         const Chunk<T> c(first(), d);
         if (MODE == WHOLE && valid == ~0ull >> (64 - A::kRows)) {
 #pragma unroll
-            for (int i = 0; i < A::kEach; ++i) *reinterpret_cast<Frag*>(tile + tile_at<T, D>(row(i), ch)) = f[i];
+            for (int i = 0; i < A::kEach; ++i) *reinterpret_cast<Frag*>(tile + tile_at<T, D>(row(i), ch)) = f[DIRECT ? 0 : i];
             return;
         }
 #pragma unroll
         for (int i = 0; i < A::kEach; ++i)
             *reinterpret_cast<Frag*>(tile + tile_at<T, D>(row(i), ch)) =
-                chunk_fixed<T, MODE>(f[i], c, d, valid >> row(i) & 1);
+                chunk_fixed<T, MODE>(f[DIRECT ? 0 : i], c, d, valid >> row(i) & 1);
     }
 };
 
 // Tiles of consecutive keys of one matrix.
-template <typename T, int D, int MODE>
+template <typename T, int D, int MODE, bool DIRECT = false>
 struct KeyTiles {
-    Mover<T, D, MODE> move;
+    Mover<T, D, MODE, DIRECT> move;
     const T* base;  // of key 0
     int64_t stride;
     int end;        // of the keys that may be read: past it, the last one is read again
@@ -235,13 +260,13 @@ struct KeyTiles {
         : base(static_cast<const T*>(p) + from), stride(stride_), end(end_) {
         move.aim([&](int i) { return (uint32_t)i * (uint32_t)stride; }, d);
     }
-    __device__ __forceinline__ void load(int key, int d) {
+    __device__ __forceinline__ void load(int key, int d, char* to) {
         if constexpr (MODE == ANY) {
             move.load_any([&](int i) { return base + (int64_t)min(key + i, end - 1) * stride; }, d);
         } else {
             if (key + AttnTile<T, D>::kRows > end)
                 move.aim([&](int i) { return (uint32_t)min(i, end - 1 - key) * (uint32_t)stride; }, d);
-            move.load(base + key * stride);
+            move.load(base + key * stride, to);
         }
     }
 };
@@ -385,9 +410,9 @@ __device__ __forceinline__ void rows_held(const AttnArgs& p, int b, int hk, int 
 }
 
 // Tiles of consecutive rows of a problem, of q or dout.
-template <typename T, int D, int MODE>
+template <typename T, int D, int MODE, bool DIRECT = false>
 struct RowTiles {
-    Mover<T, D, MODE> move;
+    Mover<T, D, MODE, DIRECT> move;
     const T* base;  // of the problem's first head
     int64_t s_n, s_h;
     __device__ __forceinline__ RowTiles(const AttnArgs& p, int b, int hk, const void* from, int64_t s_b, int64_t s_n_,
@@ -396,7 +421,7 @@ struct RowTiles {
         if (p.group == 1) move.aim([&](int i) { return (uint32_t)i * (uint32_t)s_n; }, p.d);
     }
     // rows from row0 on; past the last live one it is read again
-    __device__ __forceinline__ void load(const AttnArgs& p, int row0, int live) {
+    __device__ __forceinline__ void load(const AttnArgs& p, int row0, int live, char* to) {
         if constexpr (MODE == ANY) {
             move.load_any([&](int i) {
                 const Row w(p, 0, min(row0 + i, live - 1), true);
@@ -405,14 +430,14 @@ struct RowTiles {
         } else if (p.group == 1) {
             if (row0 + AttnTile<T, D>::kRows > live)
                 move.aim([&](int i) { return (uint32_t)min(i, live - 1 - row0) * (uint32_t)s_n; }, p.d);
-            move.load(base + row0 * s_n);
+            move.load(base + row0 * s_n, to);
         } else {
             const int first = (int)divided((uint32_t)row0, p.by_group), in = row0 - first * p.group;
             move.aim([&](int i) {
                 const uint32_t row = in + min(i, live - 1 - row0), query = divided(row, p.by_group);
                 return query * (uint32_t)s_n + (row - query * p.group) * (uint32_t)s_h;
             }, p.d);
-            move.load(base + first * s_n);
+            move.load(base + first * s_n, to);
         }
     }
 };

@@ -75,8 +75,8 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDq)) void k_attn_dq(Attn
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Keys keys(p, at.b);
     const int first = at.split * p.per;
-    KeyTiles<T, D, MODE> tile_k(p.k, at.b * p.k_b + at.hk * p.k_h, p.k_n, keys.count, p.d);
-    KeyTiles<T, D, MODE> tile_v(p.v, at.b * p.v_b + at.hk * p.v_h, p.v_n, keys.count, p.d);
+    KeyTiles<T, D, MODE, MODE == WHOLE> tile_k(p.k, at.b * p.k_b + at.hk * p.k_h, p.k_n, keys.count, p.d);
+    KeyTiles<T, D, MODE, MODE == WHOLE> tile_v(p.v, at.b * p.v_b + at.hk * p.v_h, p.v_n, keys.count, p.d);
     keys.until(first + p.per);
     const int rows = p.nq * p.group, live = live_rows(p, at.b);
     const int row0 = (at.tile * 4 + wave) * 16 * QC;
@@ -85,8 +85,8 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDq)) void k_attn_dq(Attn
     int byte = 0;
     if (tiles > 0) {
         byte = keys.byte(first, lane);
-        tile_k.load(first, p.d);
-        tile_v.load(first, p.d);
+        tile_k.load(first, p.d, s_k[0]);
+        tile_v.load(first, p.d, s_v[0]);
     }
 
     Frag q[QC][A::kSteps], dout[QC][A::kSteps];
@@ -117,17 +117,17 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDq)) void k_attn_dq(Attn
     uint64_t valid = 0;
     if (tiles > 0) {
         valid = key_bits<KT>(byte);
-        tile_k.move.store(s_k[0], valid, p.d);
-        tile_v.move.store(s_v[0], valid, p.d);
+        tile_k.move.place(s_k[0], valid, p.d);
+        tile_v.move.place(s_v[0], valid, p.d);
     }
     for (int t = 0; t < tiles; ++t) {
+        __syncthreads();
         if (t + 1 < tiles) {
             const int next = first + (t + 1) * KT;
             byte = keys.byte(next, lane);
-            tile_k.load(next, p.d);
-            tile_v.load(next, p.d);
+            tile_k.load(next, p.d, s_k[(t + 1) & 1]);
+            tile_v.load(next, p.d, s_v[(t + 1) & 1]);
         }
-        __syncthreads();
         const char* tk = s_k[t & 1];
         const char* tv = s_v[t & 1];
 #pragma unroll
@@ -203,8 +203,8 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDq)) void k_attn_dq(Attn
         }
         if (t + 1 < tiles) {
             valid = key_bits<KT>(byte);
-            tile_k.move.store(s_k[(t + 1) & 1], valid, p.d);
-            tile_v.move.store(s_v[(t + 1) & 1], valid, p.d);
+            tile_k.move.place(s_k[(t + 1) & 1], valid, p.d);
+            tile_v.move.place(s_v[(t + 1) & 1], valid, p.d);
         }
     }
     if (!p.dq) return;
@@ -289,12 +289,12 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDkv)) void k_attn_dkv(At
     const int key0 = (at.tile * 4 + wave) * 16 * KC;
     const float c2 = fabsf(p.scale) * kLog2e;
     const int tiles = keys.count > at.tile * 64 * KC ? (live - first + RT - 1) / RT : 0;
-    RowTiles<T, D, MODE> tile_q(p, at.b, at.hk, p.q, p.q_b, p.q_n, p.q_h);
-    RowTiles<T, D, MODE> tile_g(p, at.b, at.hk, p.dout, p.g_b, p.g_n, p.g_h);
+    RowTiles<T, D, MODE, MODE == WHOLE> tile_q(p, at.b, at.hk, p.q, p.q_b, p.q_n, p.q_h);
+    RowTiles<T, D, MODE, MODE == WHOLE> tile_g(p, at.b, at.hk, p.dout, p.g_b, p.g_n, p.g_h);
     float next_lse = 0.f, next_delta = 0.f;
-    auto fetch = [&](int row0) {
-        tile_q.load(p, row0, live);
-        tile_g.load(p, row0, live);
+    auto fetch = [&](int row0, int buffer) {
+        tile_q.load(p, row0, live, s_q[buffer]);
+        tile_g.load(p, row0, live, s_g[buffer]);
         if (threadIdx.x < RT) {
             const int row = row0 + (int)threadIdx.x;
             const int64_t stat = Row(p, at.hk, row, row < live).stat(p, at.b);
@@ -303,14 +303,14 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDkv)) void k_attn_dkv(At
         }
     };
     auto place = [&](int buffer, uint64_t valid) {
-        tile_q.move.store(s_q[buffer], valid, p.d);
-        tile_g.move.store(s_g[buffer], valid, p.d);
+        tile_q.move.place(s_q[buffer], valid, p.d);
+        tile_g.move.place(s_g[buffer], valid, p.d);
         if (threadIdx.x < RT)
             s_lse[buffer][threadIdx.x] = next_lse * kLog2e, s_delta[buffer][threadIdx.x] = next_delta;
     };
     // the tile's rows that count
     auto bits = [&](int row0) { return ~0ull >> (64 - min(RT, live - row0)); };
-    if (tiles > 0) fetch(first);
+    if (tiles > 0) fetch(first, 0);
 
     Frag k[KC][A::kSteps], v[KC][A::kSteps];
     bool counts[KC];
@@ -341,8 +341,8 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDkv)) void k_attn_dkv(At
         place(0, valid);
     }
     for (int t = 0; t < tiles; ++t) {
-        if (t + 1 < tiles) fetch(first + (t + 1) * RT);
         __syncthreads();
+        if (t + 1 < tiles) fetch(first + (t + 1) * RT, (t + 1) & 1);
         const char* tq = s_q[t & 1];
         const char* tg = s_g[t & 1];
 #pragma unroll
@@ -493,9 +493,9 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::occ_held(KC))) void k_attn_h
     RowTiles<T, D, MODE> tile_o(p, at.b, at.hk, p.out, d * p.heads * p.nq, d * p.heads, d);
     float next_lse = 0.f;
     auto fetch = [&](int row0) {
-        tile_q.load(p, row0, live);
-        tile_g.load(p, row0, live);
-        tile_o.load(p, row0, live);
+        tile_q.load(p, row0, live, nullptr);
+        tile_g.load(p, row0, live, nullptr);
+        tile_o.load(p, row0, live, nullptr);
         if (threadIdx.x < RT) {
             const int row = row0 + (int)threadIdx.x;
             next_lse = p.lse[Row(p, at.hk, row, row < live).stat(p, at.b)];
@@ -544,8 +544,8 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::occ_held(KC))) void k_attn_h
     for (int t = 0; t < tiles; ++t) {
         const int row0 = first + t * RT;
         const uint64_t valid = ~0ull >> (64 - min(RT, live - row0));
-        tile_q.move.store(s_q, valid, p.d);
-        tile_g.move.store(s_g, valid, p.d);
+        tile_q.move.place(s_q, valid, p.d);
+        tile_g.move.place(s_g, valid, p.d);
         {  // delta: a thread's chunks, then the threads of a row
             const Chunk<T> ch(tile_o.move.first(), p.d);
 #pragma unroll

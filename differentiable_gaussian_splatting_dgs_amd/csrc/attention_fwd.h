@@ -337,8 +337,8 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccFwd)) void k_attn_fwd(At
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Keys keys(p, at.b);
     const int first = at.split * p.per;
-    KeyTiles<T, D, MODE> tile_k(p.k, at.b * p.k_b + at.hk * p.k_h, p.k_n, keys.count, p.d);
-    KeyTiles<T, D, MODE> tile_v(p.v, at.b * p.v_b + at.hk * p.v_h, p.v_n, keys.count, p.d);
+    KeyTiles<T, D, MODE, MODE == WHOLE> tile_k(p.k, at.b * p.k_b + at.hk * p.k_h, p.k_n, keys.count, p.d);
+    KeyTiles<T, D, MODE, MODE == WHOLE> tile_v(p.v, at.b * p.v_b + at.hk * p.v_h, p.v_n, keys.count, p.d);
     keys.until(first + p.per);
     const int live = live_rows(p, at.b);
     const int row0 = (at.tile * 4 + wave) * 16 * QC;
@@ -347,8 +347,8 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccFwd)) void k_attn_fwd(At
     int byte = 0;
     if (tiles > 0) {
         byte = keys.byte(first, lane);
-        tile_k.load(first, p.d);
-        tile_v.load(first, p.d);
+        tile_k.load(first, p.d, s_k[0]);
+        tile_v.load(first, p.d, s_v[0]);
     }
     Frag q[QC][A::kSteps];
     rows_held<T, MODE>(p, at.b, at.hk, row0, live, p.q, p.q_b, p.q_n, p.q_h, p.scale < 0.f, lane, q);
@@ -356,17 +356,17 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccFwd)) void k_attn_fwd(At
     bool first_keys = true;
     if (tiles > 0) {
         valid = key_bits<KT>(byte);
-        tile_k.move.store(s_k[0], valid, p.d);
-        tile_v.move.store(s_v[0], valid, p.d);
+        tile_k.move.place(s_k[0], valid, p.d);
+        tile_v.move.place(s_v[0], valid, p.d);
     }
     for (int t = 0; t < tiles; ++t) {
+        __syncthreads();
         if (t + 1 < tiles) {
             const int next = first + (t + 1) * KT;
             byte = keys.byte(next, lane);
-            tile_k.load(next, p.d);
-            tile_v.load(next, p.d);
+            tile_k.load(next, p.d, s_k[(t + 1) & 1]);
+            tile_v.load(next, p.d, s_v[(t + 1) & 1]);
         }
-        __syncthreads();
         const char* tk = s_k[t & 1];
         const char* tv = s_v[t & 1];
         any |= valid;
@@ -390,8 +390,8 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccFwd)) void k_attn_fwd(At
         }
         if (t + 1 < tiles) {
             valid = key_bits<KT>(byte);
-            tile_k.move.store(s_k[(t + 1) & 1], valid, p.d);
-            tile_v.move.store(s_v[(t + 1) & 1], valid, p.d);
+            tile_k.move.place(s_k[(t + 1) & 1], valid, p.d);
+            tile_v.move.place(s_v[(t + 1) & 1], valid, p.d);
         }
     }
     float m[QC], l[QC];
@@ -452,12 +452,12 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccThin)) void k_attn_thin(
         char* to = s_mem + 2 * h * tiles * A::kBytes;
         for (int t = 0; t < tiles; ++t) {
             const int byte = keys.byte(t * KT, lane);
-            tile_k.load(t * KT, p.d);
-            tile_v.load(t * KT, p.d);
+            tile_k.load(t * KT, p.d, nullptr);
+            tile_v.load(t * KT, p.d, nullptr);
             const uint64_t valid = key_bits<KT>(byte);
             any |= valid;
-            tile_k.move.store(to + 2 * t * A::kBytes, valid, p.d);
-            tile_v.move.store(to + (2 * t + 1) * A::kBytes, valid, p.d);
+            tile_k.move.place(to + 2 * t * A::kBytes, valid, p.d);
+            tile_v.move.place(to + (2 * t + 1) * A::kBytes, valid, p.d);
             if (threadIdx.x == 0) s_valid[t] = valid;
         }
     }
