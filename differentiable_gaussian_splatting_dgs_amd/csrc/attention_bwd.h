@@ -75,14 +75,15 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDq)) void k_attn_dq(Attn
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Keys keys(p, at.b);
     const int first = at.split * p.per;
-    KeyTiles<T, D, MODE, MODE == WHOLE> tile_k(p.k, at.b * p.k_b + at.hk * p.k_h, p.k_n, keys.count, p.d);
-    KeyTiles<T, D, MODE, MODE == WHOLE> tile_v(p.v, at.b * p.v_b + at.hk * p.v_h, p.v_n, keys.count, p.d);
+    KeyTiles<T, D, MODE, direct(MODE)> tile_k(p.k, at.b * p.k_b + at.hk * p.k_h, p.k_n, keys.count, p.d);
+    KeyTiles<T, D, MODE, direct(MODE)> tile_v(p.v, at.b * p.v_b + at.hk * p.v_h, p.v_n, keys.count, p.d);
     keys.until(first + p.per);
     const int rows = p.nq * p.group, live = live_rows(p, at.b);
     const int row0 = (at.tile * 4 + wave) * 16 * QC;
     const float c2 = fabsf(p.scale) * kLog2e;
     const int tiles = p.dq && live > at.tile * 64 * QC ? (keys.count - first + KT - 1) / KT : 0;
     int byte = 0;
+    for (char* t : {s_k[0], s_k[1], s_v[0], s_v[1]}) tile_k.move.blank(t, p.d);
     if (tiles > 0) {
         byte = keys.byte(first, lane);
         tile_k.load(first, p.d, s_k[0]);
@@ -289,8 +290,8 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDkv)) void k_attn_dkv(At
     const int key0 = (at.tile * 4 + wave) * 16 * KC;
     const float c2 = fabsf(p.scale) * kLog2e;
     const int tiles = keys.count > at.tile * 64 * KC ? (live - first + RT - 1) / RT : 0;
-    RowTiles<T, D, MODE, MODE == WHOLE> tile_q(p, at.b, at.hk, p.q, p.q_b, p.q_n, p.q_h);
-    RowTiles<T, D, MODE, MODE == WHOLE> tile_g(p, at.b, at.hk, p.dout, p.g_b, p.g_n, p.g_h);
+    RowTiles<T, D, MODE, direct(MODE)> tile_q(p, at.b, at.hk, p.q, p.q_b, p.q_n, p.q_h);
+    RowTiles<T, D, MODE, direct(MODE)> tile_g(p, at.b, at.hk, p.dout, p.g_b, p.g_n, p.g_h);
     float next_lse = 0.f, next_delta = 0.f;
     auto fetch = [&](int row0, int buffer) {
         tile_q.load(p, row0, live, s_q[buffer]);
@@ -308,6 +309,7 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDkv)) void k_attn_dkv(At
         if (threadIdx.x < RT)
             s_lse[buffer][threadIdx.x] = next_lse * kLog2e, s_delta[buffer][threadIdx.x] = next_delta;
     };
+    for (char* t : {s_q[0], s_q[1], s_g[0], s_g[1]}) tile_q.move.blank(t, p.d);
     // the tile's rows that count
     auto bits = [&](int row0) { return ~0ull >> (64 - min(RT, live - row0)); };
     if (tiles > 0) fetch(first, 0);
@@ -1035,7 +1037,8 @@ void attn_bwd_at(const AttnArgs& p, void* workspace, hipStream_t s) {
         if (mode == WHOLE) attn_bwd_in<T, D, WHOLE>(p, workspace, s);
         else if (mode == ANY) attn_bwd_in<T, D, ANY>(p, workspace, s);
     }
-    if (mode == PART) attn_bwd_in<T, D, PART>(p, workspace, s);
+    if (mode == EVEN) attn_bwd_in<T, D, EVEN>(p, workspace, s);
+    else if (mode == PART) attn_bwd_in<T, D, PART>(p, workspace, s);
 }
 
 template <typename T>

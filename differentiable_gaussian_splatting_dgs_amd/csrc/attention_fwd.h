@@ -337,14 +337,15 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccFwd)) void k_attn_fwd(At
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Keys keys(p, at.b);
     const int first = at.split * p.per;
-    KeyTiles<T, D, MODE, MODE == WHOLE> tile_k(p.k, at.b * p.k_b + at.hk * p.k_h, p.k_n, keys.count, p.d);
-    KeyTiles<T, D, MODE, MODE == WHOLE> tile_v(p.v, at.b * p.v_b + at.hk * p.v_h, p.v_n, keys.count, p.d);
+    KeyTiles<T, D, MODE, direct(MODE)> tile_k(p.k, at.b * p.k_b + at.hk * p.k_h, p.k_n, keys.count, p.d);
+    KeyTiles<T, D, MODE, direct(MODE)> tile_v(p.v, at.b * p.v_b + at.hk * p.v_h, p.v_n, keys.count, p.d);
     keys.until(first + p.per);
     const int live = live_rows(p, at.b);
     const int row0 = (at.tile * 4 + wave) * 16 * QC;
     const int tiles = live > at.tile * 64 * QC ? (keys.count - first + KT - 1) / KT : 0;
     uint64_t valid = 0, any = 0;
     int byte = 0;
+    for (char* t : {s_k[0], s_k[1], s_v[0], s_v[1]}) tile_k.move.blank(t, p.d);
     if (tiles > 0) {
         byte = keys.byte(first, lane);
         tile_k.load(first, p.d, s_k[0]);
@@ -557,7 +558,8 @@ void attn_fwd_at(const AttnArgs& p, void* workspace, hipStream_t s) {
         if (mode == WHOLE) attn_fwd_in<T, D, WHOLE>(p, workspace, s);
         else if (mode == ANY) attn_fwd_in<T, D, ANY>(p, workspace, s);
     }
-    if (mode == PART) attn_fwd_in<T, D, PART>(p, workspace, s);
+    if (mode == EVEN) attn_fwd_in<T, D, EVEN>(p, workspace, s);
+    else if (mode == PART) attn_fwd_in<T, D, PART>(p, workspace, s);
 }
 
 // Bytes of workspace, by sizes alone: what either way to read the rows asks for.
