@@ -62,17 +62,19 @@ struct AttnTile {
 template <typename T, int D>
 struct AttnShape {
     static constexpr bool kHalf = sizeof(T) == 2;
-    static constexpr int kFwd = kHalf ? (D <= 64 ? 4 : D <= 128 ? 2 : 1) : D <= 128 ? 2 : 1;
+    static constexpr int kFwd = kHalf ? (D <= 64 ? 4 : D <= 128 ? 2 : 1) : D <= 96 ? 2 : 1;
     static constexpr int kDq = kHalf ? (D <= 128 ? 2 : 1) : D <= 64 ? 2 : 1;
     static constexpr int kDkv = kHalf ? (D <= 128 ? 2 : 1) : D <= 64 ? 2 : 1;
     static constexpr int kThin = D <= 32 ? (kHalf ? 4 : 2) : D <= 128 ? (kHalf ? 2 : 1) : 1;
     static constexpr int kOccThin = D * (int)sizeof(T) >= 512 ? 1 : 2;
-    static constexpr int kOccFwd = D * (int)sizeof(T) >= 512 ? 1 : 2;
-    static constexpr int kOccDq = D * (int)sizeof(T) >= 512 ? 1 : 2;
+    static constexpr int kOccFwd = D * (int)sizeof(T) >= 1024 ? 1 : 2;
+    static constexpr int kOccDq = D * (int)sizeof(T) >= 1024 ? 1 : 2;
     static constexpr int kHeld = kHalf ? (D <= 64 ? 4 : D <= 128 ? 2 : 1) : D <= 32 ? 4 : D <= 64 ? 2 : 1;
     // by the registers of keys, values, their gradients and a step's logits; the rest takes some 130
     static constexpr int occ_held(int kc) { return kc * (kHalf ? D / 2 + D / 4 + 16 : D + 8) <= 80 ? 2 : 1; }
-    static constexpr int kOccDkv = D * (int)sizeof(T) >= (kHalf ? 192 : 256) ? 1 : 2;
+    // by the registers of keys, values and their gradients, and what may spill: bfloat16, 30k x 600 of 160 320 us at one
+    // wave and 167 at two, 64k x 1024 of 128 (192 registers) 400 and 848
+    static constexpr int kOccDkv = kDkv * D * (kHalf ? 3 : 4) <= 576 ? 2 : 1;
 };
 
 // Keys that a wave takes at a time where rows are few: what 32 registers hold of them.
