@@ -25,7 +25,7 @@ namespace gs {
 
 constexpr int kHeadsApart = 65536;     // keys from which few rows' heads go to the waves of a block
 constexpr int kThinBlocks = 512;       // that keep their keys: two a CU
-constexpr int kThinTiles = 16;           // tiles of keys that a block keeps in LDS, at most
+constexpr int kThinTiles = 16;         // tiles of keys that a block keeps in LDS, at most
 constexpr int kThinBytes = 64 * 1024;  // and their bytes: two blocks a CU
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -58,7 +58,10 @@ struct AttnTile {
 };
 
 // 16-row tiles of queries, and of keys, that a wave holds: each more is one more use of what a wave reads from LDS,
-// for as many registers as a wave has at kOcc* waves a SIMD.
+// for as many registers as a wave has at kOcc* waves a SIMD (512 in all).  bfloat16, 64k rows on 1024 keys of 128: dq
+// takes 326 us with one tile, which LDS bounds (a fragment of 1 KB a product), 240 with two, though 60 bytes a lane spill;
+// float32 products take four times as long for a fragment and want the second wave more: 20k rows on 512 keys of 128,
+// forward 262 us with two tiles at one wave, 232 at two, 205 with one tile at two.
 template <typename T, int D>
 struct AttnShape {
     static constexpr bool kHalf = sizeof(T) == 2;
@@ -69,9 +72,9 @@ struct AttnShape {
     static constexpr int kOccThin = D * (int)sizeof(T) >= 512 ? 1 : 2;
     static constexpr int kOccFwd = D * (int)sizeof(T) >= 1024 ? 1 : 2;
     static constexpr int kOccDq = D * (int)sizeof(T) >= 1024 ? 1 : 2;
-    static constexpr int kHeld = kHalf ? (D <= 64 ? 4 : D <= 128 ? 2 : 1) : D <= 32 ? 4 : D <= 64 ? 2 : 1;
-    // by the registers of keys, values, their gradients and a step's logits; the rest takes some 130
-    static constexpr int occ_held(int kc) { return kc * (kHalf ? D / 2 + D / 4 + 16 : D + 8) <= 80 ? 2 : 1; }
+    static constexpr int kHeld = D <= (kHalf ? 128 : 64) ? 2 : 1;
+    // by the registers of keys, values, their gradients and a tile's logits; the rest takes some 130
+    static constexpr int occ_held(int kc) { return kc * ((kHalf ? D / 2 + D / 4 : D) + 32) <= 112 ? 2 : 1; }
     // by the registers of keys, values and their gradients, and what may spill: bfloat16, 30k x 600 of 160 320 us at one
     // wave and 167 at two, 64k x 1024 of 128 (192 registers) 400 and 848
     static constexpr int kOccDkv = kDkv * D * (kHalf ? 3 : 4) <= 576 ? 2 : 1;
@@ -300,6 +303,19 @@ __device__ __forceinline__ float over_groups(float v, F f) {
     return f(__builtin_bit_cast(float, s0), __builtin_bit_cast(float, s1));
 }
 
+// Sum over the 16 lanes of a group, in all of them.
+__device__ __forceinline__ float over_row(float v) {
+    auto turned = [](float v, auto by) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x120 + decltype(by)::value,
+                                                                     0xf, 0xf, true));  // row_ror
+    };
+    v += turned(v, std::integral_constant<int, 8>());
+    v += turned(v, std::integral_constant<int, 4>());
+    v += turned(v, std::integral_constant<int, 2>());
+    v += turned(v, std::integral_constant<int, 1>());
+    return v;
+}
+
 // A block's place: problem fastest, so that heads that share lines of memory run together, then the split, and each
 // XCD a band.
 struct Place {
@@ -499,13 +515,17 @@ AttnPlan plan_at(const AttnArgs& p) {
     AttnPlan a{};
     const int64_t problems = (int64_t)p.batch * p.kv_heads, rows = (int64_t)p.nq * p.group;
     const size_t row_part = (size_t)problems * rows * pitch_of(D) * 4, key_part = (size_t)problems * p.nk * pitch_of(D) * 4;
+    // Few rows: the waves share out the keys and meet at the end alone.  bfloat16, 8 rows on 1M keys of 8 heads of 32:
+    // 248 us, by the block kernel 298; 20 on 20k of 4 of 64 18.1 and 21.8; one view (1 on 256 of 4 of 64) 10.7 and 15.3,
+    // the latter two bound by the host.
     a.few = rows <= 16 ? 1 : rows <= 32 ? 2 : 0;
     a.fwd_qc = rows <= 64 * S::kFwd / 2 ? 1 : S::kFwd;
     a.dq_qc = rows <= 64 * S::kDq / 2 ? 1 : S::kDq;
     a.dkv_kc = p.nk <= 64 * S::kDkv / 2 ? 1 : S::kDkv;
     if (a.few) split(p.nk, problems, 1024, 512, 4 * FewTile<T, D>::kKeys, a.fwd_splits, a.fwd_per);
     else split(p.nk, problems * tiles_of(rows, 64 * a.fwd_qc), 512, 512, AttnTile<T, D>::kRows, a.fwd_splits, a.fwd_per);
-    // few keys and rows for two tiles a wave: blocks that keep the keys
+    // few keys and rows for two tiles a wave: blocks that keep the keys.  float16, 1M rows on 64 keys of 4 heads of 32:
+    // 142 us, by blocks of a tile of rows each 167
     const int64_t key_tiles = tiles_of(p.nk, AttnTile<T, D>::kRows);
     if (!a.few && a.fwd_splits == 1 && key_tiles <= kThinTiles && key_tiles * 2 * AttnTile<T, D>::kBytes <= kThinBytes) {
         while (a.together < 2 && p.kv_heads % (2 << a.together) == 0 &&
@@ -515,7 +535,10 @@ AttnPlan plan_at(const AttnArgs& p) {
         if (blocks >= 2 * each) a.thin = (int)each;
     }
     split(p.nk, problems * tiles_of(rows, 64 * a.dq_qc), 512, 256, AttnTile<T, D>::kRows, a.dq_splits, a.dq_per);
+    // 512 blocks are two a CU, what LDS and registers hold: more splits are more to join
     split(rows, problems * tiles_of(p.nk, 64 * a.dkv_kc), 512, 256, AttnTile<T, D>::kRows, a.dkv_splits, a.dkv_per);
+    // the backward of few rows in one pass over the keys: 8 rows on 1M keys of 8 heads of 32 bfloat16, with the forward,
+    // 869 us, by dq's and dkv's kernels 1170
     a.few_back = a.few == 2 && sizeof(T) == 4 && D > 128 ? 0 : a.few;  // their tiles fill LDS
     // heads of at most a line of memory: a wave each.  1M keys of 8 heads of 32 bfloat16 848 us against 896 (forward
     // and backward), 200k of 4 of 64 162 against 175; of 128 326 against 335, and its tiles in LDS leave room for less
@@ -523,7 +546,9 @@ AttnPlan plan_at(const AttnArgs& p) {
         while (a.few_heads < 2 && p.kv_heads % (2 << a.few_heads) == 0) ++a.few_heads;
     split(p.nk, problems >> a.few_heads, 1024, 64 * (4 >> a.few_heads), Tile<T>::KS * (4 >> a.few_heads),
           a.few_splits, a.few_per);
-    a.held = p.nk < 1 || a.few_back ? 0 : p.nk <= 64 ? 1 : p.nk <= 128 ? 2 : p.nk <= 256 ? 4 : 0;
+    // few keys: both kernels' work in one pass over the rows.  1M rows on 64 keys of 4 heads of 32 bfloat16, with the
+    // forward, 446 us against 665; 100k on 256 of 64 468 against 377, so it stops at 128 keys
+    a.held = p.nk < 1 || a.few_back ? 0 : p.nk <= 64 ? 1 : p.nk <= 128 ? 2 : 0;
     if (a.held > S::kHeld) a.held = 0;
     split(rows, problems, 512, 4 * AttnTile<T, D>::kRows, AttnTile<T, D>::kRows, a.held_splits, a.held_per);
     if (a.fwd_splits > 1) a.fwd_bytes = padded(row_part * a.fwd_splits) + padded(row_part / pitch_of(D) * 2 * a.fwd_splits);

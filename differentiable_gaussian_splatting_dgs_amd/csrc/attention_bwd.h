@@ -464,12 +464,13 @@ __device__ __forceinline__ typename Tile<T>::Frag across_frag(const char* tile, 
 
 // The gradients where a block holds all keys of a problem (64 KC of them at most), 16 KC a wave, and walks the rows of
 // its split.  ds goes through LDS, keys down and rows across, and comes back as the fragments of dq: s, P and ds are
-// made once, q, dout and out are read once and dq is written once.  delta is made where out passes by.
+// made once, q and dout are read once and dq is written once.  delta is the sum of P dP over all keys, which the waves
+// exchange in LDS: so out is not read, and its rounding, which would be a rounding of every ds of a row, is not in it.
 template <typename T, int D, int KC>
 struct HeldTile {
     static constexpr int kRows = AttnTile<T, D>::kRows, kKeys = 64 * KC;
     static constexpr int kDs = kKeys * kRows * (int)sizeof(T), kKeyBytes = kKeys * pitch_of(D) * (int)sizeof(T);
-    static constexpr int kBytes = 2 * AttnTile<T, D>::kBytes + kDs + kKeyBytes + 2 * kRows * 4;
+    static constexpr int kBytes = 2 * AttnTile<T, D>::kBytes + kDs + kKeyBytes + 5 * kRows * 4;
 };
 
 template <typename T, int D, int KC, int MODE>
@@ -480,7 +481,7 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::occ_held(KC))) void k_attn_h
     constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG, RT = A::kRows, NG = A::kGroups;
     extern __shared__ __align__(16) char s_mem[];
     char *s_q = s_mem, *s_g = s_q + A::kBytes, *s_k = s_g + A::kBytes, *s_ds = s_k + H::kKeyBytes;
-    float *s_lse = reinterpret_cast<float*>(s_ds + H::kDs), *s_delta = s_lse + RT;
+    float *s_lse = reinterpret_cast<float*>(s_ds + H::kDs), *s_sum = s_lse + RT;  // the waves' sums of P dP
     const Place at(p);
     if (at.none) return;
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
@@ -492,12 +493,10 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::occ_held(KC))) void k_attn_h
     const int64_t d = p.d;
     RowTiles<T, D, MODE> tile_q(p, at.b, at.hk, p.q, p.q_b, p.q_n, p.q_h);
     RowTiles<T, D, MODE> tile_g(p, at.b, at.hk, p.dout, p.g_b, p.g_n, p.g_h);
-    RowTiles<T, D, MODE> tile_o(p, at.b, at.hk, p.out, d * p.heads * p.nq, d * p.heads, d);
     float next_lse = 0.f;
     auto fetch = [&](int row0) {
         tile_q.load(p, row0, live, nullptr);
         tile_g.load(p, row0, live, nullptr);
-        tile_o.load(p, row0, live, nullptr);
         if (threadIdx.x < RT) {
             const int row = row0 + (int)threadIdx.x;
             next_lse = p.lse[Row(p, at.hk, row, row < live).stat(p, at.b)];
@@ -548,26 +547,12 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::occ_held(KC))) void k_attn_h
         const uint64_t valid = ~0ull >> (64 - min(RT, live - row0));
         tile_q.move.place(s_q, valid, p.d);
         tile_g.move.place(s_g, valid, p.d);
-        {  // delta: a thread's chunks, then the threads of a row
-            const Chunk<T> ch(tile_o.move.first(), p.d);
-#pragma unroll
-            for (int i = 0; i < A::kEach; ++i) {
-                const Frag a = chunk_fixed<T, MODE>(tile_o.move.f[i], ch, p.d, true);
-                const Frag b = chunk_fixed<T, MODE>(tile_g.move.f[i], ch, p.d, true);
-                float sum = 0.f;
-#pragma unroll
-                for (int j = 0; j < E; ++j) sum = fmaf((float)a[j], (float)b[j], sum);
-#pragma unroll
-                for (int o = 1; o < A::kChunks; o <<= 1) sum += __shfl_xor(sum, o, 64);
-                if (threadIdx.x % A::kChunks == 0) s_delta[tile_o.move.row(i)] = sum;
-            }
-            if (threadIdx.x < RT) s_lse[threadIdx.x] = next_lse * kLog2e;
-        }
+        if (threadIdx.x < RT) s_lse[threadIdx.x] = next_lse * kLog2e;
         __syncthreads();
         if (t + 1 < tiles) fetch(row0 + RT);
+        f32x4 s[NG][KC][TG] = {}, dp[NG][KC][TG] = {};
 #pragma unroll
         for (int rg = 0; rg < NG; ++rg) {
-            f32x4 s[KC][TG] = {}, dp[KC][TG] = {};
 #pragma unroll
             for (int u = 0; u < TG; ++u)
 #pragma unroll
@@ -576,22 +561,18 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::occ_held(KC))) void k_attn_h
                     const Frag b = row_frag<T, D>(s_g, rg * KS + out_row<T>(u, r), e, g);
 #pragma unroll
                     for (int c = 0; c < KC; ++c) {
-                        mma(s[c][u], a, k[c][e]);
-                        mma(dp[c][u], b, v[c][e]);
+                        mma(s[rg][c][u], a, k[c][e]);
+                        mma(dp[rg][c][u], b, v[c][e]);
                     }
                 }
 #pragma unroll
             for (int u = 0; u < TG; ++u) {
                 const f32x4 lse = *reinterpret_cast<const f32x4*>(&s_lse[rg * KS + E * g + 4 * u]);
-                const f32x4 delta = *reinterpret_cast<const f32x4*>(&s_delta[rg * KS + E * g + 4 * u]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int c = 0; c < KC; ++c) {
-                        const float w = __builtin_amdgcn_exp2f(fmaf(s[c][u][j], c2, shrink.shift - lse[j]));
-                        s[c][u][j] = w;
-                        dp[c][u][j] = w * (dp[c][u][j] - delta[j]);
-                    }
+                    for (int c = 0; c < KC; ++c)
+                        s[rg][c][u][j] = __builtin_amdgcn_exp2f(fmaf(s[rg][c][u][j], c2, shrink.shift - lse[j]));
             }
             // rows and keys that do not count
 #pragma unroll
@@ -602,9 +583,36 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::occ_held(KC))) void k_attn_h
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const bool in = counts[c] && (valid >> (rg * KS + E * g + 4 * u + j) & 1);
-                            s[c][u][j] = in ? s[c][u][j] : 0.f;
-                            dp[c][u][j] = in ? dp[c][u][j] : 0.f;
+                            s[rg][c][u][j] = in ? s[rg][c][u][j] : 0.f;
+                            dp[rg][c][u][j] = in ? dp[rg][c][u][j] : 0.f;
                         }
+            const float by = __builtin_amdgcn_exp2f(-shrink.shift);
+#pragma unroll
+            for (int u = 0; u < TG; ++u) {
+                f32x4 sum = s[rg][0][u] * dp[rg][0][u];
+#pragma unroll
+                for (int c = 1; c < KC; ++c)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) sum[j] = fmaf(s[rg][c][u][j], dp[rg][c][u][j], sum[j]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum[j] = over_row(sum[j]) * by;
+                if (r == 0) *reinterpret_cast<f32x4*>(&s_sum[wave * RT + rg * KS + E * g + 4 * u]) = sum;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int rg = 0; rg < NG; ++rg) {
+#pragma unroll
+            for (int u = 0; u < TG; ++u) {
+                const float* sums = s_sum + rg * KS + E * g + 4 * u;
+                f32x4 delta = *reinterpret_cast<const f32x4*>(sums);
+#pragma unroll
+                for (int i = 1; i < 4; ++i) delta += *reinterpret_cast<const f32x4*>(sums + i * RT);
+#pragma unroll
+                for (int c = 0; c < KC; ++c)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) dp[rg][c][u][j] = s[rg][c][u][j] * (dp[rg][c][u][j] - delta[j]);
+            }
             float most = 0.f;
             if constexpr (Shrink<T>::kNeeded)
 #pragma unroll
@@ -612,12 +620,16 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::occ_held(KC))) void k_attn_h
 #pragma unroll
                     for (int u = 0; u < TG; ++u)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) most = fmaxf(most, fabsf(dp[c][u][j]));
+                        for (int j = 0; j < 4; ++j) most = fmaxf(most, fabsf(dp[rg][c][u][j]));
             shrink(most, [&](float f) {
 #pragma unroll
                 for (int c = 0; c < KC; ++c) {
 #pragma unroll
-                    for (int u = 0; u < TG; ++u) s[c][u] *= f, dp[c][u] *= f;
+                    for (int u = 0; u < TG; ++u) {
+                        dp[rg][c][u] *= f;
+#pragma unroll
+                        for (int i = 0; i < NG; ++i) s[i][c][u] *= f;  // the next groups' too
+                    }
 #pragma unroll
                     for (int e = 0; e < A::kPairs; ++e)
 #pragma unroll
@@ -631,7 +643,7 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::occ_held(KC))) void k_attn_h
 #pragma unroll
                 for (int u = 0; u < TG; ++u)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) w[c][4 * u + j] = (T)s[c][u][j], ds[c][4 * u + j] = (T)dp[c][u][j];
+                    for (int j = 0; j < 4; ++j) w[c][4 * u + j] = (T)s[rg][c][u][j], ds[c][4 * u + j] = (T)dp[rg][c][u][j];
                 *reinterpret_cast<Frag*>(s_ds + tile_at<T, RT>((wave * KC + c) * 16 + r, 4 * rg + g)) = ds[c];
             }
 #pragma unroll
@@ -1006,9 +1018,11 @@ void attn_bwd_in(AttnArgs p, void* workspace, hipStream_t s) {
     if (a.held && p.nq > 0 && MODE != ANY) {
         constexpr int kMost = AttnShape<T, D>::kHeld, kMode = MODE == ANY ? PART : MODE;
         p.splits = a.held_splits, p.per = a.held_per, p.tiles = 1;
-        if (a.held == 1) hipLaunchKernelGGL((k_attn_held<T, D, 1, kMode>), grid_of(p), dim3(256), (HeldTile<T, D, 1>::kBytes), s, p);
-        else if (a.held == 2) hipLaunchKernelGGL((k_attn_held<T, D, (kMost < 2 ? kMost : 2), kMode>), grid_of(p), dim3(256), (HeldTile<T, D, (kMost < 2 ? kMost : 2)>::kBytes), s, p);
-        else hipLaunchKernelGGL((k_attn_held<T, D, kMost, kMode>), grid_of(p), dim3(256), (HeldTile<T, D, kMost>::kBytes), s, p);
+        const dim3 grid = grid_of(p);
+        if (a.held == 1)
+            hipLaunchKernelGGL((k_attn_held<T, D, 1, kMode>), grid, dim3(256), (HeldTile<T, D, 1>::kBytes), s, p);
+        else
+            hipLaunchKernelGGL((k_attn_held<T, D, kMost, kMode>), grid, dim3(256), (HeldTile<T, D, kMost>::kBytes), s, p);
         if (p.splits > 1 && (p.dk || p.dv)) GS_ATTN_SHARED(k_attn_sum, 2 * problems * p.nk, , true);
         return;
     }
