@@ -7,6 +7,9 @@ a time step) or views (an appearance code per camera); by cross attention one re
 the other.  Its outputs go to `gs.rasterize` and its gradients come back through it.
 Plumbing over the C ABI (gs_linear_*, gs_layer_norm_*, gs_attention_*, gs_dropout,
 gs_grad_*, gs_adam_step_clipped): buffers and the order of the calls.
+
+Record a backward pass into a graph while no eager autograd graph of the same leaves
+is alive: the recording may end the process otherwise.
 """
 from __future__ import annotations
 
