@@ -428,3 +428,14 @@ def test_many_heads_of_one_row(nq, nk, group):
         check(first, b, (i, nq, group))
         for part in a.split(1 << 18, 1):
             assert torch.equal(part, first[:, :1].expand_as(part)), (i, nq, group)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("nk", [1, 64, 65, 128, 129])
+@pytest.mark.parametrize("d", [20, 32, 40, 48, 96, 128, 192, 256])
+def test_few_keys(d, nk, dtype):
+    """The backward's rule on few keys from either side, at every width of the products, with rows past the length, keys
+    that do not count and heads that share them."""
+    for kind in ("all", "both"):
+        size = (2, 75, nk, 4, 2, d)
+        compare(*inputs(size, dtype), valid_of(kind, size))
