@@ -944,6 +944,8 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_at
                         a[4 * t + j] = (T)(gk[u][t][j] * (by * p.scale));
                         b[4 * t + j] = (T)(gv[u][t][j] * by);
                     }
+                // a key that does not count: its weights of 0 times an infinite row are NaN
+                if (valid != ~0ull >> (64 - KS) && !(valid >> (16 * u + r) & 1)) a = Frag{}, b = Frag{};
                 if (key < end) {  // the others are cleared below, by other lanes
                     if (p.dk) store_run(dk_base + key * out_n, KS * e + E * g, p.d, a);
                     if (p.dv) store_run(dv_base + key * out_n, KS * e + E * g, p.d, b);

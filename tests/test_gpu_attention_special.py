@@ -37,3 +37,20 @@ def test_keys_past_the_length_have_zero_gradients_beside_infinite_rows(size, sca
                 assert not bits(grad[b, int(k_lengths[b]):]).any()
         first = first or got
         assert all(torch.equal(bits(x), bits(y)) for x, y in zip(first, got))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("scale", [0.125, -0.125])
+@pytest.mark.parametrize("size", FEW + [(2, 70, 100, 4, 2, 40), (2, 70, 300, 4, 2, 40), (1, 70, 200, 2, 1, 256)])
+def test_masked_keys_have_zero_gradients_beside_infinite_rows(size, scale, dtype):
+    """A key that its mask takes out has gradients of 0 whatever the rows hold that count: no 0 times infinity or NaN."""
+    batch, nq, nk = size[:3]
+    gen = torch.Generator(device="cuda").manual_seed(nk)
+    mask = torch.rand(batch, nk, generator=gen, device="cuda") < 0.6
+    for bad in (float("inf"), float("nan")):
+        for which in (0, 3):
+            ins = attention.inputs(size, dtype)
+            ins[which][:, nq - 1, 0, 1] = bad
+            got = attention.run(*ins, (mask, None, None), scale)
+            for grad in got[3:]:
+                assert not bits(grad[~mask]).any(), (bad, which)
