@@ -5,7 +5,8 @@
 
 namespace gs {
 
-// A forward's rows: the results, or those of a split.  o is relative to the reference m.
+// A forward's rows: the results, or those of a split.  o is relative to the reference m, which stays -infinity where no
+// logit is above it: no key counts (l = 0, of a split 0 too), all logits are -infinity (0, -1) or some NaN (NaN).
 template <typename T, int D, int QC>
 __device__ __forceinline__ void forward_rows(const AttnArgs& p, const Place& at, int row0, int live, bool any,
                                              const float (&m)[QC], const float (&l)[QC],
@@ -26,7 +27,7 @@ __device__ __forceinline__ void forward_rows(const AttnArgs& p, const Place& at,
                     *reinterpret_cast<f32x4*>(p.part + to * pitch_of(D) + KS * e + E * g + 4 * u) = o[c][e][u];
             if (g == 0) {
                 p.part_stat[2 * to] = m[c];
-                p.part_stat[2 * to + 1] = any && m[c] == -INFINITY ? NAN : l[c];
+                p.part_stat[2 * to + 1] = any && m[c] == -INFINITY && l[c] == 0.f ? -1.f : l[c];
             }
             continue;
         }
@@ -45,8 +46,9 @@ __device__ __forceinline__ void forward_rows(const AttnArgs& p, const Place& at,
         }
         if (p.lse && g == 0)
             p.lse[w.stat(p, at.b)] =
-                empty || m[c] == -INFINITY ? -INFINITY
-                                           : (m[c] + __builtin_amdgcn_logf(l[c]) - Softmax<T>::kShift) * kLn2;
+                empty || (m[c] == -INFINITY && l[c] == 0.f)
+                    ? -INFINITY
+                    : (m[c] + __builtin_amdgcn_logf(l[c]) - Softmax<T>::kShift) * kLn2;
     }
 }
 
@@ -83,10 +85,8 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p) {
         const float mi = stat[(int64_t)2 * rows * i], li = stat[(int64_t)2 * rows * i + 1];
         const float w = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mi - m);
         const f32x4 o = *reinterpret_cast<const f32x4*>(part + (int64_t)rows * D * i);
-        if (mi != -INFINITY || m == -INFINITY) {
-            l = fmaf(w, li, l);
-            sum += o * w;
-        }
+        l = fmaf(w, li, l);
+        sum += o * w;
     }
     s_sum[threadIdx.x] = sum;
     s_l[threadIdx.x] = l;
@@ -99,15 +99,16 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p) {
     }
     const int b = (int)(problem / p.kv_heads), hk = (int)(problem - (int64_t)b * p.kv_heads);
     const Row w(p, hk, row, true);
-    const bool empty = row >= live_rows(p, b) || (m == -INFINITY && l == 0.f);  // NaN: logits of -infinity
-    const float inv = __builtin_amdgcn_rcpf(l);
+    const bool empty = row >= live_rows(p, b) || (m == -INFINITY && l == 0.f);
+    const float inv = m == -INFINITY ? NAN : __builtin_amdgcn_rcpf(l);
     T* out = static_cast<T*>(p.out) + w.whole(p, b) * p.d;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         if (4 * col + j < p.d) out[4 * col + j] = empty ? (T)0.f : (T)(sum[j] * inv);
     if (p.lse && col == 0)
         p.lse[w.stat(p, b)] =
-            empty || m == -INFINITY ? -INFINITY : (m + __builtin_amdgcn_logf(l) - Softmax<T>::kShift) * kLn2;
+            empty || (m == -INFINITY && l < 0.f) ? -INFINITY
+                                                 : (m + __builtin_amdgcn_logf(l) - Softmax<T>::kShift) * kLn2;
 }
 
 // What a wave's rows have come to: sums relative to a reference, which trails the maximum.  Whether it has to move is
@@ -305,8 +306,7 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 512 ? 1 : 2)) void k_at
         top[c] = fmaxf(fmaxf(s_m[0][row], s_m[1][row]), fmaxf(s_m[2][row], s_m[3][row]));
         sum[c] = 0.f;
         for (int i = 0; i < 4; ++i)
-            if (s_m[i][row] != -INFINITY)
-                sum[c] = fmaf(__builtin_amdgcn_exp2f(s_m[i][row] - top[c]), s_l[i][row], sum[c]);
+            sum[c] = fmaf(top[c] == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(s_m[i][row] - top[c]), s_l[i][row], sum[c]);
         const float by = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top[c]);
 #pragma unroll
         for (int e = 0; e < A::kPairs; ++e)

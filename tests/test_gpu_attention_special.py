@@ -54,3 +54,79 @@ def test_masked_keys_have_zero_gradients_beside_infinite_rows(size, scale, dtype
             got = attention.run(*ins, (mask, None, None), scale)
             for grad in got[3:]:
                 assert not bits(grad[~mask]).any(), (bad, which)
+
+
+def forward(q, k, v, mask=None, scale=None):
+    from differentiable_gaussian_splatting_dgs_amd import network
+    print("forward", tuple(q.shape), tuple(k.shape), q.dtype, mask is not None, scale, flush=True)
+    got = network.cross_attention_forward(q, k, v, mask, None, None, scale)
+    torch.cuda.synchronize()
+    return got
+
+
+# with keys [from, to) that are infinite or NaN, and how many on either side of them are masked: whole splits (of 1024 keys
+# at most) of few and of many rows, all keys of one wave of a block of few rows, all tiles of a block but the first and last
+RUNS = [((1, 3, 6000, 4, 2, 64), 2100, 3900, 1024), ((1, 20, 9000, 2, 2, 40), 0, 4500, 1024),
+        ((1, 100, 6000, 1, 1, 64), 2200, 6000, 1024), ((1, 100, 6000, 1, 1, 100), 1200, 4000, 1024),
+        ((1, 3, 6000, 4, 2, 64), 1500, 2500, 0), ((1, 1, 256, 2, 2, 64), 64, 128, 0), ((2, 20, 300, 2, 2, 128), 0, 128, 0),
+        ((1, 70, 500, 2, 1, 64), 64, 448, 0), ((16, 700, 64, 32, 32, 32), 0, 32, 0)]
+
+
+def around(size, first, last, margin):
+    mask = torch.ones(size[0], size[2], dtype=torch.bool, device="cuda")
+    mask[:, max(0, first - margin):first] = mask[:, last:last + margin] = False
+    return mask if margin else None
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("size,first,last,margin", RUNS)
+def test_nan_keys_reach_every_row(size, first, last, margin, dtype):
+    """Whatever shares the keys out: NaN in out and lse of the heads that read them, the others' bits as without."""
+    q, k, v, _ = attention.inputs(size, dtype)
+    mask = around(size, first, last, margin)
+    want = forward(q, k, v, mask)
+    k[:, first:last, 0, 1] = float("nan")
+    out, lse = forward(q, k, v, mask)
+    group = size[3] // size[4]
+    assert out[:, :, :group].isnan().all() and lse[:, :group].isnan().all()
+    assert torch.equal(out[:, :, group:], want[0][:, :, group:]) and torch.equal(lse[:, group:], want[1][:, group:])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("size,first,last,margin", RUNS)
+def test_nan_queries_have_nan_sums(size, first, last, margin, dtype):
+    """The row alone; others keep their bounds, not their bits: the rows of a wave move their references together."""
+    q, k, v, dout = attention.inputs(size, dtype)
+    mask = around(size, first, last, margin)
+    want = attention.exact(q, k, v, dout, mask, None, None, size[5] ** -0.5)
+    q[0, size[1] - 1, 0, 1] = float("nan")
+    got = forward(q, k, v, mask)
+    for g, w, row in zip(got, want, (got[0][0, -1, 0], got[1][0, 0, -1])):
+        assert row.isnan().all() and int(g.isnan().sum()) == row.numel()
+        attention.check(torch.where(g.isnan(), w[0], g.double()), w, (size, dtype))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("size,first,last,margin", RUNS)
+def test_keys_of_minus_infinite_logits(size, first, last, margin, dtype):
+    """Their weights are 0, of all splits' but theirs and of their own; 0 times a NaN value is NaN, as in a product; a
+    row of nothing else is 0 / 0, and the log of its sum -infinity."""
+    batch, nq, nk, heads, kv_heads, d = size
+    q, k, v, dout = attention.inputs(size, dtype)
+    q[..., 0] = q[..., 0].abs() + 0.5
+    mask = around(size, first, last, margin)
+    rest = torch.ones(batch, nk, dtype=torch.bool, device="cuda") if mask is None else mask.clone()
+    rest[:, first:last] = False
+    want = attention.exact(q, k, v, dout, rest, None, None, d ** -0.5)
+    k[:, first:last, :, 0] = -float("inf")
+    out, lse = forward(q, k, v, mask)
+    attention.check(out, want[0], ("out", size))
+    attention.check(lse, want[1], ("lse", size))
+    v[:, first:last, 0, 2] = float("nan")
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[:, :, :heads // kv_heads, 2] = True
+    again, same = forward(q, k, v, mask)
+    assert torch.equal(again.isnan(), bad) and torch.equal(same, lse)
+    k[..., 0] = -float("inf")
+    out, lse = forward(q, k, v, mask)
+    assert out.isnan().all() and torch.isneginf(lse).all()
