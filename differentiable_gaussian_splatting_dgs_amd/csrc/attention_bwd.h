@@ -43,18 +43,25 @@ __global__ __launch_bounds__(256) void k_attn_sum(AttnArgs p) {
 // error sqrt(2) of what rounding the result alone makes it (float16, 1000 keys: 0.00029 for 0.00021).  Where the result's
 // rounding enters delta, it moves all of a row's ds alike and takes dq along the mean key: 0.00032 at 60 keys and
 // 0.00043 at 4, so k_attn_held, which has all keys at hand, sums P dP instead.
-// float16: both are held times 2^13 and, should a ds not fit then, scaled down with what is summed so far (Shrink).
+// float16: both are held times 2^13; should a ds not fit then, ds are scaled down with what is summed of them so far
+// (Shrink), and P stays as it is.
 template <typename T>
 struct Shrink {
     static constexpr bool kNeeded = false;
-    static constexpr float shift = 0.f;
+    static constexpr float kWeights = 0.f, shift = 0.f;  // powers of two of P and of ds
+    static __device__ __forceinline__ bool moved() { return false; }
     template <typename Over>
     __device__ __forceinline__ void operator()(float, Over) {}
 };
 template <>
 struct Shrink<_Float16> {
     static constexpr bool kNeeded = true;
-    float shift = 13.f;
+    static constexpr float kWeights = 13.f;
+    float shift = kWeights;
+    // whether ds have another scale than P, the same in all lanes
+    __device__ __forceinline__ bool moved() const {
+        return __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, shift)) != __builtin_bit_cast(int, kWeights);
+    }
     // most: the lane's largest |ds| of this step; over(f) scales what the wave holds by f
     template <typename Over>
     __device__ __forceinline__ void operator()(float most, Over over) {
@@ -245,12 +252,13 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDq)) void k_attn_dq(Attn
 
 // The gradients of a lane's key: the results, or those of a split.
 template <typename T, int D>
-__device__ __forceinline__ void keys_out(const AttnArgs& p, const Place& at, int key, bool counts, float by,
+__device__ __forceinline__ void keys_out(const AttnArgs& p, const Place& at, int key, bool counts, float shift,
                                          const f32x4 (&dk)[AttnTile<T, D>::kPairs][Tile<T>::TG],
                                          const f32x4 (&dv)[AttnTile<T, D>::kPairs][Tile<T>::TG], int lane) {
     constexpr int E = Tile<T>::E, KS = Tile<T>::KS, TG = Tile<T>::TG;
     const int g = lane >> 4;
     if (key >= p.nk) return;
+    const float by_k = p.scale * __builtin_amdgcn_exp2f(-shift), by_v = __builtin_amdgcn_exp2f(-Shrink<T>::kWeights);
     if (p.splits > 1) {
         float* to = p.part + (at.part(p, p.nk) + key) * pitch_of(D);
         float* to_v = to + (int64_t)p.batch * p.kv_heads * p.splits * p.nk * pitch_of(D);
@@ -259,8 +267,8 @@ __device__ __forceinline__ void keys_out(const AttnArgs& p, const Place& at, int
 #pragma unroll
             for (int u = 0; u < TG; ++u) {
                 const int k = KS * e + E * g + 4 * u;
-                *reinterpret_cast<f32x4*>(to + k) = counts ? dk[e][u] * (by * p.scale) : f32x4{};
-                *reinterpret_cast<f32x4*>(to_v + k) = counts ? dv[e][u] * by : f32x4{};
+                *reinterpret_cast<f32x4*>(to + k) = counts ? dk[e][u] * by_k : f32x4{};
+                *reinterpret_cast<f32x4*>(to_v + k) = counts ? dv[e][u] * by_v : f32x4{};
             }
         return;
     }
@@ -272,8 +280,8 @@ __device__ __forceinline__ void keys_out(const AttnArgs& p, const Place& at, int
         for (int u = 0; u < TG; ++u)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                a[4 * u + j] = counts ? (T)(dk[e][u][j] * (by * p.scale)) : (T)0.f;
-                b[4 * u + j] = counts ? (T)(dv[e][u][j] * by) : (T)0.f;
+                a[4 * u + j] = counts ? (T)(dk[e][u][j] * by_k) : (T)0.f;
+                b[4 * u + j] = counts ? (T)(dv[e][u][j] * by_v) : (T)0.f;
             }
         if (p.dk) store_run(static_cast<T*>(p.dk) + row, KS * e + E * g, p.d, a);
         if (p.dv) store_run(static_cast<T*>(p.dv) + row, KS * e + E * g, p.d, b);
@@ -381,10 +389,17 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDkv)) void k_attn_dkv(At
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int c = 0; c < KC; ++c) {
-                        const float w = __builtin_amdgcn_exp2f(fmaf(s[c][u][j], c2, shrink.shift - lse[j]));
+                        const float w = __builtin_amdgcn_exp2f(fmaf(s[c][u][j], c2, Shrink<T>::kWeights - lse[j]));
                         s[c][u][j] = w;
                         dp[c][u][j] = w * (dp[c][u][j] - delta[j]);
                     }
+            }
+            if (shrink.moved()) {
+                const float f = __builtin_amdgcn_exp2f(shrink.shift - Shrink<T>::kWeights);
+#pragma unroll
+                for (int c = 0; c < KC; ++c)
+#pragma unroll
+                    for (int u = 0; u < TG; ++u) dp[c][u] *= f;
             }
             if (valid != ~0ull >> (64 - RT))
 #pragma unroll
@@ -410,11 +425,11 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDkv)) void k_attn_dkv(At
 #pragma unroll
                 for (int c = 0; c < KC; ++c) {
 #pragma unroll
-                    for (int u = 0; u < TG; ++u) s[c][u] *= f, dp[c][u] *= f;
+                    for (int u = 0; u < TG; ++u) dp[c][u] *= f;
 #pragma unroll
                     for (int e = 0; e < A::kPairs; ++e)
 #pragma unroll
-                        for (int u = 0; u < TG; ++u) dk[c][e][u] *= f, dv[c][e][u] *= f;
+                        for (int u = 0; u < TG; ++u) dk[c][e][u] *= f;
                 }
             });
             Frag w[KC], ds[KC];
@@ -442,9 +457,8 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDkv)) void k_attn_dkv(At
             place((t + 1) & 1, valid);
         }
     }
-    const float by = __builtin_amdgcn_exp2f(-shrink.shift);
 #pragma unroll
-    for (int c = 0; c < KC; ++c) keys_out<T, D>(p, at, key0 + 16 * c + r, counts[c], by, dk[c], dv[c], lane);
+    for (int c = 0; c < KC; ++c) keys_out<T, D>(p, at, key0 + 16 * c + r, counts[c], shrink.shift, dk[c], dv[c], lane);
 }
 
 // Columns [c0, c0 + 16) of keys [m0, m0 + KS) of a tile of keys down and RT rows across: lane (r, g) has row c0 + r,
@@ -583,7 +597,8 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::occ_held(KC))) void k_attn_h
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int c = 0; c < KC; ++c)
-                        s[rg][c][u][j] = __builtin_amdgcn_exp2f(fmaf(s[rg][c][u][j], c2, shrink.shift - lse[j]));
+                        s[rg][c][u][j] =
+                            __builtin_amdgcn_exp2f(fmaf(s[rg][c][u][j], c2, Shrink<T>::kWeights - lse[j]));
             }
             // rows and keys that do not count
 #pragma unroll
@@ -597,7 +612,7 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::occ_held(KC))) void k_attn_h
                             s[rg][c][u][j] = in ? s[rg][c][u][j] : 0.f;
                             dp[rg][c][u][j] = in ? dp[rg][c][u][j] : 0.f;
                         }
-            const float by = __builtin_amdgcn_exp2f(-shrink.shift);
+            const float by = __builtin_amdgcn_exp2f(-Shrink<T>::kWeights);
 #pragma unroll
             for (int u = 0; u < TG; ++u) {
                 f32x4 sum = s[rg][0][u] * dp[rg][0][u];
@@ -624,6 +639,13 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::occ_held(KC))) void k_attn_h
 #pragma unroll
                     for (int j = 0; j < 4; ++j) dp[rg][c][u][j] = s[rg][c][u][j] * (dp[rg][c][u][j] - delta[j]);
             }
+            if (shrink.moved()) {
+                const float f = __builtin_amdgcn_exp2f(shrink.shift - Shrink<T>::kWeights);
+#pragma unroll
+                for (int c = 0; c < KC; ++c)
+#pragma unroll
+                    for (int u = 0; u < TG; ++u) dp[rg][c][u] *= f;
+            }
             float most = 0.f;
             if constexpr (Shrink<T>::kNeeded)
 #pragma unroll
@@ -636,15 +658,11 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::occ_held(KC))) void k_attn_h
 #pragma unroll
                 for (int c = 0; c < KC; ++c) {
 #pragma unroll
-                    for (int u = 0; u < TG; ++u) {
-                        dp[rg][c][u] *= f;
-#pragma unroll
-                        for (int i = 0; i < NG; ++i) s[i][c][u] *= f;  // the next groups' too
-                    }
+                    for (int u = 0; u < TG; ++u) dp[rg][c][u] *= f;
 #pragma unroll
                     for (int e = 0; e < A::kPairs; ++e)
 #pragma unroll
-                        for (int u = 0; u < TG; ++u) dk[c][e][u] *= f, dv[c][e][u] *= f;
+                        for (int u = 0; u < TG; ++u) dk[c][e][u] *= f;
                 }
                 rescale(f, rg);  // what this tile's earlier groups have left for dq
             });
@@ -683,7 +701,7 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::occ_held(KC))) void k_attn_h
 #pragma unroll
                         for (int e = 0; e < A::kPairs; ++e)
 #pragma unroll
-                            for (int u = 0; u < TG; ++u) dk[c][e][u] *= f, dv[c][e][u] *= f;
+                            for (int u = 0; u < TG; ++u) dk[c][e][u] *= f;
                     shrink.shift = low;
                 }
                 __syncthreads();
@@ -727,9 +745,9 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::occ_held(KC))) void k_attn_h
             static_cast<T*>(p.dq)[Row(p, at.hk, row, true).whole(p, at.b) * d + (i - (int64_t)row * p.d)] = (T)0.f;
         }
     }
-    const float by = __builtin_amdgcn_exp2f(-shrink.shift);
 #pragma unroll
-    for (int c = 0; c < KC; ++c) keys_out<T, D>(p, at, (wave * KC + c) * 16 + r, counts[c], by, dk[c], dv[c], lane);
+    for (int c = 0; c < KC; ++c)
+        keys_out<T, D>(p, at, (wave * KC + c) * 16 + r, counts[c], shrink.shift, dk[c], dv[c], lane);
 }
 
 // The gradients of few rows: 16 QC of them, with all keys of a split, in tiles that the waves of a block share out.
@@ -868,7 +886,6 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_at
             }
         }
         if (k0 + parts * KS < end) fetch(k0 + parts * KS);
-        float most = 0.f;
 #pragma unroll
         for (int u = 0; u < TG; ++u) {
             const bool key_in = valid >> (16 * u + r) & 1;
@@ -877,17 +894,32 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_at
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const bool in = key_in && 16 * c + 4 * g + j < live;
-                    const float w = in ? __builtin_amdgcn_exp2f(fmaf(s[u][c][j], c2, shrink.shift - lse[c][j])) : 0.f;
+                    const float w =
+                        in ? __builtin_amdgcn_exp2f(fmaf(s[u][c][j], c2, Shrink<T>::kWeights - lse[c][j])) : 0.f;
                     s[u][c][j] = w;
                     dp[u][c][j] = in ? w * (dp[u][c][j] - delta[c][j]) : 0.f;
-                    if (Shrink<T>::kNeeded) most = fmaxf(most, fabsf(dp[u][c][j]));
                 }
         }
+        if (shrink.moved()) {
+            const float f = __builtin_amdgcn_exp2f(shrink.shift - Shrink<T>::kWeights);
+#pragma unroll
+            for (int u = 0; u < TG; ++u)
+#pragma unroll
+                for (int c = 0; c < QC; ++c) dp[u][c] *= f;
+        }
+        float most = 0.f;
+        if constexpr (Shrink<T>::kNeeded)
+#pragma unroll
+            for (int u = 0; u < TG; ++u)
+#pragma unroll
+                for (int c = 0; c < QC; ++c)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) most = fmaxf(most, fabsf(dp[u][c][j]));
         shrink(most, [&](float f) {
 #pragma unroll
             for (int c = 0; c < QC; ++c) {
 #pragma unroll
-                for (int u = 0; u < TG; ++u) s[u][c] *= f, dp[u][c] *= f;
+                for (int u = 0; u < TG; ++u) dp[u][c] *= f;
 #pragma unroll
                 for (int e = 0; e < A::kPairs; ++e)
 #pragma unroll
@@ -917,7 +949,8 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_at
                 *reinterpret_cast<Quad*>(tds + (16 * u + r) * F::kPitch + (16 * c + 4 * g) * (int)sizeof(T)) = quad;
             }
         wave_sync();
-        const float by = __builtin_amdgcn_exp2f(-shrink.shift);
+        const float by_k = p.scale * __builtin_amdgcn_exp2f(-shrink.shift);
+        const float by_v = __builtin_amdgcn_exp2f(-Shrink<T>::kWeights);
 #pragma unroll
         for (int e = 0; e < A::kPairs; ++e) {
             f32x4 gk[TG][TG] = {}, gv[TG][TG] = {};  // of key tile, column tile
@@ -941,8 +974,8 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_at
                 for (int t = 0; t < TG; ++t)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        a[4 * t + j] = (T)(gk[u][t][j] * (by * p.scale));
-                        b[4 * t + j] = (T)(gv[u][t][j] * by);
+                        a[4 * t + j] = (T)(gk[u][t][j] * by_k);
+                        b[4 * t + j] = (T)(gv[u][t][j] * by_v);
                     }
                 // a key that does not count: its weights of 0 times an infinite row are NaN
                 if (valid != ~0ull >> (64 - KS) && !(valid >> (16 * u + r) & 1)) a = Frag{}, b = Frag{};

@@ -130,3 +130,20 @@ def test_keys_of_minus_infinite_logits(size, first, last, margin, dtype):
     k[..., 0] = -float("inf")
     out, lse = forward(q, k, v, mask)
     assert out.isnan().all() and torch.isneginf(lse).all()
+
+
+# rows and keys of each of the backward's kernels
+BACK = [(1, 8, 500, 2, 2, 64), (1, 20, 150, 2, 1, 40), (1, 100, 100, 1, 1, 64), (1, 100, 60, 2, 1, 32),
+        (1, 100, 300, 1, 1, 64), (2, 100, 300, 2, 1, 100)]
+
+
+@pytest.mark.parametrize("size", BACK)
+def test_large_gradients_in_float16_cost_the_weights_nothing(size):
+    """dv = P^T dout is the same, bit for bit, whatever the values and with them ds are."""
+    q, k, v, dout = attention.inputs(size, torch.float16)
+    dout[:, 0] *= 4000.0
+    small = attention.run(q, k, v * 2.0 ** -10, dout, (None, None, None))
+    large = attention.run(q, k, v * 1000.0, dout, (None, None, None))
+    attention.check(small[4], attention.exact(q, k, torch.zeros_like(v), dout, None, None, None, size[5] ** -0.5)[4],
+                    ("dv", size))
+    assert torch.equal(small[4], large[4])
