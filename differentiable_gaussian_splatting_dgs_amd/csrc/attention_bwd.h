@@ -50,8 +50,8 @@ struct Shrink {
     static constexpr bool kNeeded = false;
     static constexpr float kWeights = 0.f, shift = 0.f;  // powers of two of P and of ds
     static __device__ __forceinline__ bool moved() { return false; }
-    template <typename Over>
-    __device__ __forceinline__ void operator()(float, Over) {}
+    template <typename Each, typename Over>
+    __device__ __forceinline__ void operator()(Each, Over) {}
 };
 template <>
 struct Shrink<_Float16> {
@@ -62,11 +62,15 @@ struct Shrink<_Float16> {
     __device__ __forceinline__ bool moved() const {
         return __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, shift)) != __builtin_bit_cast(int, kWeights);
     }
-    // most: the lane's largest |ds| of this step; over(f) scales what the wave holds by f
-    template <typename Over>
-    __device__ __forceinline__ void operator()(float most, Over over) {
+    // each(f) calls f with the lane's ds of this step that count; over(f) scales what the wave holds of ds by f.
+    // Infinities and NaN stay what they are, and what is beside them in a lane, of another row, is scaled to fit.
+    template <typename Each, typename Over>
+    __device__ __forceinline__ void operator()(Each each, Over over) {
+        float most = 0.f;
+        each([&](float v) { most = fmaxf(most, fabsf(v)); });
         if (!__any(most > 32768.f)) return;
-        most = most < INFINITY ? most : 0.f;  // infinities and NaN stay what they are
+        most = 0.f;
+        each([&](float v) { most = fabsf(v) < INFINITY ? fmaxf(most, fabsf(v)) : most; });
         for (int o = 1; o < 64; o <<= 1) most = fmaxf(most, __shfl_xor(most, o, 64));
         const int by = most > 16384.f ? ilogbf(most) - 13 : 0;
         over(ldexpf(1.f, -by));
@@ -181,15 +185,15 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDq)) void k_attn_dq(Attn
 #pragma unroll
                         for (int c = 0; c < QC; ++c) s[c][u][j] = in ? s[c][u][j] : 0.f;
                     }
-            float most = 0.f;
-            if constexpr (Shrink<T>::kNeeded)
+            auto each = [&](auto f) {
 #pragma unroll
                 for (int c = 0; c < QC; ++c)
 #pragma unroll
                     for (int u = 0; u < TG; ++u)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) most = fmaxf(most, fabsf(s[c][u][j]));
-            shrink(most, [&](float f) {
+                        for (int j = 0; j < 4; ++j) f(s[c][u][j]);
+            };
+            shrink(each, [&](float f) {
 #pragma unroll
                 for (int c = 0; c < QC; ++c) {
 #pragma unroll
@@ -413,15 +417,15 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::kOccDkv)) void k_attn_dkv(At
                             dp[c][u][j] = in ? dp[c][u][j] : 0.f;
                         }
                     }
-            float any = 0.f;  // keys that do not count have weights that mean nothing
-            if constexpr (Shrink<T>::kNeeded)
+            auto each = [&](auto f) {  // keys that do not count have weights that mean nothing
 #pragma unroll
                 for (int c = 0; c < KC; ++c)
 #pragma unroll
                     for (int u = 0; u < TG; ++u)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) any = fmaxf(any, counts[c] ? fabsf(dp[c][u][j]) : 0.f);
-            shrink(any, [&](float f) {
+                        for (int j = 0; j < 4; ++j) f(counts[c] ? dp[c][u][j] : 0.f);
+            };
+            shrink(each, [&](float f) {
 #pragma unroll
                 for (int c = 0; c < KC; ++c) {
 #pragma unroll
@@ -646,15 +650,15 @@ __global__ __launch_bounds__(256, (AttnShape<T, D>::occ_held(KC))) void k_attn_h
 #pragma unroll
                     for (int u = 0; u < TG; ++u) dp[rg][c][u] *= f;
             }
-            float most = 0.f;
-            if constexpr (Shrink<T>::kNeeded)
+            auto each = [&](auto f) {
 #pragma unroll
                 for (int c = 0; c < KC; ++c)
 #pragma unroll
                     for (int u = 0; u < TG; ++u)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) most = fmaxf(most, fabsf(dp[rg][c][u][j]));
-            shrink(most, [&](float f) {
+                        for (int j = 0; j < 4; ++j) f(dp[rg][c][u][j]);
+            };
+            shrink(each, [&](float f) {
 #pragma unroll
                 for (int c = 0; c < KC; ++c) {
 #pragma unroll
@@ -907,15 +911,15 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_at
 #pragma unroll
                 for (int c = 0; c < QC; ++c) dp[u][c] *= f;
         }
-        float most = 0.f;
-        if constexpr (Shrink<T>::kNeeded)
+        auto each = [&](auto f) {
 #pragma unroll
             for (int u = 0; u < TG; ++u)
 #pragma unroll
                 for (int c = 0; c < QC; ++c)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) most = fmaxf(most, fabsf(dp[u][c][j]));
-        shrink(most, [&](float f) {
+                    for (int j = 0; j < 4; ++j) f(dp[u][c][j]);
+        };
+        shrink(each, [&](float f) {
 #pragma unroll
             for (int c = 0; c < QC; ++c) {
 #pragma unroll

@@ -147,3 +147,15 @@ def test_large_gradients_in_float16_cost_the_weights_nothing(size):
     attention.check(small[4], attention.exact(q, k, torch.zeros_like(v), dout, None, None, None, size[5] ** -0.5)[4],
                     ("dv", size))
     assert torch.equal(small[4], large[4])
+
+
+@pytest.mark.parametrize("size", BACK)
+def test_an_infinite_gradient_in_float16_leaves_large_ones_finite(size):
+    """A row whose ds have to be scaled down beside one whose ds are infinite."""
+    q, k, v, dout = attention.inputs(size, torch.float16)
+    dout[:, 16 // (size[3] // size[4]) if size[1] > 32 and size[2] > 128 else 1] *= 100.0  # of the lane that has row 0
+    dout[:, 0] = 0.0
+    want = attention.exact(q, k, v, dout, None, None, None, size[5] ** -0.5)
+    dout[:, 0, 0, 3] = float("inf")
+    got = attention.run(q, k, v, dout, (None, None, None))
+    attention.check(got[2][:, 1:], [t[:, 1:] for t in want[2]], ("dq", size))
