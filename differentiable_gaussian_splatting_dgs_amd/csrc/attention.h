@@ -227,9 +227,12 @@ struct Mover {
 #pragma unroll
             for (int i = 0; i < A::kEach; ++i)
                 if (MODE == WHOLE || column(i) < d)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // m0 is nobody's to keep, but what the compiler does with it must know
                     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(run + i * 4096),
                                  "v"(at[i]), "s"(from)
-                                 : "memory");
+                                 : "memory", "m0");
+#pragma clang diagnostic pop
         } else {
 #pragma unroll
             for (int i = 0; i < A::kEach; ++i)
