@@ -819,6 +819,8 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_at
     int k0 = first + part * KS;
     const int end = live > 0 ? keys.count : 0;
     if (k0 < end) fetch(k0);
+    // all keys in one tile of each wave (and so one split, of one head a block): delta is summed from P dP
+    const bool whole = p.nk <= 4 * KS;
     // fragments down the rows: element 4 c + j (float32: j of part c) is row 16 c + 4 g + j
     for (int i = threadIdx.x; i < heads * 2 * (D / 16) * F::kParts * 64; i += 256) {
         const int l = i & 63, step = (i >> 6) % F::kParts, tile = (i >> 6) / F::kParts % (D / 16);
@@ -840,38 +842,41 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_at
     Frag q[QC][A::kSteps], dout[QC][A::kSteps];
     rows_held<T, MODE>(p, at.b, at.hk, 0, live, p.q, p.q_b, p.q_n, p.q_h, p.scale < 0.f, lane, q);
     rows_held<T, MODE>(p, at.b, at.hk, 0, live, p.dout, p.g_b, p.g_n, p.g_h, false, lane, dout);
-    if (part == 0) {
+    if (part == 0 && g == 0)
+#pragma unroll
+        for (int c = 0; c < QC; ++c) {
+            const bool in = 16 * c + r < live;
+            s_lse[own][16 * c + r] = in ? p.lse[Row(p, at.hk, 16 * c + r, in).stat(p, at.b)] * kLog2e : 0.f;
+        }
+    if (part == 0 && !whole) {
         Frag out[QC][A::kSteps];
         const int64_t row = p.d, query = row * p.heads;
         rows_held<T, MODE>(p, at.b, at.hk, 0, live, p.out, query * p.nq, query, row, false, lane, out);
 #pragma unroll
         for (int c = 0; c < QC; ++c) {
-            const bool in = 16 * c + r < live;
             float sum = 0.f;
 #pragma unroll
             for (int s = 0; s < A::kSteps; ++s)
 #pragma unroll
                 for (int j = 0; j < E; ++j) sum = fmaf((float)dout[c][s][j], (float)out[c][s][j], sum);
             sum = added(sum);
-            if (g == 0) {
-                s_lse[own][16 * c + r] = in ? p.lse[Row(p, at.hk, 16 * c + r, in).stat(p, at.b)] * kLog2e : 0.f;
-                s_delta[own][16 * c + r] = sum;
-            }
+            if (g == 0) s_delta[own][16 * c + r] = sum;
         }
     }
     __syncthreads();
-    f32x4 lse[QC], delta[QC];
+    f32x4 lse[QC], delta[QC] = {};
 #pragma unroll
     for (int c = 0; c < QC; ++c) {
         lse[c] = *reinterpret_cast<const f32x4*>(&s_lse[own][16 * c + 4 * g]);
-        delta[c] = *reinterpret_cast<const f32x4*>(&s_delta[own][16 * c + 4 * g]);
+        if (!whole) delta[c] = *reinterpret_cast<const f32x4*>(&s_delta[own][16 * c + 4 * g]);
     }
     f32x4 dq[QC][A::kPairs][TG] = {};
     Shrink<T> shrink;
     const int64_t out_n = (int64_t)p.kv_heads * p.d;
     T* dk_base = static_cast<T*>(p.dk) + (int64_t)at.b * p.nk * out_n + at.hk * p.d;
     T* dv_base = static_cast<T*>(p.dv) + (int64_t)at.b * p.nk * out_n + at.hk * p.d;
-    for (; k0 < end; k0 += parts * KS) {
+    // whole: every wave once, to meet the others; without keys its tile is zeros and nothing is stored
+    for (const int stop = whole ? max(end, k0 + 1) : end; k0 < stop; k0 += parts * KS) {
         const uint64_t valid = __ballot(byte != 0);
         f32x4 s[TG][QC] = {}, dp[TG][QC] = {};
 #pragma unroll
@@ -890,20 +895,45 @@ __global__ __launch_bounds__(256, (D * (int)sizeof(T) >= 256 ? 1 : 2)) void k_at
             }
         }
         if (k0 + parts * KS < end) fetch(k0 + parts * KS);
+        auto counts = [&](int u, int c, int j) { return (valid >> (16 * u + r) & 1) && 16 * c + 4 * g + j < live; };
 #pragma unroll
-        for (int u = 0; u < TG; ++u) {
-            const bool key_in = valid >> (16 * u + r) & 1;
+        for (int u = 0; u < TG; ++u)
 #pragma unroll
             for (int c = 0; c < QC; ++c)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bool in = key_in && 16 * c + 4 * g + j < live;
-                    const float w =
-                        in ? __builtin_amdgcn_exp2f(fmaf(s[u][c][j], c2, Shrink<T>::kWeights - lse[c][j])) : 0.f;
-                    s[u][c][j] = w;
-                    dp[u][c][j] = in ? w * (dp[u][c][j] - delta[c][j]) : 0.f;
-                }
+                for (int j = 0; j < 4; ++j)
+                    s[u][c][j] = counts(u, c, j)
+                                     ? __builtin_amdgcn_exp2f(fmaf(s[u][c][j], c2, Shrink<T>::kWeights - lse[c][j]))
+                                     : 0.f;
+        if (whole) {
+            const float by = __builtin_amdgcn_exp2f(-Shrink<T>::kWeights);
+#pragma unroll
+            for (int c = 0; c < QC; ++c) {
+                f32x4 sum = {};
+#pragma unroll
+                for (int u = 0; u < TG; ++u)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        sum[j] = counts(u, c, j) ? fmaf(s[u][c][j], dp[u][c][j], sum[j]) : sum[j];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum[j] = over_row(sum[j]) * by;
+                if (r == 0) *reinterpret_cast<f32x4*>(&s_delta[wave][16 * c + 4 * g]) = sum;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int c = 0; c < QC; ++c) {
+                delta[c] = *reinterpret_cast<const f32x4*>(&s_delta[0][16 * c + 4 * g]);
+#pragma unroll
+                for (int i = 1; i < 4; ++i) delta[c] += *reinterpret_cast<const f32x4*>(&s_delta[i][16 * c + 4 * g]);
+            }
         }
+#pragma unroll
+        for (int u = 0; u < TG; ++u)
+#pragma unroll
+            for (int c = 0; c < QC; ++c)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    dp[u][c][j] = counts(u, c, j) ? s[u][c][j] * (dp[u][c][j] - delta[c][j]) : 0.f;
         if (shrink.moved()) {
             const float f = __builtin_amdgcn_exp2f(shrink.shift - Shrink<T>::kWeights);
 #pragma unroll

@@ -159,3 +159,26 @@ def test_an_infinite_gradient_in_float16_leaves_large_ones_finite(size):
     dout[:, 0, 0, 3] = float("inf")
     got = attention.run(q, k, v, dout, (None, None, None))
     attention.check(got[2][:, 1:], [t[:, 1:] for t in want[2]], ("dq", size))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("nk", [2, 64, 128])
+@pytest.mark.parametrize("nq", [3, 12, 70])
+def test_delta_of_few_keys_is_not_rounded(nq, nk, dtype):
+    """Half of the keys have values of 1 + eps, half of 1, and all the same weight: out = 1 + eps / 2 is between two
+    numbers of the type, and ds = +-d eps / (2 nk) all of what its rounding would be taken for.  Two groups of keys, of
+    one element each: dq = +-d eps / 4 scale there.
+
+    P is within 2^-20 of 1 / nk (the log of the sum and an exp2 of about 1), and so are d P and delta; their difference
+    is eps / 2 of them, so that ds and what comes of it is within 2^-20 2 / eps, and two roundings of eps / 2 each and
+    some of float32, within 2 eps."""
+    eps, d = torch.finfo(dtype).eps, 64
+    q = torch.zeros(1, nq, 2, d, dtype=dtype, device="cuda")
+    k, v = torch.zeros(1, nk, 1, d, dtype=dtype, device="cuda"), torch.ones(1, nk, 1, d, dtype=dtype, device="cuda")
+    k[:, ::2, :, 0], k[:, 1::2, :, 1] = 1, 1
+    v[:, ::2] += eps
+    _, _, dq, dk, _ = attention.run(q, k, v, torch.ones_like(q), (None, None, None), 1.0)
+    want = torch.zeros_like(q, dtype=torch.float64)
+    want[..., 0], want[..., 1] = d * eps / 4, -d * eps / 4
+    attention.check(dq, (want, want.abs() * (2.0 ** -20 * 2 / eps + 2 * eps)), ("dq", nq, nk, dtype))
+    assert not dk.any()
