@@ -24,6 +24,12 @@ int check_shape(const gs_attention* a) {
     return GS_OK;
 }
 
+bool no_strides_below_zero(const gs_attention* a, bool back) {
+    for (int i = 0; i < 3; ++i)
+        if (a->q_stride[i] < 0 || a->k_stride[i] < 0 || a->v_stride[i] < 0 || (back && a->dout_stride[i] < 0)) return false;
+    return a->mask_stride >= 0;
+}
+
 bool aligned_to(const void* p, int size) { return (reinterpret_cast<uintptr_t>(p) & (size - 1)) == 0; }
 
 AttnArgs args_of(const gs_attention* a, const void* q, const void* k, const void* v, const uint8_t* mask,
@@ -63,7 +69,7 @@ extern "C" int gs_attention_fwd(const gs_attention* a, const void* q, const void
     int rc = check_shape(a);
     if (rc != GS_OK) return rc;
     if (a->batch == 0 || a->nq == 0) return GS_OK;
-    if (!q || !out || (a->nk > 0 && (!k || !v))) return GS_EINVAL;
+    if (!q || !out || (a->nk > 0 && (!k || !v)) || !no_strides_below_zero(a, false)) return GS_EINVAL;
     for (const void* t : {q, k, v, (const void*)out})
         if (!aligned_to(t, size_of(a->dtype))) return GS_EALIGN;
     for (const void* t : {(const void*)q_lengths, (const void*)k_lengths, (const void*)lse})
@@ -106,7 +112,7 @@ extern "C" int gs_attention_bwd(const gs_attention* a, const void* q, const void
     if (rc != GS_OK) return rc;
     if (a->batch == 0 || (a->nq == 0 && a->nk == 0)) return GS_OK;
     if (a->nq > 0 && (!q || !out || !lse || !dout)) return GS_EINVAL;
-    if (a->nk > 0 && (!k || !v)) return GS_EINVAL;
+    if ((a->nk > 0 && (!k || !v)) || !no_strides_below_zero(a, true)) return GS_EINVAL;
     for (const void* t : {q, k, v, out, dout, (const void*)dq, (const void*)dk, (const void*)dv})
         if (!aligned_to(t, size_of(a->dtype))) return GS_EALIGN;
     for (const void* t : {(const void*)q_lengths, (const void*)k_lengths, (const void*)lse})
