@@ -10,8 +10,8 @@ inline int size_of(int32_t dtype) { return dtype == GS_F32 ? 4 : 2; }
 
 int check_shape(const gs_attention* a) {
     if (!a || a->batch < 0 || a->nq < 0 || a->nk < 0 || a->heads < 1 || a->kv_heads < 1 || a->d < 1 ||
-        a->dtype < GS_F32 || a->dtype > GS_BF16 || a->heads % a->kv_heads != 0 || !isfinite(a->scale) ||
-        a->scale == 0.f)
+        a->dtype < GS_F32 || a->dtype > GS_BF16 || a->heads % a->kv_heads != 0 || a->scale == 0.f ||
+        !isfinite(a->scale * kLog2e))  // what the kernels multiply by
         return GS_EINVAL;
     // 64-row tiles of all problems are numbered in 24 bits, rows and keys in 31
     const int64_t most = (int64_t)1 << 30;

@@ -1025,6 +1025,7 @@ def gs_adam_step_clipped(tensors, beta1, beta2, eps, step, clip=None):
 # ---------------------------------------------------------------------------
 
 MAX_HEAD_DIM = 256
+MAX_SCALE = 2.35e38  # times log2 e a float32
 _like, _contiguous = torch.empty_like, torch.contiguous_format  # the quickest way to a new tensor
 _pack_attention = struct.Struct("=3q4i13qf4x").pack
 _pack_layer_norm = struct.Struct("=qii3qf4x").pack
@@ -1062,7 +1063,11 @@ def _attention_shape(q, k, v, scale):
         raise GsError(f"heads must have 1 to {MAX_HEAD_DIM} elements, got {d}")
     strides = (*_per_head(q, shape, dtype, device, "q"), *_per_head(k, k_shape, dtype, device, "k"),
                *_per_head(v, k_shape, dtype, device, "v"))
-    return shape, k_shape, code, device, d ** -0.5 if scale is None else float(scale), strides
+    if scale is None:
+        scale = d ** -0.5
+    elif not 0 < abs(scale := float(scale)) <= MAX_SCALE:
+        raise GsError(f"scale must be a number other than 0, of {MAX_SCALE:g} at most, got {scale}")
+    return shape, k_shape, code, device, scale, strides
 
 
 def _valid(mask, q_lengths, k_lengths, batch, nk, device):

@@ -740,7 +740,7 @@ int gs_adam_step_clipped(int32_t n_tensors, const gs_adam_tensor* tensors, float
  * a fixed order: results repeat bit for bit.
  * Limits: d <= GS_MAX_HEAD_DIM; nq heads / kv_heads and nk <= 2^30; 16e6 tiles of
  * 64 rows or keys over all batch items and heads of keys (GS_ECAPACITY).  scale:
- * finite and not 0.
+ * not 0, and finite times log2 e (2.35e38 at most).
  */
 #define GS_MAX_HEAD_DIM 256
 typedef struct gs_attention {

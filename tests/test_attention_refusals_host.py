@@ -3,8 +3,9 @@ before any device work."""
 import ctypes as C
 
 import pytest
+import torch
 
-from differentiable_gaussian_splatting_dgs_amd import gs
+from differentiable_gaussian_splatting_dgs_amd import gs, network
 from test_attention_host import FAKE, attention
 
 
@@ -33,3 +34,19 @@ def test_negative_strides(which, i):
 def test_negative_mask_stride():
     a = attention(mask_stride=-7)
     assert fwd(a) == -1 and bwd(a) == -1
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -3.4e38])
+def test_scales_that_overflow_times_log2_e(scale):
+    """exp is taken as exp2 of log2 e times the scale: infinity times a logit of 0 would be NaN."""
+    a = attention(scale=scale)
+    assert fwd(a) == -1 and bwd(a) == -1
+
+
+@pytest.mark.parametrize("scale", [2.4e38, 1e39, -1e300, float("inf"), float("nan"), 0, 0.0])
+def test_scales_from_python(scale, monkeypatch):
+    """The framework's error for every scale that the library refuses and for those that no float32 holds."""
+    q = torch.zeros(1, 2, 1, 8)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    with pytest.raises(gs.GsError, match="scale"):
+        network.cross_attention(q, q, q, scale=scale)
