@@ -520,17 +520,22 @@ AttnPlan plan_at(const AttnArgs& p) {
     const int64_t problems = (int64_t)p.batch * p.kv_heads, rows = (int64_t)p.nq * p.group;
     const size_t row_part = (size_t)problems * rows * pitch_of(D) * 4;
     const size_t key_part = (size_t)problems * p.nk * pitch_of(D) * 4;
-    // Few rows: the waves share out the keys and meet at the end alone.  bfloat16, 8 rows on 1M keys of 8 heads of 32:
-    // 248 us, by the block kernel 298; 20 on 20k of 4 of 64 18.1 and 21.8; 1 on 256 of 8 of 64 10.7 and 15.3,
-    // the latter two bound by the host.
+    // Few rows: the waves share out the keys and meet at the end alone.  On one GPU, by this kernel and by that of blocks:
+    // float32, 5 rows on 500k keys of 4 heads of 64 206 and 321 us, of 128 363 and 592; bfloat16, 8 rows on 1M keys of 8
+    // heads of 32 234 and 248, 32 rows, where the rule ends, 241 and 248; 8 on 20k of 4 of 64 14.7 and 15.1, 32 on 20k
+    // 16.0 and 15.5; 1 on 256 of 8 of 64 9.3 and 9.4.  Long bfloat16 keys of wider heads are slower by it: 8 on 1M of 4
+    // of 64 210 and 180, on 500k of 4 of 128 210 and 190.
     a.few = rows <= 16 ? 1 : rows <= 32 ? 2 : 0;
     a.fwd_qc = rows <= 64 * S::kFwd / 2 ? 1 : S::kFwd;
     a.dq_qc = rows <= 64 * S::kDq / 2 ? 1 : S::kDq;
     a.dkv_kc = p.nk <= 64 * S::kDkv / 2 ? 1 : S::kDkv;
     if (a.few) split(p.nk, problems, 1024, 512, 4 * FewTile<T, D>::kKeys, a.fwd_splits, a.fwd_per);
     else split(p.nk, problems * tiles_of(rows, 64 * a.fwd_qc), 512, 512, AttnTile<T, D>::kRows, a.fwd_splits, a.fwd_per);
-    // few keys and rows for two tiles a wave: blocks that keep the keys.  float16, 1M rows on 64 keys of 4 heads of 32:
-    // 142 us, by blocks of a tile of rows each 167
+    // Few keys and rows for two tiles a wave: blocks that keep the keys.  1M rows (64M / keys if that is less) of 4 heads,
+    // by this kernel and by blocks of a tile of rows each, us: bfloat16 of 32, 16 keys 127 and 187, 64 126 and 200, 128
+    // 88 and 105, 256 72 and 82, 512, where LDS ends it, 65 and 71; of 64, 16 203 and 219, 64 199 and 232, 256 102 and
+    // 106; of 128, 64 414 and 421, 128 241 and 274; float32 of 32, 16 198 and 222, 64 349 and 346, 128 327 and 318, 256
+    // 310 and 298.  Twice the blocks: 16 keys of 32 120 for 127, 64 129 for 126, the others within 4%.
     const int64_t key_tiles = tiles_of(p.nk, AttnTile<T, D>::kRows);
     if (!a.few && a.fwd_splits == 1 && key_tiles <= kThinTiles && key_tiles * 2 * AttnTile<T, D>::kBytes <= kThinBytes) {
         while (a.together < 2 && p.kv_heads % (2 << a.together) == 0 &&
@@ -543,17 +548,22 @@ AttnPlan plan_at(const AttnArgs& p) {
     split(p.nk, problems * tiles_of(rows, 64 * a.dq_qc), 512, 256, AttnTile<T, D>::kRows, a.dq_splits, a.dq_per);
     // 512 blocks are two a CU, what LDS and registers hold: more splits are more to join
     split(rows, problems * tiles_of(p.nk, 64 * a.dkv_kc), 512, 256, AttnTile<T, D>::kRows, a.dkv_splits, a.dkv_per);
-    // the backward of few rows in one pass over the keys: 8 rows on 1M keys of 8 heads of 32 bfloat16, with the forward,
-    // 869 us, by dq's and dkv's kernels 1170
+    // The backward of few rows in one pass over the keys, with the forward: 8 rows on 1M keys of 8 heads of 32 bfloat16
+    // 839 us, by dq's and dkv's kernels 1135; on 200k of 4 of 64 162 and 180, 32 rows 176 and 186, 20k keys 34 and 41
+    // (8 rows) and 39 and 43 (32); of 32 float32 149 and 249.
     a.few_back = a.few == 2 && sizeof(T) == 4 && D > 128 ? 0 : a.few;  // their tiles fill LDS
-    // heads of at most a line of memory: a wave each.  1M keys of 8 heads of 32 bfloat16 848 us against 896 (forward
-    // and backward), 200k of 4 of 64 162 against 175; of 128 326 against 335, and its tiles in LDS leave room for less
+    // Heads of at most a line of memory: a wave each.  The first of these 839 us against 887 with a block a head, 200k of
+    // 4 of 64 162 against 169, of 32 float32 149 against 166, near the rule's end 70k of 32 bfloat16 40 against 36; of
+    // 128 326 against 335, and its tiles in LDS leave room for less
     if (D * sizeof(T) <= 128 && p.nk >= kHeadsApart)
         while (a.few_heads < 2 && p.kv_heads % (2 << a.few_heads) == 0) ++a.few_heads;
     split(p.nk, problems >> a.few_heads, 1024, 64 * (4 >> a.few_heads), Tile<T>::KS * (4 >> a.few_heads),
           a.few_splits, a.few_per);
-    // few keys: both kernels' work in one pass over the rows.  1M rows on 64 keys of 4 heads of 32 bfloat16, with the
-    // forward, 446 us against 665; 100k on 256 of 64 468 against 377, so it stops at 128 keys
+    // Few keys: both kernels' work in one pass over the rows.  With the forward, 4 heads, by this kernel and by dq's and
+    // dkv's, us at 64, 96 and 128 keys: bfloat16, 1M rows of 32 444 and 596, 606 and 687, 590 and 715; 300k of 64 199
+    // and 301, 375 and 347, 365 and 361; 100k of 128 171 and 233, 219 and 276, 223 and 277; float32, 500k of 32 627 and
+    // 842, 1274 and 1236, 1367 and 1361; 200k of 64 479 and 670, 880 and 944, 952 and 1057.  100k on 256 of 64 bfloat16
+    // 468 against 377, so it stops at 128 keys.  Twice the blocks: 64 keys of 32 433 for 444, of 128 195 for 171.
     a.held = p.nk < 1 || a.few_back ? 0 : p.nk <= 64 ? 1 : p.nk <= 128 ? 2 : 0;
     if (a.held > S::kHeld) a.held = 0;
     split(rows, problems, 512, 4 * AttnTile<T, D>::kRows, AttnTile<T, D>::kRows, a.held_splits, a.held_per);

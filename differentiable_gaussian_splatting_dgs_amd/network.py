@@ -9,7 +9,9 @@ Plumbing over the C ABI (gs_linear_*, gs_layer_norm_*, gs_attention_*, gs_dropou
 gs_grad_*, gs_adam_step_clipped): buffers and the order of the calls.
 
 Record a backward pass into a graph while no eager autograd graph of the same leaves
-is alive: the recording may end the process otherwise.
+is alive.  For as long as one is, torch adds up a leaf's gradient on the stream where that
+graph was made; a backward pass recorded on another stream would have to wait for it, which
+a recording cannot, and the process may end.  Nothing that these functions see tells them.
 """
 from __future__ import annotations
 
