@@ -734,6 +734,8 @@ int gs_adam_step_clipped(int32_t n_tensors, const gs_adam_tensor* tensors, float
  * queries and keys that count, from the first on (clamped to 0 .. nq, nk).  What
  * does not count is not used, whatever it holds: its gradients are 0.  A query
  * that does not count, or has no key that does, gives out 0 and lse -infinity.
+ * NaN among its logits gives NaN in both, logits of -infinity alone NaN and
+ * -infinity.
  * Products and softmax are summed in float32; the weights, and in the backward
  * the gradients of s, enter their products rounded to the type (float16: scaled
  * into its range first).  Results are rounded once.  Sums are split and joined in

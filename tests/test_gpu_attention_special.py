@@ -182,3 +182,46 @@ def test_delta_of_few_keys_is_not_rounded(nq, nk, dtype):
     want[..., 0], want[..., 1] = d * eps / 4, -d * eps / 4
     attention.check(dq, (want, want.abs() * (2.0 ** -20 * 2 / eps + 2 * eps)), ("dq", nq, nk, dtype))
     assert not dk.any()
+
+
+def nan_expected(q, k, v, dout, valid):
+    """Where out, lse, dq, dk and dv are NaN by the definition: whatever a NaN that counts enters."""
+    mask, q_lengths, k_lengths = valid
+    batch, nq, heads, d = q.shape
+    nk, kv_heads = k.shape[1:3]
+    rows = torch.arange(nq, device="cuda") < (nq if q_lengths is None else q_lengths[:, None])
+    keys = torch.arange(nk, device="cuda") < (nk if k_lengths is None else k_lengths[:, None])
+    rows, keys = rows.expand(batch, nq), keys.expand(batch, nk) if mask is None else keys & mask
+    live = (rows & keys.any(1)[:, None])[..., None]
+
+    def by_query_head(t):
+        return t.repeat_interleave(heads // kv_heads, 1)[:, None]
+
+    def of_group(t):  # any row that shares the keys
+        return t.view(batch, nq, kv_heads, -1, *t.shape[3:]).any(3).any(1)[:, None]
+
+    in_k = (k.isnan().any(3) & keys[..., None]).any(1)
+    in_v = (v.isnan() & keys[..., None, None]).any(1)
+    in_dout = dout.isnan() & live[..., None]
+    P = (q.isnan().any(3) | by_query_head(in_k)) & live
+    dS = (P | in_dout.any(3) | by_query_head(in_v.any(2))) & live
+    return (P[..., None] | (by_query_head(in_v) & live[..., None]), P.transpose(1, 2), dS[..., None].expand_as(q),
+            (of_group(dS) & keys[..., None])[..., None].expand_as(k),
+            (of_group(P)[..., None] | of_group(in_dout)) & keys[..., None, None])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("size", [(2, 3, 900, 2, 1, 64), (1, 20, 100, 2, 2, 40), (2, 70, 100, 4, 2, 40), (2, 9, 1000, 4, 4, 7),
+                                  (2, 70, 300, 4, 2, 96), (1, 100, 6000, 1, 1, 64), (16, 700, 64, 32, 32, 32),
+                                  (1, 8, 70_001, 4, 4, 32)])
+def test_nan_goes_where_the_formulas_take_it(size, dtype):
+    """One NaN in q, k, v or dout, among what counts or not."""
+    for i, kind in enumerate(("all", "mask", "both")):
+        valid = attention.valid_of(kind, size, i)
+        for which in range(4):
+            ins = [t.contiguous() for t in attention.inputs(size, dtype, seed=i)]
+            t = ins[which]
+            t[0, t.shape[1] * (1 + i) // 4, t.shape[2] - 1, size[5] // 2] = float("nan")
+            got = attention.run(*ins, valid)
+            for name, g, want in zip(("out", "lse", "dq", "dk", "dv"), got, nan_expected(*ins, valid)):
+                assert torch.equal(g.isnan(), want.expand_as(g)), (kind, "qkvg"[which], name)
